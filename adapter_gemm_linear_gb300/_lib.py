@@ -127,6 +127,101 @@ SIGNATURES = [
     ("lora_kernel_launches", ctypes.c_uint64, []),
 ]
 
+
+# include/lora_attention.h
+
+KV_INT8 = 0
+KV_E4M3 = 1
+ROPE_MAX_PAIRS = 256
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [
+        ("ptr", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("rows", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_k_heads", ctypes.c_int32),
+        ("q", Heads),
+        ("q_out", Heads),
+        ("k", Heads),
+        ("k_out", Heads),
+        ("cos_table", ctypes.c_void_p),
+        ("sin_table", ctypes.c_void_p),
+        ("max_pos", ctypes.c_int32),
+        ("num_axes", ctypes.c_int32),
+        ("positions", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_char_p),
+        ("interleaved", ctypes.c_int32),
+        ("inverse", ctypes.c_int32),
+    ]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("format", ctypes.c_int),
+        ("num_pages", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+    ]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("max_pages", ctypes.c_int32),
+    ]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("num_q_heads", ctypes.c_int32),
+        ("q", Heads),
+        ("out", Heads),
+        ("lse", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("max_queries", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+_ROWS_ARGS = [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatch), ctypes.c_int, ctypes.POINTER(Heads),
+              ctypes.POINTER(Heads), ctypes.c_void_p]
+
+# (name, restype, argtypes) of every entry point declared in include/lora_attention.h
+ATTENTION_SIGNATURES = [
+    ("lora_rope", ctypes.c_int, [ctypes.POINTER(RopeArgs), ctypes.c_void_p]),
+    ("lora_kv_pages_bytes", ctypes.c_size_t, [ctypes.c_int32] * 4),
+    ("lora_kv_append", ctypes.c_int, _ROWS_ARGS),
+    ("lora_kv_gather", ctypes.c_int, _ROWS_ARGS),
+    ("lora_kv_attention_workspace_bytes", ctypes.c_size_t,
+     [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatch), ctypes.POINTER(AttentionArgs)]),
+    ("lora_kv_attention", ctypes.c_int,
+     [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatch), ctypes.POINTER(AttentionArgs), ctypes.c_void_p]),
+]
+
 _lock = threading.Lock()
 _lib = None
 
@@ -146,7 +241,7 @@ def lib():
                     f"liblora.so not found at {path}; build it with "
                     "`python -c 'import __graft_entry__ as g; g.build()'`")
             L = ctypes.CDLL(path)
-            for name, res, args in SIGNATURES:
+            for name, res, args in SIGNATURES + ATTENTION_SIGNATURES:
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args

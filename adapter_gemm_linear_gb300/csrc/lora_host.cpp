@@ -18,6 +18,8 @@ static thread_local int32_t g_last_cuda_error = 0;  // behind this thread's last
 
 void lora::count_launches(int n) { g_kernel_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }
 
+void lora::set_last_cuda_error(int32_t code) { g_last_cuda_error = code; }
+
 using lora::align_up;
 using lora::dtype_bytes;
 

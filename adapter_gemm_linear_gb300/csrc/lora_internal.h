@@ -168,6 +168,9 @@ struct ForwardPlan {
     bool rows_in_plan;
 };
 
+// The code lora_last_cuda_error() reports for the calling thread.
+void set_last_cuda_error(int32_t code);
+
 // Count of kernels launched by the library (lora_kernel_launches).
 void count_launches(int n);
 

@@ -402,8 +402,9 @@ lora_status_t lora_test_arm_wait_timeout(uint64_t limit_ns);
 const char *lora_status_string(lora_status_t status);
 
 /* The CUDA runtime error behind the calling thread's most recent
- * LORA_ERR_CUDA from lora_linear_forward (a cudaError_t value; 0 when that
- * call saw none), and the runtime's static name for such a code. */
+ * LORA_ERR_CUDA from lora_linear_forward or an entry point of
+ * lora_attention.h (a cudaError_t value; 0 when that call saw none), and the
+ * runtime's static name for such a code. */
 int32_t lora_last_cuda_error(void);
 const char *lora_cuda_error_name(int32_t code);
 
