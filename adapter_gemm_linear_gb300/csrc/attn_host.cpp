@@ -188,8 +188,7 @@ size_t lora_kv_attention_workspace_bytes(const lora_kv_cache_t *cache, const lor
                                          const lora_kv_attention_args_t *args) {
     lora::AttnView v;
     if (check_attention(cache, batch, args, &v) != LORA_OK) return 0;
-    const size_t n = lora::attention_workspace_bytes(v, cache->format, cache->head_dim, args->dtype);
-    return n > 256 ? n : 256;
+    return lora::decode_workspace_bytes(cache->head_dim);
 }
 
 lora_status_t lora_kv_attention(const lora_kv_cache_t *cache, const lora_kv_batch_t *batch,
@@ -198,11 +197,11 @@ lora_status_t lora_kv_attention(const lora_kv_cache_t *cache, const lora_kv_batc
     lora_status_t s = check_attention(cache, batch, args, &v);
     if (s != LORA_OK) return s;
     if (batch->rows == 0 || batch->num_seqs == 0) return LORA_OK;
-    const size_t need = lora::attention_workspace_bytes(v, cache->format, cache->head_dim, args->dtype);
+    const size_t need = lora::decode_workspace_bytes(cache->head_dim);
     if (!v.workspace || args->workspace_bytes < need) return LORA_ERR_WORKSPACE;
     if (!aligned(v.workspace, 16)) return LORA_ERR_ALIGNMENT;
     cudaError_t e = lora::device_status_ptr(&v.kv.status);
-    if (e == cudaSuccess) e = lora::launch_attention(v, cache->format, cache->head_dim, args->dtype, as_stream(stream));
+    if (e == cudaSuccess) e = lora::launch_attn_decode(v, cache->format, cache->head_dim, args->dtype, as_stream(stream));
     return e == cudaSuccess ? LORA_OK : fail(e);
 }
 

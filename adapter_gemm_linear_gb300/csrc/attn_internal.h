@@ -52,8 +52,9 @@ cudaError_t launch_kv_append(const KvView &v, lora_kv_format_t fmt, int head_dim
                              const HeadsView &k, const HeadsView &val, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,
                              const HeadsView &k, const HeadsView &val, cudaStream_t stream);
-size_t attention_workspace_bytes(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype);
-cudaError_t launch_attention(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,
-                             cudaStream_t stream);
+// Few query rows a sequence, and every fp32 call (attn_decode.cu).
+size_t decode_workspace_bytes(int head_dim);
+cudaError_t launch_attn_decode(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,
+                               cudaStream_t stream);
 
 }  // namespace lora
