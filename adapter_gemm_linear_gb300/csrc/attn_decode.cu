@@ -33,6 +33,7 @@
 
 #include "attn_device.cuh"
 #include "attn_internal.h"
+#include "attn_split.cuh"
 #include "sm100_ptx.cuh"
 
 namespace lora {
@@ -46,8 +47,6 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kChunkTiles = 8;                     // tiles of a unit of work (128 tokens)
 constexpr int kMmaRows = 16;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGrow = 8.0f;                      // log2 growth of the maximum that rescales
 constexpr float kLoScale = 2048.0f;                // 2^11: the lo parts of fp32 operands
 
 template <int D>
@@ -75,24 +74,11 @@ struct DecodeSmem {
     int32_t dead;    // a wait ran out: nobody waits any more
 };
 
-// Partial results in the workspace: two slots per CTA, [rows][D] sums, then m and l per row.
-struct JoinEntry {
-    int32_t seq, head, row_tile, last_cta;  // seq < 0: nothing to join
-};
-
-__host__ __device__ constexpr size_t partial_floats(int D) { return static_cast<size_t>(kMmaRows) * (D + 2); }
-
 __device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -104,14 +90,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
     const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
     return pack_f16((a - h.x) * kLoScale, (b - h.y) * kLoScale);
-}
-
-__device__ __forceinline__ void store4(float *p, const float4 &v, float f) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v, float f) {
-    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x * f, v.y * f), __floats2bfloat162_rn(v.z * f, v.w * f)};
-    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(h);
 }
 
 // A sequence's work: `chunks` units for each of heads x row_tiles items, over tiles [t0, t1).
@@ -189,8 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     constexpr int ROWS = tile_rows<T>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView &b = a.kv;
-    float *partials = reinterpret_cast<float *>(a.workspace);
-    JoinEntry *joins = reinterpret_cast<JoinEntry *>(partials + partial_floats(D) * 2 * gridDim.x);
+    JoinEntry *joins = join_entries(a, gridDim.x, kMmaRows, D);
 
     // ---- the plan: where this CTA's range of units begins
     for (int i = threadIdx.x; i < SLOTS; i += kThreads) {
@@ -527,8 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
         const bool whole = walk.from_start && walk.to_end;
         // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
-        const int slot_at = walk.from_start ? 1 : 0;
-        float *part = partials + (2 * static_cast<size_t>(blockIdx.x) + slot_at) * partial_floats(D);
+        float *part = partial_at(a, blockIdx.x, walk.from_start ? 1 : 0, kMmaRows, D);
         if (!whole && walk.from_start && threadIdx.x == 0) {
             const long long lastu = walk.item_end - 1;
             joins[blockIdx.x] = JoinEntry{walk.s, walk.head, walk.row_tile,
@@ -572,71 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                     part[kMmaRows * D + rt] = M;
                     part[kMmaRows * D + kMmaRows + rt] = L;
                 } else if (a.lse) {
-                    a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * 0.6931471805599453f;
+                    a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
                 }
             }
         }
     }
-}
-
-// Joins the items that span CTAs: block x takes the item that begins in CTA x
-// and goes on in the next ones, block row y a part of its rows.  It also gives
-// the rows of padding and skipped sequences their zeros, and records the
-// malformed ones.
-constexpr int kJoinThreads = 128;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnView a, int32_t ctas) {
-    constexpr int ROWS = tile_rows<T>();
-    constexpr int PER_ROW = D / 4;
-    const KvView &b = a.kv;
-    // the malformed and padding sequences do not need the kernel before
-    for (int32_t s = blockIdx.x * gridDim.y + blockIdx.y; s < b.num_seqs; s += gridDim.x * gridDim.y) {
-        const SeqRows r = read_seq(b, s, threadIdx.x == 0);
-        const int32_t off = b.offsets ? b.offsets[s] : s, end = b.offsets ? b.offsets[s + 1] : s + 1;
-        if (r.n > a.max_queries && threadIdx.x == 0) record_error(b.status, kDevBadSegment, static_cast<uint32_t>(s));
-        if (r.n > 0 && r.n <= a.max_queries) continue;
-        if (off < 0 || end > b.rows) continue;
-        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(end - off) * a.q_heads * D; i += kJoinThreads) {
-            const int64_t rh = i / D;
-            const int64_t row = off + rh / a.q_heads, h = rh % a.q_heads;
-            static_cast<T *>(a.out.p)[row * a.out.row + h * a.out.head + i % D] = from_float<T>(0.0f);
-            if (a.lse && i % D == 0) a.lse[row * a.q_heads + h] = -INFINITY;
-        }
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float *partials = reinterpret_cast<const float *>(a.workspace);
-    const JoinEntry e = reinterpret_cast<const JoinEntry *>(partials + partial_floats(D) * 2 * ctas)[blockIdx.x];
-    if (e.seq < 0) return;
-    const SeqRows r = read_seq(b, e.seq, false);
-    const int32_t rt = blockIdx.y * (kJoinThreads / PER_ROW) + threadIdx.x / PER_ROW, c = threadIdx.x % PER_ROW * 4;
-    const int32_t row = e.row_tile * ROWS + rt;
-    if (rt >= ROWS || row >= r.n * a.group) return;
-    auto part = [&](int32_t cta) {
-        return partials + (2 * static_cast<size_t>(cta) + (cta == static_cast<int32_t>(blockIdx.x) ? 1 : 0)) * partial_floats(D);
-    };
-    float M = -INFINITY;
-    for (int32_t k = blockIdx.x; k <= e.last_cta; ++k) M = fmaxf(M, part(k)[kMmaRows * D + rt]);
-    const float mu = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int32_t k = blockIdx.x; k <= e.last_cta; ++k) {
-        const float *p = part(k);
-        const float f = ex2(p[kMmaRows * D + rt] - mu);
-        L = fmaf(p[kMmaRows * D + kMmaRows + rt], f, L);
-        const float4 x = *reinterpret_cast<const float4 *>(p + rt * D + c);
-        v.x = fmaf(x.x, f, v.x);
-        v.y = fmaf(x.y, f, v.y);
-        v.z = fmaf(x.z, f, v.z);
-        v.w = fmaf(x.w, f, v.w);
-    }
-    const float inv = 1.0f / L;
-    const int32_t qi = row / a.group, qh = e.head * a.group + row % a.group;
-    T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head + c;
-    store4(dst, v, inv);
-    if (a.lse && c == 0)
-        a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 template <typename T, int D, int FMT>
@@ -654,16 +570,7 @@ cudaError_t decode_typed(const AttnView &v, cudaStream_t stream) {
     attn_decode_kernel<T, D, FMT><<<grid, kThreads, smem, stream>>>(v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, (tile_rows<T>() * (D / 4) + kJoinThreads - 1) / kJoinThreads);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, v, static_cast<int32_t>(grid));
+    e = launch_join<T, D, tile_rows<T>()>(v, grid, kMmaRows, stream);
     count_launches(2);
     return e;
 }
@@ -671,7 +578,7 @@ cudaError_t decode_typed(const AttnView &v, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_workspace_bytes(int head_dim) {
-    return static_cast<size_t>(device_sm_count()) * (partial_floats(head_dim) * 2 * sizeof(float) + sizeof(JoinEntry));
+    return split_workspace_bytes(device_sm_count(), kMmaRows, head_dim);
 }
 
 cudaError_t launch_attn_decode(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,

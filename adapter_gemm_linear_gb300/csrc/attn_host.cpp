@@ -104,6 +104,17 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
     return LORA_OK;
 }
 
+// Which kernel: the tensor-core kernel of attn_prefill.cu works on 256 query
+// rows (queries x heads that share a key/value head) at a time, that of
+// attn_decode.cu on 16 (8 in fp32).
+bool many_queries(const lora::AttnView &v, lora_dtype_t dtype) {
+    return dtype == LORA_BF16 && static_cast<int64_t>(v.max_queries) * v.group > 64;
+}
+
+size_t workspace_bytes(const lora::AttnView &v, int head_dim, lora_dtype_t dtype) {
+    return many_queries(v, dtype) ? lora::prefill_workspace_bytes(head_dim) : lora::decode_workspace_bytes(head_dim);
+}
+
 }  // namespace
 
 extern "C" {
@@ -188,7 +199,7 @@ size_t lora_kv_attention_workspace_bytes(const lora_kv_cache_t *cache, const lor
                                          const lora_kv_attention_args_t *args) {
     lora::AttnView v;
     if (check_attention(cache, batch, args, &v) != LORA_OK) return 0;
-    return lora::decode_workspace_bytes(cache->head_dim);
+    return workspace_bytes(v, cache->head_dim, args->dtype);
 }
 
 lora_status_t lora_kv_attention(const lora_kv_cache_t *cache, const lora_kv_batch_t *batch,
@@ -197,11 +208,14 @@ lora_status_t lora_kv_attention(const lora_kv_cache_t *cache, const lora_kv_batc
     lora_status_t s = check_attention(cache, batch, args, &v);
     if (s != LORA_OK) return s;
     if (batch->rows == 0 || batch->num_seqs == 0) return LORA_OK;
-    const size_t need = lora::decode_workspace_bytes(cache->head_dim);
+    const size_t need = workspace_bytes(v, cache->head_dim, args->dtype);
     if (!v.workspace || args->workspace_bytes < need) return LORA_ERR_WORKSPACE;
     if (!aligned(v.workspace, 16)) return LORA_ERR_ALIGNMENT;
     cudaError_t e = lora::device_status_ptr(&v.kv.status);
-    if (e == cudaSuccess) e = lora::launch_attn_decode(v, cache->format, cache->head_dim, args->dtype, as_stream(stream));
+    if (e == cudaSuccess)
+        e = many_queries(v, args->dtype)
+                ? lora::launch_attn_prefill(v, cache->format, cache->head_dim, as_stream(stream))
+                : lora::launch_attn_decode(v, cache->format, cache->head_dim, args->dtype, as_stream(stream));
     return e == cudaSuccess ? LORA_OK : fail(e);
 }
 

@@ -1,0 +1,865 @@
+// Attention over the 8-bit paged cache (lora_kv_attention) for many queries a
+// sequence, in bf16: prompts and chunks of prompts, on the tcgen05 tensor
+// cores.
+//
+// With hundreds of query rows per key the call is bound by the two matrix
+// products, 4 D flops per (query, head, key).  Rows are the queries of all
+// query heads that share a key/value head (row r: query r / group, head r %
+// group), so one load and conversion of a key serves group times as many rows.
+// One persistent CTA per SM works on items of 256 rows, as two tiles A and B
+// of 128, over tiles of 128 keys:
+//
+//   S_X = Q_X K^T     (M = 128 rows, N = 128 keys, both from shared memory)
+//   P_X = 2^(S_X c + log2 vs - m)      one thread per row, registers
+//   O_X += P_X V      (A = P from Tensor Memory, N = D)
+//
+//  - warps 0-3 and 4-7: the softmax of A and B, thread = row, no shuffles;
+//    while one tile's softmax runs, the other tile's products run.
+//  - warps 8-11 turn the codes into f16 tiles in shared memory (exactly), in
+//    the 128-byte-swizzled K-major layout of tcgen05.mma: K as [keys][dims], V
+//    as [dims][keys], which the cache's layout of V gives without a
+//    transposition.  Two stages each; the next tile's codes are in flight in
+//    registers meanwhile.
+//  - warp 12 issues the products; warp 13 hands out the items.
+//  - q is f16 times a power of two per row (exact for bf16), P is f16 (11
+//    bits) with the page's scale of V in its exponent, as in attn_decode.cu; a
+//    row's sums are rescaled only when its maximum grew by 2^8.
+//  - Tensor Memory: S_A, S_B (128 columns each, P over the first 64), O_A, O_B.
+// The key tiles of all items form one line that the CTAs share equally
+// (attn_split.cuh), so causal and ragged work is level to one tile.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "attn_device.cuh"
+#include "attn_internal.h"
+#include "attn_split.cuh"
+#include "sm100_ptx.cuh"
+
+namespace lora {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kRows = 256;       // query rows of an item
+constexpr int kHalf = 128;       // and of one MMA tile
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kSubs = kKeys / kKvTile;
+constexpr int kPreThreads = 512;
+constexpr int kItemRing = 4;
+constexpr int kItemReaders = 8 + 4 + 1;  // warps that read an item's entry
+constexpr int kScaleRing = 4;    // K runs at most two tiles ahead of the softmax
+constexpr uint64_t kPreWaitNs = 2000000000ull;
+
+struct Item {
+    int32_t seq, head, row_tile, last_cta;
+    int32_t off, n, len;
+    int32_t tile0, tile1;  // key tiles of this CTA; tile1 < 0: no more items
+    int32_t flags;
+};
+constexpr int kFromStart = 1, kToEnd = 2;
+
+template <int D>
+struct PrefillSmem {
+    alignas(1024) uint8_t q[2][kHalf * D * 2];
+    uint8_t k[2][kKeys * D * 2];
+    uint8_t v[2][kKeys * D * 2];
+    alignas(16) float4 scales[kScaleRing][kSubs];  // K's scale, V's, its log2 and reciprocal
+    Item items[kItemRing];
+    uint64_t item_full[kItemRing], item_empty[kItemRing];
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_done[2], drain;
+    long long warp_sum[kPreThreads / 32];
+    long long base;
+    int32_t seq;
+    uint32_t tmem;
+    int32_t dead;
+};
+
+// ---------------------------------------------------------------- PTX
+
+// D (+)= A B^T, A: f16 in Tensor Memory (two per column), B: shared memory, fp32 sums.
+__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 16 columns of the thread's TMEM lane (for the rare rescaling, where registers are short).
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Instruction descriptor of kind::f16 with f16 A and B, fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Two fp32 values at once.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---------------------------------------------------------------- the line of work
+
+// sum of floor((a i + b) / m) over 0 <= i < n, with a, b >= 0 (the Euclid-like recursion)
+__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long ans = 0;
+    while (n > 0) {
+        ans += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return ans;
+}
+
+// A sequence's row tiles: tile i covers rows [256 i, 256 i + 256) of n * group.
+struct RowTiles {
+    int32_t first, len, n, group, count, window, causal;
+
+    __device__ __forceinline__ RowTiles(const AttnView &a, const SeqRows &r)
+        : first(r.len - r.n), len(r.len), n(r.n), group(a.group),
+          count(static_cast<int32_t>((static_cast<long long>(r.n) * a.group + kRows - 1) / kRows)), window(a.window),
+          causal(a.causal) {}
+
+    // key tiles [lo, hi) that the queries of row tile i see
+    __device__ __forceinline__ int32_t hi(int32_t i) const {
+        const long long last = min(static_cast<long long>(i + 1) * kRows, static_cast<long long>(n) * group) - 1;
+        const int32_t end = causal ? first + static_cast<int32_t>(last / group) + 1 : len;
+        return (end + kKeys - 1) / kKeys;
+    }
+    __device__ __forceinline__ int32_t lo(int32_t i) const {
+        if (window <= 0) return 0;
+        const long long q0 = static_cast<long long>(i) * kRows / group;
+        return static_cast<int32_t>(max(0ll, first + q0 - window + 1) / kKeys);
+    }
+    // sum of hi - lo over the row tiles before i.  256 = 2 * 128, so hi(i) =
+    // floor((2 i + floor((255 + group (first + 128)) / 128)) / group) for every
+    // tile but the last, and lo(i) = max(0, floor((2 i + floor(group (first -
+    // window + 1) / 128)) / group)).
+    __device__ long long before(int32_t i) const {
+        long long sum;
+        if (causal) {
+            const long long c = (kRows - 1 + static_cast<long long>(group) * (first + kKeys)) / kKeys;
+            sum = floor_sum(min(i, count - 1), group, 2, c);
+            if (i == count) sum += hi(count - 1);
+        } else {
+            sum = static_cast<long long>(i) * hi(0);
+        }
+        if (window > 0) {
+            const long long x = static_cast<long long>(group) * (first - window + 1);
+            const long long e = x >= 0 ? x / kKeys : -((-x + kKeys - 1) / kKeys);
+            const long long i0 = e >= 0 ? 0 : (-e + 1) / 2;
+            if (i > i0) sum -= floor_sum(i - i0, group, 2, 2 * i0 + e);
+        }
+        return sum;
+    }
+};
+
+__device__ __forceinline__ SeqRows prefill_seq(const AttnView &a, int32_t s) {
+    SeqRows r = read_seq(a.kv, s, false);
+    if (r.n > a.max_queries) r.n = 0;
+    return r;
+}
+
+__device__ __forceinline__ long long seq_units(const AttnView &a, int32_t s) {
+    const SeqRows r = prefill_seq(a, s);
+    if (r.n == 0) return 0;
+    const RowTiles t(a, r);
+    return t.before(t.count) * a.kv.heads;
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __grid_constant__ AttnView a) {
+    extern __shared__ __align__(1024) unsigned char raw[];
+    PrefillSmem<D> &sm = *reinterpret_cast<PrefillSmem<D> *>(raw);
+    constexpr uint32_t kRowAtom = kHalf * 128;    // bytes of one atom of 128 rows
+    constexpr uint32_t kVAtom = D * 128;          // bytes of 64 keys of V
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const KvView &b = a.kv;
+    JoinEntry *joins = join_entries(a, gridDim.x, kRows, D);
+    volatile int32_t *dead = &sm.dead;
+
+    auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t site) {
+        if (*dead) return;
+        if (!mbar_wait_bounded(bar, parity, kPreWaitNs)) {
+            record_error(b.status, kDevTimeout, site);
+            *dead = 1;
+        }
+    };
+
+    // ---- set-up and plan
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kItemRing; ++i) {
+            mbar_init(&sm.item_full[i], 1);
+            mbar_init(&sm.item_empty[i], kItemReaders);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.k_full[i], 4);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.v_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_ready[i], 4);
+            mbar_init(&sm.o_done[i], 1);
+        }
+        mbar_init(&sm.drain, 1);
+        fence_mbar_init();
+        sm.dead = 0;
+        joins[blockIdx.x] = JoinEntry{-1, 0, 0, 0};
+    }
+    if (warp == 12) {
+        tmem_alloc(&sm.tmem, 512);
+        tmem_relinquish();
+    }
+    const int32_t per = (b.num_seqs + kPreThreads - 1) / kPreThreads;
+    const int32_t s0 = min(b.num_seqs, static_cast<int32_t>(threadIdx.x) * per), s1 = min(b.num_seqs, s0 + per);
+    long long mine = 0;
+    for (int32_t s = s0; s < s1; ++s) mine += seq_units(a, s);
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sm.warp_sum[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kPreThreads / 32; ++w) {
+        if (w < warp) upto += sm.warp_sum[w];
+        total += sm.warp_sum[w];
+    }
+    const long long ctas = min(total, static_cast<long long>(gridDim.x));
+    const long long w0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
+    const long long w1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+    if (w0 < w1 && upto - mine <= w0 && w0 < upto) {
+        long long at = upto - mine;
+        int32_t s = s0;
+        for (;; ++s) {
+            const long long u = seq_units(a, s);
+            if (w0 < at + u) break;
+            at += u;
+        }
+        sm.seq = s;
+        sm.base = at;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sm.tmem;
+
+    if (warp < 8) {
+        // ================================================ softmax of tile X
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        const int X = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's TMEM lanes
+        const uint32_t ts = tmem + lanes + X * 128, to = tmem + lanes + 256 + X * 128;
+        const int rt = X * kHalf + (warp & 3) * 32 + lane;             // the thread's row of the item
+        uint32_t n_item = 0, n_tile = 0, n_own = 0, n_part = 0;        // items, key tiles; those of X
+        auto get_item = [&](Item &it) {
+            const uint32_t e = n_item % kItemRing;
+            wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 50);
+            it = sm.items[e];
+            if (*dead) it.tile1 = -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.item_empty[e]);
+            ++n_item;
+        };
+        // Q_X of an item into shared memory: the thread's row, f16 times a
+        // power of two (its largest value in [2^13, 2^14)); returns the factor
+        // that turns its products with codes into log2 units
+        auto load_q = [&](const Item &it) {
+            const long long rows = static_cast<long long>(it.n) * a.group;
+            const long long row = min(static_cast<long long>(it.row_tile) * kRows + rt, rows - 1);
+            const int32_t qi = static_cast<int32_t>(row / a.group), qh = it.head * a.group + static_cast<int32_t>(row % a.group);
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
+                                                               static_cast<int64_t>(it.off + qi) * a.q.row + qh * a.q.head);
+            uint4 x[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) x[i] = __ldg(src + i);
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
+            }
+            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+            e = amax < INFINITY ? max(e, -126) : 0;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            const int r = rt - X * kHalf;
+            uint8_t *dst = sm.q[X] + r * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+                *reinterpret_cast<uint4 *>(dst + (i / 8) * kRowAtom + (((i & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full[X]);
+            return a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        };
+        auto takes_part = [&](const Item &it) {  // tile B may be empty
+            return it.tile1 >= 0 && (X == 0 || static_cast<long long>(it.n) * a.group - static_cast<long long>(it.row_tile) * kRows > kHalf);
+        };
+
+        Item it;
+        get_item(it);
+        float cr = takes_part(it) ? load_q(it) : 0.0f;
+        while (it.tile1 >= 0) {
+            if (!takes_part(it)) {
+                n_tile += it.tile1 - it.tile0;
+                get_item(it);
+                if (takes_part(it)) cr = load_q(it);
+                continue;
+            }
+            const int32_t rows = static_cast<int32_t>(min(static_cast<long long>(kRows), static_cast<long long>(it.n) * a.group - static_cast<long long>(it.row_tile) * kRows));
+            const int32_t row = it.row_tile * kRows + min(rt, rows - 1);
+            const int32_t qi = row / a.group, qh = it.head * a.group + row % a.group;
+            const int32_t pos = it.len - it.n + qi;
+            const int32_t kmax = a.causal ? pos + 1 : it.len;
+            const int32_t kmin = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            // keys that every row of the item sees
+            const int32_t all_hi = a.causal ? it.len - it.n + it.row_tile * kRows / a.group + 1 : it.len;
+            const int32_t all_lo = a.window > 0 ? it.len - it.n + (it.row_tile * kRows + rows - 1) / a.group - a.window + 1 : 0;
+            float m = -INFINITY, l = 0.0f;
+            float lvp = 0.0f, ivp = 1.0f;  // of the last page whose V is not all zero
+            bool seen = false;
+            for (int32_t t = it.tile0; t < it.tile1; ++t, ++n_tile, ++n_own) {
+                wait(&sm.s_full[X], n_own & 1u, 51 + X);
+                tc_fence_after_sync();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld_wait(s[i]);
+                const float4 *scl = sm.scales[n_tile % kScaleRing];
+                const int32_t key0 = t * kKeys;
+                if (key0 < all_lo || key0 + kKeys > all_hi) {
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e)
+                        if (key0 + e < kmin || key0 + e >= kmax) s[e >> 5][e & 31] = 0xFF800000u;  // -inf
+                }
+                if (!seen) {  // tiles so far had V = 0 and took log2 vs = 0: their sums move to this one's
+#pragma unroll
+                    for (int u = kSubs - 1; u >= 0; --u) {
+                        const float4 sc = scl[u];
+                        if (sc.y > 0.0f) {
+                            lvp = sc.z;
+                            ivp = sc.w;
+                            seen = true;
+                        }
+                    }
+                    if (seen) {
+                        m += lvp;
+                        l *= ivp;
+                    }
+                }
+                // the row's maximum, in log2 units and with V's scale
+                float mx = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u) {
+                    const float4 sc = scl[u];
+                    const float c = fmaxf(sc.x * cr, 1e-37f), lv = sc.y > 0.0f ? sc.z : lvp;
+                    const uint32_t *p = &s[u >> 1][(u & 1) * 16];
+                    float x = max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[2]));
+#pragma unroll
+                    for (int e = 3; e < 15; e += 2) x = max3(x, __uint_as_float(p[e]), __uint_as_float(p[e + 1]));
+                    x = fmaxf(x, __uint_as_float(p[15]));
+                    mx = fmaxf(mx, fmaf(x, c, lv));
+                }
+                const bool grow = mx > m + kGrow;
+                if (t == it.tile0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, grow)) {
+                    // all products of this tile so far are complete: s_full came after them
+                    const float mn = grow ? mx : m;
+                    const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn);
+                    m = mn;
+                    l *= f;
+#pragma unroll 1
+                    for (int i = 0; i < D / 16; ++i) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(to + 16 * i, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st_32x32b_x16(to + 16 * i, o);
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int u = 4 * h + v;
+                        const float4 sc = scl[u];
+                        const bool some = sc.y > 0.0f;
+                        const float c = fmaxf(sc.x * cr, 1e-37f), d = (some ? sc.z : lvp) - mu;
+                        const uint64_t c2 = pack2(c, c), d2 = pack2(d, d);
+                        const uint32_t *p = &s[u >> 1][(u & 1) * 16];
+                        uint64_t sum = 0;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float x, y;
+                            unpack2(fma2(pack2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])), c2, d2), x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            sum = e == 0 ? pack2(x, y) : add2(sum, pack2(x, y));
+                            pk[8 * v + e / 2] = pack_h2(x, y);
+                        }
+                        float x, y;
+                        unpack2(sum, x, y);
+                        l = fmaf(x + y, some ? sc.w : ivp, l);
+                        if (!some) {  // V = 0 whatever its codes
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) pk[8 * v + e] = 0u;
+                        }
+                    }
+                    tmem_st_32x32b_x32(ts + 32 * h, pk);
+                }
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u) {
+                    const float4 sc = scl[u];
+                    if (sc.y > 0.0f) {
+                        lvp = sc.z;
+                        ivp = sc.w;
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready[X]);
+            }
+            // the next item's Q (this one's products with Q_X are complete), then this one's result
+            Item next;
+            get_item(next);
+            float cr_next = 0.0f;
+            if (takes_part(next)) cr_next = load_q(next);
+            wait(&sm.o_done[X], n_part & 1u, 53 + X);
+            ++n_part;
+            tc_fence_after_sync();
+            const bool whole = (it.flags & (kFromStart | kToEnd)) == (kFromStart | kToEnd);
+            float *part = partial_at(a, blockIdx.x, it.flags & kFromStart ? 1 : 0, kRows, D);
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out.p) + static_cast<int64_t>(it.off + qi) * a.out.row + qh * a.out.head;
+            const float inv = 1.0f / l;
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + 32 * i, o);
+                tmem_ld_wait(o);
+                if (rt >= rows) continue;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        __nv_bfloat162 h[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            h[k] = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + 32 * i + e) = *reinterpret_cast<uint4 *>(h);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(part + rt * D + 32 * i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            tc_fence_before_sync();
+            if (rt < rows) {
+                if (!whole) {
+                    part[kRows * D + rt] = m;
+                    part[kRows * D + kRows + rt] = l;
+                } else if (a.lse) {
+                    a.lse[static_cast<int64_t>(it.off + qi) * a.q_heads + qh] = (m + log2f(l)) * kLn2;
+                }
+            }
+            if (!whole && (it.flags & kFromStart) && threadIdx.x == 0)
+                joins[blockIdx.x] = JoinEntry{it.seq, it.head, it.row_tile, it.last_cta};
+            it = next;
+            cr = cr_next;
+        }
+    } else if (warp < 12) {
+        // ================================================ codes to f16 tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        const int wq = warp - 8;  // the warp's 32 keys of a tile
+        constexpr int NL = 2 * D / 32;  // 16-byte pieces a lane holds of K (or V)
+        uint32_t n_item = 0, n_tile = 0;
+        const int cc = lane & 3, dpar = (lane >> 2) & 1, dq = lane >> 3;
+        // one tile of this CTA, and where the warp's two 16-key pieces of it are
+        struct Tile {
+            int32_t seq, head, len, t, end;
+            int32_t page[2];  // < 0: past the end, or not there: zeros
+        };
+        Tile cur, nxt;
+        auto advance = [&](Tile &x) {  // the next tile of the line; end < 0 when there is none
+            if (x.t + 1 < x.end) {
+                ++x.t;
+            } else {
+                const uint32_t e = n_item % kItemRing;
+                wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 60);
+                const Item &it = sm.items[e];
+                x.seq = it.seq;
+                x.head = it.head;
+                x.len = it.len;
+                x.t = it.tile0;
+                x.end = *dead ? -1 : it.tile1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.item_empty[e]);
+                ++n_item;
+            }
+        };
+        auto pages = [&](Tile &x) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int32_t key = x.t * kKeys + wq * 32 + u * kKvTile;
+                x.page[u] = x.end >= 0 && key < x.len ? read_page(b, x.seq, key >> b.page_shift) : -1;
+            }
+        };
+        auto piece = [&](const Tile &x, int u) {
+            const int32_t key = x.t * kKeys + wq * 32 + u * kKvTile;
+            return tile_offset<D>(b, max(x.page[u], 0), x.head, (key & (b.page_tokens - 1)) / kKvTile);
+        };
+        uint4 rk[NL], rv[NL];
+        float ks = 0.0f, vs = 0.0f;  // lanes 0 and 1: the scales of piece 0 and 1
+        auto load_k = [&](const Tile &x) {
+            const int64_t at[2] = {piece(x, 0), piece(x, 1)};
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int u = i / (NL / 2);
+                rk[i] = make_uint4(0, 0, 0, 0);
+                if (x.page[u] >= 0)
+                    rk[i] = __ldg(reinterpret_cast<const uint4 *>(b.k_pages + at[u]) + lane + 32 * (i % (NL / 2)));
+            }
+            if (lane < 2) {
+                const int32_t p = lane ? x.page[1] : x.page[0];
+                const int64_t sc = static_cast<int64_t>(max(p, 0)) * b.heads + x.head;
+                ks = p >= 0 ? __ldg(b.k_scales + sc) : 0.0f;
+                vs = p >= 0 ? __ldg(b.v_scales + sc) : 0.0f;
+            }
+        };
+        auto load_v = [&](const Tile &x) {
+            const int u = cc >> 1;
+            const int64_t at = piece(x, u);
+            const int32_t p = u ? x.page[1] : x.page[0];
+#pragma unroll
+            for (int k = 0; k < NL / 2; ++k) {
+                const int d4 = k * 8 + dq * 2 + dpar;
+                const uint4 *src = reinterpret_cast<const uint4 *>(b.v_pages + at + d4 * 64 + (cc & 1) * 32);
+                rv[2 * k] = rv[2 * k + 1] = make_uint4(0, 0, 0, 0);
+                if (p >= 0) {
+                    rv[2 * k] = __ldg(src);
+                    rv[2 * k + 1] = __ldg(src + 1);
+                }
+            }
+        };
+        cur.t = 0;
+        cur.end = 0;
+        advance(cur);
+        pages(cur);
+        if (cur.end >= 0) load_k(cur);
+        while (cur.end >= 0) {
+            const uint32_t stage = n_tile & 1u, ph = (n_tile >> 1) & 1u;
+            load_v(cur);
+            nxt = cur;
+            advance(nxt);
+            pages(nxt);
+            // K: row = key, 16 dimensions of one key a piece
+            wait(&sm.k_empty[stage], ph ^ 1u, 61);
+            if (lane < 2) sm.scales[n_tile % kScaleRing][wq * 2 + lane] = make_float4(ks, vs, log2f(vs), 1.0f / vs);
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int c = lane + 32 * (i % (NL / 2));  // piece within the 16 keys: [atom][key][16 dims]
+                const int row = wq * 32 + (i / (NL / 2)) * kKvTile + (c >> 2) % kKvTile, p = c & 3;
+                uint8_t *dst = sm.k[stage] + (c / 64) * kRowAtom + row * 128;
+                uint32_t w[8];
+                codes_to_f16<FMT>(rk[i].x, w[0], w[1]);
+                codes_to_f16<FMT>(rk[i].y, w[2], w[3]);
+                codes_to_f16<FMT>(rk[i].z, w[4], w[5]);
+                codes_to_f16<FMT>(rk[i].w, w[6], w[7]);
+                *reinterpret_cast<uint4 *>(dst + (((2 * p) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(dst + (((2 * p + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.k_full[stage]);
+            if (nxt.end >= 0) load_k(nxt);
+            // V: row = dimension, 8 keys a piece; keys past the end are zeros
+            // (their codes may be anything, and 0 * NaN is not 0)
+            wait(&sm.v_empty[stage], ph ^ 1u, 62);
+            const int32_t q0 = cur.t * kKeys + wq * 32 + cc * 8;
+            uint32_t keep[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int past = q0 + 4 * h + 4 - cur.len;
+                keep[h] = past <= 0 ? 0xFFFFFFFFu : past >= 4 ? 0u : 0xFFFFFFFFu >> (8 * past);
+            }
+            uint8_t *vbase = sm.v[stage] + (wq >> 1) * kVAtom;
+            const int c8 = (wq & 1) * 4 + cc;
+#pragma unroll
+            for (int k = 0; k < NL / 2; ++k) {
+                const int d4 = k * 8 + dq * 2 + dpar;
+                const uint32_t wa[4] = {rv[2 * k].x, rv[2 * k].y, rv[2 * k].z, rv[2 * k].w};
+                const uint32_t wb[4] = {rv[2 * k + 1].x, rv[2 * k + 1].y, rv[2 * k + 1].z, rv[2 * k + 1].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w[4];
+                    codes_to_f16<FMT>(wa[e] & keep[0], w[0], w[1]);
+                    codes_to_f16<FMT>(wb[e] & keep[1], w[2], w[3]);
+                    const int d = 4 * d4 + e;
+                    *reinterpret_cast<uint4 *>(vbase + d * 128 + ((c8 ^ (d & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_full[stage]);
+            cur = nxt;
+            ++n_tile;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 12 && lane == 0) {
+            // ============================================ the products
+            constexpr uint32_t idesc_s = idesc_f16_f32(kHalf, kKeys), idesc_o = idesc_f16_f32(kHalf, D);
+            uint32_t n_item = 0, n_tile = 0, n_a = 0, n_b = 0, n_qa = 0, n_qb = 0;
+            auto scores = [&](int X, uint32_t stage) {
+                const uint64_t qd = desc_kmajor_sw128(smem_u32(sm.q[X])), kd = desc_kmajor_sw128(smem_u32(sm.k[stage]));
+                if (!*dead)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k / 4) * (kRowAtom >> 4) + (k % 4) * 2;
+                        mma_bf16_f32(tmem + X * 128, qd + at, kd + at, idesc_s, k > 0);
+                    }
+                mma_commit(&sm.s_full[X]);
+            };
+            auto values = [&](int X, uint32_t stage, bool first) {
+                const uint64_t vd = desc_kmajor_sw128(smem_u32(sm.v[stage]));
+                if (!*dead)
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_f16_ts(tmem + 256 + X * 128, tmem + X * 128 + k * 8,
+                                   vd + (k / 4) * (kVAtom >> 4) + (k % 4) * 2, idesc_o, !first || k > 0);
+            };
+            while (true) {
+                const uint32_t e = n_item % kItemRing;
+                wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 70);
+                const int32_t nt = sm.items[e].tile1 - sm.items[e].tile0, stop = sm.items[e].tile1 < 0;
+                const bool has_b = static_cast<long long>(sm.items[e].n) * a.group -
+                                       static_cast<long long>(sm.items[e].row_tile) * kRows > kHalf;
+                mbar_arrive(&sm.item_empty[e]);
+                ++n_item;
+                if (stop || *dead) break;
+                wait(&sm.q_full[0], n_qa++ & 1u, 71);
+                wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
+                tc_fence_after_sync();
+                scores(0, n_tile & 1u);
+                if (has_b) {
+                    wait(&sm.q_full[1], n_qb++ & 1u, 73);
+                    tc_fence_after_sync();
+                    scores(1, n_tile & 1u);
+                }
+                mma_commit(&sm.k_empty[n_tile & 1u]);
+                for (int32_t j = 0; j < nt; ++j, ++n_tile) {
+                    const uint32_t st = n_tile & 1u, ph = (n_tile >> 1) & 1u;
+                    const uint32_t st1 = (n_tile + 1) & 1u, ph1 = ((n_tile + 1) >> 1) & 1u;
+                    const bool more = j + 1 < nt;
+                    wait(&sm.v_full[st], ph, 74);
+                    wait(&sm.p_ready[0], n_a++ & 1u, 75);
+                    tc_fence_after_sync();
+                    values(0, st, j == 0);
+                    if (more) {
+                        wait(&sm.k_full[st1], ph1, 76);
+                        tc_fence_after_sync();
+                        scores(0, st1);
+                    } else {
+                        mma_commit(&sm.o_done[0]);
+                    }
+                    if (has_b) {
+                        wait(&sm.p_ready[1], n_b++ & 1u, 77);
+                        tc_fence_after_sync();
+                        values(1, st, j == 0);
+                        if (more) scores(1, st1);
+                        else mma_commit(&sm.o_done[1]);
+                    }
+                    mma_commit(&sm.v_empty[st]);
+                    if (more) mma_commit(&sm.k_empty[st1]);
+                }
+            }
+            // nothing of this thread's may be in flight when Tensor Memory is freed
+            mma_commit(&sm.drain);
+            mbar_wait_bounded(&sm.drain, 0, kPreWaitNs);
+        } else if (warp == 13 && lane == 0) {
+            // ============================================ the items
+            uint32_t n_item = 0;
+            auto publish = [&](const Item &it) {
+                const uint32_t e = n_item % kItemRing;
+                wait(&sm.item_empty[e], ((n_item / kItemRing) & 1u) ^ 1u, 80);
+                sm.items[e] = it;
+                mbar_arrive(&sm.item_full[e]);
+                ++n_item;
+            };
+            Item it;
+            if (w0 < w1) {
+                it.seq = sm.seq;
+                SeqRows r = prefill_seq(a, it.seq);
+                int32_t count;
+                int32_t skip;  // tiles of the first item that belong to the CTA before
+                {
+                    const RowTiles t(a, r);
+                    const long long units = t.before(t.count);
+                    const long long local = w0 - sm.base;
+                    it.head = static_cast<int32_t>(local / units);
+                    const long long u = local - it.head * units;
+                    int32_t lo = 0, hi = t.count - 1;  // the last row tile with before(i) <= u
+                    while (lo < hi) {
+                        const int32_t mid = (lo + hi + 1) >> 1;
+                        if (t.before(mid) <= u) lo = mid; else hi = mid - 1;
+                    }
+                    it.row_tile = lo;
+                    skip = static_cast<int32_t>(u - t.before(lo));
+                    count = t.count;
+                }
+                long long w = w0;
+                while (w < w1) {
+                    const RowTiles t(a, r);
+                    const int32_t lo = t.lo(it.row_tile), hi = t.hi(it.row_tile);
+                    it.off = r.off;
+                    it.n = r.n;
+                    it.len = r.len;
+                    it.tile0 = lo + skip;
+                    it.tile1 = static_cast<int32_t>(min(static_cast<long long>(hi), it.tile0 + (w1 - w)));
+                    it.flags = (skip == 0 ? kFromStart : 0) | (it.tile1 == hi ? kToEnd : 0);
+                    it.last_cta = static_cast<int32_t>(((w + (hi - it.tile0)) * ctas - 1) / total);
+                    w += it.tile1 - it.tile0;
+                    publish(it);
+                    if (*dead) break;
+                    skip = 0;
+                    if (w >= w1) break;
+                    if (++it.row_tile == count) {
+                        it.row_tile = 0;
+                        if (++it.head == b.heads) {
+                            it.head = 0;
+                            do r = prefill_seq(a, ++it.seq); while (r.n == 0);
+                            count = RowTiles(a, r).count;
+                        }
+                    }
+                }
+            }
+            it.tile0 = 0;
+            it.tile1 = -1;
+            publish(it);
+        }
+        __syncwarp();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int FMT>
+cudaError_t prefill_typed(const AttnView &v, cudaStream_t stream) {
+    static uint64_t ctx[128] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // more than half of an SM's shared memory even for D = 64: a CTA takes all of its Tensor Memory
+    const int smem = static_cast<int>(sizeof(PrefillSmem<D>) > 128 * 1024 ? sizeof(PrefillSmem<D>) : 128 * 1024);
+    if (dev < 0 || dev >= 128 || first_use_in_context(&ctx[dev])) {
+        e = cudaFuncSetAttribute(attn_prefill_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int grid = device_sm_count();
+    attn_prefill_kernel<D, FMT><<<grid, kPreThreads, smem, stream>>>(v);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_join<__nv_bfloat16, D, kRows>(v, grid, kRows, stream);
+    count_launches(2);
+    return e;
+}
+
+}  // namespace
+
+size_t prefill_workspace_bytes(int head_dim) { return split_workspace_bytes(device_sm_count(), kRows, head_dim); }
+
+cudaError_t launch_attn_prefill(const AttnView &v, lora_kv_format_t fmt, int head_dim, cudaStream_t stream) {
+    if (head_dim == 64)
+        return fmt == LORA_KV_INT8 ? prefill_typed<64, LORA_KV_INT8>(v, stream) : prefill_typed<64, LORA_KV_E4M3>(v, stream);
+    return fmt == LORA_KV_INT8 ? prefill_typed<128, LORA_KV_INT8>(v, stream) : prefill_typed<128, LORA_KV_E4M3>(v, stream);
+}
+
+}  // namespace lora

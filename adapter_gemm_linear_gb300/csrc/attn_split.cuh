@@ -1,0 +1,123 @@
+// What the attention kernels that cut their keys over CTAs share: where a
+// CTA's partial results go, and the kernel that joins them.
+//
+// The units of all items (sequence, key/value head, tile of query rows) form
+// one line, of which every CTA takes an equal contiguous range.  A CTA holds
+// the beginning of at most one item that goes on in the next CTA (slot 1),
+// and the middle or end of at most one that began before (slot 0).
+#pragma once
+
+#include "attn_device.cuh"
+
+namespace lora {
+
+struct JoinEntry {
+    int32_t seq, head, row_tile, last_cta;  // seq < 0: nothing to join
+};
+
+// Floats of one partial result: [rows][D] sums, then the rows' maximum (log2 units) and sum.
+__host__ __device__ constexpr size_t partial_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
+
+__host__ __device__ constexpr size_t split_workspace_bytes(int ctas, int rows, int D) {
+    return static_cast<size_t>(ctas) * (partial_floats(rows, D) * 2 * sizeof(float) + sizeof(JoinEntry));
+}
+
+__device__ __forceinline__ JoinEntry *join_entries(const AttnView &a, int32_t ctas, int rows, int D) {
+    return reinterpret_cast<JoinEntry *>(reinterpret_cast<float *>(a.workspace) + partial_floats(rows, D) * 2 * ctas);
+}
+
+__device__ __forceinline__ float *partial_at(const AttnView &a, int32_t cta, int slot, int rows, int D) {
+    return reinterpret_cast<float *>(a.workspace) + (2 * static_cast<size_t>(cta) + slot) * partial_floats(rows, D);
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.0f;  // log2 growth of a row's maximum that rescales its sums
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void store4(float *p, const float4 &v, float f) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v, float f) {
+    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x * f, v.y * f), __floats2bfloat162_rn(v.z * f, v.w * f)};
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(h);
+}
+
+// Joins the items that span CTAs: block x takes the item that begins in CTA x
+// and goes on in the next ones, block row y four (D = 128) or eight of its
+// rows.  It also gives the rows of padding and skipped sequences their zeros,
+// and records the malformed ones.
+constexpr int kJoinThreads = 128;
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnView a, int32_t ctas,
+                                                                 int32_t slot_rows) {
+    constexpr int PER_ROW = D / 4;
+    const KvView &b = a.kv;
+    // the malformed and padding sequences do not need the kernel before
+    for (int32_t s = blockIdx.x * gridDim.y + blockIdx.y; s < b.num_seqs; s += gridDim.x * gridDim.y) {
+        const SeqRows r = read_seq(b, s, threadIdx.x == 0);
+        const int32_t off = b.offsets ? b.offsets[s] : s, end = b.offsets ? b.offsets[s + 1] : s + 1;
+        if (r.n > a.max_queries && threadIdx.x == 0) record_error(b.status, kDevBadSegment, static_cast<uint32_t>(s));
+        if (r.n > 0 && r.n <= a.max_queries) continue;
+        if (off < 0 || end > b.rows) continue;
+        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(end - off) * a.q_heads * D; i += kJoinThreads) {
+            const int64_t rh = i / D;
+            const int64_t row = off + rh / a.q_heads, h = rh % a.q_heads;
+            static_cast<T *>(a.out.p)[row * a.out.row + h * a.out.head + i % D] = from_float<T>(0.0f);
+            if (a.lse && i % D == 0) a.lse[row * a.q_heads + h] = -INFINITY;
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const JoinEntry e = join_entries(a, ctas, slot_rows, D)[blockIdx.x];
+    if (e.seq < 0) return;
+    const SeqRows r = read_seq(b, e.seq, false);
+    const int32_t rt = blockIdx.y * (kJoinThreads / PER_ROW) + threadIdx.x / PER_ROW, c = threadIdx.x % PER_ROW * 4;
+    const int32_t row = e.row_tile * ROWS + rt;
+    if (rt >= ROWS || row >= r.n * a.group) return;
+    auto part = [&](int32_t cta) {
+        return partial_at(a, cta, cta == static_cast<int32_t>(blockIdx.x) ? 1 : 0, slot_rows, D);
+    };
+    float M = -INFINITY;
+    for (int32_t k = blockIdx.x; k <= e.last_cta; ++k) M = fmaxf(M, part(k)[slot_rows * D + rt]);
+    const float mu = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int32_t k = blockIdx.x; k <= e.last_cta; ++k) {
+        const float *p = part(k);
+        const float f = ex2(p[slot_rows * D + rt] - mu);
+        L = fmaf(p[slot_rows * D + slot_rows + rt], f, L);
+        const float4 x = *reinterpret_cast<const float4 *>(p + rt * D + c);
+        v.x = fmaf(x.x, f, v.x);
+        v.y = fmaf(x.y, f, v.y);
+        v.z = fmaf(x.z, f, v.z);
+        v.w = fmaf(x.w, f, v.w);
+    }
+    const int32_t qi = row / a.group, qh = e.head * a.group + row % a.group;
+    store4(static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head + c, v, 1.0f / L);
+    if (a.lse && c == 0) a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
+}
+
+// Starts the join behind the kernel that was launched last on the stream.
+template <typename T, int D, int ROWS>
+cudaError_t launch_join(const AttnView &v, int ctas, int slot_rows, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (ROWS * (D / 4) + kJoinThreads - 1) / kJoinThreads);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, ROWS>, v, static_cast<int32_t>(ctas),
+                              static_cast<int32_t>(slot_rows));
+}
+
+}  // namespace lora
