@@ -18,9 +18,12 @@
 //  - warps 8-11 turn the codes into f16 tiles in shared memory (exactly), in
 //    the 128-byte-swizzled K-major layout of tcgen05.mma: K as [keys][dims], V
 //    as [dims][keys], which the cache's layout of V gives without a
-//    transposition.  Two stages each; the next tile's codes are in flight in
-//    registers meanwhile.
-//  - warp 12 issues the products; warp 13 hands out the items.
+//    transposition.  Two stages each; the next tile's codes are on their way
+//    by bulk copies meanwhile (loads into registers were slower by half: with
+//    213 KB of shared memory taken, what is left of the L1 holds too few of
+//    them in flight).
+//  - warp 12 issues the products; warp 13 hands out the items, and warp 14
+//    looks up the pages and scales of the key tiles, eight tiles ahead.
 //  - q is f16 times a power of two per row (exact for bf16), P is f16 (11
 //    bits) with the page's scale of V in its exponent, as in attn_decode.cu; a
 //    row's sums are rescaled only when its maximum grew by 2^8.
@@ -47,8 +50,8 @@ constexpr int kKeys = 128;       // keys of a tile
 constexpr int kSubs = kKeys / kKvTile;
 constexpr int kPreThreads = 512;
 constexpr int kItemRing = 4;
-constexpr int kItemReaders = 8 + 4 + 1;  // warps that read an item's entry
-constexpr int kScaleRing = 4;    // K runs at most two tiles ahead of the softmax
+constexpr int kItemReaders = 8 + 1 + 1;  // warps that read an item's entry
+constexpr int kTileRing = 8;             // key tiles looked up ahead
 constexpr uint64_t kPreWaitNs = 2000000000ull;
 
 struct Item {
@@ -59,14 +62,27 @@ struct Item {
 };
 constexpr int kFromStart = 1, kToEnd = 2;
 
+// A key tile of the CTA's line: where its 16-key pieces are, and their scales.
+struct KeyTile {
+    float4 scales[kSubs];  // K's scale, V's, its log2 and reciprocal
+    int64_t at[kSubs];     // offset in k_pages and v_pages; < 0: past the end or not there, zeros
+    int32_t key0, len;     // first key, the sequence's length; key0 < 0: no more tiles
+    int32_t pad[2];
+};
+
 template <int D>
 struct PrefillSmem {
     alignas(1024) uint8_t q[2][kHalf * D * 2];
     uint8_t k[2][kKeys * D * 2];
     uint8_t v[2][kKeys * D * 2];
-    alignas(16) float4 scales[kScaleRing][kSubs];  // K's scale, V's, its log2 and reciprocal
+    // codes on their way: per converting warp its two 16-key pieces of K and of
+    // V, the second of V 16 bytes off so that both are read without conflicts
+    uint8_t k_codes[4][2][kKvTile * D];
+    uint8_t v_codes[4][2 * kKvTile * D + 16];
+    alignas(16) KeyTile tiles[kTileRing];
     Item items[kItemRing];
-    uint64_t item_full[kItemRing], item_empty[kItemRing];
+    uint64_t item_full[kItemRing], item_empty[kItemRing], tile_full[kTileRing], tile_empty[kTileRing];
+    uint64_t k_landed[4], v_landed[4];
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_done[2], drain;
     long long warp_sum[kPreThreads / 32];
     long long base;
@@ -260,6 +276,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             mbar_init(&sm.item_full[i], 1);
             mbar_init(&sm.item_empty[i], kItemReaders);
         }
+        for (int i = 0; i < kTileRing; ++i) {
+            mbar_init(&sm.tile_full[i], 1);
+            mbar_init(&sm.tile_empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 4);
             mbar_init(&sm.k_full[i], 4);
@@ -269,6 +289,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_ready[i], 4);
             mbar_init(&sm.o_done[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm.k_landed[i], 1);
+            mbar_init(&sm.v_landed[i], 1);
         }
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
@@ -399,6 +423,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             float lvp = 0.0f, ivp = 1.0f;  // of the last page whose V is not all zero
             bool seen = false;
             for (int32_t t = it.tile0; t < it.tile1; ++t, ++n_tile, ++n_own) {
+                wait(&sm.tile_full[n_tile % kTileRing], (n_tile / kTileRing) & 1u, 55);
                 wait(&sm.s_full[X], n_own & 1u, 51 + X);
                 tc_fence_after_sync();
                 uint32_t s[4][32];
@@ -406,7 +431,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tmem_ld_wait(s[i]);
-                const float4 *scl = sm.scales[n_tile % kScaleRing];
+                const float4 *scl = sm.tiles[n_tile % kTileRing].scales;
                 const int32_t key0 = t * kKeys;
                 if (key0 < all_lo || key0 + kKeys > all_hi) {
 #pragma unroll
@@ -556,110 +581,85 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         const int wq = warp - 8;  // the warp's 32 keys of a tile
         constexpr int NL = 2 * D / 32;  // 16-byte pieces a lane holds of K (or V)
-        uint32_t n_item = 0, n_tile = 0;
+        uint32_t n_tile = 0;
         const int cc = lane & 3, dpar = (lane >> 2) & 1, dq = lane >> 3;
-        // one tile of this CTA, and where the warp's two 16-key pieces of it are
+        // of one tile: its first key, the length, and where the warp's two 16-key pieces are
         struct Tile {
-            int32_t seq, head, len, t, end;
-            int32_t page[2];  // < 0: past the end, or not there: zeros
+            int32_t key0, len;
+            int64_t at[2];
         };
         Tile cur, nxt;
-        auto advance = [&](Tile &x) {  // the next tile of the line; end < 0 when there is none
-            if (x.t + 1 < x.end) {
-                ++x.t;
-            } else {
-                const uint32_t e = n_item % kItemRing;
-                wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 60);
-                const Item &it = sm.items[e];
-                x.seq = it.seq;
-                x.head = it.head;
-                x.len = it.len;
-                x.t = it.tile0;
-                x.end = *dead ? -1 : it.tile1;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.item_empty[e]);
-                ++n_item;
+        auto look = [&](Tile &x, uint32_t n) {
+            const uint32_t e = n % kTileRing;
+            wait(&sm.tile_full[e], (n / kTileRing) & 1u, 60);
+            x.key0 = *dead ? -1 : sm.tiles[e].key0;
+            x.len = sm.tiles[e].len;
+            x.at[0] = sm.tiles[e].at[2 * wq];
+            x.at[1] = sm.tiles[e].at[2 * wq + 1];
+        };
+        // bulk copies of the warp's pieces into its shared memory; whether there are any
+        uint32_t n_k = 0, n_v = 0;  // copies waited for so far
+        auto fetch = [&](const Tile &x, const uint8_t *pages, uint8_t *dst, uint32_t stride, uint64_t *bar) {
+            const bool any = x.key0 >= 0 && (x.at[0] >= 0 || x.at[1] >= 0);
+            if (any && lane == 0) {
+                mbar_arrive_expect_tx(bar, kKvTile * D * ((x.at[0] >= 0) + (x.at[1] >= 0)));
+                if (x.at[0] >= 0) bulk_load(dst, pages + x.at[0], kKvTile * D, bar);
+                if (x.at[1] >= 0) bulk_load(dst + stride, pages + x.at[1], kKvTile * D, bar);
             }
+            return any;
         };
-        auto pages = [&](Tile &x) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int32_t key = x.t * kKeys + wq * 32 + u * kKvTile;
-                x.page[u] = x.end >= 0 && key < x.len ? read_page(b, x.seq, key >> b.page_shift) : -1;
-            }
-        };
-        auto piece = [&](const Tile &x, int u) {
-            const int32_t key = x.t * kKeys + wq * 32 + u * kKvTile;
-            return tile_offset<D>(b, max(x.page[u], 0), x.head, (key & (b.page_tokens - 1)) / kKvTile);
-        };
-        uint4 rk[NL], rv[NL];
-        float ks = 0.0f, vs = 0.0f;  // lanes 0 and 1: the scales of piece 0 and 1
-        auto load_k = [&](const Tile &x) {
-            const int64_t at[2] = {piece(x, 0), piece(x, 1)};
+        uint8_t *kc = sm.k_codes[wq][0], *vc = sm.v_codes[wq];
+        look(cur, 0);
+        bool any_k = fetch(cur, b.k_pages, kc, kKvTile * D, &sm.k_landed[wq]);
+        bool any_v = fetch(cur, b.v_pages, vc, kKvTile * D + 16, &sm.v_landed[wq]);
+        while (cur.key0 >= 0) {
+            const uint32_t stage = n_tile & 1u, ph = (n_tile >> 1) & 1u;
+            look(nxt, n_tile + 1);
+            uint4 r[NL];
+            if (any_k) wait(&sm.k_landed[wq], n_k++ & 1u, 63);
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int u = i / (NL / 2);
-                rk[i] = make_uint4(0, 0, 0, 0);
-                if (x.page[u] >= 0)
-                    rk[i] = __ldg(reinterpret_cast<const uint4 *>(b.k_pages + at[u]) + lane + 32 * (i % (NL / 2)));
+                r[i] = make_uint4(0, 0, 0, 0);
+                if (cur.at[u] >= 0) r[i] = *reinterpret_cast<const uint4 *>(kc + 16 * (lane + 32 * i));
             }
-            if (lane < 2) {
-                const int32_t p = lane ? x.page[1] : x.page[0];
-                const int64_t sc = static_cast<int64_t>(max(p, 0)) * b.heads + x.head;
-                ks = p >= 0 ? __ldg(b.k_scales + sc) : 0.0f;
-                vs = p >= 0 ? __ldg(b.v_scales + sc) : 0.0f;
-            }
-        };
-        auto load_v = [&](const Tile &x) {
-            const int u = cc >> 1;
-            const int64_t at = piece(x, u);
-            const int32_t p = u ? x.page[1] : x.page[0];
-#pragma unroll
-            for (int k = 0; k < NL / 2; ++k) {
-                const int d4 = k * 8 + dq * 2 + dpar;
-                const uint4 *src = reinterpret_cast<const uint4 *>(b.v_pages + at + d4 * 64 + (cc & 1) * 32);
-                rv[2 * k] = rv[2 * k + 1] = make_uint4(0, 0, 0, 0);
-                if (p >= 0) {
-                    rv[2 * k] = __ldg(src);
-                    rv[2 * k + 1] = __ldg(src + 1);
-                }
-            }
-        };
-        cur.t = 0;
-        cur.end = 0;
-        advance(cur);
-        pages(cur);
-        if (cur.end >= 0) load_k(cur);
-        while (cur.end >= 0) {
-            const uint32_t stage = n_tile & 1u, ph = (n_tile >> 1) & 1u;
-            load_v(cur);
-            nxt = cur;
-            advance(nxt);
-            pages(nxt);
+            __syncwarp();
+            any_k = fetch(nxt, b.k_pages, kc, kKvTile * D, &sm.k_landed[wq]);
             // K: row = key, 16 dimensions of one key a piece
             wait(&sm.k_empty[stage], ph ^ 1u, 61);
-            if (lane < 2) sm.scales[n_tile % kScaleRing][wq * 2 + lane] = make_float4(ks, vs, log2f(vs), 1.0f / vs);
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int c = lane + 32 * (i % (NL / 2));  // piece within the 16 keys: [atom][key][16 dims]
                 const int row = wq * 32 + (i / (NL / 2)) * kKvTile + (c >> 2) % kKvTile, p = c & 3;
                 uint8_t *dst = sm.k[stage] + (c / 64) * kRowAtom + row * 128;
                 uint32_t w[8];
-                codes_to_f16<FMT>(rk[i].x, w[0], w[1]);
-                codes_to_f16<FMT>(rk[i].y, w[2], w[3]);
-                codes_to_f16<FMT>(rk[i].z, w[4], w[5]);
-                codes_to_f16<FMT>(rk[i].w, w[6], w[7]);
+                codes_to_f16<FMT>(r[i].x, w[0], w[1]);
+                codes_to_f16<FMT>(r[i].y, w[2], w[3]);
+                codes_to_f16<FMT>(r[i].z, w[4], w[5]);
+                codes_to_f16<FMT>(r[i].w, w[6], w[7]);
                 *reinterpret_cast<uint4 *>(dst + (((2 * p) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(dst + (((2 * p + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
             }
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.k_full[stage]);
-            if (nxt.end >= 0) load_k(nxt);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
             // (their codes may be anything, and 0 * NaN is not 0)
+            if (any_v) wait(&sm.v_landed[wq], n_v++ & 1u, 64);
+            const int64_t at_v = cc >> 1 ? cur.at[1] : cur.at[0];
+#pragma unroll
+            for (int k = 0; k < NL / 2; ++k) {
+                const uint8_t *src = vc + (cc >> 1) * (kKvTile * D + 16) + (k * 8 + dq * 2 + dpar) * 64 + (cc & 1) * 32;
+                r[2 * k] = r[2 * k + 1] = make_uint4(0, 0, 0, 0);
+                if (at_v >= 0) {
+                    r[2 * k] = *reinterpret_cast<const uint4 *>(src);
+                    r[2 * k + 1] = *reinterpret_cast<const uint4 *>(src + 16);
+                }
+            }
+            __syncwarp();
+            any_v = fetch(nxt, b.v_pages, vc, kKvTile * D + 16, &sm.v_landed[wq]);
             wait(&sm.v_empty[stage], ph ^ 1u, 62);
-            const int32_t q0 = cur.t * kKeys + wq * 32 + cc * 8;
+            const int32_t q0 = cur.key0 + wq * 32 + cc * 8;
             uint32_t keep[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -671,8 +671,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
 #pragma unroll
             for (int k = 0; k < NL / 2; ++k) {
                 const int d4 = k * 8 + dq * 2 + dpar;
-                const uint32_t wa[4] = {rv[2 * k].x, rv[2 * k].y, rv[2 * k].z, rv[2 * k].w};
-                const uint32_t wb[4] = {rv[2 * k + 1].x, rv[2 * k + 1].y, rv[2 * k + 1].z, rv[2 * k + 1].w};
+                const uint32_t wa[4] = {r[2 * k].x, r[2 * k].y, r[2 * k].z, r[2 * k].w};
+                const uint32_t wb[4] = {r[2 * k + 1].x, r[2 * k + 1].y, r[2 * k + 1].z, r[2 * k + 1].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t w[4];
@@ -687,6 +687,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             if (lane == 0) mbar_arrive(&sm.v_full[stage]);
             cur = nxt;
             ++n_tile;
+        }
+        if (*dead) {  // after a time-out: copies that nobody has waited for
+            if (any_k) mbar_wait_bounded(&sm.k_landed[wq], n_k & 1u, kPreWaitNs);
+            if (any_v) mbar_wait_bounded(&sm.v_landed[wq], n_v & 1u, kPreWaitNs);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
@@ -754,6 +758,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         else mma_commit(&sm.o_done[1]);
                     }
                     mma_commit(&sm.v_empty[st]);
+                    mma_commit(&sm.tile_empty[n_tile % kTileRing]);  // (the softmax has read its scales)
                     if (more) mma_commit(&sm.k_empty[st1]);
                 }
             }
@@ -820,6 +825,50 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             it.tile0 = 0;
             it.tile1 = -1;
             publish(it);
+        }
+        if (warp == 14) {
+            // ============================================ pages and scales of the key tiles
+            uint32_t n_item = 0, n_tile = 0;
+            const int sub = lane & 7;
+            while (true) {
+                const uint32_t e = n_item % kItemRing;
+                wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 90);
+                const int32_t seq = sm.items[e].seq, head = sm.items[e].head, len = sm.items[e].len;
+                const int32_t tile0 = sm.items[e].tile0, tile1 = *dead ? -1 : sm.items[e].tile1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.item_empty[e]);
+                ++n_item;
+                // four tiles at a time: lane = (tile, piece)
+                for (int32_t t0 = tile0; t0 < max(tile1, tile0 + 1); t0 += 4) {
+                    const int32_t t = t0 + (lane >> 3), key = t * kKeys + sub * kKvTile;
+                    int64_t at = -1;
+                    float ks = 0.0f, vs = 0.0f;
+                    if (t < tile1 && key < len) {
+                        const int32_t page = read_page(b, seq, key >> b.page_shift);
+                        if (page >= 0) {
+                            at = tile_offset<D>(b, page, head, (key & (b.page_tokens - 1)) / kKvTile);
+                            ks = __ldg(b.k_scales + static_cast<int64_t>(page) * b.heads + head);
+                            vs = __ldg(b.v_scales + static_cast<int64_t>(page) * b.heads + head);
+                        }
+                    }
+                    for (int q = 0; q < 4 && t0 + q < max(tile1, tile0 + 1); ++q) {
+                        const uint32_t r = n_tile % kTileRing;
+                        wait(&sm.tile_empty[r], ((n_tile / kTileRing) & 1u) ^ 1u, 91);
+                        if ((lane >> 3) == q) {
+                            sm.tiles[r].scales[sub] = make_float4(ks, vs, log2f(vs), 1.0f / vs);
+                            sm.tiles[r].at[sub] = at;
+                            if (sub == 0) {
+                                sm.tiles[r].key0 = tile1 < 0 ? -1 : t * kKeys;
+                                sm.tiles[r].len = len;
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.tile_full[r]);
+                        ++n_tile;
+                    }
+                }
+                if (tile1 < 0) break;
+            }
         }
         __syncwarp();
     }
