@@ -89,6 +89,7 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
     if (!(a->scale > 0.0f) || !isfinite(a->scale)) return LORA_ERR_INVALID_ARG;
     if (a->num_q_heads % c->num_heads || a->num_q_heads / c->num_heads > lora::kMaxGroup)
         return LORA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(b->rows) * a->num_q_heads > INT32_MAX) return LORA_ERR_UNSUPPORTED;
     s = check_heads(&a->q, a->dtype, b->rows, &v->q);
     if (s == LORA_OK) s = check_heads(&a->out, a->dtype, b->rows, &v->out);
     if (s != LORA_OK) return s;

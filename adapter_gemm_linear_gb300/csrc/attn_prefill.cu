@@ -19,9 +19,10 @@
 //    the 128-byte-swizzled K-major layout of tcgen05.mma: K as [keys][dims], V
 //    as [dims][keys], which the cache's layout of V gives without a
 //    transposition.  Two stages each; the next tile's codes are on their way
-//    by bulk copies meanwhile (loads into registers were slower by half: with
-//    213 KB of shared memory taken, what is left of the L1 holds too few of
-//    them in flight).
+//    to shared memory meanwhile by 16-byte asynchronous copies, each thread's
+//    its own (loads into registers took half as long again: with 225 KB of
+//    shared memory taken, what is left of the L1 holds too few in flight;
+//    and 32 bulk copies of 2 KB a tile take the copy engine 2 us).
 //  - warp 12 issues the products; warp 13 hands out the items, and warp 14
 //    looks up the pages and scales of the key tiles, eight tiles ahead.
 //  - q is f16 times a power of two per row (exact for bf16), P is f16 (11
@@ -52,7 +53,7 @@ constexpr int kPreThreads = 512;
 constexpr int kItemRing = 4;
 constexpr int kItemReaders = 8 + 1 + 1;  // warps that read an item's entry
 constexpr int kTileRing = 8;             // key tiles looked up ahead
-constexpr uint64_t kPreWaitNs = 2000000000ull;
+constexpr long long kWaitClocks = 4000000000ll;  // about 2 s: far beyond any legitimate wait
 
 struct Item {
     int32_t seq, head, row_tile, last_cta;
@@ -75,18 +76,17 @@ struct PrefillSmem {
     alignas(1024) uint8_t q[2][kHalf * D * 2];
     uint8_t k[2][kKeys * D * 2];
     uint8_t v[2][kKeys * D * 2];
-    // codes on their way: per converting warp its two 16-key pieces of K and of
-    // V, the second of V 16 bytes off so that both are read without conflicts
-    uint8_t k_codes[4][2][kKvTile * D];
-    uint8_t v_codes[4][2 * kKvTile * D + 16];
+    // codes on their way, of K and of V: 16-byte pieces of the converting
+    // threads, each read by the thread that fetched it
+    uint4 codes[2][2 * D / 32][128];
     alignas(16) KeyTile tiles[kTileRing];
     Item items[kItemRing];
     uint64_t item_full[kItemRing], item_empty[kItemRing], tile_full[kTileRing], tile_empty[kTileRing];
-    uint64_t k_landed[4], v_landed[4];
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_done[2], drain;
     long long warp_sum[kPreThreads / 32];
     long long base;
     int32_t seq;
+    int32_t head0, row_tile0, skip0;  // where the CTA's line begins
     uint32_t tmem;
     int32_t dead;
 };
@@ -102,6 +102,14 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
         "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// The descriptor of desc_kmajor_sw128 with this low word.
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
+    constexpr uint32_t high = (1024 >> 4) | (1u << 14) | (2u << 29);
+    uint64_t d;
+    asm volatile("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "n"(high));
+    return d;
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t *r) {
@@ -143,6 +151,12 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// 16 bytes from global to shared memory, asynchronously; zeros if not `there`.
+__device__ __forceinline__ void copy16(void *smem_dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+
 // Two fp32 values at once.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
@@ -173,63 +187,80 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return r;
 }
 
+// Wait for a phase of an mbarrier, bounded by the SM's clock: reading it costs
+// a few cycles, where the global timer costs a good part of the wait.
+__device__ __forceinline__ bool wait_clocks(uint64_t *bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > kWaitClocks) return false;
+    }
+}
+
 // ---------------------------------------------------------------- the line of work
 
-// sum of floor((a i + b) / m) over 0 <= i < n, with a, b >= 0 (the Euclid-like recursion)
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum of floor((a i + b) / m) over 0 <= i < n (the Euclid-like recursion);
+// every a n + b on the way fits 32 bits, as rows * group does.
+__device__ __noinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     long long ans = 0;
     while (n > 0) {
-        ans += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
-        a %= m;
-        b %= m;
-        const long long y = a * n + b;
+        if (a >= m) {
+            ans += static_cast<long long>(a / m) * (static_cast<long long>(n) * (n - 1) / 2);
+            a %= m;
+        }
+        if (b >= m) {
+            ans += static_cast<long long>(b / m) * n;
+            b %= m;
+        }
+        const uint32_t y = a * n + b;
         if (y < m) break;
         n = y / m;
         b = y % m;
-        const long long t = m;
+        const uint32_t t = m;
         m = a;
         a = t;
     }
     return ans;
 }
 
-// A sequence's row tiles: tile i covers rows [256 i, 256 i + 256) of n * group.
+// A sequence's row tiles: tile i covers rows [256 i, 256 i + 256) of n *
+// group.  (The host refuses calls with 2^31 rows * group or more.)
 struct RowTiles {
-    int32_t first, len, n, group, count, window, causal;
+    int32_t first, len, rows, group, count, window, causal;
 
     __device__ __forceinline__ RowTiles(const AttnView &a, const SeqRows &r)
-        : first(r.len - r.n), len(r.len), n(r.n), group(a.group),
-          count(static_cast<int32_t>((static_cast<long long>(r.n) * a.group + kRows - 1) / kRows)), window(a.window),
-          causal(a.causal) {}
+        : first(r.len - r.n), len(r.len), rows(r.n * a.group), group(a.group), count((rows + kRows - 1) / kRows),
+          window(a.window), causal(a.causal) {}
 
     // key tiles [lo, hi) that the queries of row tile i see
     __device__ __forceinline__ int32_t hi(int32_t i) const {
-        const long long last = min(static_cast<long long>(i + 1) * kRows, static_cast<long long>(n) * group) - 1;
-        const int32_t end = causal ? first + static_cast<int32_t>(last / group) + 1 : len;
-        return (end + kKeys - 1) / kKeys;
+        const int32_t last = min(i * kRows + kRows - 1, rows - 1);
+        const int32_t end = causal ? first + last / group + 1 : len;
+        return static_cast<int32_t>((static_cast<uint32_t>(end) + kKeys - 1) / kKeys);
     }
     __device__ __forceinline__ int32_t lo(int32_t i) const {
         if (window <= 0) return 0;
-        const long long q0 = static_cast<long long>(i) * kRows / group;
-        return static_cast<int32_t>(max(0ll, first + q0 - window + 1) / kKeys);
+        return max(0, first + i * kRows / group - window + 1) / kKeys;
     }
     // sum of hi - lo over the row tiles before i.  256 = 2 * 128, so hi(i) =
     // floor((2 i + floor((255 + group (first + 128)) / 128)) / group) for every
     // tile but the last, and lo(i) = max(0, floor((2 i + floor(group (first -
     // window + 1) / 128)) / group)).
-    __device__ long long before(int32_t i) const {
+    __device__ __forceinline__ long long before(int32_t i) const {
         long long sum;
         if (causal) {
-            const long long c = (kRows - 1 + static_cast<long long>(group) * (first + kKeys)) / kKeys;
-            sum = floor_sum(min(i, count - 1), group, 2, c);
+            const long long c = (kRows - 1 + static_cast<long long>(group) * (first + kKeys)) >> 7;
+            sum = floor_sum(min(i, count - 1), group, 2, static_cast<uint32_t>(c));
             if (i == count) sum += hi(count - 1);
         } else {
             sum = static_cast<long long>(i) * hi(0);
         }
         if (window > 0) {
             const long long x = static_cast<long long>(group) * (first - window + 1);
-            const long long e = x >= 0 ? x / kKeys : -((-x + kKeys - 1) / kKeys);
-            const long long i0 = e >= 0 ? 0 : (-e + 1) / 2;
+            const int32_t e = static_cast<int32_t>(x >> 7);  // floor, of negative numbers too
+            const int32_t i0 = e >= 0 ? 0 : (1 - e) / 2;
             if (i > i0) sum -= floor_sum(i - i0, group, 2, 2 * i0 + e);
         }
         return sum;
@@ -260,14 +291,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView &b = a.kv;
     JoinEntry *joins = join_entries(a, gridDim.x, kRows, D);
-    volatile int32_t *dead = &sm.dead;
+    volatile int32_t *dead = &sm.dead;  // where a wait ran out (0: none did); then nobody waits any more
 
-    auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t site) {
-        if (*dead) return;
-        if (!mbar_wait_bounded(bar, parity, kPreWaitNs)) {
-            record_error(b.status, kDevTimeout, site);
-            *dead = 1;
-        }
+    auto wait = [&](uint64_t *bar, uint32_t parity, int32_t site) {
+        if (!mbar_try_wait(bar, parity) && !*dead && !wait_clocks(bar, parity)) *dead = site;
     };
 
     // ---- set-up and plan
@@ -289,10 +316,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_ready[i], 4);
             mbar_init(&sm.o_done[i], 1);
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&sm.k_landed[i], 1);
-            mbar_init(&sm.v_landed[i], 1);
         }
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
@@ -338,10 +361,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = sm.tmem;
+    if (w0 < w1) {  // the first item: the row tile i with before(i) <= u < before(i + 1)
+        const RowTiles t(a, prefill_seq(a, sm.seq));
+        const long long units = t.before(t.count), local = w0 - sm.base;
+        const int32_t head = static_cast<int32_t>(local / units);
+        const long long u = local - head * units;
+        for (int32_t i = threadIdx.x; i < t.count; i += kPreThreads) {
+            const long long at = t.before(i);
+            if (at <= u && u < at + t.hi(i) - t.lo(i)) {
+                sm.head0 = head;
+                sm.row_tile0 = i;
+                sm.skip0 = static_cast<int32_t>(u - at);
+            }
+        }
+    }
+    __syncthreads();
 
     if (warp < 8) {
         // ================================================ softmax of tile X
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int X = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's TMEM lanes
         const uint32_t ts = tmem + lanes + X * 128, to = tmem + lanes + 256 + X * 128;
@@ -356,48 +394,54 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             if (lane == 0) mbar_arrive(&sm.item_empty[e]);
             ++n_item;
         };
-        // Q_X of an item into shared memory: the thread's row, f16 times a
-        // power of two (its largest value in [2^13, 2^14)); returns the factor
-        // that turns its products with codes into log2 units
+        // Q_X of an item into shared memory: f16 times a power of two per row
+        // (its largest value in [2^13, 2^14)); returns the factor that turns
+        // the thread's row's products with codes into log2 units.  A warp reads
+        // its 32 rows several at a time, 16 bytes a lane.
         auto load_q = [&](const Item &it) {
-            const long long rows = static_cast<long long>(it.n) * a.group;
-            const long long row = min(static_cast<long long>(it.row_tile) * kRows + rt, rows - 1);
-            const int32_t qi = static_cast<int32_t>(row / a.group), qh = it.head * a.group + static_cast<int32_t>(row % a.group);
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
-                                                               static_cast<int64_t>(it.off + qi) * a.q.row + qh * a.q.head);
-            uint4 x[D / 8];
+            constexpr int LANES = D / 8;         // lanes of a row
+            constexpr int AT_ONCE = 32 / LANES;  // rows of a load
+            const int piece = lane % LANES, base = X * kHalf + (warp & 3) * 32 + lane / LANES;
+            const int32_t rows = it.n * a.group;
+            uint4 x[LANES];
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) x[i] = __ldg(src + i);
-            float amax = 0.0f;
+            for (int i = 0; i < LANES; ++i) {
+                const int32_t row = min(it.row_tile * kRows + base + i * AT_ONCE, rows - 1);
+                const int32_t qi = row / a.group, qh = it.head * a.group + row % a.group;
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
+                                                             static_cast<int64_t>(it.off + qi) * a.q.row + qh * a.q.head) + piece);
+            }
+            float mine = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = 0; i < LANES; ++i) {
                 const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                float amax = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
-            }
-            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
-            e = amax < INFINITY ? max(e, -126) : 0;
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            const int r = rt - X * kHalf;
-            uint8_t *dst = sm.q[X] + r * 128;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+                e = amax < INFINITY ? max(e, -126) : 0;
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                // the row of lane L is L: row i * AT_ONCE + L % AT_ONCE, held by lanes (L % AT_ONCE) * LANES + ...
+                const float up = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 + e) << 23), lane % AT_ONCE * LANES);
+                if (lane / AT_ONCE == i) mine = up;
                 uint32_t h[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-                *reinterpret_cast<uint4 *>(dst + (i / 8) * kRowAtom + (((i & 7) ^ (r & 7)) << 4)) =
+                const int r = base - X * kHalf + i * AT_ONCE;
+                *reinterpret_cast<uint4 *>(sm.q[X] + r * 128 + (piece / 8) * kRowAtom + (((piece & 7) ^ (r & 7)) << 4)) =
                     make_uint4(h[0], h[1], h[2], h[3]);
             }
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_full[X]);
-            return a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            return a.scale * kLog2e * mine;
         };
         auto takes_part = [&](const Item &it) {  // tile B may be empty
-            return it.tile1 >= 0 && (X == 0 || static_cast<long long>(it.n) * a.group - static_cast<long long>(it.row_tile) * kRows > kHalf);
+            return it.tile1 >= 0 && (X == 0 || it.n * a.group - it.row_tile * kRows > kHalf);
         };
 
         Item it;
@@ -410,7 +454,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 if (takes_part(it)) cr = load_q(it);
                 continue;
             }
-            const int32_t rows = static_cast<int32_t>(min(static_cast<long long>(kRows), static_cast<long long>(it.n) * a.group - static_cast<long long>(it.row_tile) * kRows));
+            const int32_t rows = min(kRows, it.n * a.group - it.row_tile * kRows);
             const int32_t row = it.row_tile * kRows + min(rt, rows - 1);
             const int32_t qi = row / a.group, qh = it.head * a.group + row % a.group;
             const int32_t pos = it.len - it.n + qi;
@@ -578,7 +622,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         }
     } else if (warp < 12) {
         // ================================================ codes to f16 tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int wq = warp - 8;  // the warp's 32 keys of a tile
         constexpr int NL = 2 * D / 32;  // 16-byte pieces a lane holds of K (or V)
         uint32_t n_tile = 0;
@@ -597,34 +641,42 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             x.at[0] = sm.tiles[e].at[2 * wq];
             x.at[1] = sm.tiles[e].at[2 * wq + 1];
         };
-        // bulk copies of the warp's pieces into its shared memory; whether there are any
-        uint32_t n_k = 0, n_v = 0;  // copies waited for so far
-        auto fetch = [&](const Tile &x, const uint8_t *pages, uint8_t *dst, uint32_t stride, uint64_t *bar) {
-            const bool any = x.key0 >= 0 && (x.at[0] >= 0 || x.at[1] >= 0);
-            if (any && lane == 0) {
-                mbar_arrive_expect_tx(bar, kKvTile * D * ((x.at[0] >= 0) + (x.at[1] >= 0)));
-                if (x.at[0] >= 0) bulk_load(dst, pages + x.at[0], kKvTile * D, bar);
-                if (x.at[1] >= 0) bulk_load(dst + stride, pages + x.at[1], kKvTile * D, bar);
+        uint4 *kc = &sm.codes[0][0][wq * 32 + lane], *vc = &sm.codes[1][0][wq * 32 + lane];
+        // the thread's pieces of a tile, one asynchronous group of 16-byte copies; zeros where there is no page
+        auto fetch_k = [&](const Tile &x) {
+            if (x.key0 >= 0) {
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const int64_t at = x.at[i / (NL / 2)];
+                    copy16(kc + 128 * i, b.k_pages + max(at, int64_t{0}) + 16 * (lane + 32 * (i % (NL / 2))), at >= 0);
+                }
             }
-            return any;
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        uint8_t *kc = sm.k_codes[wq][0], *vc = sm.v_codes[wq];
+        auto fetch_v = [&](const Tile &x) {
+            if (x.key0 >= 0) {
+                const int64_t at = cc >> 1 ? x.at[1] : x.at[0];
+                const uint8_t *src = b.v_pages + max(at, int64_t{0}) + (dq * 2 + dpar) * 64 + (cc & 1) * 32;
+#pragma unroll
+                for (int k = 0; k < NL / 2; ++k) {
+                    copy16(vc + 128 * (2 * k), src + k * 512, at >= 0);
+                    copy16(vc + 128 * (2 * k + 1), src + k * 512 + 16, at >= 0);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        auto landed = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };  // all groups but the newest
         look(cur, 0);
-        bool any_k = fetch(cur, b.k_pages, kc, kKvTile * D, &sm.k_landed[wq]);
-        bool any_v = fetch(cur, b.v_pages, vc, kKvTile * D + 16, &sm.v_landed[wq]);
+        fetch_k(cur);
+        fetch_v(cur);
         while (cur.key0 >= 0) {
             const uint32_t stage = n_tile & 1u, ph = (n_tile >> 1) & 1u;
             look(nxt, n_tile + 1);
             uint4 r[NL];
-            if (any_k) wait(&sm.k_landed[wq], n_k++ & 1u, 63);
+            landed();
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int u = i / (NL / 2);
-                r[i] = make_uint4(0, 0, 0, 0);
-                if (cur.at[u] >= 0) r[i] = *reinterpret_cast<const uint4 *>(kc + 16 * (lane + 32 * i));
-            }
-            __syncwarp();
-            any_k = fetch(nxt, b.k_pages, kc, kKvTile * D, &sm.k_landed[wq]);
+            for (int i = 0; i < NL; ++i) r[i] = kc[128 * i];
+            fetch_k(nxt);
             // K: row = key, 16 dimensions of one key a piece
             wait(&sm.k_empty[stage], ph ^ 1u, 61);
 #pragma unroll
@@ -645,19 +697,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             if (lane == 0) mbar_arrive(&sm.k_full[stage]);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
             // (their codes may be anything, and 0 * NaN is not 0)
-            if (any_v) wait(&sm.v_landed[wq], n_v++ & 1u, 64);
-            const int64_t at_v = cc >> 1 ? cur.at[1] : cur.at[0];
+            landed();
 #pragma unroll
-            for (int k = 0; k < NL / 2; ++k) {
-                const uint8_t *src = vc + (cc >> 1) * (kKvTile * D + 16) + (k * 8 + dq * 2 + dpar) * 64 + (cc & 1) * 32;
-                r[2 * k] = r[2 * k + 1] = make_uint4(0, 0, 0, 0);
-                if (at_v >= 0) {
-                    r[2 * k] = *reinterpret_cast<const uint4 *>(src);
-                    r[2 * k + 1] = *reinterpret_cast<const uint4 *>(src + 16);
-                }
-            }
-            __syncwarp();
-            any_v = fetch(nxt, b.v_pages, vc, kKvTile * D + 16, &sm.v_landed[wq]);
+            for (int i = 0; i < NL; ++i) r[i] = vc[128 * i];
+            fetch_v(nxt);
             wait(&sm.v_empty[stage], ph ^ 1u, 62);
             const int32_t q0 = cur.key0 + wq * 32 + cc * 8;
             uint32_t keep[2];
@@ -688,44 +731,48 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             cur = nxt;
             ++n_tile;
         }
-        if (*dead) {  // after a time-out: copies that nobody has waited for
-            if (any_k) mbar_wait_bounded(&sm.k_landed[wq], n_k & 1u, kPreWaitNs);
-            if (any_v) mbar_wait_bounded(&sm.v_landed[wq], n_v & 1u, kPreWaitNs);
-        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 12 && lane == 0) {
             // ============================================ the products
             constexpr uint32_t idesc_s = idesc_f16_f32(kHalf, kKeys), idesc_o = idesc_f16_f32(kHalf, D);
-            uint32_t n_item = 0, n_tile = 0, n_a = 0, n_b = 0, n_qa = 0, n_qb = 0;
+            uint32_t n_item = 0, n_tile = 0, n_b = 0, n_qb = 0;
+            // The descriptors' low words (their address fields) are made anew for
+            // each group of products: kept over the loop, they would not fit the
+            // registers, and a spilled one costs a trip to the L2.
+            auto low = [](const void *p) {
+                uint32_t w = static_cast<uint32_t>(desc_kmajor_sw128(smem_u32(p)));
+                asm volatile("" : "+r"(w));
+                return w;
+            };
             auto scores = [&](int X, uint32_t stage) {
-                const uint64_t qd = desc_kmajor_sw128(smem_u32(sm.q[X])), kd = desc_kmajor_sw128(smem_u32(sm.k[stage]));
+                const uint32_t q = low(sm.q[X]), k = low(sm.k[stage]);
                 if (!*dead)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = (k / 4) * (kRowAtom >> 4) + (k % 4) * 2;
-                        mma_bf16_f32(tmem + X * 128, qd + at, kd + at, idesc_s, k > 0);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t at = (i / 4) * (kRowAtom >> 4) + (i % 4) * 2;
+                        mma_bf16_f32(tmem + X * 128, desc_of(q + at), desc_of(k + at), idesc_s, i > 0);
                     }
                 mma_commit(&sm.s_full[X]);
             };
             auto values = [&](int X, uint32_t stage, bool first) {
-                const uint64_t vd = desc_kmajor_sw128(smem_u32(sm.v[stage]));
+                const uint32_t v = low(sm.v[stage]);
                 if (!*dead)
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_f16_ts(tmem + 256 + X * 128, tmem + X * 128 + k * 8,
-                                   vd + (k / 4) * (kVAtom >> 4) + (k % 4) * 2, idesc_o, !first || k > 0);
+                    for (int i = 0; i < kKeys / 16; ++i)
+                        mma_f16_ts(tmem + 256 + X * 128, tmem + X * 128 + i * 8,
+                                   desc_of(v + (i / 4) * (kVAtom >> 4) + (i % 4) * 2), idesc_o, !first || i > 0);
             };
             while (true) {
                 const uint32_t e = n_item % kItemRing;
                 wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 70);
                 const int32_t nt = sm.items[e].tile1 - sm.items[e].tile0, stop = sm.items[e].tile1 < 0;
-                const bool has_b = static_cast<long long>(sm.items[e].n) * a.group -
-                                       static_cast<long long>(sm.items[e].row_tile) * kRows > kHalf;
+                const bool has_b = sm.items[e].n * a.group - sm.items[e].row_tile * kRows > kHalf;
                 mbar_arrive(&sm.item_empty[e]);
                 ++n_item;
                 if (stop || *dead) break;
-                wait(&sm.q_full[0], n_qa++ & 1u, 71);
+                wait(&sm.q_full[0], (n_item - 1) & 1u, 71);
                 wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
                 tc_fence_after_sync();
                 scores(0, n_tile & 1u);
@@ -740,7 +787,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     const uint32_t st1 = (n_tile + 1) & 1u, ph1 = ((n_tile + 1) >> 1) & 1u;
                     const bool more = j + 1 < nt;
                     wait(&sm.v_full[st], ph, 74);
-                    wait(&sm.p_ready[0], n_a++ & 1u, 75);
+                    wait(&sm.p_ready[0], n_tile & 1u, 75);
                     tc_fence_after_sync();
                     values(0, st, j == 0);
                     if (more) {
@@ -764,7 +811,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             }
             // nothing of this thread's may be in flight when Tensor Memory is freed
             mma_commit(&sm.drain);
-            mbar_wait_bounded(&sm.drain, 0, kPreWaitNs);
+            if (!mbar_try_wait(&sm.drain, 0)) wait_clocks(&sm.drain, 0);
         } else if (warp == 13 && lane == 0) {
             // ============================================ the items
             uint32_t n_item = 0;
@@ -778,24 +825,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             Item it;
             if (w0 < w1) {
                 it.seq = sm.seq;
+                it.head = sm.head0;
+                it.row_tile = sm.row_tile0;
+                int32_t skip = sm.skip0;  // tiles of the first item that belong to the CTA before
                 SeqRows r = prefill_seq(a, it.seq);
-                int32_t count;
-                int32_t skip;  // tiles of the first item that belong to the CTA before
-                {
-                    const RowTiles t(a, r);
-                    const long long units = t.before(t.count);
-                    const long long local = w0 - sm.base;
-                    it.head = static_cast<int32_t>(local / units);
-                    const long long u = local - it.head * units;
-                    int32_t lo = 0, hi = t.count - 1;  // the last row tile with before(i) <= u
-                    while (lo < hi) {
-                        const int32_t mid = (lo + hi + 1) >> 1;
-                        if (t.before(mid) <= u) lo = mid; else hi = mid - 1;
-                    }
-                    it.row_tile = lo;
-                    skip = static_cast<int32_t>(u - t.before(lo));
-                    count = t.count;
-                }
+                int32_t count = RowTiles(a, r).count;
                 long long w = w0;
                 while (w < w1) {
                     const RowTiles t(a, r);
@@ -874,6 +908,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     }
     tc_fence_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && *dead) record_error(b.status, kDevTimeout, static_cast<uint32_t>(*dead));
     if (warp == 12) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);

@@ -180,7 +180,8 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * Precision: products with the codes exact, fp32 sums; probabilities enter
  * the second product with 11 significant bits for bf16 calls, 22 for fp32.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (num_q_heads /
- * num_heads over 64; num_q_heads not a multiple), WORKSPACE, CUDA.
+ * num_heads over 64; num_q_heads not a multiple; rows * num_q_heads of 2^31
+ * or more), WORKSPACE, CUDA.
  */
 typedef struct lora_kv_attention_args {
     lora_dtype_t dtype;      /* of q and out */
