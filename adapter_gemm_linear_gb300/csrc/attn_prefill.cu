@@ -65,10 +65,18 @@ constexpr int kFromStart = 1, kToEnd = 2;
 
 // A key tile of the CTA's line: where its 16-key pieces are, and their scales.
 struct KeyTile {
-    float4 scales[kSubs];  // K's scale, V's, its log2 and reciprocal
-    int64_t at[kSubs];     // offset in k_pages and v_pages; < 0: past the end or not there, zeros
-    int32_t key0, len;     // first key, the sequence's length; key0 < 0: no more tiles
-    int32_t pad[2];
+    // Of each piece K's scale, and log2 and reciprocal of V's.  A piece whose V
+    // is zero (scale 0) takes those of a neighbour: any would do, and that one
+    // keeps the exponents together.
+    float4 scales[kSubs];
+    int64_t at[kSubs];    // offset in k_pages; < 0: past the end or not there, zeros
+    int64_t at_v[kSubs];  // and in v_pages
+    int32_t key0, len;    // first key, the sequence's length; key0 < 0: no more tiles
+    // The item's first tile with a V that is not zero, if tiles before it took
+    // log2 vs = 0: what their sums are multiplied by (in log2 and as a factor)
+    int32_t rebase;
+    float rebase_lv, rebase_iv;
+    int32_t pad[3];
 };
 
 template <int D>
@@ -82,7 +90,7 @@ struct PrefillSmem {
     alignas(16) KeyTile tiles[kTileRing];
     Item items[kItemRing];
     uint64_t item_full[kItemRing], item_empty[kItemRing], tile_full[kTileRing], tile_empty[kTileRing];
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_done[2], drain;
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2][2], o_done[2], drain;
     long long warp_sum[kPreThreads / 32];
     long long base;
     int32_t seq;
@@ -93,6 +101,17 @@ struct PrefillSmem {
 
 // ---------------------------------------------------------------- PTX
 
+// One lane of the (converged) warp, known to be one to the compiler.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // D (+)= A B^T, A: f16 in Tensor Memory (two per column), B: shared memory, fp32 sums.
 __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -102,14 +121,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
         "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// The descriptor of desc_kmajor_sw128 with this low word.
-__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
-    constexpr uint32_t high = (1024 >> 4) | (1u << 14) | (2u << 29);
-    uint64_t d;
-    asm volatile("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "n"(high));
-    return d;
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t *r) {
@@ -187,13 +198,13 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return r;
 }
 
-// Wait for a phase of an mbarrier, bounded by the SM's clock: reading it costs
-// a few cycles, where the global timer costs a good part of the wait.
+// Wait for a phase of an mbarrier, bounded by the SM's clock (cheaper to read
+// than the global timer).
 __device__ __forceinline__ bool wait_clocks(uint64_t *bar, uint32_t parity) {
     const long long t0 = clock64();
     while (true) {
 #pragma unroll 1
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 8; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (clock64() - t0 > kWaitClocks) return false;
     }
@@ -280,6 +291,30 @@ __device__ __forceinline__ long long seq_units(const AttnView &a, int32_t s) {
     return t.before(t.count) * a.kv.heads;
 }
 
+// ---------------------------------------------------------------- the products
+//
+// Tensor Memory columns: S_A 0, S_B 128 (P over their first 64), O_A 256, O_B 384.
+
+template <int D>
+__device__ __forceinline__ void issue_scores(PrefillSmem<D> &sm, uint32_t X, uint32_t stage) {
+    const uint64_t q = desc_kmajor_sw128(smem_u32(sm.q[0])) + X * (sizeof(sm.q[0]) >> 4);
+    const uint64_t k = desc_kmajor_sw128(smem_u32(sm.k[0])) + stage * (sizeof(sm.k[0]) >> 4);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        const uint32_t at = (i / 4) * (kHalf * 128 >> 4) + (i % 4) * 2;
+        mma_bf16_f32(X * 128, q + at, k + at, idesc_f16_f32(kHalf, kKeys), i > 0);
+    }
+}
+
+// Half h of the keys.
+template <int D>
+__device__ __forceinline__ void issue_values(PrefillSmem<D> &sm, uint32_t X, uint32_t stage, uint32_t h, bool accumulate) {
+    const uint64_t v = desc_kmajor_sw128(smem_u32(sm.v[0])) + stage * (sizeof(sm.v[0]) >> 4) + h * (D * 128 >> 4);
+#pragma unroll
+    for (int i = 0; i < kKeys / 32; ++i)
+        mma_f16_ts(256 + X * 128, X * 128 + h * 32 + i * 8, v + i * 2, idesc_f16_f32(kHalf, D), i > 0 || accumulate);
+}
+
 // ---------------------------------------------------------------- kernel
 
 template <int D, int FMT>
@@ -288,7 +323,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     PrefillSmem<D> &sm = *reinterpret_cast<PrefillSmem<D> *>(raw);
     constexpr uint32_t kRowAtom = kHalf * 128;    // bytes of one atom of 128 rows
     constexpr uint32_t kVAtom = D * 128;          // bytes of 64 keys of V
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the same for the warp, which the compiler cannot know of threadIdx.x / 32:
+    // the roles below may then use uniform registers)
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const KvView &b = a.kv;
     JoinEntry *joins = join_entries(a, gridDim.x, kRows, D);
     volatile int32_t *dead = &sm.dead;  // where a wait ran out (0: none did); then nobody waits any more
@@ -314,7 +351,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             mbar_init(&sm.v_full[i], 4);
             mbar_init(&sm.v_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_ready[i], 4);
+            mbar_init(&sm.p_ready[i][0], 4);
+            mbar_init(&sm.p_ready[i][1], 4);
             mbar_init(&sm.o_done[i], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -379,7 +417,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
 
     if (warp < 8) {
         // ================================================ softmax of tile X
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int X = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's TMEM lanes
         const uint32_t ts = tmem + lanes + X * 128, to = tmem + lanes + 256 + X * 128;
@@ -464,56 +501,65 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             const int32_t all_hi = a.causal ? it.len - it.n + it.row_tile * kRows / a.group + 1 : it.len;
             const int32_t all_lo = a.window > 0 ? it.len - it.n + (it.row_tile * kRows + rows - 1) / a.group - a.window + 1 : 0;
             float m = -INFINITY, l = 0.0f;
-            float lvp = 0.0f, ivp = 1.0f;  // of the last page whose V is not all zero
-            bool seen = false;
             for (int32_t t = it.tile0; t < it.tile1; ++t, ++n_tile, ++n_own) {
                 wait(&sm.tile_full[n_tile % kTileRing], (n_tile / kTileRing) & 1u, 55);
                 wait(&sm.s_full[X], n_own & 1u, 51 + X);
                 tc_fence_after_sync();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld_wait(s[i]);
-                const float4 *scl = sm.tiles[n_tile % kTileRing].scales;
+                const KeyTile &tile = sm.tiles[n_tile % kTileRing];
                 const int32_t key0 = t * kKeys;
-                if (key0 < all_lo || key0 + kKeys > all_hi) {
+                if (__builtin_expect(key0 < all_lo || key0 + kKeys > all_hi, 0)) {
+                    // keys that the row does not see: -inf, in place
+#pragma unroll 1
+                    for (int i = 0; i < kKeys; i += 16) {
+                        uint32_t x[16];
+                        tmem_ld_32x32b_x16(ts + i, x);
 #pragma unroll
-                    for (int e = 0; e < kKeys; ++e)
-                        if (key0 + e < kmin || key0 + e >= kmax) s[e >> 5][e & 31] = 0xFF800000u;  // -inf
-                }
-                if (!seen) {  // tiles so far had V = 0 and took log2 vs = 0: their sums move to this one's
-#pragma unroll
-                    for (int u = kSubs - 1; u >= 0; --u) {
-                        const float4 sc = scl[u];
-                        if (sc.y > 0.0f) {
-                            lvp = sc.z;
-                            ivp = sc.w;
-                            seen = true;
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            if (key0 + i + e < kmin || key0 + i + e >= kmax) x[e] = 0xFF800000u;
+                        tmem_st_32x32b_x16(ts + i, x);
                     }
-                    if (seen) {
-                        m += lvp;
-                        l *= ivp;
-                    }
+                    tmem_st_wait();
                 }
-                // the row's maximum, in log2 units and with V's scale
+                // S is read twice, 64 columns at a time, in loops: the four roles'
+                // code has to stay small, for warps that wait for instructions
+                // were the largest loss (and all of S in registers would take
+                // them from the other roles)
+                uint32_t s[2][32];
+                auto load_s = [&](int h) {
+                    tmem_ld_32x32b_x32(ts + 64 * h, s[0]);
+                    tmem_ld_32x32b_x32(ts + 64 * h + 32, s[1]);
+                    tmem_ld_wait(s[0]);
+                    tmem_ld_wait(s[1]);
+                };
+                if (__builtin_expect(tile.rebase, 0)) {
+                    m += tile.rebase_lv;
+                    l *= tile.rebase_iv;
+                }
+                // the row's maximum, in log2 units and with V's scale (a factor
+                // of 0 would make NaN of what is masked)
                 float mx = -INFINITY;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    load_s(h);
 #pragma unroll
-                for (int u = 0; u < kSubs; ++u) {
-                    const float4 sc = scl[u];
-                    const float c = fmaxf(sc.x * cr, 1e-37f), lv = sc.y > 0.0f ? sc.z : lvp;
-                    const uint32_t *p = &s[u >> 1][(u & 1) * 16];
-                    float x = max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[2]));
+                    for (int v = 0; v < 4; ++v) {
+                        const float2 sc = *reinterpret_cast<const float2 *>(&tile.scales[4 * h + v]);
+                        const uint32_t *p = &s[v >> 1][(v & 1) * 16];
+                        float x = max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[2]));
+                        float y = max3(__uint_as_float(p[3]), __uint_as_float(p[4]), __uint_as_float(p[5]));
 #pragma unroll
-                    for (int e = 3; e < 15; e += 2) x = max3(x, __uint_as_float(p[e]), __uint_as_float(p[e + 1]));
-                    x = fmaxf(x, __uint_as_float(p[15]));
-                    mx = fmaxf(mx, fmaf(x, c, lv));
+                        for (int e = 6; e < 14; e += 4) {
+                            x = max3(x, __uint_as_float(p[e]), __uint_as_float(p[e + 1]));
+                            y = max3(y, __uint_as_float(p[e + 2]), __uint_as_float(p[e + 3]));
+                        }
+                        x = max3(x, __uint_as_float(p[14]), __uint_as_float(p[15]));
+                        mx = fmaxf(mx, fmaf(fmaxf(x, y), fmaxf(sc.x * cr, 1e-37f), sc.y));
+                    }
                 }
                 const bool grow = mx > m + kGrow;
                 if (t == it.tile0) {
                     m = mx;
-                } else if (__any_sync(0xffffffffu, grow)) {
+                } else if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
                     // all products of this tile so far are complete: s_full came after them
                     const float mn = grow ? mx : m;
                     const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn);
@@ -529,17 +575,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     }
                 }
                 const float mu = m == -INFINITY ? 0.0f : m;
-#pragma unroll
+                // P in two halves, so that the product with the first half's V starts early
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
+                    load_s(h);
                     uint32_t pk[32];
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        const int u = 4 * h + v;
-                        const float4 sc = scl[u];
-                        const bool some = sc.y > 0.0f;
-                        const float c = fmaxf(sc.x * cr, 1e-37f), d = (some ? sc.z : lvp) - mu;
+                        const float4 sc = tile.scales[4 * h + v];
+                        const float c = fmaxf(sc.x * cr, 1e-37f), d = sc.y - mu;
                         const uint64_t c2 = pack2(c, c), d2 = pack2(d, d);
-                        const uint32_t *p = &s[u >> 1][(u & 1) * 16];
+                        const uint32_t *p = &s[v >> 1][(v & 1) * 16];
                         uint64_t sum = 0;
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
@@ -552,26 +598,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         }
                         float x, y;
                         unpack2(sum, x, y);
-                        l = fmaf(x + y, some ? sc.w : ivp, l);
-                        if (!some) {  // V = 0 whatever its codes
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) pk[8 * v + e] = 0u;
-                        }
+                        l = fmaf(x + y, sc.z, l);
                     }
                     tmem_st_32x32b_x32(ts + 32 * h, pk);
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_ready[X][h]);
                 }
-#pragma unroll
-                for (int u = 0; u < kSubs; ++u) {
-                    const float4 sc = scl[u];
-                    if (sc.y > 0.0f) {
-                        lvp = sc.z;
-                        ivp = sc.w;
-                    }
-                }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_ready[X]);
             }
             // the next item's Q (this one's products with Q_X are complete), then this one's result
             Item next;
@@ -622,7 +656,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         }
     } else if (warp < 12) {
         // ================================================ codes to f16 tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int wq = warp - 8;  // the warp's 32 keys of a tile
         constexpr int NL = 2 * D / 32;  // 16-byte pieces a lane holds of K (or V)
         uint32_t n_tile = 0;
@@ -630,7 +663,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         // of one tile: its first key, the length, and where the warp's two 16-key pieces are
         struct Tile {
             int32_t key0, len;
-            int64_t at[2];
+            int64_t at[2], at_v;  // (of V the thread's own)
         };
         Tile cur, nxt;
         auto look = [&](Tile &x, uint32_t n) {
@@ -640,91 +673,85 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             x.len = sm.tiles[e].len;
             x.at[0] = sm.tiles[e].at[2 * wq];
             x.at[1] = sm.tiles[e].at[2 * wq + 1];
+            x.at_v = sm.tiles[e].at_v[2 * wq + (cc >> 1)];
         };
         uint4 *kc = &sm.codes[0][0][wq * 32 + lane], *vc = &sm.codes[1][0][wq * 32 + lane];
-        // the thread's pieces of a tile, one asynchronous group of 16-byte copies; zeros where there is no page
-        auto fetch_k = [&](const Tile &x) {
-            if (x.key0 >= 0) {
-#pragma unroll
-                for (int i = 0; i < NL; ++i) {
-                    const int64_t at = x.at[i / (NL / 2)];
-                    copy16(kc + 128 * i, b.k_pages + max(at, int64_t{0}) + 16 * (lane + 32 * (i % (NL / 2))), at >= 0);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+        // the thread's piece i of a tile; zeros where there is no page
+        auto fetch_k = [&](const Tile &x, int i) {
+            const int64_t at = i < NL / 2 ? x.at[0] : x.at[1];
+            copy16(kc + 128 * i, b.k_pages + max(at, int64_t{0}) + 16 * (lane + 32 * (i % (NL / 2))), at >= 0);
         };
-        auto fetch_v = [&](const Tile &x) {
-            if (x.key0 >= 0) {
-                const int64_t at = cc >> 1 ? x.at[1] : x.at[0];
-                const uint8_t *src = b.v_pages + max(at, int64_t{0}) + (dq * 2 + dpar) * 64 + (cc & 1) * 32;
-#pragma unroll
-                for (int k = 0; k < NL / 2; ++k) {
-                    copy16(vc + 128 * (2 * k), src + k * 512, at >= 0);
-                    copy16(vc + 128 * (2 * k + 1), src + k * 512 + 16, at >= 0);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+        auto fetch_v = [&](const Tile &x, int i) {
+            copy16(vc + 128 * i, b.v_pages + max(x.at_v, int64_t{0}) + (dq * 2 + dpar) * 64 + (cc & 1) * 32 + (i >> 1) * 512 + (i & 1) * 16,
+                   x.at_v >= 0);
         };
+        auto fetched = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+        // Where the thread's pieces go (all but constants).  K: piece i is of key
+        // 32 wq + 16 (i / (NL / 2)) + 8 (i % 2) + lane / 4, so the row's place
+        // in the swizzle is lane / 4; 16 dimensions, two 16-byte chunks.  V: of
+        // dimensions 4 d4 .. 4 d4 + 3, d4 = 8 k + 2 dq + dpar, 8 keys.
+        const int kr = lane >> 2, kp = lane & 3;
+        const uint32_t k_at = (wq * 32 + kr) * 128, k_c0 = ((2 * kp) ^ kr) << 4, k_c1 = ((2 * kp + 1) ^ kr) << 4;
+        const uint32_t v_at = (wq >> 1) * kVAtom + (8 * dq + 4 * dpar) * 128, v_c = ((wq & 1) * 4 + cc) ^ (4 * dpar);
         auto landed = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };  // all groups but the newest
         look(cur, 0);
-        fetch_k(cur);
-        fetch_v(cur);
+        for (int i = 0; cur.key0 >= 0 && i < NL; ++i) fetch_k(cur, i);
+        fetched();
+        for (int i = 0; cur.key0 >= 0 && i < NL; ++i) fetch_v(cur, i);
+        fetched();
         while (cur.key0 >= 0) {
             const uint32_t stage = n_tile & 1u, ph = (n_tile >> 1) & 1u;
             look(nxt, n_tile + 1);
-            uint4 r[NL];
-            landed();
-#pragma unroll
-            for (int i = 0; i < NL; ++i) r[i] = kc[128 * i];
-            fetch_k(nxt);
+            const bool more = nxt.key0 >= 0;
             // K: row = key, 16 dimensions of one key a piece
             wait(&sm.k_empty[stage], ph ^ 1u, 61);
-#pragma unroll
+            landed();
+            uint8_t *kdst = sm.k[stage] + k_at;
+#pragma unroll 2
             for (int i = 0; i < NL; ++i) {
-                const int c = lane + 32 * (i % (NL / 2));  // piece within the 16 keys: [atom][key][16 dims]
-                const int row = wq * 32 + (i / (NL / 2)) * kKvTile + (c >> 2) % kKvTile, p = c & 3;
-                uint8_t *dst = sm.k[stage] + (c / 64) * kRowAtom + row * 128;
+                const uint4 r = kc[128 * i];
+                if (more) fetch_k(nxt, i);
+                uint8_t *dst = kdst + (i / (NL / 2)) * (kKvTile * 128) + (i % 2) * 1024 + (i % (NL / 2)) / 2 * kRowAtom;
                 uint32_t w[8];
-                codes_to_f16<FMT>(r[i].x, w[0], w[1]);
-                codes_to_f16<FMT>(r[i].y, w[2], w[3]);
-                codes_to_f16<FMT>(r[i].z, w[4], w[5]);
-                codes_to_f16<FMT>(r[i].w, w[6], w[7]);
-                *reinterpret_cast<uint4 *>(dst + (((2 * p) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4 *>(dst + (((2 * p + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                codes_to_f16<FMT>(r.x, w[0], w[1]);
+                codes_to_f16<FMT>(r.y, w[2], w[3]);
+                codes_to_f16<FMT>(r.z, w[4], w[5]);
+                codes_to_f16<FMT>(r.w, w[6], w[7]);
+                *reinterpret_cast<uint4 *>(dst + k_c0) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(dst + k_c1) = make_uint4(w[4], w[5], w[6], w[7]);
             }
+            fetched();
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.k_full[stage]);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
             // (their codes may be anything, and 0 * NaN is not 0)
-            landed();
-#pragma unroll
-            for (int i = 0; i < NL; ++i) r[i] = vc[128 * i];
-            fetch_v(nxt);
             wait(&sm.v_empty[stage], ph ^ 1u, 62);
-            const int32_t q0 = cur.key0 + wq * 32 + cc * 8;
+            landed();
             uint32_t keep[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int past = q0 + 4 * h + 4 - cur.len;
-                keep[h] = past <= 0 ? 0xFFFFFFFFu : past >= 4 ? 0u : 0xFFFFFFFFu >> (8 * past);
+            for (int i = 0; i < 2; ++i) {
+                const int past = cur.key0 + wq * 32 + cc * 8 + 4 * i + 4 - cur.len;
+                keep[i] = past <= 0 ? 0xFFFFFFFFu : past >= 4 ? 0u : 0xFFFFFFFFu >> (8 * past);
             }
-            uint8_t *vbase = sm.v[stage] + (wq >> 1) * kVAtom;
-            const int c8 = (wq & 1) * 4 + cc;
-#pragma unroll
-            for (int k = 0; k < NL / 2; ++k) {
-                const int d4 = k * 8 + dq * 2 + dpar;
-                const uint32_t wa[4] = {r[2 * k].x, r[2 * k].y, r[2 * k].z, r[2 * k].w};
-                const uint32_t wb[4] = {r[2 * k + 1].x, r[2 * k + 1].y, r[2 * k + 1].z, r[2 * k + 1].w};
+            uint8_t *vdst = sm.v[stage] + v_at;
+#pragma unroll 1
+            for (int k = 0; k < NL / 2; ++k, vdst += 4096) {
+                const uint4 ra = vc[128 * (2 * k)], rb = vc[128 * (2 * k + 1)];
+                if (more) {
+                    fetch_v(nxt, 2 * k);
+                    fetch_v(nxt, 2 * k + 1);
+                }
+                const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t w[4];
                     codes_to_f16<FMT>(wa[e] & keep[0], w[0], w[1]);
                     codes_to_f16<FMT>(wb[e] & keep[1], w[2], w[3]);
-                    const int d = 4 * d4 + e;
-                    *reinterpret_cast<uint4 *>(vbase + d * 128 + ((c8 ^ (d & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(vdst + e * 128 + ((v_c ^ e) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            fetched();
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.v_full[stage]);
@@ -733,84 +760,70 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {
             // ============================================ the products
-            constexpr uint32_t idesc_s = idesc_f16_f32(kHalf, kKeys), idesc_o = idesc_f16_f32(kHalf, D);
+            auto commit = [](uint64_t *bar) {
+                if (elect_one()) mma_commit(bar);
+                __syncwarp();
+            };
             uint32_t n_item = 0, n_tile = 0, n_b = 0, n_qb = 0;
-            // The descriptors' low words (their address fields) are made anew for
-            // each group of products: kept over the loop, they would not fit the
-            // registers, and a spilled one costs a trip to the L2.
-            auto low = [](const void *p) {
-                uint32_t w = static_cast<uint32_t>(desc_kmajor_sw128(smem_u32(p)));
-                asm volatile("" : "+r"(w));
-                return w;
-            };
-            auto scores = [&](int X, uint32_t stage) {
-                const uint32_t q = low(sm.q[X]), k = low(sm.k[stage]);
-                if (!*dead)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t at = (i / 4) * (kRowAtom >> 4) + (i % 4) * 2;
-                        mma_bf16_f32(tmem + X * 128, desc_of(q + at), desc_of(k + at), idesc_s, i > 0);
-                    }
-                mma_commit(&sm.s_full[X]);
-            };
-            auto values = [&](int X, uint32_t stage, bool first) {
-                const uint32_t v = low(sm.v[stage]);
-                if (!*dead)
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        mma_f16_ts(tmem + 256 + X * 128, tmem + X * 128 + i * 8,
-                                   desc_of(v + (i / 4) * (kVAtom >> 4) + (i % 4) * 2), idesc_o, !first || i > 0);
+            // (Tensor Memory begins at column 0: the CTA has all of it)
+            auto scores = [&](uint32_t X, uint32_t stage) {
+                if (elect_one()) {
+                    issue_scores(sm, X, stage);
+                    mma_commit(&sm.s_full[X]);
+                }
+                __syncwarp();
             };
             while (true) {
                 const uint32_t e = n_item % kItemRing;
                 wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 70);
                 const int32_t nt = sm.items[e].tile1 - sm.items[e].tile0, stop = sm.items[e].tile1 < 0;
-                const bool has_b = sm.items[e].n * a.group - sm.items[e].row_tile * kRows > kHalf;
-                mbar_arrive(&sm.item_empty[e]);
-                ++n_item;
+                const uint32_t nx = sm.items[e].n * a.group - sm.items[e].row_tile * kRows > kHalf ? 2 : 1;  // tile B may be empty
+                __syncwarp();
+                if (elect_one()) mbar_arrive(&sm.item_empty[e]);
                 if (stop || *dead) break;
-                wait(&sm.q_full[0], (n_item - 1) & 1u, 71);
                 wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
-                tc_fence_after_sync();
-                scores(0, n_tile & 1u);
-                if (has_b) {
-                    wait(&sm.q_full[1], n_qb++ & 1u, 73);
+#pragma unroll 1
+                for (uint32_t X = 0; X < nx; ++X) {
+                    wait(&sm.q_full[X], (X ? n_qb : n_item) & 1u, 71);
                     tc_fence_after_sync();
-                    scores(1, n_tile & 1u);
+                    scores(X, n_tile & 1u);
                 }
-                mma_commit(&sm.k_empty[n_tile & 1u]);
+                ++n_item;
+                n_qb += nx - 1;
+                commit(&sm.k_empty[n_tile & 1u]);
+#pragma unroll 1
                 for (int32_t j = 0; j < nt; ++j, ++n_tile) {
                     const uint32_t st = n_tile & 1u, ph = (n_tile >> 1) & 1u;
                     const uint32_t st1 = (n_tile + 1) & 1u, ph1 = ((n_tile + 1) >> 1) & 1u;
                     const bool more = j + 1 < nt;
                     wait(&sm.v_full[st], ph, 74);
-                    wait(&sm.p_ready[0], n_tile & 1u, 75);
-                    tc_fence_after_sync();
-                    values(0, st, j == 0);
-                    if (more) {
-                        wait(&sm.k_full[st1], ph1, 76);
-                        tc_fence_after_sync();
-                        scores(0, st1);
-                    } else {
-                        mma_commit(&sm.o_done[0]);
+#pragma unroll 1
+                    for (uint32_t X = 0; X < nx; ++X) {
+#pragma unroll 1
+                        for (uint32_t h = 0; h < 2; ++h) {
+                            wait(&sm.p_ready[X][h], (X ? n_b : n_tile) & 1u, 75);
+                            tc_fence_after_sync();
+                            if (elect_one()) issue_values(sm, X, st, h, j > 0 || h > 0);
+                            __syncwarp();
+                        }
+                        if (more) {
+                            if (X == 0) wait(&sm.k_full[st1], ph1, 76);
+                            tc_fence_after_sync();
+                            scores(X, st1);
+                        } else {
+                            commit(&sm.o_done[X]);
+                        }
                     }
-                    if (has_b) {
-                        wait(&sm.p_ready[1], n_b++ & 1u, 77);
-                        tc_fence_after_sync();
-                        values(1, st, j == 0);
-                        if (more) scores(1, st1);
-                        else mma_commit(&sm.o_done[1]);
-                    }
-                    mma_commit(&sm.v_empty[st]);
-                    mma_commit(&sm.tile_empty[n_tile % kTileRing]);  // (the softmax has read its scales)
-                    if (more) mma_commit(&sm.k_empty[st1]);
+                    n_b += nx - 1;
+                    commit(&sm.v_empty[st]);
+                    commit(&sm.tile_empty[n_tile % kTileRing]);  // (the softmax has read its scales)
+                    if (more) commit(&sm.k_empty[st1]);
                 }
             }
             // nothing of this thread's may be in flight when Tensor Memory is freed
-            mma_commit(&sm.drain);
+            commit(&sm.drain);
             if (!mbar_try_wait(&sm.drain, 0)) wait_clocks(&sm.drain, 0);
         } else if (warp == 13 && lane == 0) {
             // ============================================ the items
@@ -873,6 +886,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 if (lane == 0) mbar_arrive(&sm.item_empty[e]);
                 ++n_item;
                 // four tiles at a time: lane = (tile, piece)
+                float lv_last = 0.0f, iv_last = 1.0f;
+                bool seen = false;  // a piece whose V is not zero
                 for (int32_t t0 = tile0; t0 < max(tile1, tile0 + 1); t0 += 4) {
                     const int32_t t = t0 + (lane >> 3), key = t * kKeys + sub * kKvTile;
                     int64_t at = -1;
@@ -885,20 +900,41 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             vs = __ldg(b.v_scales + static_cast<int64_t>(page) * b.heads + head);
                         }
                     }
+                    __syncwarp();
+                    const uint32_t some = __ballot_sync(0xffffffffu, vs > 0.0f);
+                    // a piece without takes the last one's before it, or else the first of its own tile
+                    const uint32_t before = some & (0xFFFFFFFFu >> (31 - lane)), own = some & (0xFFu << (lane & 24));
+                    const int from = before ? 31 - __clz(before) : own && !seen ? __ffs(own) - 1 : -1;
+                    float lv = vs > 0.0f ? log2f(vs) : 0.0f, iv = vs > 0.0f ? 1.0f / vs : 1.0f;
+                    const float lv_from = __shfl_sync(0xffffffffu, lv, max(from, 0));
+                    const float iv_from = __shfl_sync(0xffffffffu, iv, max(from, 0));
+                    lv = from >= 0 ? lv_from : lv_last;
+                    iv = from >= 0 ? iv_from : iv_last;
+                    // the tile in which the item's first such piece is
+                    const bool first = !seen && some && ((__ffs(some) - 1) >> 3) == (lane >> 3) && t > tile0;
                     for (int q = 0; q < 4 && t0 + q < max(tile1, tile0 + 1); ++q) {
                         const uint32_t r = n_tile % kTileRing;
                         wait(&sm.tile_empty[r], ((n_tile / kTileRing) & 1u) ^ 1u, 91);
                         if ((lane >> 3) == q) {
-                            sm.tiles[r].scales[sub] = make_float4(ks, vs, log2f(vs), 1.0f / vs);
+                            sm.tiles[r].scales[sub] = make_float4(ks, lv, iv, 0.0f);
                             sm.tiles[r].at[sub] = at;
+                            sm.tiles[r].at_v[sub] = vs > 0.0f ? at : -1;
                             if (sub == 0) {
                                 sm.tiles[r].key0 = tile1 < 0 ? -1 : t * kKeys;
                                 sm.tiles[r].len = len;
+                                sm.tiles[r].rebase = first;
+                                sm.tiles[r].rebase_lv = lv;
+                                sm.tiles[r].rebase_iv = iv;
                             }
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.tile_full[r]);
                         ++n_tile;
+                    }
+                    if (some) {
+                        lv_last = __shfl_sync(0xffffffffu, lv, 31 - __clz(some));
+                        iv_last = __shfl_sync(0xffffffffu, iv, 31 - __clz(some));
+                        seen = true;
                     }
                 }
                 if (tile1 < 0) break;
