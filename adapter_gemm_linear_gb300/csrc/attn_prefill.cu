@@ -90,7 +90,7 @@ struct PrefillSmem {
     alignas(16) KeyTile tiles[kTileRing];
     Item items[kItemRing];
     uint64_t item_full[kItemRing], item_empty[kItemRing], tile_full[kTileRing], tile_empty[kTileRing];
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2][2], o_done[2], drain;
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2][2], half_done[2], o_done[2], drain;
     long long warp_sum[kPreThreads / 32];
     long long base;
     int32_t seq;
@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_ready[i][0], 4);
             mbar_init(&sm.p_ready[i][1], 4);
+            mbar_init(&sm.half_done[i], 1);
             mbar_init(&sm.o_done[i], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -520,27 +521,26 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     }
                     tmem_st_wait();
                 }
-                // S is read twice, 64 columns at a time, in loops: the four roles'
-                // code has to stay small, for warps that wait for instructions
-                // were the largest loss (and all of S in registers would take
-                // them from the other roles)
-                uint32_t s[2][32];
-                auto load_s = [&](int h) {
-                    tmem_ld_32x32b_x32(ts + 64 * h, s[0]);
-                    tmem_ld_32x32b_x32(ts + 64 * h + 32, s[1]);
-                    tmem_ld_wait(s[0]);
-                    tmem_ld_wait(s[1]);
-                };
                 if (__builtin_expect(tile.rebase, 0)) {
                     m += tile.rebase_lv;
                     l *= tile.rebase_iv;
                 }
-                // the row's maximum, in log2 units and with V's scale (a factor
-                // of 0 would make NaN of what is masked)
-                float mx = -INFINITY;
+                // Two halves of 64 keys, one after the other, each with the row's
+                // maximum so far: the product with the first half's V runs while
+                // the second is in work.  (A loop, and no more than half of S in
+                // registers: the four roles' code and registers have to stay
+                // small, for warps that waited for instructions, and spills, had
+                // been the largest losses.)
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    load_s(h);
+                    uint32_t s[2][32];
+                    tmem_ld_32x32b_x32(ts + 64 * h, s[0]);
+                    tmem_ld_32x32b_x32(ts + 64 * h + 32, s[1]);
+                    tmem_ld_wait(s[0]);
+                    tmem_ld_wait(s[1]);
+                    // the maximum, in log2 units and with V's scale (a factor of
+                    // 0 would make NaN of what is masked)
+                    float mx = -INFINITY, c[4], d[4];
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         const float2 sc = *reinterpret_cast<const float2 *>(&tile.scales[4 * h + v]);
@@ -553,38 +553,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             y = max3(y, __uint_as_float(p[e + 2]), __uint_as_float(p[e + 3]));
                         }
                         x = max3(x, __uint_as_float(p[14]), __uint_as_float(p[15]));
-                        mx = fmaxf(mx, fmaf(fmaxf(x, y), fmaxf(sc.x * cr, 1e-37f), sc.y));
+                        c[v] = fmaxf(sc.x * cr, 1e-37f);
+                        d[v] = sc.y;
+                        mx = fmaxf(mx, fmaf(fmaxf(x, y), c[v], d[v]));
                     }
-                }
-                const bool grow = mx > m + kGrow;
-                if (t == it.tile0) {
-                    m = mx;
-                } else if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
-                    // all products of this tile so far are complete: s_full came after them
-                    const float mn = grow ? mx : m;
-                    const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn);
-                    m = mn;
-                    l *= f;
+                    const bool grow = mx > m + kGrow;
+                    if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+                        const float mn = grow ? mx : m;
+                        const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (t > it.tile0 || h > 0) {
+                            // the products so far are complete: of earlier tiles since
+                            // s_full, of this one's first half when half_done says so
+                            if (h > 0) {
+                                wait(&sm.half_done[X], n_own & 1u, 57);
+                                tc_fence_after_sync();
+                            }
 #pragma unroll 1
-                    for (int i = 0; i < D / 16; ++i) {
-                        uint32_t o[16];
-                        tmem_ld_32x32b_x16(to + 16 * i, o);
+                            for (int i = 0; i < D / 16; ++i) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(to + 16 * i, o);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st_32x32b_x16(to + 16 * i, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st_32x32b_x16(to + 16 * i, o);
+                            }
+                        }
                     }
-                }
-                const float mu = m == -INFINITY ? 0.0f : m;
-                // P in two halves, so that the product with the first half's V starts early
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    load_s(h);
+                    const float mu = m == -INFINITY ? 0.0f : m;
                     uint32_t pk[32];
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        const float4 sc = tile.scales[4 * h + v];
-                        const float c = fmaxf(sc.x * cr, 1e-37f), d = sc.y - mu;
-                        const uint64_t c2 = pack2(c, c), d2 = pack2(d, d);
+                        const uint64_t c2 = pack2(c[v], c[v]), d2 = pack2(d[v] - mu, d[v] - mu);
                         const uint32_t *p = &s[v >> 1][(v & 1) * 16];
                         uint64_t sum = 0;
 #pragma unroll
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         }
                         float x, y;
                         unpack2(sum, x, y);
-                        l = fmaf(x + y, sc.z, l);
+                        l = fmaf(x + y, tile.scales[4 * h + v].z, l);
                     }
                     tmem_st_32x32b_x32(ts + 32 * h, pk);
                     tmem_st_wait();
@@ -805,7 +805,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         for (uint32_t h = 0; h < 2; ++h) {
                             wait(&sm.p_ready[X][h], (X ? n_b : n_tile) & 1u, 75);
                             tc_fence_after_sync();
-                            if (elect_one()) issue_values(sm, X, st, h, j > 0 || h > 0);
+                            if (elect_one()) {
+                                issue_values(sm, X, st, h, j > 0 || h > 0);
+                                if (h == 0) mma_commit(&sm.half_done[X]);
+                            }
                             __syncwarp();
                         }
                         if (more) {
