@@ -25,8 +25,8 @@
 //    rows g and g + 8 of the MMA's 16, so a thread holds both parts' sums: 22
 //    significant bits at the cost of half the rows.
 //  - The page's scale of V is folded into the exponent: p' = 2^(s + log2 vs -
-//    m), o sums p' codes, l sums p' / vs.  p' <= 2^8 whatever the scales, so
-//    f16 holds it.  m follows the maximum only when that grows by 2^8, so the
+//    m), o sums p' codes, l sums p' / vs.  p' <= 2^14 whatever the scales, so
+//    f16 holds it.  m follows the maximum only when that grows by 2^14, so the
 //    sums are rarely rescaled.
 #include <cuda_runtime.h>
 #include <math.h>

@@ -27,7 +27,7 @@
 //    looks up the pages and scales of the key tiles, eight tiles ahead.
 //  - q is f16 times a power of two per row (exact for bf16), P is f16 (11
 //    bits) with the page's scale of V in its exponent, as in attn_decode.cu; a
-//    row's sums are rescaled only when its maximum grew by 2^8.
+//    row's sums are rescaled only when its maximum grew by 2^14.
 //  - Tensor Memory: S_A, S_B (128 columns each, P over the first 64), O_A, O_B.
 // The key tiles of all items form one line that the CTAs share equally
 // (attn_split.cuh), so causal and ragged work is level to one tile.
@@ -827,15 +827,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             }
             // nothing of this thread's may be in flight when Tensor Memory is freed
             commit(&sm.drain);
-            if (!mbar_try_wait(&sm.drain, 0)) wait_clocks(&sm.drain, 0);
-        } else if (warp == 13 && lane == 0) {
+            wait_clocks(&sm.drain, 0);
+        } else if (warp == 13) {
             // ============================================ the items
             uint32_t n_item = 0;
             auto publish = [&](const Item &it) {
                 const uint32_t e = n_item % kItemRing;
                 wait(&sm.item_empty[e], ((n_item / kItemRing) & 1u) ^ 1u, 80);
-                sm.items[e] = it;
-                mbar_arrive(&sm.item_full[e]);
+                if (lane == 0) {
+                    sm.items[e] = it;
+                    mbar_arrive(&sm.item_full[e]);
+                }
+                __syncwarp();
                 ++n_item;
             };
             Item it;
