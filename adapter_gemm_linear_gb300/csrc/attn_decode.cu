@@ -558,14 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
 template <typename T, int D, int FMT>
 cudaError_t decode_typed(const AttnView &v, cudaStream_t stream) {
     static uint64_t ctx[128] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    constexpr int smem = static_cast<int>(sizeof(DecodeSmem<D>));
+    static_assert(smem <= 227 * 1024, "the shared memory of one CTA");
+    cudaError_t e = allow_smem(attn_decode_kernel<T, D, FMT>, smem, ctx);
     if (e != cudaSuccess) return e;
-    const int smem = static_cast<int>(sizeof(DecodeSmem<D>));
-    if (dev < 0 || dev >= 128 || first_use_in_context(&ctx[dev])) {
-        e = cudaFuncSetAttribute(attn_decode_kernel<T, D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
     const int grid = device_sm_count();
     attn_decode_kernel<T, D, FMT><<<grid, kThreads, smem, stream>>>(v);
     e = cudaGetLastError();

@@ -15,7 +15,7 @@
 //
 //  - warps 0-3 and 4-7: the softmax of A and B, thread = row, no shuffles;
 //    while one tile's softmax runs, the other tile's products run.
-//  - warps 8-11 turn the codes into f16 tiles in shared memory (exactly), in
+//  - warps 8-11 turn the codes, and the queries, into f16 tiles in shared memory (exactly), in
 //    the 128-byte-swizzled K-major layout of tcgen05.mma: K as [keys][dims], V
 //    as [dims][keys], which the cache's layout of V gives without a
 //    transposition.  Two stages each; the next tile's codes are on their way
@@ -24,7 +24,7 @@
 //    shared memory taken, what is left of the L1 holds too few in flight;
 //    and 32 bulk copies of 2 KB a tile take the copy engine 2 us).
 //  - warp 12 issues the products; warp 13 hands out the items, and warp 14
-//    looks up the pages and scales of the key tiles, eight tiles ahead.
+//    looks up the pages and scales of the key tiles, four tiles ahead.
 //  - q is f16 times a power of two per row (exact for bf16), P is f16 (11
 //    bits) with the page's scale of V in its exponent, as in attn_decode.cu; a
 //    row's sums are rescaled only when its maximum grew by 2^14.
@@ -52,7 +52,11 @@ constexpr int kSubs = kKeys / kKvTile;
 constexpr int kPreThreads = 512;
 constexpr int kItemRing = 4;
 constexpr int kItemReaders = 8 + 1 + 1;  // warps that read an item's entry
-constexpr int kTileRing = 8;             // key tiles looked up ahead
+constexpr int kTileRing = 4;             // key tiles looked up ahead
+// What beginning and ending an item costs, in key tiles: an item has so many
+// units of the line more than key tiles, in front.  (Short prompts have items
+// of one tile; without this the CTAs that got them took twice as long.)
+constexpr int kItemUnits = 5;
 constexpr long long kWaitClocks = 4000000000ll;  // about 2 s: far beyond any legitimate wait
 
 struct Item {
@@ -72,12 +76,14 @@ struct KeyTile {
     int64_t at[kSubs];    // offset in k_pages; < 0: past the end or not there, zeros
     int64_t at_v[kSubs];  // and in v_pages
     int32_t key0, len;    // first key, the sequence's length; key0 < 0: no more tiles
+    int32_t off, n, head, row_tile;  // of an item's first tile: its queries (n = 0 in its other tiles)
     // The item's first tile with a V that is not zero, if tiles before it took
     // log2 vs = 0: what their sums are multiplied by (in log2 and as a factor)
     int32_t rebase;
     float rebase_lv, rebase_iv;
     int32_t pad[3];
 };
+static_assert(sizeof(KeyTile) % 16 == 0, "scales are read as 16-byte pieces");
 
 template <int D>
 struct PrefillSmem {
@@ -88,9 +94,10 @@ struct PrefillSmem {
     // threads, each read by the thread that fetched it
     uint4 codes[2][2 * D / 32][128];
     alignas(16) KeyTile tiles[kTileRing];
+    int8_t q_exponent[2][2 * kHalf];  // of an item's rows, by the item's parity: q is 2^this times what is in q
     Item items[kItemRing];
     uint64_t item_full[kItemRing], item_empty[kItemRing], tile_full[kTileRing], tile_empty[kTileRing];
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2][2], half_done[2], o_done[2], drain;
+    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2][2], half_done[2], o_done[2], drain;
     long long warp_sum[kPreThreads / 32];
     long long base;
     int32_t seq;
@@ -255,7 +262,7 @@ struct RowTiles {
         if (window <= 0) return 0;
         return max(0, first + i * kRows / group - window + 1) / kKeys;
     }
-    // sum of hi - lo over the row tiles before i.  256 = 2 * 128, so hi(i) =
+    // units of the row tiles before i: kItemUnits and hi - lo each.  256 = 2 * 128, so hi(i) =
     // floor((2 i + floor((255 + group (first + 128)) / 128)) / group) for every
     // tile but the last, and lo(i) = max(0, floor((2 i + floor(group (first -
     // window + 1) / 128)) / group)).
@@ -274,7 +281,7 @@ struct RowTiles {
             const int32_t i0 = e >= 0 ? 0 : (1 - e) / 2;
             if (i > i0) sum -= floor_sum(i - i0, group, 2, 2 * i0 + e);
         }
-        return sum;
+        return sum + static_cast<long long>(i) * kItemUnits;
     }
 };
 
@@ -346,6 +353,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.k_full[i], 4);
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_full[i], 4);
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         const long long u = local - head * units;
         for (int32_t i = threadIdx.x; i < t.count; i += kPreThreads) {
             const long long at = t.before(i);
-            if (at <= u && u < at + t.hi(i) - t.lo(i)) {
+            if (at <= u && u < at + kItemUnits + t.hi(i) - t.lo(i)) {
                 sm.head0 = head;
                 sm.row_tile0 = i;
                 sm.skip0 = static_cast<int32_t>(u - at);
@@ -432,64 +440,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             if (lane == 0) mbar_arrive(&sm.item_empty[e]);
             ++n_item;
         };
-        // Q_X of an item into shared memory: f16 times a power of two per row
-        // (its largest value in [2^13, 2^14)); returns the factor that turns
-        // the thread's row's products with codes into log2 units.  A warp reads
-        // its 32 rows several at a time, 16 bytes a lane.
-        auto load_q = [&](const Item &it) {
-            constexpr int LANES = D / 8;         // lanes of a row
-            constexpr int AT_ONCE = 32 / LANES;  // rows of a load
-            const int piece = lane % LANES, base = X * kHalf + (warp & 3) * 32 + lane / LANES;
-            const int32_t rows = it.n * a.group;
-            uint4 x[LANES];
-#pragma unroll
-            for (int i = 0; i < LANES; ++i) {
-                const int32_t row = min(it.row_tile * kRows + base + i * AT_ONCE, rows - 1);
-                const int32_t qi = row / a.group, qh = it.head * a.group + row % a.group;
-                x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
-                                                             static_cast<int64_t>(it.off + qi) * a.q.row + qh * a.q.head) + piece);
-            }
-            float mine = 0.0f;
-#pragma unroll
-            for (int i = 0; i < LANES; ++i) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                float amax = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
-#pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
-                e = amax < INFINITY ? max(e, -126) : 0;
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                // the row of lane L is L: row i * AT_ONCE + L % AT_ONCE, held by lanes (L % AT_ONCE) * LANES + ...
-                const float up = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 + e) << 23), lane % AT_ONCE * LANES);
-                if (lane / AT_ONCE == i) mine = up;
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-                const int r = base - X * kHalf + i * AT_ONCE;
-                *reinterpret_cast<uint4 *>(sm.q[X] + r * 128 + (piece / 8) * kRowAtom + (((piece & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.q_full[X]);
-            return a.scale * kLog2e * mine;
-        };
         auto takes_part = [&](const Item &it) {  // tile B may be empty
             return it.tile1 >= 0 && (X == 0 || it.n * a.group - it.row_tile * kRows > kHalf);
         };
 
         Item it;
         get_item(it);
-        float cr = takes_part(it) ? load_q(it) : 0.0f;
         while (it.tile1 >= 0) {
             if (!takes_part(it)) {
                 n_tile += it.tile1 - it.tile0;
                 get_item(it);
-                if (takes_part(it)) cr = load_q(it);
                 continue;
             }
             const int32_t rows = min(kRows, it.n * a.group - it.row_tile * kRows);
@@ -501,11 +461,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             // keys that every row of the item sees
             const int32_t all_hi = a.causal ? it.len - it.n + it.row_tile * kRows / a.group + 1 : it.len;
             const int32_t all_lo = a.window > 0 ? it.len - it.n + (it.row_tile * kRows + rows - 1) / a.group - a.window + 1 : 0;
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f, cr = 0.0f;
             for (int32_t t = it.tile0; t < it.tile1; ++t, ++n_tile, ++n_own) {
                 wait(&sm.tile_full[n_tile % kTileRing], (n_tile / kTileRing) & 1u, 55);
                 wait(&sm.s_full[X], n_own & 1u, 51 + X);
                 tc_fence_after_sync();
+                if (t == it.tile0) cr = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + sm.q_exponent[(n_item - 1) & 1u][rt]) << 23);
                 const KeyTile &tile = sm.tiles[n_tile % kTileRing];
                 const int32_t key0 = t * kKeys;
                 if (__builtin_expect(key0 < all_lo || key0 + kKeys > all_hi, 0)) {
@@ -607,11 +568,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     if (lane == 0) mbar_arrive(&sm.p_ready[X][h]);
                 }
             }
-            // the next item's Q (this one's products with Q_X are complete), then this one's result
-            Item next;
-            get_item(next);
-            float cr_next = 0.0f;
-            if (takes_part(next)) cr_next = load_q(next);
             wait(&sm.o_done[X], n_part & 1u, 53 + X);
             ++n_part;
             tc_fence_after_sync();
@@ -651,8 +607,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             }
             if (!whole && (it.flags & kFromStart) && threadIdx.x == 0)
                 joins[blockIdx.x] = JoinEntry{it.seq, it.head, it.row_tile, it.last_cta};
-            it = next;
-            cr = cr_next;
+            get_item(it);
         }
     } else if (warp < 12) {
         // ================================================ codes to f16 tiles
@@ -664,6 +619,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         struct Tile {
             int32_t key0, len;
             int64_t at[2], at_v;  // (of V the thread's own)
+            int32_t off, n, head, row_tile;
         };
         Tile cur, nxt;
         auto look = [&](Tile &x, uint32_t n) {
@@ -674,6 +630,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             x.at[0] = sm.tiles[e].at[2 * wq];
             x.at[1] = sm.tiles[e].at[2 * wq + 1];
             x.at_v = sm.tiles[e].at_v[2 * wq + (cc >> 1)];
+            x.n = sm.tiles[e].n;
+            x.off = sm.tiles[e].off;
+            x.head = sm.tiles[e].head;
+            x.row_tile = sm.tiles[e].row_tile;
         };
         uint4 *kc = &sm.codes[0][0][wq * 32 + lane], *vc = &sm.codes[1][0][wq * 32 + lane];
         // the thread's piece i of a tile; zeros where there is no page
@@ -694,6 +654,54 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         const uint32_t k_at = (wq * 32 + kr) * 128, k_c0 = ((2 * kp) ^ kr) << 4, k_c1 = ((2 * kp + 1) ^ kr) << 4;
         const uint32_t v_at = (wq >> 1) * kVAtom + (8 * dq + 4 * dpar) * 128, v_c = ((wq & 1) * 4 + cc) ^ (4 * dpar);
         auto landed = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };  // all groups but the newest
+        // An item's Q_A and Q_B into shared memory: f16 times a power of two per
+        // row (its largest value in [2^13, 2^14)).  A warp reads its 32 rows
+        // several at a time, 16 bytes a lane.
+        uint32_t n_q = 0, n_qx[2] = {0, 0};
+        auto load_q = [&](const Tile &t) {
+            constexpr int LANES = D / 8;         // lanes of a row
+            constexpr int AT_ONCE = 32 / LANES;  // rows of a load
+            const int piece = lane % LANES;
+            const int32_t rows = t.n * a.group, row0 = t.row_tile * kRows;
+#pragma unroll 1
+            for (int X = 0; X < (rows - row0 > kHalf ? 2 : 1); ++X) {
+                const int base = wq * 32 + lane / LANES;  // of Q_X
+                uint4 x[LANES];
+#pragma unroll
+                for (int i = 0; i < LANES; ++i) {
+                    const int32_t row = min(row0 + X * kHalf + base + i * AT_ONCE, rows - 1);
+                    const int32_t qi = row / a.group, qh = t.head * a.group + row % a.group;
+                    x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
+                                                                 static_cast<int64_t>(t.off + qi) * a.q.row + qh * a.q.head) + piece);
+                }
+                wait(&sm.q_empty[X], (n_qx[X]++ & 1u) ^ 1u, 65);
+#pragma unroll
+                for (int i = 0; i < LANES; ++i) {
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
+#pragma unroll
+                    for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+                    e = amax < INFINITY ? max(e, -126) : 0;
+                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    const int r = base + i * AT_ONCE;
+                    if (piece == 0) sm.q_exponent[n_q & 1u][X * kHalf + r] = static_cast<int8_t>(e);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+                    *reinterpret_cast<uint4 *>(sm.q[X] + r * 128 + (piece / 8) * kRowAtom + (((piece & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_full[X]);
+            }
+            ++n_q;
+        };
         look(cur, 0);
         for (int i = 0; cur.key0 >= 0 && i < NL; ++i) fetch_k(cur, i);
         fetched();
@@ -724,6 +732,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.k_full[stage]);
+            if (cur.n > 0) load_q(cur);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
             // (their codes may be anything, and 0 * NaN is not 0)
             wait(&sm.v_empty[stage], ph ^ 1u, 62);
@@ -789,6 +798,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     wait(&sm.q_full[X], (X ? n_qb : n_item) & 1u, 71);
                     tc_fence_after_sync();
                     scores(X, n_tile & 1u);
+                    if (nt == 1) commit(&sm.q_empty[X]);
                 }
                 ++n_item;
                 n_qb += nx - 1;
@@ -815,6 +825,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             if (X == 0) wait(&sm.k_full[st1], ph1, 76);
                             tc_fence_after_sync();
                             scores(X, st1);
+                            if (j + 2 == nt) commit(&sm.q_empty[X]);
                         } else {
                             commit(&sm.o_done[X]);
                         }
@@ -846,25 +857,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 it.seq = sm.seq;
                 it.head = sm.head0;
                 it.row_tile = sm.row_tile0;
-                int32_t skip = sm.skip0;  // tiles of the first item that belong to the CTA before
+                int32_t skip = sm.skip0;  // units of the first item that belong to the CTA before
                 SeqRows r = prefill_seq(a, it.seq);
                 int32_t count = RowTiles(a, r).count;
                 long long w = w0;
-                while (w < w1) {
+                while (true) {
                     const RowTiles t(a, r);
-                    const int32_t lo = t.lo(it.row_tile), hi = t.hi(it.row_tile);
+                    const int32_t lo = t.lo(it.row_tile), hi = t.hi(it.row_tile), units = kItemUnits + hi - lo;
+                    const int32_t take = static_cast<int32_t>(min(static_cast<long long>(units - skip), w1 - w));
                     it.off = r.off;
                     it.n = r.n;
                     it.len = r.len;
-                    it.tile0 = lo + skip;
-                    it.tile1 = static_cast<int32_t>(min(static_cast<long long>(hi), it.tile0 + (w1 - w)));
-                    it.flags = (skip == 0 ? kFromStart : 0) | (it.tile1 == hi ? kToEnd : 0);
-                    it.last_cta = static_cast<int32_t>(((w + (hi - it.tile0)) * ctas - 1) / total);
-                    w += it.tile1 - it.tile0;
-                    publish(it);
-                    if (*dead) break;
+                    it.tile0 = lo + max(skip - kItemUnits, 0);
+                    it.tile1 = lo + skip + take - kItemUnits;
+                    it.flags = (it.tile0 == lo ? kFromStart : 0) | (it.tile1 == hi ? kToEnd : 0);
+                    it.last_cta = static_cast<int32_t>(((w + (units - skip)) * ctas - 1) / total);
+                    if (it.tile1 > it.tile0) publish(it);
+                    w += take;
+                    if (w >= w1 || *dead) break;
                     skip = 0;
-                    if (w >= w1) break;
                     if (++it.row_tile == count) {
                         it.row_tile = 0;
                         if (++it.head == b.heads) {
@@ -888,6 +899,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 90);
                 const int32_t seq = sm.items[e].seq, head = sm.items[e].head, len = sm.items[e].len;
                 const int32_t tile0 = sm.items[e].tile0, tile1 = *dead ? -1 : sm.items[e].tile1;
+                const int32_t off = sm.items[e].off, n = sm.items[e].n, row_tile = sm.items[e].row_tile;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.item_empty[e]);
                 ++n_item;
@@ -928,6 +940,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             if (sub == 0) {
                                 sm.tiles[r].key0 = tile1 < 0 ? -1 : t * kKeys;
                                 sm.tiles[r].len = len;
+                                sm.tiles[r].off = off;
+                                sm.tiles[r].n = t == tile0 ? n : 0;
+                                sm.tiles[r].head = head;
+                                sm.tiles[r].row_tile = row_tile;
                                 sm.tiles[r].rebase = first;
                                 sm.tiles[r].rebase_lv = lv;
                                 sm.tiles[r].rebase_iv = iv;
@@ -960,15 +976,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
 template <int D, int FMT>
 cudaError_t prefill_typed(const AttnView &v, cudaStream_t stream) {
     static uint64_t ctx[128] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     // more than half of an SM's shared memory even for D = 64: a CTA takes all of its Tensor Memory
-    const int smem = static_cast<int>(sizeof(PrefillSmem<D>) > 128 * 1024 ? sizeof(PrefillSmem<D>) : 128 * 1024);
-    if (dev < 0 || dev >= 128 || first_use_in_context(&ctx[dev])) {
-        e = cudaFuncSetAttribute(attn_prefill_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    constexpr int smem = static_cast<int>(sizeof(PrefillSmem<D>) > 128 * 1024 ? sizeof(PrefillSmem<D>) : 128 * 1024);
+    static_assert(smem <= 227 * 1024, "the shared memory of one CTA");
+    cudaError_t e = allow_smem(attn_prefill_kernel<D, FMT>, smem, ctx);
+    if (e != cudaSuccess) return e;
     const int grid = device_sm_count();
     attn_prefill_kernel<D, FMT><<<grid, kPreThreads, smem, stream>>>(v);
     e = cudaGetLastError();

@@ -107,6 +107,25 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     if (a.lse && c == 0) a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
 }
 
+// Opts a kernel in to `bytes` of shared memory, once per device and context (`ctx`: what has been done).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, uint64_t (&ctx)[128]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    uint64_t seen = ctx[dev];
+    if (first_use_in_context(&seen)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) {
+            cudaGetLastError();  // reported here, not by the next launch
+            return e;
+        }
+        ctx[dev] = seen;
+    }
+    return cudaSuccess;
+}
+
 // Starts the join behind the kernel that was launched last on the stream.
 template <typename T, int D, int ROWS>
 cudaError_t launch_join(const AttnView &v, int ctas, int slot_rows, cudaStream_t stream) {
