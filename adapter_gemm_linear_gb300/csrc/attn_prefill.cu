@@ -654,52 +654,66 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         const uint32_t k_at = (wq * 32 + kr) * 128, k_c0 = ((2 * kp) ^ kr) << 4, k_c1 = ((2 * kp + 1) ^ kr) << 4;
         const uint32_t v_at = (wq >> 1) * kVAtom + (8 * dq + 4 * dpar) * 128, v_c = ((wq & 1) * 4 + cc) ^ (4 * dpar);
         auto landed = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };  // all groups but the newest
-        // An item's Q_A and Q_B into shared memory: f16 times a power of two per
-        // row (its largest value in [2^13, 2^14)).  A warp reads its 32 rows
-        // several at a time, 16 bytes a lane.
-        uint32_t n_q = 0, n_qx[2] = {0, 0};
-        auto load_q = [&](const Tile &t) {
+        // An item's Q_A and Q_B, the warp's 32 rows of each: copied to their
+        // places as bf16, several rows at a time and 16 bytes a lane ...
+        uint32_t n_q = 0, n_qb = 0;
+        auto q_tiles = [&](const Tile &t) { return t.n * a.group - t.row_tile * kRows > kHalf ? 2 : 1; };
+        auto q_place = [&](int X, int r, int piece) {
+            return reinterpret_cast<uint4 *>(sm.q[X] + (wq * 32 + r) * 128 + (piece / 8) * kRowAtom + (((piece ^ r) & 7) << 4));
+        };
+        auto fetch_q = [&](const Tile &t) {
             constexpr int LANES = D / 8;         // lanes of a row
-            constexpr int AT_ONCE = 32 / LANES;  // rows of a load
+            constexpr int AT_ONCE = 32 / LANES;  // rows of a copy
             const int piece = lane % LANES;
-            const int32_t rows = t.n * a.group, row0 = t.row_tile * kRows;
 #pragma unroll 1
-            for (int X = 0; X < (rows - row0 > kHalf ? 2 : 1); ++X) {
-                const int base = wq * 32 + lane / LANES;  // of Q_X
-                uint4 x[LANES];
-#pragma unroll
+            for (int X = 0; X < q_tiles(t); ++X) {
+                const int32_t row = t.row_tile * kRows + X * kHalf + wq * 32 + lane, qi = row / a.group;  // the lane's row
+                const long long mine = row < t.n * a.group
+                    ? (static_cast<int64_t>(t.off + qi) * a.q.row + static_cast<int64_t>(t.head * a.group + row - qi * a.group) * a.q.head) * 2
+                    : -1;  // past the last: zeros
+                wait(&sm.q_empty[X], ((X ? n_qb : n_q) & 1u) ^ 1u, 65);
+#pragma unroll 2
                 for (int i = 0; i < LANES; ++i) {
-                    const int32_t row = min(row0 + X * kHalf + base + i * AT_ONCE, rows - 1);
-                    const int32_t qi = row / a.group, qh = t.head * a.group + row % a.group;
-                    x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
-                                                                 static_cast<int64_t>(t.off + qi) * a.q.row + qh * a.q.head) + piece);
+                    const int r = i * AT_ONCE + lane / LANES;
+                    const long long at = __shfl_sync(0xffffffffu, mine, r);
+                    copy16(q_place(X, r, piece), static_cast<const uint8_t *>(a.q.p) + max(at, 0ll) + piece * 16, at >= 0);
                 }
-                wait(&sm.q_empty[X], (n_qx[X]++ & 1u) ^ 1u, 65);
-#pragma unroll
-                for (int i = 0; i < LANES; ++i) {
-                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                    float amax = 0.0f;
+            }
+        };
+        // ... and turned in place into f16 times a power of two per row (its
+        // largest value in [2^13, 2^14)), a row a lane.
+        auto convert_q = [&](const Tile &t) {
+#pragma unroll 1
+            for (int X = 0; X < q_tiles(t); ++X) {
+                float amax = 0.0f;
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 x = *q_place(X, lane, i);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
-#pragma unroll
-                    for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
-                    e = amax < INFINITY ? max(e, -126) : 0;
-                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    const int r = base + i * AT_ONCE;
-                    if (piece == 0) sm.q_exponent[n_q & 1u][X * kHalf + r] = static_cast<int8_t>(e);
+                }
+                int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+                e = amax < INFINITY ? max(e, -126) : 0;
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                sm.q_exponent[n_q & 1u][X * kHalf + wq * 32 + lane] = static_cast<int8_t>(e);
+#pragma unroll 2
+                for (int i = 0; i < D / 8; ++i) {
+                    uint4 *at = q_place(X, lane, i);
+                    const uint4 x = *at;
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t h[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-                    *reinterpret_cast<uint4 *>(sm.q[X] + r * 128 + (piece / 8) * kRowAtom + (((piece & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(h[0], h[1], h[2], h[3]);
+                    *at = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.q_full[X]);
             }
+            n_qb += q_tiles(t) - 1;
             ++n_q;
         };
         look(cur, 0);
@@ -732,11 +746,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.k_full[stage]);
-            if (cur.n > 0) load_q(cur);
+            const bool first = cur.n > 0;  // tile of an item: its queries, on their way while V is converted
+            if (first) {
+                fetch_q(cur);
+                fetched();
+            }
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
             // (their codes may be anything, and 0 * NaN is not 0)
             wait(&sm.v_empty[stage], ph ^ 1u, 62);
-            landed();
+            if (first) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            else landed();
             uint32_t keep[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -764,6 +783,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.v_full[stage]);
+            if (first) {
+                landed();
+                __syncwarp();  // every lane's copies
+                convert_q(cur);
+            }
             cur = nxt;
             ++n_tile;
         }
