@@ -56,7 +56,7 @@ constexpr int kTileRing = 4;             // key tiles looked up ahead
 // What beginning and ending an item costs, in key tiles: an item has so many
 // units of the line more than key tiles, in front.  (Short prompts have items
 // of one tile; without this the CTAs that got them took twice as long.)
-constexpr int kItemUnits = 5;
+constexpr int kItemUnits = 4;
 constexpr long long kWaitClocks = 4000000000ll;  // about 2 s: far beyond any legitimate wait
 
 struct Item {
@@ -661,60 +661,59 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         auto q_place = [&](int X, int r, int piece) {
             return reinterpret_cast<uint4 *>(sm.q[X] + (wq * 32 + r) * 128 + (piece / 8) * kRowAtom + (((piece ^ r) & 7) << 4));
         };
-        auto fetch_q = [&](const Tile &t) {
+        auto fetch_q = [&](const Tile &t, int X) {
             constexpr int LANES = D / 8;         // lanes of a row
             constexpr int AT_ONCE = 32 / LANES;  // rows of a copy
-            const int piece = lane % LANES;
+            constexpr int TURN = 8 / AT_ONCE;    // copies after which the swizzle repeats
+            const int piece = lane % LANES, sub = lane / LANES;
+            const int32_t row = t.row_tile * kRows + X * kHalf + wq * 32 + lane, qi = row / a.group;  // the lane's row
+            const long long mine = row < t.n * a.group
+                ? (static_cast<int64_t>(t.off + qi) * a.q.row + static_cast<int64_t>(t.head * a.group + row - qi * a.group) * a.q.head) * 2
+                : -1;  // past the last: zeros
+            uint8_t *dst = sm.q[X] + (wq * 32 + sub) * 128 + (piece / 8) * kRowAtom;
+            const uint32_t swizzle = ((piece ^ sub) & 7) << 4;
+            wait(&sm.q_empty[X], ((X ? n_qb : n_q) & 1u) ^ 1u, 65);
 #pragma unroll 1
-            for (int X = 0; X < q_tiles(t); ++X) {
-                const int32_t row = t.row_tile * kRows + X * kHalf + wq * 32 + lane, qi = row / a.group;  // the lane's row
-                const long long mine = row < t.n * a.group
-                    ? (static_cast<int64_t>(t.off + qi) * a.q.row + static_cast<int64_t>(t.head * a.group + row - qi * a.group) * a.q.head) * 2
-                    : -1;  // past the last: zeros
-                wait(&sm.q_empty[X], ((X ? n_qb : n_q) & 1u) ^ 1u, 65);
-#pragma unroll 2
-                for (int i = 0; i < LANES; ++i) {
-                    const int r = i * AT_ONCE + lane / LANES;
-                    const long long at = __shfl_sync(0xffffffffu, mine, r);
-                    copy16(q_place(X, r, piece), static_cast<const uint8_t *>(a.q.p) + max(at, 0ll) + piece * 16, at >= 0);
+            for (int r = sub; r < 32; r += 8, dst += 1024) {
+#pragma unroll
+                for (int i = 0; i < TURN; ++i) {
+                    const long long at = __shfl_sync(0xffffffffu, mine, r + i * AT_ONCE);
+                    copy16(dst + i * AT_ONCE * 128 + (swizzle ^ (i * AT_ONCE << 4)), static_cast<const uint8_t *>(a.q.p) + max(at, 0ll) + piece * 16, at >= 0);
                 }
             }
+            fetched();
         };
         // ... and turned in place into f16 times a power of two per row (its
         // largest value in [2^13, 2^14)), a row a lane.
-        auto convert_q = [&](const Tile &t) {
-#pragma unroll 1
-            for (int X = 0; X < q_tiles(t); ++X) {
-                float amax = 0.0f;
+        auto convert_q = [&](int X) {
+            __syncwarp();  // every lane's copies
+            float amax = 0.0f;
 #pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = *q_place(X, lane, i);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 x = *q_place(X, lane, i);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
-                }
-                int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
-                e = amax < INFINITY ? max(e, -126) : 0;
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                sm.q_exponent[n_q & 1u][X * kHalf + wq * 32 + lane] = static_cast<int8_t>(e);
-#pragma unroll 2
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 *at = q_place(X, lane, i);
-                    const uint4 x = *at;
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t h[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-                    *at = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.q_full[X]);
+                for (int k = 0; k < 4; ++k)
+                    amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
             }
-            n_qb += q_tiles(t) - 1;
-            ++n_q;
+            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+            e = amax < INFINITY ? max(e, -126) : 0;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            sm.q_exponent[n_q & 1u][X * kHalf + wq * 32 + lane] = static_cast<int8_t>(e);
+#pragma unroll 2
+            for (int i = 0; i < D / 8; ++i) {
+                uint4 *at = q_place(X, lane, i);
+                const uint4 x = *at;
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+                *at = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full[X]);
         };
         look(cur, 0);
         for (int i = 0; cur.key0 >= 0 && i < NL; ++i) fetch_k(cur, i);
@@ -747,10 +746,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.k_full[stage]);
             const bool first = cur.n > 0;  // tile of an item: its queries, on their way while V is converted
-            if (first) {
-                fetch_q(cur);
-                fetched();
-            }
+            if (first) fetch_q(cur, 0);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
             // (their codes may be anything, and 0 * NaN is not 0)
             wait(&sm.v_empty[stage], ph ^ 1u, 62);
@@ -784,9 +780,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.v_full[stage]);
             if (first) {
-                landed();
-                __syncwarp();  // every lane's copies
-                convert_q(cur);
+                const bool both = q_tiles(cur) > 1;
+                if (both) fetch_q(cur, 1);
+                else fetched();
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                convert_q(0);
+                if (both) {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    convert_q(1);
+                    ++n_qb;
+                }
+                ++n_q;
             }
             cur = nxt;
             ++n_tile;
