@@ -9,21 +9,29 @@
 //    equal contiguous ranges, so ragged lengths and few long sequences load
 //    every SM alike.  An item that spans CTAs is joined by attn_join_kernel
 //    from fp32 partial results (o, m, l), in a fixed order.
-//  - A producer warp streams the 16-token tiles of K and V codes with bulk
-//    copies into a ring of shared memory, 128 KiB deep; eight consumer warps
-//    take the tiles in turn, each with its own running softmax, and are
-//    merged in shared memory at an item's end.
+//  - The consumer warps (15 of them for up to eight query rows, else 11) take
+//    the 16-token tiles in turn, each with its own running softmax, and are
+//    merged in shared memory at an item's end.  Every thread fetches the codes
+//    that it will use itself, two tiles ahead, by 16-byte asynchronous copies
+//    to shared memory: no barrier is between a copy and its use.  (One warp
+//    that fed all by bulk copies of 2 KiB was held at one copy per 85 ns and
+//    SM: 3.6 TB/s with heads of 128, 1.9 with heads of 64.)  One more warp looks
+//    up the tiles' pages and scales ahead of them.
 //  - The codes become f16 in registers (exactly) and feed warp MMAs
-//    (16 x 8 x 16, fp32 sums): S = q K^T with the 16 query rows as M and
-//    8 tokens as N, then o += p V with the same registers of S as A operand.
-//    The tiles' layout in the cache is the fragments' layout: a thread's 16
-//    bytes of K are 16 dimensions of one token (four k-steps, the order of
-//    the dimensions within a k-step being free as long as q follows it); its
-//    16 bytes of V are four dimensions x the four tokens whose p it holds.
+//    (16 x 8 x 16, fp32 sums) with the few query rows as the narrow side:
+//    S^T = K q^T with 16 tokens as M and eight rows as N, then o^T += V^T p^T
+//    with 16 dimensions as M; p changes from S's layout to that of a B operand
+//    by two 8 x 8 transpositions in the warp.  The tiles' layout in the cache is
+//    the fragments' layout: a thread's 16 bytes of K are 16 dimensions of one
+//    token (four k-steps, the order of the dimensions within a k-step being
+//    free as long as q follows it); its 16 bytes of V are four dimensions x
+//    the four tokens whose p it holds.  (With the rows as M, half of the MMAs
+//    and exponentials of eight rows were for rows that are not there, and O
+//    took twice the registers, for eight warps instead of 15: 517 us instead
+//    of TIME256 for 256 sequences of 4096 tokens, 64 heads on 8.)
 //  - q enters as f16 times a power of two per row (exact for bf16).  In fp32
-//    calls q and p are each split in two f16 parts, hi + lo 2^-11, put in
-//    rows g and g + 8 of the MMA's 16, so a thread holds both parts' sums: 22
-//    significant bits at the cost of half the rows.
+//    calls q and p are each split in two f16 parts, hi + lo 2^-11, as two
+//    column tiles of the MMA whose sums are added: 22 significant bits.
 //  - The page's scale of V is folded into the exponent: p' = 2^(s + log2 vs -
 //    m), o sums p' codes, l sums p' / vs.  p' <= 2^14 whatever the scales, so
 //    f16 holds it.  m follows the maximum only when that grows by 2^14, so the
@@ -42,33 +50,42 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 8;                          // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kChunkTiles = 8;                     // tiles of a unit of work (128 tokens)
-constexpr int kMmaRows = 16;
+constexpr int kSlotRows = 16;                      // rows a partial result has place for
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLoScale = 2048.0f;                // 2^11: the lo parts of fp32 operands
 
-template <int D>
-__host__ __device__ constexpr int slots() { return 128 * 1024 / (2 * kKvTile * D); }
+// Query rows of an item, with NT column tiles of eight; fp32 takes two for the parts of eight rows.
+template <typename T, int NT>
+__host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? 4 * NT : 8 * NT; }
 
-template <typename T>
-__host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? kMmaRows / 2 : kMmaRows; }  // query rows of an item
+// Consumer warps: with the producer a multiple of four, by which registers are
+// given out, and as many as that leaves 128 (or 168) a thread.
+template <int NT>
+__host__ __device__ constexpr int consumers() { return NT == 1 ? 15 : 11; }
 
-// One tile's page scales, made by the producer: K's scale, log2 and reciprocal of V's.
-struct TileScales {
+// What the looking-up warp says of a tile: where its codes are (in k_pages and
+// in v_pages; < 0: not there, zeros), and K's scale, V's, its log2 and reciprocal.
+struct alignas(16) TileInfo {
     float ks, vs, lv, ivs;
+    int64_t at;
+    int64_t pad;
 };
+constexpr int64_t kNoTile = -1, kEndOfLine = -2;
 
-template <int D>
+constexpr int kBatch = 32, kBatches = 8;  // tiles looked up at once, and ahead
+
+template <int D, int NT>
 struct DecodeSmem {
-    alignas(128) uint8_t ring[slots<D>()][2][kKvTile * D];
-    float o[kWarps][kMmaRows][D + 4];  // merge: padded against bank conflicts
-    float m[kWarps][kMmaRows], l[kWarps][kMmaRows];
-    alignas(16) TileScales scales[slots<D>()];
-    uint64_t full[slots<D>()], empty[slots<D>()];
-    uint32_t issued[slots<D>()];  // tiles loaded into the slot so far
-    long long warp_sum[kThreads / 32];
+    static constexpr int kWarps = consumers<NT>();
+    static constexpr int kPieces = D / 32;           // 16-byte pieces a lane takes of a tile of K (and of V)
+    static constexpr int kDepth = D == 128 ? 2 : 4;  // tiles a warp fetches ahead
+    uint4 codes[kWarps][kDepth][2][kPieces][32];     // [.., K or V, piece, lane]
+    float o[kWarps][8 * NT][D + 4];                  // merge: padded against bank conflicts
+    float m[kWarps][8 * NT], l[kWarps][8 * NT];
+    TileInfo info[kBatches][kBatch];
+    uint64_t full[kBatches], empty[kBatches];
+    long long warp_sum[kWarps + 1];
     long long base;  // first unit of the sequence the CTA begins in
     int32_t seq;
     int32_t dead;    // a wait ran out: nobody waits any more
@@ -92,6 +109,13 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
     return pack_f16((a - h.x) * kLoScale, (b - h.y) * kLoScale);
 }
 
+// An 8 x 8 matrix of f16 (a thread: row lane / 4, columns 2 (lane % 4) and the next) transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 // A sequence's work: `chunks` units for each of heads x row_tiles items, over tiles [t0, t1).
 struct SeqWork {
     SeqRows r;
@@ -99,7 +123,7 @@ struct SeqWork {
     long long units;
 };
 
-template <typename T>
+template <int ROWS>
 __device__ __forceinline__ SeqWork seq_work(const AttnView &a, int32_t s) {
     SeqWork w;
     w.r = read_seq(a.kv, s, false);
@@ -111,14 +135,14 @@ __device__ __forceinline__ SeqWork seq_work(const AttnView &a, int32_t s) {
         w.t0 = begin / kKvTile;
         w.t1 = (w.r.len + kKvTile - 1) / kKvTile;
         w.chunks = (w.t1 - w.t0 + kChunkTiles - 1) / kChunkTiles;
-        w.row_tiles = (w.r.n * a.group + tile_rows<T>() - 1) / tile_rows<T>();
+        w.row_tiles = (w.r.n * a.group + ROWS - 1) / ROWS;
     }
     w.units = static_cast<long long>(w.chunks) * w.row_tiles * a.kv.heads;
     return w;
 }
 
 // One CTA's walk over its units [w, end): item by item.
-template <typename T>
+template <int ROWS>
 struct Walk {
     const AttnView &a;
     long long w, end, base;
@@ -131,14 +155,14 @@ struct Walk {
 
     __device__ __forceinline__ Walk(const AttnView &v, long long w0, long long w1, int32_t seq, long long seq_base)
         : a(v), w(w0), end(w1), base(seq_base), s(seq) {
-        if (w < end) work = seq_work<T>(a, s);
+        if (w < end) work = seq_work<ROWS>(a, s);
     }
 
     __device__ __forceinline__ bool next() {
         if (w >= end) return false;
         while (w >= base + work.units) {
             base += work.units;
-            work = seq_work<T>(a, ++s);
+            work = seq_work<ROWS>(a, ++s);
         }
         const long long local = w - base;
         const long long item = local / work.chunks;
@@ -158,28 +182,29 @@ struct Walk {
 
 // The query rows [row_tile * tile_rows, ...) of (sequence, key/value head): row r is query r / group of the
 // sequence, query head head * group + r % group.
-template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_constant__ AttnView a) {
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__((consumers<NT>() + 1) * 32, 1) attn_decode_kernel(const __grid_constant__ AttnView a) {
     extern __shared__ __align__(128) unsigned char raw[];
-    DecodeSmem<D> &sm = *reinterpret_cast<DecodeSmem<D> *>(raw);
-    constexpr int SLOTS = slots<D>();
+    DecodeSmem<D, NT> &sm = *reinterpret_cast<DecodeSmem<D, NT> *>(raw);
+    using Smem = DecodeSmem<D, NT>;
     constexpr bool SPLIT = sizeof(T) == 4;  // fp32: operands in two f16 parts
-    constexpr int ROWS = tile_rows<T>();
+    constexpr int ROWS = tile_rows<T, NT>();
+    constexpr int kWarps = consumers<NT>(), kThreads = (kWarps + 1) * 32;
+    constexpr int RT = SPLIT ? 1 : NT;  // column tiles of rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView &b = a.kv;
-    JoinEntry *joins = join_entries(a, gridDim.x, kMmaRows, D);
+    JoinEntry *joins = join_entries(a, gridDim.x, kSlotRows, D);
 
     // ---- the plan: where this CTA's range of units begins
-    for (int i = threadIdx.x; i < SLOTS; i += kThreads) {
-        mbar_init(&sm.full[i], 1);
-        mbar_init(&sm.empty[i], 1);
-        sm.issued[i] = 0;
+    if (threadIdx.x < kBatches) {
+        mbar_init(&sm.full[threadIdx.x], 1);
+        mbar_init(&sm.empty[threadIdx.x], kWarps);
+        fence_mbar_init();
     }
-    fence_mbar_init();
     const int32_t per = (b.num_seqs + kThreads - 1) / kThreads;
     const int32_t s0 = min(b.num_seqs, static_cast<int32_t>(threadIdx.x) * per), s1 = min(b.num_seqs, s0 + per);
     long long mine = 0;
-    for (int32_t s = s0; s < s1; ++s) mine += seq_work<T>(a, s).units;
+    for (int32_t s = s0; s < s1; ++s) mine += seq_work<ROWS>(a, s).units;
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -206,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         long long at = upto - mine;
         int32_t s = s0;
         for (;; ++s) {
-            const long long u = seq_work<T>(a, s).units;
+            const long long u = seq_work<ROWS>(a, s).units;
             if (w0 < at + u) break;
             at += u;
         }
@@ -214,89 +239,113 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         sm.base = at;
     }
     __syncthreads();
-    Walk<T> walk(a, w0, w1, sm.seq, sm.base);
+    Walk<ROWS> walk(a, w0, w1, sm.seq, sm.base);
     volatile int32_t *dead = &sm.dead;
 
+    auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t site) {
+        if (*dead || mbar_wait_bounded(bar, parity, kWaitNs)) return;
+        record_error(b.status, kDevTimeout, site);
+        *dead = 1;
+    };
+
     if (warp == kWarps) {
-        // ---- producer: lane l loads tiles l, l + 32, ... of an item
-        uint32_t i0 = 0;  // tiles of the items before
-        while (walk.next()) {
-            const int32_t count = walk.tile1 - walk.tile0;
-            const int tile_shift = b.page_shift - 4;  // tiles of a page, as a shift
-            int32_t page = -1;
-            float ks = 0.0f, vs = 0.0f;
-            auto fetch = [&](int32_t t) {
-                page = read_page(b, walk.s, t >> tile_shift);
-                const int64_t at = static_cast<int64_t>(page) * b.heads + walk.head;
-                ks = page < 0 ? 0.0f : __ldg(b.k_scales + at);
-                vs = page < 0 ? 0.0f : __ldg(b.v_scales + at);
-            };
-            if (lane < count) fetch(walk.tile0 + lane);
-            for (int32_t j0 = 0; j0 < count; j0 += 32) {
-                const int32_t j = j0 + lane;
-                const int32_t t = walk.tile0 + j;
-                const int32_t pg = page;
-                TileScales sc;
-                sc.ks = ks;
-                sc.vs = vs;
-                sc.lv = log2f(vs);
-                sc.ivs = 1.0f / vs;
-                const int64_t at = tile_offset<D>(b, pg < 0 ? 0 : pg, walk.head, t & ((1 << tile_shift) - 1));
-                if (j + 32 < count) fetch(t + 32);
-                // four tiles at a time, so that none waits for a slot far behind its own
-                for (int q = 0; q < 8; ++q) {
-                    if ((lane >> 2) != q || j >= count) continue;
-                    const uint32_t i = i0 + j, slot = i % SLOTS;
-                    if (!*dead && !mbar_wait_bounded(&sm.empty[slot], ((i / SLOTS) & 1u) ^ 1u, kWaitNs)) {
-                        record_error(b.status, kDevTimeout, 40);
-                        *dead = 1;
+        // ---- pages and scales of the CTA's tiles, 32 at a time, a lane each
+        const int tile_shift = b.page_shift - 4;  // tiles of a page, as a shift
+        int32_t next = 0, end = 0;  // the item's tiles that are not given out
+        bool more = true;
+        // (past the last tile the consumers still look for as many as they fetch ahead)
+        for (int32_t n = 0, past = 0; past < kWarps * Smem::kDepth; ++n) {
+            int32_t seq = -1, head = 0, t = 0;
+            for (int fill = 0; fill < kBatch;) {
+                if (next == end) {
+                    more = more && walk.next();
+                    if (!more) {
+                        past += kBatch - fill;
+                        break;
                     }
-                    if (*dead) continue;
-                    sm.scales[slot] = sc;
-                    sm.issued[slot] = i / SLOTS + 1;
-                    if (pg < 0) {  // a page that is not there reads as zeros
-                        for (int k = 0; k < 2 * kKvTile * D / 16; ++k)
-                            reinterpret_cast<uint4 *>(sm.ring[slot][0])[k] = make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_shared();  // before a later copy into the slot
-                        mbar_arrive(&sm.full[slot]);
-                    } else {
-                        mbar_arrive_expect_tx(&sm.full[slot], 2 * kKvTile * D);
-                        bulk_load(sm.ring[slot][0], b.k_pages + at, kKvTile * D, &sm.full[slot]);
-                        bulk_load(sm.ring[slot][1], b.v_pages + at, kKvTile * D, &sm.full[slot]);
-                    }
+                    next = walk.tile0;
+                    end = walk.tile1;
                 }
-                __syncwarp();
+                const int take = min(kBatch - fill, end - next);
+                if (lane >= fill && lane < fill + take) {
+                    seq = walk.s;
+                    head = walk.head;
+                    t = next + lane - fill;
+                }
+                fill += take;
+                next += take;
             }
-            i0 += count;
-        }
-        // after a time-out copies may be in flight that nobody has waited for
-        if (*dead) {
+            TileInfo x = {0.0f, 0.0f, 0.0f, 0.0f, kEndOfLine, 0};
+            if (seq >= 0) {
+                const int32_t page = read_page(b, seq, t >> tile_shift);
+                x.at = kNoTile;
+                if (page >= 0) {
+                    x.at = tile_offset<D>(b, page, head, t & ((1 << tile_shift) - 1));
+                    const int64_t sc = static_cast<int64_t>(page) * b.heads + head;
+                    x.ks = __ldg(b.k_scales + sc);
+                    x.vs = __ldg(b.v_scales + sc);
+                    x.lv = log2f(x.vs);
+                    x.ivs = 1.0f / x.vs;
+                }
+            }
             __syncwarp();
-            for (int k = lane; k < SLOTS; k += 32)
-                if (sm.issued[k]) mbar_wait_bounded(&sm.full[k], (sm.issued[k] - 1) & 1u, kWaitNs);
+            wait(&sm.empty[n % kBatches], ((n / kBatches) & 1u) ^ 1u, 40);
+            sm.info[n % kBatches][lane] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[n % kBatches]);
+            if (*dead) break;
         }
         return;
     }
 
     // ---- consumers
     const int g = lane >> 2, tig = lane & 3;
+    // S^T: rows g and g + 8 are tokens 4 (g / 2) + g % 2 and that + 2, so that
+    // after the transposition a thread holds p of tokens 4 tig .. 4 tig + 3
+    const int tok = 4 * (g >> 1) + (g & 1);
+    auto fetch_k = [&](int64_t at, uint32_t slot) {
+        const uint8_t *src = b.k_pages + max(at, int64_t{0}) + tok * 64 + tig * 16;
+#pragma unroll
+        for (int i = 0; i < Smem::kPieces; ++i)  // [64 dimensions][token or that + 2]
+            if (at != kEndOfLine) copy16(&sm.codes[warp][slot][0][i][lane], src + (i >> 1) * (kKvTile * 64) + (i & 1) * 128, at >= 0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto fetch_v = [&](int64_t at, uint32_t slot) {
+        const uint8_t *src = b.v_pages + max(at, int64_t{0}) + g * 64 + tig * 16;
+#pragma unroll
+        for (int i = 0; i < Smem::kPieces; ++i)
+            if (at != kEndOfLine) copy16(&sm.codes[warp][slot][1][i][lane], src + i * 512, at >= 0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // where tile i of the CTA's line is; waits for its batch if it is the warp's first of it
+    auto look = [&](uint32_t i) {
+        const uint32_t n = i / kBatch;
+        if (i % kBatch < kWarps) wait(&sm.full[n % kBatches], (n / kBatches) & 1u, 41);
+        return *dead ? kEndOfLine : sm.info[n % kBatches][i % kBatch].at;
+    };
+    auto landed = [] { asm volatile("cp.async.wait_group %0;" ::"n"(2 * Smem::kDepth - 1) : "memory"); };
+    for (uint32_t d = 0; d < Smem::kDepth; ++d) {
+        const int64_t at = look(warp + d * kWarps);
+        fetch_k(at, d);
+        fetch_v(at, d);
+    }
+    uint32_t taken = 0;  // tiles the warp has used
     uint32_t i0 = 0;
     bool merged = false;  // whether the merge buffer may still be read by others
     while (walk.next()) {
         const SeqRows &r = walk.work.r;
         const int32_t rows = min(ROWS, r.n * a.group - walk.row_tile * ROWS);
-        // q as A fragments: row g (and g + 8), dimensions 64 h + 16 tig + 4 j + 0..3 in k-step (h, j)
-        uint32_t qf[D / 16][4];
-        float cr[2];             // score scale of the two rows, in log2 units
-        int32_t kmin[2], kmax[2];
+        // q as B fragments: column g of tile u is row 8 u + g, dimensions 64 h +
+        // 16 tig + 4 j + 0..3 in k-step (h, j)
+        uint32_t qf[NT][D / 16][2];
+        // of the rows 8 u + 2 tig + i that the thread's scores belong to: the
+        // score scale in log2 units and the keys seen
+        float cr[RT][2];
+        int32_t kmin[RT][2], kmax[RT][2];
 #pragma unroll
-        for (int u = 0; u < (SPLIT ? 1 : 2); ++u) {
-            const int32_t rt = g + 8 * u;
-            const int32_t row = walk.row_tile * ROWS + min(rt, rows - 1);  // rows past the last repeat it
+        for (int u = 0; u < RT; ++u) {
+            const int32_t row = walk.row_tile * ROWS + min(8 * u + g, rows - 1);  // rows past the last repeat it
             const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
-            const int32_t pos = r.len - r.n + qi;
-            kmax[u] = a.causal ? pos + 1 : r.len;
-            kmin[u] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
             const T *src = static_cast<const T *>(a.q.p) + static_cast<int64_t>(r.off + qi) * a.q.row + qh * a.q.head;
             float x[D / 4];
             float amax = 0.0f;
@@ -314,23 +363,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
             e = amax < INFINITY ? max(e, -126) : 0;
             const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            cr[u] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            const float up = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            const int32_t pos = r.len - r.n + qi;
+            const int32_t hi = a.causal ? pos + 1 : r.len, lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // from the lanes of row 8 u + 2 tig + i
+                cr[u][i] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * i);
+                kmax[u][i] = __shfl_sync(0xffffffffu, hi, 8 * tig + 4 * i);
+                kmin[u][i] = __shfl_sync(0xffffffffu, lo, 8 * tig + 4 * i);
+            }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const float *v = x + 4 * k;
-                const uint32_t p0 = pack_f16(v[0] * down, v[1] * down), p1 = pack_f16(v[2] * down, v[3] * down);
-                qf[k][u] = p0;
-                qf[k][2 + u] = p1;
+                qf[u][k][0] = pack_f16(v[0] * down, v[1] * down);
+                qf[u][k][1] = pack_f16(v[2] * down, v[3] * down);
                 if (SPLIT) {
-                    qf[k][1] = pack_rest(v[0] * down, v[1] * down, p0);
-                    qf[k][3] = pack_rest(v[2] * down, v[3] * down, p1);
+                    qf[NT - 1][k][0] = pack_rest(v[0] * down, v[1] * down, qf[0][k][0]);
+                    qf[NT - 1][k][1] = pack_rest(v[2] * down, v[3] * down, qf[0][k][1]);
                 }
             }
-        }
-        if (SPLIT) {
-            cr[1] = cr[0];
-            kmin[1] = kmin[0];
-            kmax[1] = kmax[0];
         }
         // keys that every row of the item sees: tiles within need no mask
         const int32_t pos0 = r.len - r.n + walk.row_tile * ROWS / a.group;
@@ -338,179 +389,198 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         const int32_t all_hi = a.causal ? pos0 + 1 : r.len;
         const int32_t all_lo = a.window > 0 ? max(0, pos1 - a.window + 1) : 0;
 
-        float o[D / 8][4];
+        float o[NT][D / 16][4];  // o^T: rows d = 4 (g + 8 (k / 2)) + 2 (k % 2) and d + 1, columns 2 tig and the next
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) o[u][k][0] = o[u][k][1] = o[u][k][2] = o[u][k][3] = 0.0f;
+        float m[RT][2], l[RT][2];
+#pragma unroll
+        for (int u = 0; u < RT; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[u][i] = -INFINITY;
+                l[u][i] = 0.0f;
+            }
         bool seen = false;  // a tile whose V is not all zero
         float lv = 0.0f, ivs = 1.0f;
 
         const int32_t count = walk.tile1 - walk.tile0;
         // this warp's tiles: those whose running number is the warp's modulo kWarps
         for (int32_t j = (warp - static_cast<int32_t>(i0 % kWarps) + kWarps) % kWarps; j < count; j += kWarps) {
-            const uint32_t i = i0 + j, slot = i % SLOTS;
-            if (!*dead && !mbar_wait_bounded(&sm.full[slot], (i / SLOTS) & 1u, kWaitNs)) {
-                record_error(b.status, kDevTimeout, 41);
-                *dead = 1;
-            }
+            const uint32_t i = i0 + j, slot = taken++ % Smem::kDepth;
             const int32_t key0 = (walk.tile0 + j) * kKvTile;
-            const uint8_t *kt = sm.ring[slot][0], *vt = sm.ring[slot][1];
-            const TileScales sc = sm.scales[slot];
-            // S: n-tile u, column n is token 4 (n / 2) + 2 u + n % 2, so that a
-            // thread's columns 2 tig, 2 tig + 1 of both are tokens 4 tig .. 4 tig + 3
-            float s[2][4];
+            const TileInfo &info = sm.info[i / kBatch % kBatches][i % kBatch];
+            const float ks = info.ks, vs = info.vs;
+            const int64_t ahead = look(i + Smem::kDepth * kWarps);
+            float s[NT][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.0f;
-                const int tok = 4 * (g >> 1) + 2 * u + (g & 1);
+            for (int u = 0; u < NT; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.0f;
+            landed();
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(kt + h * (kKvTile * 64) + tok * 64 + tig * 16);
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+            for (int h = 0; h < D / 64; ++h) {
+                const uint4 wa = sm.codes[warp][slot][0][2 * h][lane], wb = sm.codes[warp][slot][0][2 * h + 1][lane];
+                const uint32_t was[4] = {wa.x, wa.y, wa.z, wa.w}, wbs[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t b0, b1;
-                        codes_to_f16<FMT>(ws[k], b0, b1);
-                        mma_16816_f16(s[u], qf[4 * h + k], b0, b1);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t f[4];
+                    codes_to_f16<FMT>(was[k], f[0], f[2]);
+                    codes_to_f16<FMT>(wbs[k], f[1], f[3]);
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) mma_16816_f16(s[u], f, qf[u][4 * h + k][0], qf[u][4 * h + k][1]);
                 }
             }
+            fetch_k(ahead, slot);
             // scores in log2 units, with V's scale
-            if (sc.vs > 0.0f) {
-                lv = sc.lv;
-                ivs = sc.ivs;
+            if (vs > 0.0f) {
+                lv = info.lv;
+                ivs = info.ivs;
                 if (!seen) {  // tiles so far had V = 0 and took lv = 0: their sums move to this one's
                     seen = true;
-                    m[0] += lv;
-                    m[1] += lv;
-                    l[0] *= ivs;
-                    l[1] *= ivs;
+#pragma unroll
+                    for (int u = 0; u < RT; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            m[u][i] += lv;
+                            l[u][i] *= ivs;
+                        }
                 }
             }
-            float z[2][4];  // [row][token]
+            float z[RT][4];  // [2 * token half + row]
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < RT; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (SPLIT) {
-                        z[0][2 * u + e] = fmaf(fmaf(s[u][2 + e], 1.0f / kLoScale, s[u][e]), sc.ks * cr[0], lv);
-                    } else {
-                        z[0][2 * u + e] = fmaf(s[u][e], sc.ks * cr[0], lv);
-                        z[1][2 * u + e] = fmaf(s[u][2 + e], sc.ks * cr[1], lv);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float sum = SPLIT ? fmaf(s[NT - 1][e], 1.0f / kLoScale, s[0][e]) : s[u][e];
+                    z[u][e] = fmaf(sum, ks * cr[u][e & 1], lv);
                 }
             if (key0 < all_lo || key0 + kKvTile > all_hi) {
 #pragma unroll
-                for (int rr = 0; rr < (SPLIT ? 1 : 2); ++rr)
+                for (int u = 0; u < RT; ++u)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int32_t key = key0 + 4 * tig + e;
-                        if (key < kmin[rr] || key >= kmax[rr]) z[rr][e] = -INFINITY;
+                        const int32_t key = key0 + tok + (e & 2);
+                        if (key < kmin[u][e & 1] || key >= kmax[u][e & 1]) z[u][e] = -INFINITY;
                     }
             }
-            uint32_t pf[4];
             bool grow = false;
-            float mx[2];
+            float mx[RT][2];
 #pragma unroll
-            for (int rr = 0; rr < (SPLIT ? 1 : 2); ++rr) {
-                float x = fmaxf(fmaxf(z[rr][0], z[rr][1]), fmaxf(z[rr][2], z[rr][3]));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                mx[rr] = x;
-                grow = grow || x > m[rr] + kGrow;  // (also from m = -inf)
-            }
+            for (int u = 0; u < RT; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = fmaxf(z[u][i], z[u][i + 2]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    mx[u][i] = x;
+                    grow = grow || x > m[u][i] + kGrow;  // (also from m = -inf)
+                }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int rr = 0; rr < (SPLIT ? 1 : 2); ++rr) {
-                    const float mn = fmaxf(m[rr], mx[rr]);
-                    const float f = m[rr] == -INFINITY ? 0.0f : ex2(m[rr] - mn);
-                    m[rr] = mn;
-                    l[rr] *= f;
+                for (int u = 0; u < RT; ++u)
 #pragma unroll
-                    for (int k = 0; k < D / 8; ++k) {
-                        o[k][2 * rr] *= f;
-                        o[k][2 * rr + 1] *= f;
-                        if (SPLIT) {
-                            o[k][2] *= f;
-                            o[k][3] *= f;
+                    for (int i = 0; i < 2; ++i) {
+                        const float mn = fmaxf(m[u][i], mx[u][i]);
+                        const float f = m[u][i] == -INFINITY ? 0.0f : ex2(m[u][i] - mn);
+                        m[u][i] = mn;
+                        l[u][i] *= f;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            o[u][k][i] *= f;
+                            o[u][k][i + 2] *= f;
+                            if (SPLIT) {
+                                o[NT - 1][k][i] *= f;
+                                o[NT - 1][k][i + 2] *= f;
+                            }
                         }
                     }
-                }
             }
+            uint32_t pf[NT][2];  // p^T as B fragments
 #pragma unroll
-            for (int rr = 0; rr < (SPLIT ? 1 : 2); ++rr) {
-                const float mu = m[rr] == -INFINITY ? 0.0f : m[rr];
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2(z[rr][e] - mu);
-                l[rr] = fmaf((p[0] + p[1]) + (p[2] + p[3]), ivs, l[rr]);
-                pf[rr] = pack_f16(p[0], p[1]);
-                pf[2 + rr] = pack_f16(p[2], p[3]);
+            for (int u = 0; u < RT; ++u) {
+                const float m0 = m[u][0] == -INFINITY ? 0.0f : m[u][0], m1 = m[u][1] == -INFINITY ? 0.0f : m[u][1];
+                const float p[4] = {ex2(z[u][0] - m0), ex2(z[u][1] - m1), ex2(z[u][2] - m0), ex2(z[u][3] - m1)};
+                l[u][0] = fmaf(p[0] + p[2], ivs, l[u][0]);
+                l[u][1] = fmaf(p[1] + p[3], ivs, l[u][1]);
+                const uint32_t h0 = pack_f16(p[0], p[1]), h1 = pack_f16(p[2], p[3]);
+                pf[u][0] = transpose_8x8(h0);
+                pf[u][1] = transpose_8x8(h1);
                 if (SPLIT) {
-                    pf[1] = pack_rest(p[0], p[1], pf[0]);
-                    pf[3] = pack_rest(p[2], p[3], pf[2]);
+                    pf[NT - 1][0] = transpose_8x8(pack_rest(p[0], p[1], h0));
+                    pf[NT - 1][1] = transpose_8x8(pack_rest(p[2], p[3], h1));
                 }
             }
-            if (!(sc.vs > 0.0f)) pf[0] = pf[1] = pf[2] = pf[3] = 0u;  // V = 0 whatever its codes
+            if (!(vs > 0.0f)) {  // V = 0 whatever its codes
+#pragma unroll
+                for (int u = 0; u < NT; ++u) pf[u][0] = pf[u][1] = 0u;
+            }
             // codes of V past the sequence's end are whatever was there; in
             // int8 p = 0 removes them, in e4m3 they may be NaN
             const int past = FMT == LORA_KV_E4M3 ? key0 + 4 * tig + 4 - r.len : 0;
             const uint32_t keep = past <= 0 ? 0xFFFFFFFFu : past >= 4 ? 0u : 0xFFFFFFFFu >> (8 * past);
+            landed();
 #pragma unroll
             for (int jj = 0; jj < D / 32; ++jj) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(vt + (g + 8 * jj) * 64 + tig * 16);
+                const uint4 w = sm.codes[warp][slot][1][jj][lane];
                 const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t b0, b1;
-                    codes_to_f16<FMT>(FMT == LORA_KV_E4M3 ? ws[k] & keep : ws[k], b0, b1);
-                    mma_16816_f16(o[4 * jj + k], pf, b0, b1);
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t f[4];
+                    codes_to_f16<FMT>(FMT == LORA_KV_E4M3 ? ws[2 * k] & keep : ws[2 * k], f[0], f[2]);
+                    codes_to_f16<FMT>(FMT == LORA_KV_E4M3 ? ws[2 * k + 1] & keep : ws[2 * k + 1], f[1], f[3]);
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) mma_16816_f16(o[u][2 * jj + k], f, pf[u][0], pf[u][1]);
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[slot]);
+            fetch_v(ahead, slot);
+            // the warp's last tile of a batch
+            if (i % kBatch >= kBatch - kWarps) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty[i / kBatch % kBatches]);
+            }
         }
         i0 += count;
 
-        // ---- merge the warps: row g's sums of dimensions 32 jj + 8 tig + 0..7
+        // ---- merge the warps
         if (merged) asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // the buffer has been read
         merged = true;
 #pragma unroll
-        for (int rr = 0; rr < (SPLIT ? 1 : 2); ++rr) {
-            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
-            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
-            const int rt = g + 8 * rr;
-            if (rt >= rows) continue;
-            if (tig == 0) {
-                sm.m[warp][rt] = m[rr];
-                sm.l[warp][rt] = l[rr];
-            }
+        for (int u = 0; u < RT; ++u)
 #pragma unroll
-            for (int jj = 0; jj < D / 32; ++jj)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float4 v;
-                    const int c = 2 * rr + half;
-                    v.x = o[4 * jj][c]; v.y = o[4 * jj + 1][c]; v.z = o[4 * jj + 2][c]; v.w = o[4 * jj + 3][c];
-                    if (SPLIT) {
-                        v.x = fmaf(o[4 * jj][2 + half], 1.0f / kLoScale, v.x);
-                        v.y = fmaf(o[4 * jj + 1][2 + half], 1.0f / kLoScale, v.y);
-                        v.z = fmaf(o[4 * jj + 2][2 + half], 1.0f / kLoScale, v.z);
-                        v.w = fmaf(o[4 * jj + 3][2 + half], 1.0f / kLoScale, v.w);
-                    }
-                    *reinterpret_cast<float4 *>(&sm.o[warp][rt][32 * jj + 8 * tig + 4 * half]) = v;
+            for (int i = 0; i < 2; ++i) {
+                float sum = l[u][i];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int rt = 8 * u + 2 * tig + i;
+                if (rt >= rows) continue;
+                if (g == 0) {
+                    sm.m[warp][rt] = m[u][i];
+                    sm.l[warp][rt] = sum;
                 }
-        }
+#pragma unroll
+                for (int jj = 0; jj < D / 32; ++jj) {
+                    float4 v = make_float4(o[u][2 * jj][i], o[u][2 * jj][i + 2], o[u][2 * jj + 1][i], o[u][2 * jj + 1][i + 2]);
+                    if (SPLIT) {
+                        v.x = fmaf(o[NT - 1][2 * jj][i], 1.0f / kLoScale, v.x);
+                        v.y = fmaf(o[NT - 1][2 * jj][i + 2], 1.0f / kLoScale, v.y);
+                        v.z = fmaf(o[NT - 1][2 * jj + 1][i], 1.0f / kLoScale, v.z);
+                        v.w = fmaf(o[NT - 1][2 * jj + 1][i + 2], 1.0f / kLoScale, v.w);
+                    }
+                    *reinterpret_cast<float4 *>(&sm.o[warp][rt][32 * jj + 4 * g]) = v;
+                }
+            }
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
         const bool whole = walk.from_start && walk.to_end;
         // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
-        float *part = partial_at(a, blockIdx.x, walk.from_start ? 1 : 0, kMmaRows, D);
+        float *part = partial_at(a, blockIdx.x, walk.from_start ? 1 : 0, kSlotRows, D);
         if (!whole && walk.from_start && threadIdx.x == 0) {
             const long long lastu = walk.item_end - 1;
             joins[blockIdx.x] = JoinEntry{walk.s, walk.head, walk.row_tile,
                                           static_cast<int32_t>(((lastu + 1) * ctas - 1) / total)};
         }
-        constexpr int PER_ROW = kWarps * 32 / kMmaRows;  // 16 threads a row
+        constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
         const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
         if (rt < rows) {
             float M = -INFINITY, L = 0.0f, f[kWarps];
@@ -545,36 +615,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             }
             if (c0 == 0) {
                 if (!whole) {
-                    part[kMmaRows * D + rt] = M;
-                    part[kMmaRows * D + kMmaRows + rt] = L;
+                    part[kSlotRows * D + rt] = M;
+                    part[kSlotRows * D + kSlotRows + rt] = L;
                 } else if (a.lse) {
                     a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
                 }
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int D, int FMT, int NT>
+cudaError_t decode_tiles(const AttnView &v, cudaStream_t stream) {
+    static uint64_t ctx[128] = {};
+    constexpr int smem = static_cast<int>(sizeof(DecodeSmem<D, NT>));
+    static_assert(smem <= 227 * 1024, "the shared memory of one CTA");
+    cudaError_t e = allow_smem(attn_decode_kernel<T, D, FMT, NT>, smem, ctx);
+    if (e != cudaSuccess) return e;
+    const int grid = device_sm_count();
+    attn_decode_kernel<T, D, FMT, NT><<<grid, (consumers<NT>() + 1) * 32, smem, stream>>>(v);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_join<T, D, tile_rows<T, NT>()>(v, grid, kSlotRows, stream);
+    count_launches(2);
+    return e;
 }
 
 template <typename T, int D, int FMT>
 cudaError_t decode_typed(const AttnView &v, cudaStream_t stream) {
-    static uint64_t ctx[128] = {};
-    constexpr int smem = static_cast<int>(sizeof(DecodeSmem<D>));
-    static_assert(smem <= 227 * 1024, "the shared memory of one CTA");
-    cudaError_t e = allow_smem(attn_decode_kernel<T, D, FMT>, smem, ctx);
-    if (e != cudaSuccess) return e;
-    const int grid = device_sm_count();
-    attn_decode_kernel<T, D, FMT><<<grid, kThreads, smem, stream>>>(v);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    e = launch_join<T, D, tile_rows<T>()>(v, grid, kMmaRows, stream);
-    count_launches(2);
-    return e;
+    if constexpr (sizeof(T) == 4) return decode_tiles<T, D, FMT, 2>(v, stream);
+    // one column tile of eight rows where that is all that any sequence has
+    else if (static_cast<int64_t>(v.max_queries) * v.group <= 8) return decode_tiles<T, D, FMT, 1>(v, stream);
+    else return decode_tiles<T, D, FMT, 2>(v, stream);
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(int head_dim) {
-    return split_workspace_bytes(device_sm_count(), kMmaRows, head_dim);
+    return split_workspace_bytes(device_sm_count(), kSlotRows, head_dim);
 }
 
 cudaError_t launch_attn_decode(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,

@@ -169,12 +169,6 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// 16 bytes from global to shared memory, asynchronously; zeros if not `there`.
-__device__ __forceinline__ void copy16(void *smem_dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(there ? 16 : 0)
-                 : "memory");
-}
-
 // Two fp32 values at once.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;

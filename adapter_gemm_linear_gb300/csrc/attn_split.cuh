@@ -8,6 +8,7 @@
 #pragma once
 
 #include "attn_device.cuh"
+#include "sm100_ptx.cuh"
 
 namespace lora {
 
@@ -49,6 +50,12 @@ __device__ __forceinline__ void store4(float *p, const float4 &v, float f) {
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v, float f) {
     __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x * f, v.y * f), __floats2bfloat162_rn(v.z * f, v.w * f)};
     *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(h);
+}
+
+// 16 bytes from global to shared memory, asynchronously; zeros if not `there`.
+__device__ __forceinline__ void copy16(void *smem_dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(smem_dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
 }
 
 // Joins the items that span CTAs: block x takes the item that begins in CTA x
