@@ -4,15 +4,14 @@
 // With few query rows each key and value is used a handful of times, so the
 // call is bound by reading the codes: 2 D bytes per token and key/value head.
 // What the kernel does about it:
-//  - One persistent CTA per SM.  The keys of all (sequence, key/value head,
+//  - Persistent CTAs.  The keys of all (sequence, key/value head,
 //    tile of query rows) items, cut in chunks of 128 tokens, are dealt out in
 //    equal contiguous ranges, so ragged lengths and few long sequences load
 //    every SM alike.  An item that spans CTAs is joined by attn_join_kernel
 //    from fp32 partial results (o, m, l), in a fixed order.
-//  - The consumer warps (15 of them for up to eight query rows, else 11) take
-//    the 16-token tiles in turn, each with its own running softmax, and are
-//    merged in shared memory at an item's end.  Every thread fetches the codes
-//    that it will use itself, two tiles ahead, by 16-byte asynchronous copies
+//  - A CTA's four or five consumer warps take the 16-token tiles in turn, each
+//    with its own running softmax, and are merged in shared memory at an item's
+//    end.  Every thread fetches the codes that it will use itself, tiles ahead, by 16-byte asynchronous copies
 //    to shared memory: no barrier is between a copy and its use.  (One warp
 //    that fed all by bulk copies of 2 KiB was held at one copy per 85 ns and
 //    SM: 3.6 TB/s with heads of 128, 1.9 with heads of 64.)  One more warp looks
@@ -59,10 +58,13 @@ constexpr float kLoScale = 2048.0f;                // 2^11: the lo parts of fp32
 template <typename T, int NT>
 __host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? 4 * NT : 8 * NT; }
 
-// Consumer warps: with the producer a multiple of four, by which registers are
-// given out, and as many as that leaves 128 (or 168) a thread.
+// Several small CTAs per SM, so that while one merges its warps or begins an
+// item the others' copies keep the memory busy: three of four consumer warps
+// for up to eight query rows (128 registers a thread), else two of five (168).
 template <int NT>
-__host__ __device__ constexpr int consumers() { return NT == 1 ? 15 : 11; }
+__host__ __device__ constexpr int consumers() { return NT == 1 ? 4 : 5; }
+template <int NT>
+__host__ __device__ constexpr int ctas_per_sm() { return NT == 1 ? 3 : 2; }
 
 // What the looking-up warp says of a tile: where its codes are (in k_pages and
 // in v_pages; < 0: not there, zeros), and K's scale, V's, its log2 and reciprocal.
@@ -79,7 +81,7 @@ template <int D, int NT>
 struct DecodeSmem {
     static constexpr int kWarps = consumers<NT>();
     static constexpr int kPieces = D / 32;           // 16-byte pieces a lane takes of a tile of K (and of V)
-    static constexpr int kDepth = D == 128 ? 2 : 4;  // tiles a warp fetches ahead
+    static constexpr int kDepth = D == 128 ? 3 : 6;  // tiles a warp fetches ahead
     uint4 codes[kWarps][kDepth][2][kPieces][32];     // [.., K or V, piece, lane]
     float o[kWarps][8 * NT][D + 4];                  // merge: padded against bank conflicts
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
@@ -183,7 +185,7 @@ struct Walk {
 // The query rows [row_tile * tile_rows, ...) of (sequence, key/value head): row r is query r / group of the
 // sequence, query head head * group + r % group.
 template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__((consumers<NT>() + 1) * 32, 1) attn_decode_kernel(const __grid_constant__ AttnView a) {
+__global__ void __launch_bounds__((consumers<NT>() + 1) * 32, ctas_per_sm<NT>()) attn_decode_kernel(const __grid_constant__ AttnView a) {
     extern __shared__ __align__(128) unsigned char raw[];
     DecodeSmem<D, NT> &sm = *reinterpret_cast<DecodeSmem<D, NT> *>(raw);
     using Smem = DecodeSmem<D, NT>;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__((consumers<NT>() + 1) * 32, 1) attn_decode_ker
     if (lane == 31) sm.warp_sum[warp] = upto;
     if (threadIdx.x == 0) {
         sm.dead = 0;
-        joins[blockIdx.x] = JoinEntry{-1, 0, 0, 0};
+        joins[blockIdx.x].last_cta = -1;
     }
     __syncthreads();
     long long total = 0;
@@ -577,8 +579,8 @@ __global__ void __launch_bounds__((consumers<NT>() + 1) * 32, 1) attn_decode_ker
         float *part = partial_at(a, blockIdx.x, walk.from_start ? 1 : 0, kSlotRows, D);
         if (!whole && walk.from_start && threadIdx.x == 0) {
             const long long lastu = walk.item_end - 1;
-            joins[blockIdx.x] = JoinEntry{walk.s, walk.head, walk.row_tile,
-                                          static_cast<int32_t>(((lastu + 1) * ctas - 1) / total)};
+            joins[blockIdx.x] = JoinEntry{static_cast<int32_t>(((lastu + 1) * ctas - 1) / total), walk.head, r.off,
+                                          walk.row_tile * ROWS, rows, {}};
         }
         constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
         const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
@@ -630,10 +632,10 @@ template <typename T, int D, int FMT, int NT>
 cudaError_t decode_tiles(const AttnView &v, cudaStream_t stream) {
     static uint64_t ctx[128] = {};
     constexpr int smem = static_cast<int>(sizeof(DecodeSmem<D, NT>));
-    static_assert(smem <= 227 * 1024, "the shared memory of one CTA");
+    static_assert((smem + 1024) * ctas_per_sm<NT>() <= 228 * 1024, "the shared memory of an SM");
     cudaError_t e = allow_smem(attn_decode_kernel<T, D, FMT, NT>, smem, ctx);
     if (e != cudaSuccess) return e;
-    const int grid = device_sm_count();
+    const int grid = device_sm_count() * ctas_per_sm<NT>();
     attn_decode_kernel<T, D, FMT, NT><<<grid, (consumers<NT>() + 1) * 32, smem, stream>>>(v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -653,7 +655,7 @@ cudaError_t decode_typed(const AttnView &v, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_workspace_bytes(int head_dim) {
-    return split_workspace_bytes(device_sm_count(), kSlotRows, head_dim);
+    return split_workspace_bytes(device_sm_count() * ctas_per_sm<1>(), kSlotRows, head_dim);
 }
 
 cudaError_t launch_attn_decode(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,

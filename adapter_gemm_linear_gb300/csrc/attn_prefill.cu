@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
         sm.dead = 0;
-        joins[blockIdx.x] = JoinEntry{-1, 0, 0, 0};
+        joins[blockIdx.x].last_cta = -1;
     }
     if (warp == 12) {
         tmem_alloc(&sm.tmem, 512);
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 }
             }
             if (!whole && (it.flags & kFromStart) && threadIdx.x == 0)
-                joins[blockIdx.x] = JoinEntry{it.seq, it.head, it.row_tile, it.last_cta};
+                joins[blockIdx.x] = JoinEntry{it.last_cta, it.head, it.off, it.row_tile * kRows, rows, {}};
             get_item(it);
         }
     } else if (warp < 12) {

@@ -12,8 +12,11 @@
 
 namespace lora {
 
-struct JoinEntry {
-    int32_t seq, head, row_tile, last_cta;  // seq < 0: nothing to join
+struct alignas(16) JoinEntry {
+    int32_t last_cta;        // < 0: nothing to join
+    int32_t head, off;       // key/value head, the sequence's first row
+    int32_t row, rows;       // the item's first query row and its number of them
+    int32_t pad[3];
 };
 
 // Floats of one partial result: [rows][D] sums, then the rows' maximum (log2 units) and sum.
@@ -85,33 +88,46 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const JoinEntry e = join_entries(a, ctas, slot_rows, D)[blockIdx.x];
-    if (e.seq < 0) return;
-    const SeqRows r = read_seq(b, e.seq, false);
     const int32_t rt = blockIdx.y * (kJoinThreads / PER_ROW) + threadIdx.x / PER_ROW, c = threadIdx.x % PER_ROW * 4;
-    const int32_t row = e.row_tile * ROWS + rt;
-    if (rt >= ROWS || row >= r.n * a.group) return;
-    auto part = [&](int32_t cta) {
-        return partial_at(a, cta, cta == static_cast<int32_t>(blockIdx.x) ? 1 : 0, slot_rows, D);
-    };
-    float M = -INFINITY;
-    for (int32_t k = blockIdx.x; k <= e.last_cta; ++k) M = fmaxf(M, part(k)[slot_rows * D + rt]);
-    const float mu = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
+    if (e.last_cta < 0 || rt >= e.rows) return;
+    const int32_t row = e.row + rt;
+    // the partial results in order, eight at a time in flight
+    constexpr int AT_ONCE = 8;
+    float M = -INFINITY, L = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int32_t k = blockIdx.x; k <= e.last_cta; ++k) {
-        const float *p = part(k);
-        const float f = ex2(p[slot_rows * D + rt] - mu);
-        L = fmaf(p[slot_rows * D + slot_rows + rt], f, L);
-        const float4 x = *reinterpret_cast<const float4 *>(p + rt * D + c);
-        v.x = fmaf(x.x, f, v.x);
-        v.y = fmaf(x.y, f, v.y);
-        v.z = fmaf(x.z, f, v.z);
-        v.w = fmaf(x.w, f, v.w);
+    for (int32_t k0 = blockIdx.x; k0 <= e.last_cta; k0 += AT_ONCE) {
+        float m[AT_ONCE], l[AT_ONCE];
+        float4 x[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int32_t k = min(k0 + i, e.last_cta);
+            const float *p = partial_at(a, k, k == static_cast<int32_t>(blockIdx.x) ? 1 : 0, slot_rows, D);
+            m[i] = k0 + i <= e.last_cta ? __ldg(p + slot_rows * D + rt) : -INFINITY;
+            l[i] = __ldg(p + slot_rows * D + slot_rows + rt);
+            x[i] = __ldg(reinterpret_cast<const float4 *>(p + rt * D + c));
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) mn = fmaxf(mn, m[i]);
+        const float mu = mn == -INFINITY ? 0.0f : mn;
+        const float f0 = ex2(M - mu);
+        M = mn;
+        L *= f0;
+        v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            if (k0 + i > e.last_cta) break;
+            const float f = ex2(m[i] - mu);
+            L = fmaf(l[i], f, L);
+            v.x = fmaf(x[i].x, f, v.x);
+            v.y = fmaf(x[i].y, f, v.y);
+            v.z = fmaf(x[i].z, f, v.z);
+            v.w = fmaf(x[i].w, f, v.w);
+        }
     }
     const int32_t qi = row / a.group, qh = e.head * a.group + row % a.group;
-    store4(static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head + c, v, 1.0f / L);
-    if (a.lse && c == 0) a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
+    store4(static_cast<T *>(a.out.p) + static_cast<int64_t>(e.off + qi) * a.out.row + qh * a.out.head + c, v, 1.0f / L);
+    if (a.lse && c == 0) a.lse[static_cast<int64_t>(e.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
 }
 
 // Opts a kernel in to `bytes` of shared memory, once per device and context (`ctx`: what has been done).
