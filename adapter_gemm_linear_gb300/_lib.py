@@ -207,19 +207,18 @@ class AttentionArgs(ctypes.Structure):
     ]
 
 
-_ROWS_ARGS = [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatch), ctypes.c_int, ctypes.POINTER(Heads),
-              ctypes.POINTER(Heads), ctypes.c_void_p]
+# Structures are passed by address: of the ctypes structures above, or of
+# bytes packed to the same layout.
+_ROWS_ARGS = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
 
 # (name, restype, argtypes) of every entry point declared in include/lora_attention.h
 ATTENTION_SIGNATURES = [
-    ("lora_rope", ctypes.c_int, [ctypes.POINTER(RopeArgs), ctypes.c_void_p]),
+    ("lora_rope", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     ("lora_kv_pages_bytes", ctypes.c_size_t, [ctypes.c_int32] * 4),
     ("lora_kv_append", ctypes.c_int, _ROWS_ARGS),
     ("lora_kv_gather", ctypes.c_int, _ROWS_ARGS),
-    ("lora_kv_attention_workspace_bytes", ctypes.c_size_t,
-     [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatch), ctypes.POINTER(AttentionArgs)]),
-    ("lora_kv_attention", ctypes.c_int,
-     [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatch), ctypes.POINTER(AttentionArgs), ctypes.c_void_p]),
+    ("lora_kv_attention_workspace_bytes", ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    ("lora_kv_attention", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
 ]
 
 _lock = threading.Lock()

@@ -15,9 +15,10 @@ pages that hold its tokens.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -28,43 +29,69 @@ from .api import LoraError, lora_dtype
 
 _FORMATS = {"int8": (_lib.KV_INT8, torch.int8), "e4m3": (_lib.KV_E4M3, torch.float8_e4m3fn)}
 
+# A decode step makes these calls once per layer with a few microseconds of
+# work each, so the argument structures of include/lora_attention.h are packed
+# in one go (ctypes takes a microsecond for every few fields it sets) and the
+# stream is asked for as a bare handle.
+_ROPE_ARGS = struct.Struct("@6i PqqPqqPqqPqq PPiiPPii")
+_BATCH = struct.Struct("@iiPPPi0P")
+_HEADS = struct.Struct("@Pqq")
+_ATTENTION_ARGS = struct.Struct("@iiPqqPqqPfiiiPN")
+assert _ROPE_ARGS.size == ctypes.sizeof(_lib.RopeArgs) and _BATCH.size == ctypes.sizeof(_lib.KvBatch)
+assert _HEADS.size == ctypes.sizeof(_lib.Heads) and _ATTENTION_ARGS.size == ctypes.sizeof(_lib.AttentionArgs)
 
-def _heads(t: torch.Tensor, name: str, device: torch.device) -> _lib.Heads:
-    if t.dim() != 3 or (t.stride(2) != 1 and t.numel() > 0):
+_DTYPES = {torch.bfloat16: _lib.LORA_BF16, torch.float32: _lib.LORA_FP32}
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _heads(t: torch.Tensor, name: str, device: int) -> Tuple[int, int, int]:
+    strides = t.stride()
+    if len(strides) != 3 or (strides[2] != 1 and t.numel() > 0):
         raise ValueError(f"{name} must be [rows, heads, head_dim] with contiguous heads")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return _lib.Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected device {device}")
+    return t.data_ptr(), strides[0], strides[1]
 
 
-def _index(t: torch.Tensor, name: str, device: torch.device) -> int:
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be contiguous int32 on {device}")
+def _index(t: torch.Tensor, name: str, device: int) -> int:
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be contiguous int32 on device {device}")
     return t.data_ptr()
 
 
-@contextlib.contextmanager
-def _launching(device: torch.device, stream: Optional[torch.cuda.Stream], tensors):
-    """The handle of the stream to launch on, with it and the device current
-    (so that outputs come from that stream's memory), and the caller's tensors
-    kept until the stream has passed the call."""
-    if stream is None:
-        if device.index is None or device.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.device(device):
-                yield torch.cuda.current_stream().cuda_stream
-        return
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+def _dtype(t: torch.dtype) -> int:
+    code = _DTYPES.get(t)
+    return lora_dtype(t) if code is None else code  # (lora_dtype says what is wrong)
 
 
 def _call(status: int, what: str) -> None:
     if status != 0:
         raise LoraError(status, what)
+
+
+def _on_stream(f):
+    """f with the keyword ``stream``: on that stream (so that outputs come from
+    its memory and the caller's tensors are kept until it has passed the call)
+    and its device; without, on the current stream of the tensors' device."""
+
+    @functools.wraps(f)
+    def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
+        if stream is None:
+            device = args[0].device.index if isinstance(args[0], KvCache) else args[0].get_device()
+            if device < 0 or device == torch.cuda.current_device():
+                return f(*args, **kw)
+            with torch.cuda.device(device):
+                return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            result = f(*args, **kw)
+        for t in list(args) + list(kw.values()):
+            for x in (t.k_pages, t.v_pages, t.k_scales, t.v_scales) if isinstance(t, KvCache) else (t,):
+                if isinstance(x, torch.Tensor):
+                    x.record_stream(stream)
+        return result
+
+    return call
 
 
 def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
@@ -75,10 +102,11 @@ def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"
     return angle.cos().float(), angle.sin().float()
 
 
+@_on_stream
 def rope(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor,
          axes: Optional[Sequence[int]] = None, interleaved: bool = False, inverse: bool = False,
-         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
-         stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+         q_out: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """lora_rope: q [rows, q_heads, D] and k [rows, k_heads, D] (or None)
     turned by their rows' positions -> (q_out, k_out), new tensors unless
     given (``q_out=q`` works in place).
@@ -86,37 +114,43 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: tor
     ``cos``/``sin``: float32 [max_pos, rot_dim/2] (rope_tables); ``positions``:
     int32 [rows], or [axes, rows] for positions of several axes (time, height,
     width), with ``axes[i]`` the axis of pair i (default: axis 0).
-    ``inverse`` turns the other way: the gradient of the call, or its undoing."""
-    device = q.device
-    if cos.dtype != torch.float32 or cos.dim() != 2 or not cos.is_contiguous() or \
-            sin.dtype != torch.float32 or sin.shape != cos.shape or not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous float32 [max_pos, rot_dim/2]")
-    if cos.device != device or sin.device != device:
-        raise ValueError(f"cos and sin must be on {device}")
-    rows, D = int(q.shape[0]), int(q.shape[-1])
+    ``inverse`` turns the other way: the gradient of the call, or its undoing.
+    ``stream``: launch there instead of on the current stream."""
+    device, shape = q.get_device(), q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    rows, q_heads, D = shape
+    table = cos.shape
+    if len(table) != 2 or sin.shape != table or cos.dtype != torch.float32 or sin.dtype != torch.float32 or \
+            not cos.is_contiguous() or not sin.is_contiguous() or cos.get_device() != device or sin.get_device() != device:
+        raise ValueError(f"cos and sin must be contiguous float32 [max_pos, rot_dim/2] on device {device}")
     if positions.dim() not in (1, 2) or positions.shape[-1] != rows:
         raise ValueError("positions must be [rows] or [axes, rows]")
-    if axes is not None and len(axes) != cos.shape[1]:
-        raise ValueError(f"axes must name one axis for each of the {cos.shape[1]} pairs")
-    if k is not None and (k.dtype != q.dtype or k.shape[0] != rows or k.shape[-1] != D):
-        raise ValueError("k must have q's dtype, rows and head_dim")
-    with _launching(device, stream, (q, k, cos, sin, positions, q_out, k_out)) as st:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=device)
-        for x, y, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-            if x is not None and (y.shape != x.shape or y.dtype != q.dtype):
-                raise ValueError(f"{name} must have its input's shape and dtype")
-        none = _lib.Heads(None, 0, 0)
-        args = _lib.RopeArgs(
-            lora_dtype(q.dtype), rows, D, 2 * int(cos.shape[1]), int(q.shape[1]), 0 if k is None else int(k.shape[1]),
-            _heads(q, "q", device), _heads(q_out, "q_out", device),
-            none if k is None else _heads(k, "k", device), none if k is None else _heads(k_out, "k_out", device),
-            cos.data_ptr(), sin.data_ptr(), int(cos.shape[0]), 1 if positions.dim() == 1 else int(positions.shape[0]),
-            _index(positions, "positions", device), None if axes is None else bytes(axes), int(interleaved),
-            int(inverse))
-        _call(_lib.lib().lora_rope(ctypes.byref(args), st), "lora_rope")
+    if axes is not None and len(axes) != table[1]:
+        raise ValueError(f"axes must name one axis for each of the {table[1]} pairs")
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must have q's shape and dtype")
+    k_heads, kh, koh = 0, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        k_shape = k.shape
+        if k.dtype != q.dtype or len(k_shape) != 3 or k_shape[0] != rows or k_shape[2] != D:
+            raise ValueError("k must be [rows, k_heads, head_dim] with q's dtype, rows and head_dim")
+        k_heads = k_shape[1]
+        if k_out is None:
+            k_out = torch.empty(k_shape, dtype=q.dtype, device=q.device)
+        elif k_out.shape != k_shape or k_out.dtype != q.dtype:
+            raise ValueError("k_out must have k's shape and dtype")
+        kh, koh = _heads(k, "k", device), _heads(k_out, "k_out", device)
+    pair_axis = None if axes is None else bytes(axes)
+    axis_ptr = 0 if axes is None else ctypes.cast(pair_axis, ctypes.c_void_p).value
+    args = _ROPE_ARGS.pack(
+        _dtype(q.dtype), rows, D, 2 * table[1], q_heads, k_heads, *_heads(q, "q", device),
+        *_heads(q_out, "q_out", device), *kh, *koh, cos.data_ptr(), sin.data_ptr(), table[0],
+        1 if positions.dim() == 1 else positions.shape[0], _index(positions, "positions", device), axis_ptr,
+        interleaved, inverse)
+    _call(_lib.lib().lora_rope(args, _current_stream(device)), "lora_rope")
     return q_out, k_out if k is not None else None
 
 
@@ -163,75 +197,78 @@ class KvCache:
         self.k_scales = tensor(k_scales, tiles[:2], torch.float32, "k_scales")
         self.v_scales = tensor(v_scales, tiles[:2], torch.float32, "v_scales")
         self.device = self.k_pages.device
+        self._workspace = {}  # bytes of an attention call's workspace, by what they depend on
         self._desc = _lib.KvCacheDesc(code, self.num_pages, self.num_heads, D, self.page_tokens,
                                       self.k_pages.data_ptr(), self.v_pages.data_ptr(), self.k_scales.data_ptr(),
                                       self.v_scales.data_ptr())
         self._ref = ctypes.byref(self._desc)
 
     def _batch(self, rows: int, block_table: torch.Tensor, seq_lens: torch.Tensor,
-               offsets: Optional[torch.Tensor]) -> _lib.KvBatch:
-        S = int(seq_lens.shape[0])
-        if block_table.dim() != 2 or block_table.shape[0] != S:
+               offsets: Optional[torch.Tensor]) -> bytes:
+        device, S = self.device.index, seq_lens.shape[0]
+        table = block_table.shape
+        if len(table) != 2 or table[0] != S:
             raise ValueError(f"block_table must be [{S}, max_pages]")
         if offsets is not None and offsets.shape != (S + 1,):
             raise ValueError(f"offsets must be [{S + 1}]")
-        return _lib.KvBatch(S, rows, _index(seq_lens, "seq_lens", self.device),
-                            None if offsets is None else _index(offsets, "offsets", self.device),
-                            _index(block_table, "block_table", self.device), int(block_table.shape[1]))
+        return _BATCH.pack(S, rows, _index(seq_lens, "seq_lens", device),
+                           0 if offsets is None else _index(offsets, "offsets", device),
+                           _index(block_table, "block_table", device), table[1])
 
     def _check(self, t: torch.Tensor, name: str) -> None:
         if t.dim() != 3 or t.shape[1:] != (self.num_heads, self.head_dim):
             raise ValueError(f"{name} must be [rows, {self.num_heads}, {self.head_dim}]")
 
+    @_on_stream
     def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
-               offsets: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+               offsets: Optional[torch.Tensor] = None) -> None:
         """lora_kv_append: quantise the rows' k and v [rows, num_heads, head_dim]
-        into their sequences' pages, as the last tokens of seq_lens tokens."""
+        into their sequences' pages, as the last tokens of seq_lens tokens.
+        ``stream``: launch there instead of on the current stream."""
         self._check(k, "k")
         self._check(v, "v")
         if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
             raise ValueError("k and v must have the same dtype and rows")
-        with _launching(self.device, stream, (k, v, block_table, seq_lens, offsets, self.k_pages, self.v_pages,
-                                              self.k_scales, self.v_scales)) as st:
-            b = self._batch(int(k.shape[0]), block_table, seq_lens, offsets)
-            kh, vh = _heads(k, "k", self.device), _heads(v, "v", self.device)
-            _call(_lib.lib().lora_kv_append(self._ref, ctypes.byref(b), lora_dtype(k.dtype), ctypes.byref(kh),
-                                            ctypes.byref(vh), st), "lora_kv_append")
+        device = self.device.index
+        _call(_lib.lib().lora_kv_append(
+            self._ref, self._batch(k.shape[0], block_table, seq_lens, offsets), _dtype(k.dtype),
+            _HEADS.pack(*_heads(k, "k", device)), _HEADS.pack(*_heads(v, "v", device)), _current_stream(device)),
+            "lora_kv_append")
 
+    @_on_stream
     def gather(self, block_table: torch.Tensor, seq_lens: torch.Tensor, offsets: Optional[torch.Tensor] = None,
                rows: Optional[int] = None, dtype: torch.dtype = torch.bfloat16, k_out: Optional[torch.Tensor] = None,
-               v_out: Optional[torch.Tensor] = None,
-               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+               v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """lora_kv_gather: the rows' keys and values, dequantised -> (k, v)
         [rows, num_heads, head_dim], new tensors of ``dtype`` unless given.
-        ``rows`` (needed with offsets and no k_out) is offsets' last value."""
+        ``rows`` (needed with offsets and no k_out) is offsets' last value.
+        ``stream``: launch there instead of on the current stream."""
         if k_out is not None:
             self._check(k_out, "k_out")
-            rows, dtype = int(k_out.shape[0]), k_out.dtype
+            rows, dtype = k_out.shape[0], k_out.dtype
         elif rows is None:
             if offsets is not None:
                 raise ValueError("give rows (offsets' last value), or k_out and v_out")
-            rows = int(seq_lens.shape[0])
-        with _launching(self.device, stream, (block_table, seq_lens, offsets, k_out, v_out, self.k_pages,
-                                              self.v_pages, self.k_scales, self.v_scales)) as st:
-            shape = (rows, self.num_heads, self.head_dim)
-            if k_out is None:
-                k_out = torch.empty(shape, dtype=dtype, device=self.device)
-            if v_out is None:
-                v_out = torch.empty(shape, dtype=dtype, device=self.device)
-            if v_out.shape != shape or v_out.dtype != dtype:
-                raise ValueError("v_out must have k_out's shape and dtype")
-            b = self._batch(rows, block_table, seq_lens, offsets)
-            kh, vh = _heads(k_out, "k_out", self.device), _heads(v_out, "v_out", self.device)
-            _call(_lib.lib().lora_kv_gather(self._ref, ctypes.byref(b), lora_dtype(dtype), ctypes.byref(kh),
-                                            ctypes.byref(vh), st), "lora_kv_gather")
+            rows = seq_lens.shape[0]
+        shape, device = (rows, self.num_heads, self.head_dim), self.device.index
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=self.device)
+        elif v_out.shape != shape or v_out.dtype != dtype:
+            raise ValueError("v_out must have k_out's shape and dtype")
+        _call(_lib.lib().lora_kv_gather(
+            self._ref, self._batch(rows, block_table, seq_lens, offsets), _dtype(dtype),
+            _HEADS.pack(*_heads(k_out, "k_out", device)), _HEADS.pack(*_heads(v_out, "v_out", device)),
+            _current_stream(device)), "lora_kv_gather")
         return k_out, v_out
 
+    @_on_stream
     def attention(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                   offsets: Optional[torch.Tensor] = None, max_queries: Optional[int] = None, causal: bool = True,
                   window: int = 0, scale: Optional[float] = None, return_lse: bool = False,
                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+                  workspace: Optional[torch.Tensor] = None):
         """lora_kv_attention: softmax attention of q [rows, q_heads, head_dim]
         over the sequences' cached keys and values -> out like q (and, with
         ``return_lse`` or ``lse`` given, the float32 [rows, q_heads] log of the
@@ -239,36 +276,39 @@ class KvCache:
 
         ``max_queries`` bounds the rows of one sequence (default: 1 without
         offsets, else all rows); ``window`` > 0 limits a query to the last
-        ``window`` positions up to its own; ``scale`` defaults to head_dim^-0.5."""
-        if q.dim() != 3 or q.shape[2] != self.head_dim:
+        ``window`` positions up to its own; ``scale`` defaults to head_dim^-0.5.
+        ``stream``: launch there instead of on the current stream."""
+        shape, device = q.shape, self.device.index
+        if len(shape) != 3 or shape[2] != self.head_dim:
             raise ValueError(f"q must be [rows, q_heads, {self.head_dim}]")
-        rows, Hq = int(q.shape[0]), int(q.shape[1])
+        rows, Hq, _ = shape
         if max_queries is None:
             max_queries = 1 if offsets is None else max(1, rows)
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
-        with _launching(self.device, stream, (q, block_table, seq_lens, offsets, out, lse, workspace, self.k_pages,
-                                              self.v_pages, self.k_scales, self.v_scales)) as st:
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-            elif out.shape != q.shape or out.dtype != q.dtype:
-                raise ValueError("out must have q's shape and dtype")
-            if lse is None:
-                if return_lse:
-                    lse = torch.empty((rows, Hq), dtype=torch.float32, device=self.device)
-            elif lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous() \
-                    or lse.device != self.device:
-                raise ValueError(f"lse must be contiguous float32 [{rows}, {Hq}] on {self.device}")
-            b = self._batch(rows, block_table, seq_lens, offsets)
-            args = _lib.AttentionArgs(lora_dtype(q.dtype), Hq, _heads(q, "q", self.device),
-                                      _heads(out, "out", self.device), None if lse is None else lse.data_ptr(),
-                                      scale, int(causal), int(window), int(max_queries), None, 0)
-            bref, aref = ctypes.byref(b), ctypes.byref(args)
-            L = _lib.lib()
-            if workspace is None:
-                need = int(L.lora_kv_attention_workspace_bytes(self._ref, bref, aref))
-                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
-            args.workspace = workspace.data_ptr()
-            args.workspace_bytes = workspace.numel() * workspace.element_size()
-            _call(L.lora_kv_attention(self._ref, bref, aref, st), "lora_kv_attention")
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=self.device)
+        elif out.shape != shape or out.dtype != q.dtype:
+            raise ValueError("out must have q's shape and dtype")
+        if lse is None:
+            if return_lse:
+                lse = torch.empty((rows, Hq), dtype=torch.float32, device=self.device)
+        elif lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous() \
+                or lse.get_device() != device:
+            raise ValueError(f"lse must be contiguous float32 [{rows}, {Hq}] on {self.device}")
+        batch = self._batch(rows, block_table, seq_lens, offsets)
+        head = (_dtype(q.dtype), Hq, *_heads(q, "q", device), *_heads(out, "out", device),
+                0 if lse is None else lse.data_ptr(), scale, causal, window, max_queries)
+        L = _lib.lib()
+        if workspace is None:
+            key = (head[0], Hq, max_queries, device)
+            need = self._workspace.get(key)
+            if need is None:
+                need = L.lora_kv_attention_workspace_bytes(self._ref, batch, _ATTENTION_ARGS.pack(*head, 0, 0))
+                if need:
+                    self._workspace[key] = need
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        _call(L.lora_kv_attention(self._ref, batch, _ATTENTION_ARGS.pack(
+            *head, workspace.data_ptr(), workspace.numel() * workspace.element_size()), _current_stream(device)),
+            "lora_kv_attention")
         return (out, lse) if lse is not None else out
