@@ -129,6 +129,7 @@ lora_status_t lora_rope(const lora_rope_args_t *a, void *stream) {
     if (a->rot_dim < 16 || a->rot_dim > a->head_dim || a->rot_dim > 2 * LORA_ROPE_MAX_PAIRS)
         return LORA_ERR_INVALID_ARG;
     if (a->head_dim % 8 || a->rot_dim % 16) return LORA_ERR_ALIGNMENT;
+    if (a->head_dim > 1024) return LORA_ERR_UNSUPPORTED;
     lora::RopeView v;
     lora_status_t s = check_heads(&a->q, a->dtype, a->rows, &v.q);
     if (s == LORA_OK) s = check_heads(&a->q_out, a->dtype, a->rows, &v.q_out);

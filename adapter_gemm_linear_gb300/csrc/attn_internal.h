@@ -35,6 +35,7 @@ struct RopeView {
     int32_t rows, head_dim, rot_dim, q_heads, k_heads, max_pos, num_axes;
     int32_t interleaved, inverse;
     uint8_t pair_axis[LORA_ROPE_MAX_PAIRS];
+    uint8_t chunk_axis[LORA_ROPE_MAX_PAIRS / 4];  // of a thread's pairs, or LORA_ROPE_MAX_AXES where they differ
 };
 
 struct AttnView {

@@ -50,14 +50,15 @@ typedef struct lora_heads {
  * call and is also its gradient.  Dimensions past rot_dim are copied.  An
  * output may be its own input (same pointer and strides); other overlaps are
  * not allowed.  Arithmetic in fp32, one rounding to the dtype.
- * Errors: INVALID_ARG, ALIGNMENT, DTYPE, CUDA.  A position outside
+ * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (head_dim over 1024),
+ * CUDA.  A position outside
  * [0, max_pos) leaves its pairs unturned and is recorded (DEVICE_INDEX,
  * detail = row).
  */
 typedef struct lora_rope_args {
     lora_dtype_t dtype;
     int32_t rows;             /* >= 0; 0 is a no-op */
-    int32_t head_dim;         /* multiple of 8 */
+    int32_t head_dim;         /* multiple of 8, up to 1024 */
     int32_t rot_dim;          /* multiple of 16, 16 .. min(head_dim, 2*LORA_ROPE_MAX_PAIRS) */
     int32_t num_q_heads;      /* >= 1 */
     int32_t num_k_heads;      /* >= 0; 0: q only */
