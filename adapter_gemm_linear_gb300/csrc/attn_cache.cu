@@ -4,12 +4,14 @@
 // Both are bound by memory: append reads a value once in its dtype and writes
 // one byte, gather the other way round; a handful of operations a value.
 //
-// Append: one warp holds one 16-token tile of one (page, head) of K or V in
-// registers, the warps of a page share the page's largest magnitude through
-// shared memory, and the values are scaled, rounded and stored from the same
-// registers, so the rows are read once.  Codes that are there already are
-// only touched where the page's scale grows (or, in V's tiles, where they
-// share a 16-byte piece with a new token).
+// Append: one warp takes one 16-token tile of one (page, head) of K or V; the
+// warps of a page share the page's largest magnitude through shared memory.
+// The rows are read twice, for the magnitude and for the codes, the second
+// time from the L1.  The code is kept short and rolled: a warp runs it once,
+// and with everything unrolled and held in registers fetching instructions
+// took most of 65 us for 8192 tokens of 8 heads (now TIMEAPPEND).  Codes that
+// are there already are only touched where the page's scale grows (or, in
+// V's tiles, where they share a 16-byte piece with a new token).
 #include <cuda_runtime.h>
 
 #include "attn_device.cuh"
@@ -84,76 +86,57 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
     return e4m3_pair(v[0] * ratio, v[1] * ratio) | (e4m3_pair(v[2] * ratio, v[3] * ratio) << 16);
 }
 
-// 8 values of 16 (bf16) or 32 (fp32) bytes, as loaded.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float *v) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-};
-template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float *v) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-};
+// Four values.
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+    v[0] = __uint_as_float(w.x << 16);
+    v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(w.y << 16);
+    v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load4(const float *p, float *v) {
+    const float4 w = __ldg(reinterpret_cast<const float4 *>(p));
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+}
 
-// One page of one head, K or V: new tokens [lo, hi) (positions; `slot` is the
-// page's place in the sequence).  `tile` is the warp's 16-token tile of the
-// page.  All threads of the page's warps call it together.
-template <typename T, int D, int FMT, bool IS_V>
-__device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x, const SeqRows &r, int32_t page,
+// One page of one head, K or V: new tokens [lo, hi) (positions).  `tile` is the
+// warp's 16-token tile of the page.  All threads of the page's warps call it
+// together.  A lane's 16-byte piece of codes is 16 dimensions of a token (K),
+// or four dimensions of a token quad (V), the lanes' pieces in memory order.
+template <typename T, int D, int FMT>
+__device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x, bool is_v, const SeqRows &r, int32_t page,
                                             int32_t head, int32_t lo, int32_t hi, int32_t tile, float *unit_amax,
                                             int32_t unit_warps, int lane) {
-    constexpr int N8 = kKvTile * D / 8 / 32;  // 8-value pieces a lane holds
-    uint8_t *pages = IS_V ? b.v_pages : b.k_pages;
-    float *scale_at = (IS_V ? b.v_scales : b.k_scales) + static_cast<int64_t>(page) * b.heads + head;
-    const int32_t p0 = lo & ~(b.page_tokens - 1);      // position of the page's first token
-    const int32_t t0 = p0 + tile * kKvTile;            // and of the tile's
+    constexpr int PIECES = kKvTile * D / 16 / 32;  // of a lane
+    uint8_t *pages = is_v ? b.v_pages : b.k_pages;
+    float *scale_at = (is_v ? b.v_scales : b.k_scales) + static_cast<int64_t>(page) * b.heads + head;
+    const int32_t p0 = lo & ~(b.page_tokens - 1);  // position of the page's first token
+    const int32_t t0 = p0 + tile * kKvTile;        // and of the tile's
     const float old_s = lo > p0 ? *scale_at : 0.0f;
-    const T *src = static_cast<const T *>(x.p) + head * x.head;
-    Raw8<T> raw[N8];
+    // of position p: row r.off + p - (r.len - r.n)
+    const T *src = static_cast<const T *>(x.p) + head * x.head + static_cast<int64_t>(r.off - (r.len - r.n)) * x.row;
+    // the values of piece i, zero where the token is not new: groups of four
+    // along the dimensions, of one token (K) or one of each of four (V)
+    auto token = [&](int i) { return is_v ? (lane & 3) * 4 : ((lane + 32 * i) >> 2) % kKvTile; };
+    auto dim = [&](int i) { return is_v ? ((lane + 32 * i) >> 2) * 4 : ((lane + 32 * i) >> 6) * 64 + (lane & 3) * 16; };
+    auto load = [&](int i, float (&v)[4][4]) {
+        const int32_t pos = t0 + token(i), d = dim(i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int32_t p = is_v ? pos + k : pos;
+            v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.0f;
+            if (p >= lo && p < hi) load4(src + static_cast<int64_t>(p) * x.row + d + (is_v ? 0 : 4 * k), v[k]);
+        }
+    };
     float amax = 0.0f;
+#pragma unroll 2
+    for (int i = 0; i < PIECES; ++i) {
+        float v[4][4];
+        load(i, v);
 #pragma unroll
-    for (int i = 0; i < N8; ++i) {
-        // K: lane = (token, 16-value piece), two pieces of 8 in a row; V: lane
-        // = (8 dimensions, token quad), i over the quad's tokens
-        int32_t t, d;
-        if (IS_V) {
-            t = (lane & 3) * 4 + (i & 3);
-            d = (lane >> 2) * 8 + (i >> 2) * 64;
-        } else {
-            const int32_t c = lane + (i >> 1) * 32;
-            t = c / (D / 16);
-            d = c % (D / 16) * 16 + (i & 1) * 8;
-        }
-        const int32_t pos = t0 + t;
-        if (pos >= lo && pos < hi) {
-            raw[i].load(src + static_cast<int64_t>(r.off + pos - (r.len - r.n)) * x.row + d);
-            float v[8];
-            raw[i].get(v);
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(v[e]));
-        } else {
-            raw[i].zero();
-        }
+            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, finite_abs(v[k][e]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -168,62 +151,37 @@ __device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x,
     const float ratio = s > 0.0f ? __fdiv_rn(old_s, s) : 0.0f;
     __syncwarp();  // every lane has read the old scale
     if (tile == 0 && lane == 0) *scale_at = s;
-    if (t0 >= hi) return;
     const bool grown = s != old_s;
-    uint8_t *out = pages + tile_offset<D>(b, page, head, tile);
-    if (!IS_V) {
+    uint4 *out = reinterpret_cast<uint4 *>(pages + tile_offset<D>(b, page, head, tile));
+#pragma unroll 1
+    for (int i = 0; i < PIECES; ++i) {
+        const int32_t pos = t0 + token(i), tokens = is_v ? 4 : 1;
+        const int32_t older = min(max(lo - pos, 0), tokens);  // of the piece's tokens
+        if (pos >= hi || (older == tokens && !grown)) continue;
+        float v[4][4];
+        load(i, v);
+        if (is_v) {  // codes of four tokens side by side
 #pragma unroll
-        for (int i = 0; i < N8; i += 2) {
-            const int32_t c = lane + (i >> 1) * 32;
-            const int32_t t = c / (D / 16), d = c % (D / 16) * 16;
-            const int32_t pos = t0 + t;
-            uint4 *at = reinterpret_cast<uint4 *>(out + d / 64 * (kKvTile * 64) + t * 64 + d % 64);
-            uint4 w;
-            if (pos >= lo && pos < hi) {
-                float v[16];
-                raw[i].get(v);
-                raw[i + 1].get(v + 8);
-                w = make_uint4(encode4<FMT>(v, s, inv), encode4<FMT>(v + 4, s, inv), encode4<FMT>(v + 8, s, inv),
-                               encode4<FMT>(v + 12, s, inv));
-            } else if (pos < lo && grown) {
-                w = *at;
-                w = make_uint4(rescale4<FMT>(w.x, ratio), rescale4<FMT>(w.y, ratio), rescale4<FMT>(w.z, ratio),
-                               rescale4<FMT>(w.w, ratio));
-            } else {
-                continue;
-            }
-            *at = w;
-        }
-    } else {
-        const int32_t q0 = t0 + (lane & 3) * 4;  // the lane's token quad
-        if (q0 >= hi || (q0 + 4 <= lo && !grown)) return;
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < N8; i += 4) {
-            float v[4][8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) raw[i + j].get(v[j]);
-            const int32_t d = (lane >> 2) * 8 + (i >> 2) * 64;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // four dimensions each
-                uint4 *at = reinterpret_cast<uint4 *>(out + (d / 4 + half) * 64 + (lane & 3) * 16);
-                const bool older = q0 < lo;  // the quad has older tokens
-                uint4 was = make_uint4(0, 0, 0, 0);
-                if (older) was = *at;
-                const uint32_t ow[4] = {was.x, was.y, was.z, was.w};
-                uint32_t nw[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float four[4] = {v[0][half * 4 + e], v[1][half * 4 + e], v[2][half * 4 + e], v[3][half * 4 + e]};
-                    nw[e] = encode4<FMT>(four, s, inv);
-                    if (older) {
-                        const uint32_t keep = q0 + 4 <= lo ? 0xFFFFFFFFu : (1u << (8 * (lo - q0))) - 1u;
-                        const uint32_t o = grown ? rescale4<FMT>(ow[e], ratio) : ow[e];
-                        nw[e] = (o & keep) | (nw[e] & ~keep);
-                    }
+                for (int e = 0; e < k; ++e) {
+                    const float t = v[k][e];
+                    v[k][e] = v[e][k];
+                    v[e][k] = t;
                 }
-                *at = make_uint4(nw[0], nw[1], nw[2], nw[3]);
-            }
         }
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = encode4<FMT>(v[k], s, inv);
+        uint4 *at = out + lane + 32 * i;
+        if (older > 0) {
+            const uint4 was = *at;
+            const uint32_t ow[4] = {was.x, was.y, was.z, was.w};
+            const uint32_t keep = older == tokens ? 0xFFFFFFFFu : (1u << (8 * older)) - 1u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = ((grown ? rescale4<FMT>(ow[k], ratio) : ow[k]) & keep) | (w[k] & ~keep);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -243,7 +201,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     // threads past the last head stay for the block's barriers, without a page
     const bool has_head = hv < 2 * b.heads;
     const int32_t head = hv < b.heads ? hv : hv - b.heads;
-    for_pieces(b, blockIdx.x, b.page_shift, blockIdx.y == 0 && threadIdx.x == 0,
+    for_pieces(b, blockIdx.x, b.page_shift, blockIdx.y == 0 && threadIdx.x < 32,
                [&](int32_t s, const SeqRows &r, int32_t lo, int32_t hi) {
                    const int32_t page = read_page(b, s, lo >> b.page_shift);
                    if (page < 0) return;  // the same for every thread of the block
@@ -254,11 +212,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
                        }
                        return;
                    }
-                   float *am = amax + u * unit_warps;
-                   if (hv < b.heads)
-                       append_page<T, D, FMT, false>(b, k, r, page, head, lo, hi, tile, am, unit_warps, lane);
-                   else
-                       append_page<T, D, FMT, true>(b, v, r, page, head, lo, hi, tile, am, unit_warps, lane);
+                   append_page<T, D, FMT>(b, hv < b.heads ? k : v, hv >= b.heads, r, page, head, lo, hi, tile,
+                                          amax + u * unit_warps, unit_warps, lane);
                });
 }
 
@@ -287,7 +242,7 @@ __global__ void __launch_bounds__(128) kv_gather_kernel(const __grid_constant__ 
     const bool is_v = hv >= b.heads;
     const int32_t head = is_v ? hv - b.heads : hv;
     const HeadsView &x = is_v ? v : k;
-    for_pieces(b, blockIdx.x, 4, blockIdx.y == 0 && threadIdx.x == 0,
+    for_pieces(b, blockIdx.x, 4, blockIdx.y == 0 && threadIdx.x < 32,
                [&](int32_t s, const SeqRows &r, int32_t lo, int32_t hi) {
         const int32_t page = read_page(b, s, lo >> b.page_shift);
         const int32_t t0 = lo & ~(kKvTile - 1);

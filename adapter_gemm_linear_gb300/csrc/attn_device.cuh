@@ -49,41 +49,72 @@ __device__ __forceinline__ int64_t tile_offset(const KvView &b, int32_t page, in
     return ((static_cast<int64_t>(page) * b.heads + head) * (b.page_tokens / kKvTile) + g) * (kKvTile * D);
 }
 
+// The first index in [0, n) at which a non-decreasing `above(index)` holds (n
+// if none), by a whole warp: 32 questions at a time.
+template <typename F>
+__device__ __forceinline__ int32_t warp_search(int32_t n, F above) {
+    const int lane = threadIdx.x & 31;
+    int32_t lo = 0;
+    while (n > 0) {
+        const int32_t step = (n + 31) >> 5;
+        const int32_t end = min(static_cast<int32_t>(lane + 1) * step, n);  // of the lane's part
+        const uint32_t yes = __ballot_sync(0xffffffffu, lane * step < n && above(lo + end - 1));
+        if (yes == 0) return lo + n;
+        const int first = __ffs(yes) - 1;
+        lo += first * step;
+        n = step == 1 ? 0 : min(step, n - first * step);
+    }
+    return lo;
+}
+
 // The new rows of a batch cut where the token position is a multiple of 2^shift
 // (a page, or a tile of 16): unit u < num_seqs is the first, possibly partial,
 // piece of sequence u; unit num_seqs + w holds the pieces that begin within
 // rows [w * 2^shift, (w + 1) * 2^shift), at most one per sequence.  f(s, r, lo,
-// hi) gets the sequence, its rows, and the token positions [lo, hi) of a piece.
+// hi) gets the sequence, its rows, and the token positions [lo, hi) of a piece;
+// whole warps call it, and all of a block's with the same unit take the same
+// steps.  (f stands here once, as its code, run once by each warp, takes longer
+// to fetch than to execute.)
 template <typename F>
 __device__ __forceinline__ void for_pieces(const KvView &b, int32_t unit, int shift, bool report, F f) {
+    const int lane = threadIdx.x & 31;
     const int32_t size = 1 << shift;
-    if (unit < b.num_seqs) {
-        const SeqRows r = read_seq(b, unit, report);
-        if (r.n > 0) {
-            const int32_t lo = r.len - r.n;
-            f(unit, r, lo, min(r.len, ((lo >> shift) + 1) << shift));
-        }
-        return;
-    }
+    const bool head = unit < b.num_seqs;
     const int64_t w0 = static_cast<int64_t>(unit - b.num_seqs) << shift;
     // the first sequence whose rows end past w0 (offsets do not decrease; if
     // they do, the pieces found are some of the valid ones, and the unit of
     // the bad sequence records it)
-    int32_t a = 0, z = b.num_seqs;
-    while (a < z) {
-        const int32_t m = (a + z) >> 1;
-        if (b.offsets[m + 1] > w0) z = m; else a = m + 1;
-    }
-    for (int32_t s = a; s < b.num_seqs; ++s) {
-        if (b.offsets[s] >= w0 + size) break;
-        const SeqRows r = read_seq(b, s, false);
-        if (r.n <= 0) continue;
-        const int32_t first = r.len - r.n;  // position of row off
-        // the least boundary position past the first row's with its row at w0 or later
-        const int64_t from = max(static_cast<int64_t>(first) + 1, first + (w0 - r.off));
-        const int64_t lo = ((from + size - 1) >> shift) << shift;
-        if (lo >= r.len || r.off + (lo - first) >= w0 + size) continue;
-        f(s, r, static_cast<int32_t>(lo), static_cast<int32_t>(min(static_cast<int64_t>(r.len), lo + size)));
+    int32_t s0 = head ? unit : warp_search(b.num_seqs, [&](int32_t m) { return b.offsets[m + 1] > w0; });
+    const int32_t s_end = head ? unit + 1 : b.num_seqs;
+    for (; s0 < s_end; s0 += 32) {
+        // a sequence a lane
+        const int32_t s = s0 + lane;
+        SeqRows r = {0, 0, 0};
+        int64_t lo = 0;
+        bool has = false, past = false;
+        if (s < s_end) {
+            past = !head && b.offsets[s] >= w0 + size;
+            if (!past) r = read_seq(b, s, report && head);
+            if (r.n > 0) {
+                const int32_t first = r.len - r.n;  // position of row off
+                lo = first;
+                if (!head) {  // the least boundary past the first row's position with its row at w0 or later
+                    const int64_t from = max(static_cast<int64_t>(first) + 1, first + (w0 - r.off));
+                    lo = ((from + size - 1) >> shift) << shift;
+                }
+                has = lo < r.len && (head || r.off + (lo - first) < w0 + size);
+            }
+        }
+        for (uint32_t left = __ballot_sync(0xffffffffu, has); left; left &= left - 1) {
+            const int from = __ffs(left) - 1;
+            SeqRows x;
+            x.off = __shfl_sync(0xffffffffu, r.off, from);
+            x.n = __shfl_sync(0xffffffffu, r.n, from);
+            x.len = __shfl_sync(0xffffffffu, r.len, from);
+            const int32_t p = __shfl_sync(0xffffffffu, static_cast<int32_t>(lo), from);
+            f(s0 + from, x, p, static_cast<int32_t>(min(static_cast<int64_t>(x.len), ((static_cast<int64_t>(p) >> shift) + 1) << shift)));
+        }
+        if (__any_sync(0xffffffffu, past)) break;
     }
 }
 
