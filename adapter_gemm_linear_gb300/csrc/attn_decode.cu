@@ -59,12 +59,14 @@ template <typename T, int NT>
 __host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? 4 * NT : 8 * NT; }
 
 // Several small CTAs per SM, so that while one merges its warps or begins an
-// item the others' copies keep the memory busy: three of four consumer warps
-// for up to eight query rows (128 registers a thread), else two of five (168).
-template <int NT>
-__host__ __device__ constexpr int consumers() { return NT == 1 ? 4 : 5; }
-template <int NT>
-__host__ __device__ constexpr int ctas_per_sm() { return NT == 1 ? 3 : 2; }
+// item the others' copies keep the memory busy; as many warps as the registers
+// allow: three of four consumers at 128 a thread for one column tile of
+// heads of 128 (and two tiles of heads of 64), two of five at 168 for two,
+// four of four at 96 for one of heads of 64.
+template <int D, int NT>
+__host__ __device__ constexpr int consumers() { return D == 128 && NT == 2 ? 5 : 4; }
+template <int D, int NT>
+__host__ __device__ constexpr int ctas_per_sm() { return D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3); }
 
 // What the looking-up warp says of a tile: where its codes are (in k_pages and
 // in v_pages; < 0: not there, zeros), and K's scale, V's, its log2 and reciprocal.
@@ -79,9 +81,9 @@ constexpr int kBatch = 32, kBatches = 8;  // tiles looked up at once, and ahead
 
 template <int D, int NT>
 struct DecodeSmem {
-    static constexpr int kWarps = consumers<NT>();
+    static constexpr int kWarps = consumers<D, NT>();
     static constexpr int kPieces = D / 32;           // 16-byte pieces a lane takes of a tile of K (and of V)
-    static constexpr int kDepth = D == 128 ? 3 : 6;  // tiles a warp fetches ahead
+    static constexpr int kDepth = D == 128 ? 3 : NT == 1 ? 4 : 5;  // tiles a warp fetches ahead
     uint4 codes[kWarps][kDepth][2][kPieces][32];     // [.., K or V, piece, lane]
     float o[kWarps][8 * NT][D + 4];                  // merge: padded against bank conflicts
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
@@ -185,13 +187,13 @@ struct Walk {
 // The query rows [row_tile * tile_rows, ...) of (sequence, key/value head): row r is query r / group of the
 // sequence, query head head * group + r % group.
 template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__((consumers<NT>() + 1) * 32, ctas_per_sm<NT>()) attn_decode_kernel(const __grid_constant__ AttnView a) {
+__global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, NT>()) attn_decode_kernel(const __grid_constant__ AttnView a) {
     extern __shared__ __align__(128) unsigned char raw[];
     DecodeSmem<D, NT> &sm = *reinterpret_cast<DecodeSmem<D, NT> *>(raw);
     using Smem = DecodeSmem<D, NT>;
     constexpr bool SPLIT = sizeof(T) == 4;  // fp32: operands in two f16 parts
     constexpr int ROWS = tile_rows<T, NT>();
-    constexpr int kWarps = consumers<NT>(), kThreads = (kWarps + 1) * 32;
+    constexpr int kWarps = consumers<D, NT>(), kThreads = (kWarps + 1) * 32;
     constexpr int RT = SPLIT ? 1 : NT;  // column tiles of rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView &b = a.kv;
@@ -632,11 +634,11 @@ template <typename T, int D, int FMT, int NT>
 cudaError_t decode_tiles(const AttnView &v, cudaStream_t stream) {
     static uint64_t ctx[128] = {};
     constexpr int smem = static_cast<int>(sizeof(DecodeSmem<D, NT>));
-    static_assert((smem + 1024) * ctas_per_sm<NT>() <= 228 * 1024, "the shared memory of an SM");
+    static_assert((smem + 1024) * ctas_per_sm<D, NT>() <= 228 * 1024, "the shared memory of an SM");
     cudaError_t e = allow_smem(attn_decode_kernel<T, D, FMT, NT>, smem, ctx);
     if (e != cudaSuccess) return e;
-    const int grid = device_sm_count() * ctas_per_sm<NT>();
-    attn_decode_kernel<T, D, FMT, NT><<<grid, (consumers<NT>() + 1) * 32, smem, stream>>>(v);
+    const int grid = device_sm_count() * ctas_per_sm<D, NT>();
+    attn_decode_kernel<T, D, FMT, NT><<<grid, (consumers<D, NT>() + 1) * 32, smem, stream>>>(v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = launch_join<T, D, tile_rows<T, NT>()>(v, grid, kSlotRows, stream);
@@ -655,7 +657,8 @@ cudaError_t decode_typed(const AttnView &v, cudaStream_t stream) {
 }  // namespace
 
 size_t decode_workspace_bytes(int head_dim) {
-    return split_workspace_bytes(device_sm_count() * ctas_per_sm<1>(), kSlotRows, head_dim);
+    constexpr int kMostCtas = 4;  // per SM
+    return split_workspace_bytes(device_sm_count() * kMostCtas, kSlotRows, head_dim);
 }
 
 cudaError_t launch_attn_decode(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,
