@@ -169,6 +169,19 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// 32 bytes to global memory, a whole sector at once where the address is a
+// multiple of 32 (every lane writes a row of its own).
+__device__ __forceinline__ void store_32(void *p, const uint32_t (&w)[8]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // Two fp32 values at once.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
@@ -577,17 +590,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 if (rt >= rows) continue;
                 if (whole) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        __nv_bfloat162 h[4];
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t h[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            h[k] = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + 32 * i + e) = *reinterpret_cast<uint4 *>(h);
+                        for (int k = 0; k < 8; ++k) {
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                            h[k] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
+                        store_32(dst + 32 * i + e, h);
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(part + rt * D + 32 * i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 32; e += 8) {
+                        const uint32_t w[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                        store_32(part + rt * D + 32 * i + e, w);
+                    }
                 }
             }
             tc_fence_before_sync();
