@@ -233,7 +233,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *v) {
 // One warp per (16-token tile, head, K or V).  grid.x: pieces of the rows cut
 // at multiples of 16 tokens; grid.y: groups of four (K or V, head).
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(128) kv_gather_kernel(const __grid_constant__ KvView b,
+__global__ void __launch_bounds__(128, 8) kv_gather_kernel(const __grid_constant__ KvView b,
                                                         const __grid_constant__ HeadsView k,
                                                         const __grid_constant__ HeadsView v) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

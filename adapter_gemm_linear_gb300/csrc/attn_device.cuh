@@ -27,7 +27,7 @@ __device__ __forceinline__ SeqRows read_seq(const KvView &b, int32_t s, bool rep
         if (report) record_error(b.status, kDevBadSegment, static_cast<uint32_t>(s));
         r.off = r.n = r.len = 0;
     }
-    if (r.len < 0 || r.len > static_cast<int64_t>(b.max_pages) * b.page_tokens) {
+    if (r.len < 0 || r.len > (1 << 30) || r.len > static_cast<int64_t>(b.max_pages) * b.page_tokens) {
         if (report) record_error(b.status, kDevBadBlock, static_cast<uint32_t>(s));
         r.n = r.len = 0;
     }

@@ -5,7 +5,8 @@
  *
  * The conventions of lora.h hold for every entry point: plain C, the caller
  * owns all device memory, work is ordered on `stream`, device pointers are
- * 16-byte aligned, errors found on the host leave all state unchanged, and
+ * 16-byte aligned (arrays of lengths, offsets, positions and page numbers 4-byte
+ * aligned), errors found on the host leave all state unchanged, and
  * errors found by kernels are recorded in the status word that
  * lora_get_device_status() reads.  No call allocates device memory, waits
  * for the device or reads device memory from the host, so every call can be
@@ -120,8 +121,8 @@ size_t lora_kv_pages_bytes(int32_t num_pages, int32_t num_heads, int32_t head_di
  * A sequence of length 0 is padding (its rows stand for no token); one
  * without rows is passed over.  Recorded by the kernels, the sequence then
  * skipped: offsets not within [0, rows] or decreasing, more rows than
- * tokens (SEGMENTS, detail = s); a length below 0 or past max_pages pages
- * (DEVICE_INDEX, detail = s).  A table entry outside [0, num_pages) that is
+ * tokens (SEGMENTS, detail = s); a length below 0, past max_pages pages or
+ * past 2^30 (DEVICE_INDEX, detail = s).  A table entry outside [0, num_pages) that is
  * needed is recorded (DEVICE_INDEX, detail = s); its tokens are not written,
  * and read as zeros.
  */
