@@ -16,7 +16,6 @@ pages that hold its tokens.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import struct
 from typing import Optional, Sequence, Tuple
@@ -43,6 +42,7 @@ assert _HEADS.size == ctypes.sizeof(_lib.Heads) and _ATTENTION_ARGS.size == ctyp
 _DTYPES = {torch.bfloat16: _lib.LORA_BF16, torch.float32: _lib.LORA_FP32}
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _heads(t: torch.Tensor, name: str, device: int) -> Tuple[int, int, int]:
@@ -70,28 +70,20 @@ def _call(status: int, what: str) -> None:
         raise LoraError(status, what)
 
 
-def _on_stream(f):
-    """f with the keyword ``stream``: on that stream (so that outputs come from
-    its memory and the caller's tensors are kept until it has passed the call)
-    and its device; without, on the current stream of the tensors' device."""
-
-    @functools.wraps(f)
-    def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
-        if stream is None:
-            device = args[0].device.index if isinstance(args[0], KvCache) else args[0].get_device()
-            if device < 0 or device == torch.cuda.current_device():
-                return f(*args, **kw)
-            with torch.cuda.device(device):
-                return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            result = f(*args, **kw)
-        for t in list(args) + list(kw.values()):
-            for x in (t.k_pages, t.v_pages, t.k_scales, t.v_scales) if isinstance(t, KvCache) else (t,):
-                if isinstance(x, torch.Tensor):
-                    x.record_stream(stream)
-        return result
-
-    return call
+def _elsewhere(f, device: int, stream: Optional[torch.cuda.Stream], args, **kw):
+    """f(*args, **kw) with `device` current and, if given, on `stream`: outputs
+    come from that stream's memory, and the caller's tensors are kept until it
+    has passed the call."""
+    if stream is None:
+        with torch.cuda.device(device):
+            return f(*args, **kw)
+    with torch.cuda.stream(stream):
+        result = f(*args, **kw)
+    for t in list(args) + list(kw.values()):
+        for x in (t.k_pages, t.v_pages, t.k_scales, t.v_scales) if isinstance(t, KvCache) else (t,):
+            if isinstance(x, torch.Tensor):
+                x.record_stream(stream)
+    return result
 
 
 def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
@@ -102,11 +94,10 @@ def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"
     return angle.cos().float(), angle.sin().float()
 
 
-@_on_stream
 def rope(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor,
          axes: Optional[Sequence[int]] = None, interleaved: bool = False, inverse: bool = False,
-         q_out: Optional[torch.Tensor] = None,
-         k_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+         stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """lora_rope: q [rows, q_heads, D] and k [rows, k_heads, D] (or None)
     turned by their rows' positions -> (q_out, k_out), new tensors unless
     given (``q_out=q`` works in place).
@@ -117,6 +108,9 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: tor
     ``inverse`` turns the other way: the gradient of the call, or its undoing.
     ``stream``: launch there instead of on the current stream."""
     device, shape = q.get_device(), q.shape
+    if stream is not None or (device >= 0 and device != _current_device()):
+        return _elsewhere(rope, device, stream, (q, k, cos, sin, positions), axes=axes, interleaved=interleaved,
+                          inverse=inverse, q_out=q_out, k_out=k_out)
     if len(shape) != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
     rows, q_heads, D = shape
@@ -197,6 +191,7 @@ class KvCache:
         self.k_scales = tensor(k_scales, tiles[:2], torch.float32, "k_scales")
         self.v_scales = tensor(v_scales, tiles[:2], torch.float32, "v_scales")
         self.device = self.k_pages.device
+        self._device = self.k_pages.get_device()
         self._workspace = {}  # bytes of an attention call's workspace, by what they depend on
         self._desc = _lib.KvCacheDesc(code, self.num_pages, self.num_heads, D, self.page_tokens,
                                       self.k_pages.data_ptr(), self.v_pages.data_ptr(), self.k_scales.data_ptr(),
@@ -205,7 +200,7 @@ class KvCache:
 
     def _batch(self, rows: int, block_table: torch.Tensor, seq_lens: torch.Tensor,
                offsets: Optional[torch.Tensor]) -> bytes:
-        device, S = self.device.index, seq_lens.shape[0]
+        device, S = self._device, seq_lens.shape[0]
         table = block_table.shape
         if len(table) != 2 or table[0] != S:
             raise ValueError(f"block_table must be [{S}, max_pages]")
@@ -216,33 +211,39 @@ class KvCache:
                            _index(block_table, "block_table", device), table[1])
 
     def _check(self, t: torch.Tensor, name: str) -> None:
-        if t.dim() != 3 or t.shape[1:] != (self.num_heads, self.head_dim):
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != self.num_heads or shape[2] != self.head_dim:
             raise ValueError(f"{name} must be [rows, {self.num_heads}, {self.head_dim}]")
 
-    @_on_stream
     def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
-               offsets: Optional[torch.Tensor] = None) -> None:
+               offsets: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
         """lora_kv_append: quantise the rows' k and v [rows, num_heads, head_dim]
         into their sequences' pages, as the last tokens of seq_lens tokens.
         ``stream``: launch there instead of on the current stream."""
+        device = self._device
+        if stream is not None or device != _current_device():
+            return _elsewhere(KvCache.append, device, stream, (self, k, v, block_table, seq_lens, offsets))
         self._check(k, "k")
         self._check(v, "v")
         if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
             raise ValueError("k and v must have the same dtype and rows")
-        device = self.device.index
         _call(_lib.lib().lora_kv_append(
             self._ref, self._batch(k.shape[0], block_table, seq_lens, offsets), _dtype(k.dtype),
             _HEADS.pack(*_heads(k, "k", device)), _HEADS.pack(*_heads(v, "v", device)), _current_stream(device)),
             "lora_kv_append")
 
-    @_on_stream
     def gather(self, block_table: torch.Tensor, seq_lens: torch.Tensor, offsets: Optional[torch.Tensor] = None,
                rows: Optional[int] = None, dtype: torch.dtype = torch.bfloat16, k_out: Optional[torch.Tensor] = None,
-               v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+               v_out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """lora_kv_gather: the rows' keys and values, dequantised -> (k, v)
         [rows, num_heads, head_dim], new tensors of ``dtype`` unless given.
         ``rows`` (needed with offsets and no k_out) is offsets' last value.
         ``stream``: launch there instead of on the current stream."""
+        device = self._device
+        if stream is not None or device != _current_device():
+            return _elsewhere(KvCache.gather, device, stream, (self, block_table, seq_lens, offsets), rows=rows,
+                              dtype=dtype, k_out=k_out, v_out=v_out)
         if k_out is not None:
             self._check(k_out, "k_out")
             rows, dtype = k_out.shape[0], k_out.dtype
@@ -250,7 +251,7 @@ class KvCache:
             if offsets is not None:
                 raise ValueError("give rows (offsets' last value), or k_out and v_out")
             rows = seq_lens.shape[0]
-        shape, device = (rows, self.num_heads, self.head_dim), self.device.index
+        shape = (rows, self.num_heads, self.head_dim)
         if k_out is None:
             k_out = torch.empty(shape, dtype=dtype, device=self.device)
         if v_out is None:
@@ -263,12 +264,11 @@ class KvCache:
             _current_stream(device)), "lora_kv_gather")
         return k_out, v_out
 
-    @_on_stream
     def attention(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                   offsets: Optional[torch.Tensor] = None, max_queries: Optional[int] = None, causal: bool = True,
                   window: int = 0, scale: Optional[float] = None, return_lse: bool = False,
                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                  workspace: Optional[torch.Tensor] = None):
+                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
         """lora_kv_attention: softmax attention of q [rows, q_heads, head_dim]
         over the sequences' cached keys and values -> out like q (and, with
         ``return_lse`` or ``lse`` given, the float32 [rows, q_heads] log of the
@@ -278,7 +278,11 @@ class KvCache:
         offsets, else all rows); ``window`` > 0 limits a query to the last
         ``window`` positions up to its own; ``scale`` defaults to head_dim^-0.5.
         ``stream``: launch there instead of on the current stream."""
-        shape, device = q.shape, self.device.index
+        shape, device = q.shape, self._device
+        if stream is not None or device != _current_device():
+            return _elsewhere(KvCache.attention, device, stream, (self, q, block_table, seq_lens, offsets),
+                              max_queries=max_queries, causal=causal, window=window, scale=scale,
+                              return_lse=return_lse, out=out, lse=lse, workspace=workspace)
         if len(shape) != 3 or shape[2] != self.head_dim:
             raise ValueError(f"q must be [rows, q_heads, {self.head_dim}]")
         rows, Hq, _ = shape
