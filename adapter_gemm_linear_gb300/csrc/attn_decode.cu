@@ -199,6 +199,10 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     const KvView &b = a.kv;
     JoinEntry *joins = join_entries(a, gridDim.x, kSlotRows, D);
 
+    // the joining kernel may come in as soon as there is room beside CTAs that
+    // run or have none of the work; it waits for this one's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
     // ---- the plan: where this CTA's range of units begins
     if (threadIdx.x < kBatches) {
         mbar_init(&sm.full[threadIdx.x], 1);

@@ -348,6 +348,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         if (!mbar_try_wait(bar, parity) && !*dead && !wait_clocks(bar, parity)) *dead = site;
     };
 
+    // the joining kernel may come in as soon as there is room beside CTAs that
+    // run or have none of the work; it waits for this one's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
     // ---- set-up and plan
     if (threadIdx.x == 0) {
         for (int i = 0; i < kItemRing; ++i) {
