@@ -645,7 +645,7 @@ cudaError_t decode_tiles(const AttnView &v, cudaStream_t stream) {
     attn_decode_kernel<T, D, FMT, NT><<<grid, (consumers<D, NT>() + 1) * 32, smem, stream>>>(v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_join<T, D, tile_rows<T, NT>()>(v, grid, kSlotRows, stream);
+    e = launch_join<T, D, tile_rows<T, NT>(), 4>(v, grid, kSlotRows, stream);
     count_launches(2);
     return e;
 }

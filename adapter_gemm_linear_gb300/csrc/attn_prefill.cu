@@ -1028,7 +1028,7 @@ cudaError_t prefill_typed(const AttnView &v, cudaStream_t stream) {
     attn_prefill_kernel<D, FMT><<<grid, kPreThreads, smem, stream>>>(v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_join<__nv_bfloat16, D, kRows>(v, grid, kRows, stream);
+    e = launch_join<__nv_bfloat16, D, kRows, 1>(v, grid, kRows, stream);
     count_launches(2);
     return e;
 }
