@@ -5,13 +5,17 @@
 // one byte, gather the other way round; a handful of operations a value.
 //
 // Append: one warp takes one 16-token tile of one (page, head) of K or V; the
-// warps of a page share the page's largest magnitude through shared memory.
-// The rows are read twice, for the magnitude and for the codes, the second
-// time from the L1.  The code is kept short and rolled: a warp runs it once,
-// and with everything unrolled and held in registers fetching instructions
-// took most of 65 us for 8192 tokens of 8 heads (now TIMEAPPEND).  Codes that
-// are there already are only touched where the page's scale grows (or, in
-// V's tiles, where they share a 16-byte piece with a new token).
+// warps of a page share the page's largest magnitude through shared memory, and
+// hold their rows as they were read until the scale is known.  Codes that are
+// there already are only touched where the page's scale grows (or, in V's
+// tiles, where they share a 16-byte piece with a new token).
+// What bounds it is the chain of dependent reads (the sequence, its page, the
+// rows), which as many warps as possible have to cover, and the instructions a
+// value (about ten): magnitudes are compared two at a time, and an int8 code
+// takes one fused multiply-add that rounds and one that checks.  8192 tokens of
+// 8 heads of 128 take 22 us (50 MB), one token of each of 256 sequences 15.5.
+// With 128 registers a thread instead of 80: 24 and 16.4; with the rows read
+// twice by rolled code that rounds with conversion instructions: 31.5 and 18.4.
 #include <cuda_runtime.h>
 
 #include "attn_device.cuh"
@@ -40,16 +44,16 @@ __device__ __forceinline__ float scale_for(float a) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// x / s rounded to the nearest code, as int8 bits.  x * inv (inv = 1/s
-// rounded) is within 3e-5 of x / s for quotients up to 128, so the two round
-// alike unless the product lies nearer than that to a half; there the
-// quotient itself decides.
-__device__ __forceinline__ int32_t int8_code(float x, float s, float inv) {
-    const float y = x * inv;
-    if (!(y == y)) return 0;
-    float r = rintf(y);
-    if (fabsf(fabsf(y - r) - 0.5f) < 1e-4f) r = rintf(__fdiv_rn(x, s));
-    return static_cast<int32_t>(fminf(fmaxf(r, -127.0f), 127.0f));
+// Adding it rounds a float below 2^22 to an integer (ties to even), whose low
+// byte is the sum's: one add where a rounding and a conversion instruction
+// would take eight times as long each.
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+
+// The low bytes of four floats, in order.
+__device__ __forceinline__ uint32_t low_bytes(const float (&t)[4]) {
+    const uint32_t a = __byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(t[2]), __float_as_uint(t[3]), 0x0040);
+    return __byte_perm(a, b, 0x5410);
 }
 
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
@@ -58,15 +62,34 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     return r;
 }
 
-// Four values to four codes, low byte first.
+// Four values to int8 codes by the quotients themselves; NaN becomes 0.
+__device__ __noinline__ uint32_t int8_codes_near(float4 x, float s) {
+    float t[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float q = __fdiv_rn(t[i], s);
+        t[i] = kRound + (q == q ? fminf(fmaxf(rintf(q), -127.0f), 127.0f) : 0.0f);
+    }
+    return low_bytes(t);
+}
+
+// Four values to four codes, low byte first; inv = 1/s, rounded.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(const float *x, float s, float inv) {
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], float s, float inv) {
     if (!(s > 0.0f)) return 0u;
     if (FMT == LORA_KV_INT8) {
-        uint32_t w = 0;
+        // x * inv is within 3e-5 of x / s for quotients up to 128, so the two
+        // round alike unless the product lies nearer than that to a half; there
+        // (and where x is not finite) the quotients decide
+        float t[4];
+        bool sure = true;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w |= (static_cast<uint32_t>(int8_code(x[i], s, inv)) & 0xFFu) << (8 * i);
-        return w;
+        for (int i = 0; i < 4; ++i) {
+            t[i] = fmaf(x[i], inv, kRound);
+            sure = sure && fabsf(fmaf(x[i], inv, kRound - t[i])) < 0.4999f;
+        }
+        if (!sure) return int8_codes_near(make_float4(x[0], x[1], x[2], x[3]), s);
+        return low_bytes(t);
     }
     return e4m3_pair(x[0] * inv, x[1] * inv) | (e4m3_pair(x[2] * inv, x[3] * inv) << 16);
 }
@@ -77,39 +100,75 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
     float v[4];
     codes_to_float<FMT>(w, v);
     if (FMT == LORA_KV_INT8) {
-        uint32_t r = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r |= (static_cast<uint32_t>(static_cast<int32_t>(rintf(v[i] * ratio))) & 0xFFu) << (8 * i);
-        return r;
+        for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(__fmul_rn(v[i], ratio), kRound);
+        return low_bytes(v);
     }
     return e4m3_pair(v[0] * ratio, v[1] * ratio) | (e4m3_pair(v[2] * ratio, v[3] * ratio) << 16);
 }
 
-// Four values.
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-    v[0] = __uint_as_float(w.x << 16);
-    v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(w.y << 16);
-    v[3] = __uint_as_float(w.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void load4(const float *p, float *v) {
-    const float4 w = __ldg(reinterpret_cast<const float4 *>(p));
-    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-}
+// A lane's piece as it was read: [four groups][four values].
+template <typename T>
+struct Raw;
+
+template <>
+struct Raw<__nv_bfloat16> {
+    uint32_t w[4][2];
+    __device__ __forceinline__ void load_row(int k, const __nv_bfloat16 *p) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[k][0] = x.x; w[k][1] = x.y;
+    }
+    __device__ __forceinline__ void load_all(const __nv_bfloat16 *p) {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + k / 2);
+            w[k][0] = x.x; w[k][1] = x.y; w[k + 1][0] = x.z; w[k + 1][1] = x.w;
+        }
+    }
+    __device__ __forceinline__ void clear(int k) { w[k][0] = w[k][1] = 0u; }
+    __device__ __forceinline__ float value(int k, int e) const {
+        return __uint_as_float(e & 1 ? w[k][e >> 1] & 0xFFFF0000u : w[k][e >> 1] << 16);
+    }
+    // the largest magnitude, infinities among them; NaN does not count
+    __device__ __forceinline__ float largest() const {
+        __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[0][0]));
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i >> 1][i & 1])));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+};
+
+template <>
+struct Raw<float> {
+    float4 w[4];
+    __device__ __forceinline__ void load_row(int k, const float *p) { w[k] = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void load_all(const float *p) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load_row(k, p + 4 * k);
+    }
+    __device__ __forceinline__ void clear(int k) { w[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ float value(int k, int e) const { return e == 0 ? w[k].x : e == 1 ? w[k].y : e == 2 ? w[k].z : w[k].w; }
+    __device__ __forceinline__ float largest() const {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(value(i >> 2, i & 3)));
+        return m;
+    }
+};
 
 // One page of one head, K or V: new tokens [lo, hi) (positions).  `tile` is the
 // warp's 16-token tile of the page.  All threads of the page's warps call it
 // together.  A lane's 16-byte piece of codes is 16 dimensions of a token (K),
 // or four dimensions of a token quad (V), the lanes' pieces in memory order.
-template <typename T, int D, int FMT>
-__device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x, bool is_v, const SeqRows &r, int32_t page,
-                                            int32_t head, int32_t lo, int32_t hi, int32_t tile, float *unit_amax,
-                                            int32_t unit_warps, int lane) {
+template <typename T, int D, int FMT, bool IS_V>
+__device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x, const SeqRows &r, int32_t page, int32_t head,
+                                            int32_t lo, int32_t hi, int32_t tile, float *unit_amax, int32_t unit_warps,
+                                            int lane) {
     constexpr int PIECES = kKvTile * D / 16 / 32;  // of a lane
-    uint8_t *pages = is_v ? b.v_pages : b.k_pages;
-    float *scale_at = (is_v ? b.v_scales : b.k_scales) + static_cast<int64_t>(page) * b.heads + head;
+    constexpr int TOKENS = IS_V ? 4 : 1;           // of a piece
+    uint8_t *pages = IS_V ? b.v_pages : b.k_pages;
+    float *scale_at = (IS_V ? b.v_scales : b.k_scales) + static_cast<int64_t>(page) * b.heads + head;
+    uint4 *out = reinterpret_cast<uint4 *>(pages + tile_offset<D>(b, page, head, tile)) + lane;
     const int32_t p0 = lo & ~(b.page_tokens - 1);  // position of the page's first token
     const int32_t t0 = p0 + tile * kKvTile;        // and of the tile's
     const float old_s = lo > p0 ? *scale_at : 0.0f;
@@ -117,26 +176,45 @@ __device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x,
     const T *src = static_cast<const T *>(x.p) + head * x.head + static_cast<int64_t>(r.off - (r.len - r.n)) * x.row;
     // the values of piece i, zero where the token is not new: groups of four
     // along the dimensions, of one token (K) or one of each of four (V)
-    auto token = [&](int i) { return is_v ? (lane & 3) * 4 : ((lane + 32 * i) >> 2) % kKvTile; };
-    auto dim = [&](int i) { return is_v ? ((lane + 32 * i) >> 2) * 4 : ((lane + 32 * i) >> 6) * 64 + (lane & 3) * 16; };
-    auto load = [&](int i, float (&v)[4][4]) {
-        const int32_t pos = t0 + token(i), d = dim(i);
+    auto token = [&](int i) { return IS_V ? (lane & 3) * 4 : ((lane + 32 * i) >> 2) % kKvTile; };
+    auto dim = [&](int i) { return IS_V ? ((lane + 32 * i) >> 2) * 4 : ((lane + 32 * i) >> 6) * 64 + (lane & 3) * 16; };
+    auto load = [&](int i, Raw<T> &v) {
+        const int32_t pos = t0 + token(i);
+        const T *at = src + static_cast<int64_t>(pos) * x.row + dim(i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int32_t p = is_v ? pos + k : pos;
-            v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.0f;
-            if (p >= lo && p < hi) load4(src + static_cast<int64_t>(p) * x.row + d + (is_v ? 0 : 4 * k), v[k]);
+        for (int k = 0; k < 4; ++k) v.clear(k);
+        if (IS_V) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (pos + k >= lo && pos + k < hi) v.load_row(k, at + k * x.row);
+        } else if (pos >= lo && pos < hi) {
+            v.load_all(at);
         }
     };
-    float amax = 0.0f;
-#pragma unroll 2
+    // tokens of piece i that are there already
+    auto older_of = [&](int i) { return min(max(lo - (t0 + token(i)), 0), TOKENS); };
+    Raw<T> v[PIECES];
+    uint4 was[IS_V ? PIECES : 1];  // the codes beside which new ones go
+#pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        float v[4][4];
-        load(i, v);
+        if (IS_V && lo > t0) {
+            const int32_t older = older_of(i);
+            if (older > 0 && older < TOKENS) was[i] = out[32 * i];
+        }
+        load(i, v[i]);
+    }
+    float amax = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+    for (int i = 0; i < PIECES; ++i) amax = fmaxf(amax, v[i].largest());
+    if (__any_sync(0xffffffffu, amax == INFINITY)) {  // again, without the infinities
+        amax = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < PIECES; ++i) {
+            Raw<T> y;
+            load(i, y);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, finite_abs(v[k][e]));
+            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(y.value(e >> 2, e & 3)));
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -152,36 +230,35 @@ __device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x,
     __syncwarp();  // every lane has read the old scale
     if (tile == 0 && lane == 0) *scale_at = s;
     const bool grown = s != old_s;
-    uint4 *out = reinterpret_cast<uint4 *>(pages + tile_offset<D>(b, page, head, tile));
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int32_t pos = t0 + token(i), tokens = is_v ? 4 : 1;
-        const int32_t older = min(max(lo - pos, 0), tokens);  // of the piece's tokens
-        if (pos >= hi || (older == tokens && !grown)) continue;
-        float v[4][4];
-        load(i, v);
-        if (is_v) {  // codes of four tokens side by side
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int e = 0; e < k; ++e) {
-                    const float t = v[k][e];
-                    v[k][e] = v[e][k];
-                    v[e][k] = t;
-                }
-        }
+        const int32_t older = older_of(i);
+        if (t0 + token(i) >= hi || older == TOKENS) continue;
         uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = encode4<FMT>(v[k], s, inv);
-        uint4 *at = out + lane + 32 * i;
-        if (older > 0) {
-            const uint4 was = *at;
-            const uint32_t ow[4] = {was.x, was.y, was.z, was.w};
-            const uint32_t keep = older == tokens ? 0xFFFFFFFFu : (1u << (8 * older)) - 1u;
+        for (int k = 0; k < 4; ++k) {
+            float y[4];  // V: four tokens side by side
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = IS_V ? v[i].value(e, k) : v[i].value(k, e);
+            w[k] = encode4<FMT>(y, s, inv);
+        }
+        if (IS_V && older > 0) {
+            const uint32_t ow[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
+            const uint32_t keep = (1u << (8 * older)) - 1u;
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = ((grown ? rescale4<FMT>(ow[k], ratio) : ow[k]) & keep) | (w[k] & ~keep);
         }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        out[32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (grown && lo > t0) {  // the pieces of older tokens alone
+#pragma unroll 1
+        for (int i = 0; i < PIECES; ++i) {
+            if (older_of(i) < TOKENS) continue;
+            uint4 *at = out + 32 * i;
+            const uint4 y = *at;
+            *at = make_uint4(rescale4<FMT>(y.x, ratio), rescale4<FMT>(y.y, ratio), rescale4<FMT>(y.z, ratio),
+                             rescale4<FMT>(y.w, ratio));
+        }
     }
 }
 
@@ -189,7 +266,7 @@ __device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x,
 // piece as fit four warps, eight for pages of 128).  grid.x: pieces of the
 // new rows; grid.y: groups of (K or V, head).
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvView b,
+__global__ void __launch_bounds__(256, 3) kv_append_kernel(const __grid_constant__ KvView b,
                                                         const __grid_constant__ HeadsView k,
                                                         const __grid_constant__ HeadsView v) {
     __shared__ float amax[8];
@@ -212,8 +289,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
                        }
                        return;
                    }
-                   append_page<T, D, FMT>(b, hv < b.heads ? k : v, hv >= b.heads, r, page, head, lo, hi, tile,
-                                          amax + u * unit_warps, unit_warps, lane);
+                   float *const unit_amax = amax + u * unit_warps;
+                   if (hv < b.heads) append_page<T, D, FMT, false>(b, k, r, page, head, lo, hi, tile, unit_amax, unit_warps, lane);
+                   else append_page<T, D, FMT, true>(b, v, r, page, head, lo, hi, tile, unit_amax, unit_warps, lane);
                });
 }
 

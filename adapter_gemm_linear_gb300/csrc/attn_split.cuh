@@ -74,7 +74,7 @@ __device__ __forceinline__ void add_scaled(float4 &v, float &L, float f, const f
 // results of a row go to G groups of threads in turn, which take up to eight at
 // a time, so that all loads of an item in up to 8 G CTAs are in flight together:
 // what bounds the kernel is their latency.  (Both kernels for one sequence of
-// 4096 tokens, 64 heads on 8, each of these in 32 CTAs: 14.3 us with G = 4,
+// 2000 tokens, 32 heads on 8, each of these in 16 CTAs: 14.3 us with G = 4,
 // 18.4 with 1, 16.4 with 8.)  Every sum's order is fixed.
 // The kernel also gives the rows of padding and skipped sequences their zeros,
 // and records the malformed ones.
