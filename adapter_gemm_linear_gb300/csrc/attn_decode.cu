@@ -472,7 +472,8 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     const float sum = SPLIT ? fmaf(s[NT - 1][e], 1.0f / kLoScale, s[0][e]) : s[u][e];
                     z[u][e] = fmaf(sum, ks * cr[u][e & 1], lv);
                 }
-            if (key0 < all_lo || key0 + kKvTile > all_hi) {
+            const bool edge = key0 < all_lo || key0 + kKvTile > all_hi;  // some row does not see some key
+            if (edge) {
 #pragma unroll
                 for (int u = 0; u < RT; ++u)
 #pragma unroll
@@ -538,6 +539,46 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             const int past = FMT == LORA_KV_E4M3 ? key0 + 4 * tig + 4 - r.len : 0;
             const uint32_t keep = past <= 0 ? 0xFFFFFFFFu : past >= 4 ? 0u : 0xFFFFFFFFu >> (8 * past);
             landed();
+            if (FMT == LORA_KV_E4M3 && edge) {
+                // p = 0 does not keep a NaN of V from a row that does not see its
+                // token: such codes become 0, and the rows that do see them get
+                // the NaN from here
+                uint32_t some = 0;
+#pragma unroll
+                for (int jj = 0; jj < D / 32; ++jj) {
+                    const uint4 w = sm.codes[warp][slot][1][jj][lane];
+                    some |= e4m3_nan(w.x & keep) | e4m3_nan(w.y & keep) | e4m3_nan(w.z & keep) | e4m3_nan(w.w & keep);
+                }
+                if (__builtin_expect(__any_sync(0xffffffffu, some != 0), 0)) {
+                    uint32_t seen[RT][2];  // the tile's tokens that the row sees, a bit each
+#pragma unroll
+                    for (int u = 0; u < RT; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int from = min(max(kmin[u][i] - key0, 0), 16), to = min(max(kmax[u][i] - key0, 0), 16);
+                            seen[u][i] = ((1u << to) - 1u) & ~((1u << from) - 1u);
+                        }
+#pragma unroll
+                    for (int jj = 0; jj < D / 32; ++jj) {
+                        const uint4 w = sm.codes[warp][slot][1][jj][lane];
+                        uint32_t ws[4] = {w.x & keep, w.y & keep, w.z & keep, w.w & keep};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // dimension q of the piece's four
+                            const uint32_t nan = e4m3_nan(ws[q]);
+                            uint32_t tokens = ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (4 * tig);
+                            tokens |= __shfl_xor_sync(0xffffffffu, tokens, 1);
+                            tokens |= __shfl_xor_sync(0xffffffffu, tokens, 2);
+#pragma unroll
+                            for (int u = 0; u < RT; ++u)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (tokens & seen[u][i]) o[u][2 * jj + (q >> 1)][i + 2 * (q & 1)] = __int_as_float(0x7FFFFFFF);
+                            ws[q] = e4m3_without(ws[q], nan);
+                        }
+                        sm.codes[warp][slot][1][jj][lane] = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+                    }
+                }
+            }
 #pragma unroll
             for (int jj = 0; jj < D / 32; ++jj) {
                 const uint4 w = sm.codes[warp][slot][1][jj][lane];

@@ -127,6 +127,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
     return r;
 }
 
+// The bytes of four e4m3 codes that are NaN: their top bits.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// The same codes with 0 for NaN, where `nan` says so.
+__device__ __forceinline__ uint32_t e4m3_without(uint32_t w, uint32_t nan) { return w & ~((nan >> 7) * 0xFFu); }
+
 // Four codes to four f16 values (exactly), in order: lo holds codes 0 and 1.
 // An int8 code c is (c + 128) + 1024 as an f16 whose low byte is c ^ 0x80,
 // less 1152.

@@ -88,7 +88,8 @@ struct KeyTile {
     // log2 vs = 0: what their sums are multiplied by (in log2 and as a factor)
     int32_t rebase;
     float rebase_lv, rebase_iv;
-    int32_t pad[3];
+    int32_t edge;  // some row of the item does not see some key
+    int32_t pad[2];
 };
 static_assert(sizeof(KeyTile) % 16 == 0, "scales are read as 16-byte pieces");
 
@@ -108,6 +109,7 @@ struct PrefillSmem {
     long long warp_sum[kPreThreads / 32];
     long long base;
     int32_t seq;
+    int32_t nan_item[kItemRing];      // number (from 1) of the last item with a NaN hidden in V, by number
     int32_t head0, row_tile0, skip0;  // where the CTA's line begins
     uint32_t tmem;
     int32_t dead;
@@ -336,6 +338,32 @@ __device__ __forceinline__ void issue_values(PrefillSmem<D> &sm, uint32_t X, uin
         mma_f16_ts(256 + X * 128, X * 128 + h * 32 + i * 8, v + i * 2, idesc_f16_f32(kHalf, D), i > 0 || accumulate);
 }
 
+// Of dimensions [d0, d0 + 32): a bit for each in which V is NaN at a key that
+// the row sees, [kmin, kmax), in one of the tiles [tile0, tile1) that not
+// every row sees whole.  (In those NaN codes are taken as 0 by the product,
+// as p = 0 would not keep them from the rows that do not see the key.)
+template <int D>
+__device__ __noinline__ uint32_t nan_dims(const KvView &b, int32_t seq, int32_t head, int32_t tile0, int32_t tile1, int32_t all_lo,
+                                          int32_t all_hi, int32_t kmin, int32_t kmax, int32_t d0) {
+    uint32_t mask = 0;
+    for (int32_t k = tile0 * kKeys; k < tile1 * kKeys; k += kKvTile) {
+        const int32_t key0 = k & ~(kKeys - 1);
+        if ((key0 >= all_lo && key0 + kKeys <= all_hi) || k >= kmax || k + kKvTile <= kmin) continue;
+        const int32_t page = b.table[static_cast<int64_t>(seq) * b.max_pages + (k >> b.page_shift)];
+        if (page < 0 || page >= b.num_pages || !(b.v_scales[static_cast<int64_t>(page) * b.heads + head] > 0.0f)) continue;
+        const uint32_t *v = reinterpret_cast<const uint32_t *>(
+            b.v_pages + tile_offset<D>(b, page, head, (k & (b.page_tokens - 1)) / kKvTile));
+        for (int q = 0; q < 4; ++q) {
+            uint32_t seen = 0;
+            for (int t = 0; t < 4; ++t)
+                if (k + 4 * q + t >= kmin && k + 4 * q + t < kmax) seen |= 0x80u << (8 * t);
+            for (int d = 0; seen && d < 32; ++d)
+                if (e4m3_nan(v[((d0 + d) / 4 * 4 + q) * 4 + d % 4]) & seen) mask |= 1u << d;
+        }
+    }
+    return mask;
+}
+
 // ---------------------------------------------------------------- kernel
 
 template <int D, int FMT>
@@ -385,6 +413,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
         sm.dead = 0;
+        for (int i = 0; i < kItemRing; ++i) sm.nan_item[i] = 0;
         joins[blockIdx.x].last_cta = -1;
     }
     if (warp == 12) {
@@ -593,12 +622,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             float *part = partial_at(a, blockIdx.x, it.flags & kFromStart ? 1 : 0, kRows, D);
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out.p) + static_cast<int64_t>(it.off + qi) * a.out.row + qh * a.out.head;
             const float inv = 1.0f / l;
+            const bool hidden = FMT == LORA_KV_E4M3 && *static_cast<volatile int32_t *>(&sm.nan_item[n_item % kItemRing]) == static_cast<int32_t>(n_item);
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(to + 32 * i, o);
                 tmem_ld_wait(o);
                 if (rt >= rows) continue;
+                if (FMT == LORA_KV_E4M3 && __builtin_expect(hidden, 0)) {
+                    const uint32_t nan = nan_dims<D>(b, it.seq, it.head, it.tile0, it.tile1, all_lo, all_hi, kmin, kmax, 32 * i);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (nan >> e & 1u) o[e] = 0x7FFFFFFFu;
+                }
                 if (whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 16) {
@@ -641,7 +677,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         struct Tile {
             int32_t key0, len;
             int64_t at[2], at_v;  // (of V the thread's own)
-            int32_t off, n, head, row_tile;
+            int32_t off, n, head, row_tile, edge;
         };
         Tile cur, nxt;
         auto look = [&](Tile &x, uint32_t n) {
@@ -656,6 +692,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             x.off = sm.tiles[e].off;
             x.head = sm.tiles[e].head;
             x.row_tile = sm.tiles[e].row_tile;
+            x.edge = sm.tiles[e].edge;
         };
         uint4 *kc = &sm.codes[0][0][wq * 32 + lane], *vc = &sm.codes[1][0][wq * 32 + lane];
         // the thread's piece i of a tile; zeros where there is no page
@@ -779,6 +816,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             for (int i = 0; i < 2; ++i) {
                 const int past = cur.key0 + wq * 32 + cc * 8 + 4 * i + 4 - cur.len;
                 keep[i] = past <= 0 ? 0xFFFFFFFFu : past >= 4 ? 0u : 0xFFFFFFFFu >> (8 * past);
+            }
+            if (FMT == LORA_KV_E4M3 && cur.edge) {
+                // NaN of keys that not every row sees: taken out, and noted for the item (nan_dims)
+                bool some = false;
+#pragma unroll 1
+                for (int i = 0; i < NL; ++i) {
+                    const uint4 r = vc[128 * i];
+                    uint32_t w[4] = {r.x, r.y, r.z, r.w}, any = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t nan = e4m3_nan(w[e] & ((i & 1) ? keep[1] : keep[0]));
+                        any |= nan;
+                        w[e] = e4m3_without(w[e], nan);
+                    }
+                    if (any) {
+                        vc[128 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        some = true;
+                    }
+                }
+                const uint32_t item = n_q + (first ? 1u : 0u);
+                if (some) sm.nan_item[item % kItemRing] = static_cast<int32_t>(item);
             }
             uint8_t *vdst = sm.v[stage] + v_at;
 #pragma unroll 1
@@ -950,6 +1008,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 const int32_t seq = sm.items[e].seq, head = sm.items[e].head, len = sm.items[e].len;
                 const int32_t tile0 = sm.items[e].tile0, tile1 = *dead ? -1 : sm.items[e].tile1;
                 const int32_t off = sm.items[e].off, n = sm.items[e].n, row_tile = sm.items[e].row_tile;
+                // keys that every row of the item sees
+                const int32_t all_hi = a.causal ? len - n + row_tile * kRows / a.group + 1 : len;
+                const int32_t last_row = min((row_tile + 1) * kRows, n * a.group) - 1;
+                const int32_t all_lo = a.window > 0 ? len - n + last_row / a.group - a.window + 1 : 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.item_empty[e]);
                 ++n_item;
@@ -994,6 +1056,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                                 sm.tiles[r].n = t == tile0 ? n : 0;
                                 sm.tiles[r].head = head;
                                 sm.tiles[r].row_tile = row_tile;
+                                sm.tiles[r].edge = t * kKeys < all_lo || t * kKeys + kKeys > all_hi;
                                 sm.tiles[r].rebase = first;
                                 sm.tiles[r].rebase_lv = lv;
                                 sm.tiles[r].rebase_iv = iv;

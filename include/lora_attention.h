@@ -176,6 +176,7 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  *
  * Query head h reads key/value head h / (num_q_heads / num_heads).  A query
  * that sees no key (padding, skipped sequences) has out = 0 and lse = -inf.
+ * A NaN in the cache reaches the queries that see its token, and no others.
  * Rows outside every sequence are not written.
  * max_queries bounds the rows of one sequence (it chooses the kernel); a
  * sequence with more rows is recorded (SEGMENTS) and skipped.

@@ -409,6 +409,37 @@ def test_attention_query_ranges(n, width, scale):
         check_attention(cache, rng, dtype, 4, [n], [90], table, lens, offs, q_width=width, scale=scale)
 
 
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("dtype,n,before,D,page", [("bf16", 1, 100, 128, 16), ("bf16", 2, 100, 128, 16), ("bf16", 4, 5000, 64, 64),
+                                                   ("fp32", 3, 100, 128, 32), ("bf16", 40, 100, 128, 16), ("bf16", 150, 100, 64, 128),
+                                                   ("bf16", 70, 3000, 128, 64)])
+def test_attention_nan_values_reach_the_rows_that_see_them(dtype, n, before, D, page, window):
+    """NaN codes of V (e4m3): NaN in that dimension for the rows that see the token, and nothing else changes."""
+    rng, cache, table, lens, offs = setup(51 + n, [n, 3], [before, 9], page, "e4m3", 2, D)
+    L, G = before + n, 4
+    bad = [(L - 1, 0, 3, 0x7F), (L - n // 2 - 1, 1, D - 1, 0xFF), (before - 20, 0, 33, 0x7F), (before - 29, 1, 0, 0xFF)]
+    q, _ = draw(rng, (n + 3, 2 * G, D), dtype)
+
+    def run(codes):
+        vp = cache.v_pages.view(torch.uint8).cpu()
+        for (t, h, d, _), c in zip(bad, codes):
+            vp[int(table[0][t // page]), h, t % page // 16, d // 4, t % 16 // 4, d % 4, t % 4] = c
+        cache.v_pages.view(torch.uint8).copy_(vp)
+        return cache.attention(q, dev(table), dev(lens), dev(offs), window=window, return_lse=True, max_queries=max(n, 3))
+
+    clean, clean_lse = run([0] * len(bad))
+    out, lse = run([c for *_, c in bad])
+    want = torch.zeros((n + 3, 2 * G, D), dtype=torch.bool)
+    for i in range(n):
+        for t, h, d, _ in bad:
+            if t <= before + i and (window == 0 or t > before + i - window):
+                want[i, h * G:(h + 1) * G, d] = True
+    want = want.to(DEV)
+    assert status() == 0 and bool(torch.isfinite(clean).all())
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(out[~want], clean[~want]) and torch.equal(lse, clean_lse)
+
+
 def test_attention_nan_and_infinite_queries_stay_in_their_row():
     for n in (2, 40):
         rng, cache, table, lens, offs = setup(41, [n, n], [50, 60], 16, "int8", 1, 128)
