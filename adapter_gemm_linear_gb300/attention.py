@@ -305,7 +305,7 @@ class KvCache:
                 0 if lse is None else lse.data_ptr(), scale, causal, window, max_queries)
         L = _lib.lib()
         if workspace is None:
-            key = (head[0], Hq, max_queries, device)
+            key = (head[0], Hq, max_queries, rows, block_table.shape, device)
             need = self._workspace.get(key)
             if need is None:
                 need = L.lora_kv_attention_workspace_bytes(self._ref, batch, _ATTENTION_ARGS.pack(*head, 0, 0))

@@ -1,5 +1,6 @@
 // Host side of lora_attention.h: argument validation and dispatch.  No entry
 // point here allocates device memory or waits for the device.
+#include <algorithm>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -109,9 +110,19 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
 // heads that share a key/value head) at a time, the tensor-core kernel of
 // attn_prefill.cu on 256, and is faster as soon as the first would take more
 // than one pass: 64 sequences of 4096 tokens, 8 heads of 128, with 16 rows
-// 141 against 190 us, with 32 rows 258 against 192 us.
+// 141 against 190 us, with 32 rows 258 against 192 us.  But it takes some 20 us
+// to get going, so where the tables have no room for more than eight of the
+// first's units of work an SM (16 rows x 128 keys), those are done sooner: 128
+// queries of 32 heads on 8 on their own keys (512 units) 18.4 against 26.6 us,
+// 64 on 1064 (1152 units) 28.7 against 30.7, 178 x 2 heads on 7673 (1440
+// units) 38.9 against 34.8, 4 x 128 queries (2048 units) 49 against 28.7.
 bool many_queries(const lora::AttnView &v, lora_dtype_t dtype) {
-    return dtype == LORA_BF16 && static_cast<int64_t>(v.max_queries) * v.group > 16;
+    const int64_t rows = static_cast<int64_t>(v.max_queries) * v.group;  // of a sequence, at most
+    if (dtype != LORA_BF16 || rows <= 16) return false;
+    const double row_tiles = std::min(static_cast<double>(v.kv.num_seqs) * static_cast<double>((rows + 15) / 16),
+                                      static_cast<double>(v.kv.rows) * v.group / 16 + v.kv.num_seqs);
+    const double chunks = (static_cast<double>(v.kv.max_pages) * v.kv.page_tokens + 127) / 128;
+    return row_tiles * v.kv.heads * chunks > 8.0 * lora::device_sm_count();
 }
 
 size_t workspace_bytes(const lora::AttnView &v, int head_dim, lora_dtype_t dtype) {

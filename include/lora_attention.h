@@ -178,7 +178,7 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * that sees no key (padding, skipped sequences) has out = 0 and lse = -inf.
  * A NaN in the cache reaches the queries that see its token, and no others.
  * Rows outside every sequence are not written.
- * max_queries bounds the rows of one sequence (it chooses the kernel); a
+ * max_queries bounds the rows of one sequence (it and max_pages choose the kernel); a
  * sequence with more rows is recorded (SEGMENTS) and skipped.
  * Precision: products with the codes exact, fp32 sums; probabilities enter
  * the second product with 11 significant bits for bf16 calls, 22 for fp32.

@@ -158,14 +158,15 @@ def rope(x, cos, sin, positions, axes, interleaved, inverse=False):
     return y
 
 
-def make_batch(rng, news, befores, page, spare=3):
-    """(table int32 [S, max], lens, offs, num_pages): pages scattered, unused entries out of range."""
+def make_batch(rng, news, befores, page, spare=3, room=2048):
+    """(table int32 [S, max], lens, offs, num_pages): pages scattered, unused entries out of range; `room` columns
+    more than needed (attention of several queries chooses its kernel by what a table has room for)."""
     lens = [a + b for a, b in zip(news, befores)]
     offs = np.concatenate(([0], np.cumsum(news))).astype(np.int32)
     per = [-(-x // page) for x in lens]
     num = sum(per) + spare
     order = rng.permutation(num)
-    table = np.full((len(lens), max(per + [1]) + 1), -7, np.int32)
+    table = np.full((len(lens), max(per + [1]) + 1 + room), -7, np.int32)
     at = 0
     for s, c in enumerate(per):
         table[s, :c] = order[at:at + c]

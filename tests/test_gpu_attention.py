@@ -282,9 +282,9 @@ def check_attention(cache, rng, dtype, Hq, news, befores, table, lens, offs, cau
     return out, lse
 
 
-def setup(seed, news, befores, page, fmt, H, D):
+def setup(seed, news, befores, page, fmt, H, D, **kw):
     rng = np.random.default_rng(seed)
-    table, lens, offs, num = R.make_batch(rng, news, befores, page)
+    table, lens, offs, num = R.make_batch(rng, news, befores, page, **kw)
     cache = KvCache(num, H, D, page, fmt)
     R.random_codes(rng, cache)
     return rng, cache, table, lens, offs
@@ -310,6 +310,17 @@ def test_attention_several_queries(dtype, fmt, page, D, H, G, window, causal):
     for news, befores in (([4] * 3, [0, 61, 200]), ([2, 0, 7, 1], [5, 9, 0, 90]), ([37, 130], [0, 45]), ([1, 300], [600, 0])):
         rng, cache, table, lens, offs = setup(page + D + G + len(news), news, befores, page, fmt, H, D)
         check_attention(cache, rng, dtype, H * G, news, befores, table, lens, offs, causal, window)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("news,befores,page,D,H,G,window,causal", [
+    ([17], [0], 16, 128, 1, 1, 0, True), ([40, 3, 1], [5, 70, 300], 16, 128, 2, 4, 0, True),
+    ([33], [130], 32, 64, 3, 5, 20, True), ([50, 20], [0, 11], 64, 128, 1, 8, 0, False), ([100], [400], 128, 64, 1, 4, 90, False),
+])
+def test_attention_several_queries_in_small_tables(fmt, news, befores, page, D, H, G, window, causal):
+    """bf16, more than 16 query rows a sequence, tables with little room: several tiles of rows of the decode kernel."""
+    rng, cache, table, lens, offs = setup(61 + D + G, news, befores, page, fmt, H, D, room=0)
+    check_attention(cache, rng, "bf16", H * G, news, befores, table, lens, offs, causal=causal, window=window)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -409,13 +420,13 @@ def test_attention_query_ranges(n, width, scale):
         check_attention(cache, rng, dtype, 4, [n], [90], table, lens, offs, q_width=width, scale=scale)
 
 
-@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("window,room", [(0, 2048), (30, 2048), (30, 0)])
 @pytest.mark.parametrize("dtype,n,before,D,page", [("bf16", 1, 100, 128, 16), ("bf16", 2, 100, 128, 16), ("bf16", 4, 5000, 64, 64),
                                                    ("fp32", 3, 100, 128, 32), ("bf16", 40, 100, 128, 16), ("bf16", 150, 100, 64, 128),
                                                    ("bf16", 70, 3000, 128, 64)])
-def test_attention_nan_values_reach_the_rows_that_see_them(dtype, n, before, D, page, window):
+def test_attention_nan_values_reach_the_rows_that_see_them(dtype, n, before, D, page, window, room):
     """NaN codes of V (e4m3): NaN in that dimension for the rows that see the token, and nothing else changes."""
-    rng, cache, table, lens, offs = setup(51 + n, [n, 3], [before, 9], page, "e4m3", 2, D)
+    rng, cache, table, lens, offs = setup(51 + n, [n, 3], [before, 9], page, "e4m3", 2, D, room=room)
     L, G = before + n, 4
     bad = [(L - 1, 0, 3, 0x7F), (L - n // 2 - 1, 1, D - 1, 0xFF), (before - 20, 0, 33, 0x7F), (before - 29, 1, 0, 0xFF)]
     q, _ = draw(rng, (n + 3, 2 * G, D), dtype)
