@@ -218,6 +218,21 @@ __device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x,
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (amax == 0.0f && t0 < hi && lo < t0 + kKvTile) {
+        // new tokens without a finite value but zeros: an infinity or a NaN
+        // among them needs a code, and so a scale, the least one (by way of the
+        // least float, which leaves the scale alone wherever the page's other
+        // tiles have a finite value)
+        bool some = false;
+#pragma unroll 1
+        for (int i = 0; i < PIECES; ++i) {
+            Raw<T> y;
+            load(i, y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) some = some || !(fabsf(y.value(e >> 2, e & 3)) < INFINITY);
+        }
+        if (__any_sync(0xffffffffu, some)) amax = __uint_as_float(1u);
+    }
     if (unit_warps > 1) {
         if (lane == 0) unit_amax[tile] = amax;
         __syncthreads();

@@ -148,9 +148,11 @@ typedef struct lora_kv_batch {
  *          are rescaled by s0 / s, exactly unless they fall below the
  *          format's least normal.
  * All of it in fp32.  Infinities take the largest code, NaN code 0 in int8
- * and NaN in e4m3; neither moves the scale of its neighbours.  A page with
- * no value but zeros has scale 0.  Pages are not shared: no two sequences of
- * a call may write the same page.
+ * and NaN in e4m3; neither moves the scale of its neighbours, but where the
+ * call's new values have no finite one but zeros, an infinity or NaN among them
+ * counts as the least a > 0 (s is 2^-120 at least), so that it has a code.  A
+ * page with no value but zeros has scale 0.  Pages are not shared: no two
+ * sequences of a call may write the same page.
  * k, v: the rows' [num_heads][head_dim] in `dtype`.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (head_dim, page_tokens
  * or format), CUDA.
