@@ -34,10 +34,11 @@
 //  - q enters as f16 times a power of two per row (exact for bf16).  In fp32
 //    calls q and p are each split in two f16 parts, hi + lo 2^-11, as two
 //    column tiles of the MMA whose sums are added: 22 significant bits.
-//  - The page's scale of V is folded into the exponent: p' = 2^(s + log2 vs -
-//    m), o sums p' codes, l sums p' / vs.  p' <= 2^14 whatever the scales, so
-//    f16 holds it.  m follows the maximum only when that grows by 2^14, so the
-//    sums are rarely rescaled.
+//  - The page's scale of V is folded into the exponent, relative to a reference
+//    scale vr (attn_split.cuh): p' = 2^(s + log2 (vs / vr) - m), o sums p' codes,
+//    l sums p' vr / vs.  p' <= 2^14 whatever the scales, so f16 holds it.  m
+//    follows the maximum only when that grows by 2^14, so the sums are rarely
+//    rescaled.
 // Measured, with the join: 256 sequences of about 4096 tokens, 64 heads on 8 of
 // 128, int8: 318 us, 5.8 TB/s (0.86 of a copy's rate; SMs that reach the memory
 // less well end last).  4 sequences of 131072, e4m3: 183 us, 5.9 TB/s.  One of
@@ -86,6 +87,7 @@ struct alignas(16) TileInfo {
     int64_t pad;
 };
 constexpr int64_t kNoTile = -1, kEndOfLine = -2;
+constexpr float kNoReference = -1e30f;  // below every page's log2 scale
 
 constexpr int kBatch = 32, kBatches = 8;  // tiles looked up at once, and ahead
 
@@ -97,6 +99,7 @@ struct DecodeSmem {
     uint4 codes[kWarps][kDepth][2][kPieces][32];     // [.., K or V, piece, lane]
     float o[kWarps][8 * NT][D + 4];                  // merge: padded against bank conflicts
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
+    float vr[kWarps];
     TileInfo info[kBatches][kBatch];
     uint64_t full[kBatches], empty[kBatches];
     long long warp_sum[kWarps + 1];
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 fill += take;
                 next += take;
             }
-            TileInfo x = {0.0f, 0.0f, 0.0f, 0.0f, kEndOfLine, 0};
+            TileInfo x = {0.0f, 0.0f, -INFINITY, INFINITY, kEndOfLine, 0};
             if (seq >= 0) {
                 const int32_t page = read_page(b, seq, t >> tile_shift);
                 x.at = kNoTile;
@@ -420,8 +423,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 m[u][i] = -INFINITY;
                 l[u][i] = 0.0f;
             }
-        bool seen = false;  // a tile whose V is not all zero
-        float lv = 0.0f, ivs = 1.0f;
+        float vr = 1.0f, ref = kNoReference;  // the reference scale of V and its log2 (attn_split.cuh)
 
         const int32_t count = walk.tile1 - walk.tile0;
         // this warp's tiles: those whose running number is the warp's modulo kWarps
@@ -429,7 +431,35 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             const uint32_t i = i0 + j, slot = taken++ % Smem::kDepth;
             const int32_t key0 = (walk.tile0 + j) * kKvTile;
             const TileInfo &info = sm.info[i / kBatch % kBatches][i % kBatch];
-            const float ks = info.ks, vs = info.vs;
+            const float ks = info.ks;
+            if (__builtin_expect(info.lv - ref > kSpread, 0)) {  // a new reference, the first or a far larger one
+                if (ref != kNoReference) {
+                    const float step = info.lv - ref;
+#pragma unroll
+                    for (int u = 0; u < RT; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float sum = l[u][e];
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                            const float lower = reference_shift(step, sum), f = ex2(lower - step);
+                            m[u][e] -= lower;
+                            l[u][e] *= ex2(lower);
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                o[u][k][e] *= f;
+                                o[u][k][e + 2] *= f;
+                                if (SPLIT) {
+                                    o[NT - 1][k][e] *= f;
+                                    o[NT - 1][k][e + 2] *= f;
+                                }
+                            }
+                        }
+                }
+                ref = info.lv;
+                vr = info.vs;
+            }
             const int64_t ahead = look(i + Smem::kDepth * kWarps);
             float s[NT][4];
 #pragma unroll
@@ -449,21 +479,10 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 }
             }
             fetch_k(ahead, slot);
+            // V's scale relative to the reference, in log2, and what takes it
+            // out again; of a V that is zero the least
+            const float lv = fmaxf(info.lv - ref, -kSpread), ivs = fminf(vr * info.ivs, kSpreadFactor);
             // scores in log2 units, with V's scale
-            if (vs > 0.0f) {
-                lv = info.lv;
-                ivs = info.ivs;
-                if (!seen) {  // tiles so far had V = 0 and took lv = 0: their sums move to this one's
-                    seen = true;
-#pragma unroll
-                    for (int u = 0; u < RT; ++u)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            m[u][i] += lv;
-                            l[u][i] *= ivs;
-                        }
-                }
-            }
             float z[RT][4];  // [2 * token half + row]
 #pragma unroll
             for (int u = 0; u < RT; ++u)
@@ -530,7 +549,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     pf[NT - 1][1] = transpose_8x8(pack_rest(p[2], p[3], h1));
                 }
             }
-            if (!(vs > 0.0f)) {  // V = 0 whatever its codes
+            if (lv <= -kSpread) {  // V = 0 whatever its codes, or nothing beside the reference
 #pragma unroll
                 for (int u = 0; u < NT; ++u) pf[u][0] = pf[u][1] = 0u;
             }
@@ -630,6 +649,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     *reinterpret_cast<float4 *>(&sm.o[warp][rt][32 * jj + 4 * g]) = v;
                 }
             }
+        if (lane == 0) sm.vr[warp] = vr;
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
         const bool whole = walk.from_start && walk.to_end;
         // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
@@ -642,7 +662,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
         const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
         if (rt < rows) {
-            float M = -INFINITY, L = 0.0f, f[kWarps];
+            float M = -INFINITY, L = 0.0f, f[kWarps], scale[kWarps];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][rt]);
             const float mu = M == -INFINITY ? 0.0f : M;
@@ -650,8 +670,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             for (int w = 0; w < kWarps; ++w) {
                 f[w] = ex2(sm.m[w][rt] - mu);
                 L = fmaf(sm.l[w][rt], f[w], L);
+                scale[w] = sm.vr[w];
             }
-            const float inv = 1.0f / L;
+            // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
+            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) f[w] *= inv;
             const int32_t row = walk.row_tile * ROWS + rt;
             const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
             T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head;
@@ -661,23 +685,23 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][rt][c]);
-                    v.x = fmaf(x.x, f[w], v.x);
-                    v.y = fmaf(x.y, f[w], v.y);
-                    v.z = fmaf(x.z, f[w], v.z);
-                    v.w = fmaf(x.w, f[w], v.w);
+                    v.x = fmaf(x.x * f[w], scale[w], v.x);
+                    v.y = fmaf(x.y * f[w], scale[w], v.y);
+                    v.z = fmaf(x.z * f[w], scale[w], v.z);
+                    v.w = fmaf(x.w * f[w], scale[w], v.w);
                 }
                 if (whole) {
-                    store4(dst + c, v, inv);
+                    store4(dst + c, v, 1.0f);
                 } else {
                     *reinterpret_cast<float4 *>(part + rt * D + c) = v;
                 }
             }
             if (c0 == 0) {
+                const float lse = M + log2f(L);
                 if (!whole) {
-                    part[kSlotRows * D + rt] = M;
-                    part[kSlotRows * D + kSlotRows + rt] = L;
+                    part[kSlotRows * D + rt] = lse;
                 } else if (a.lse) {
-                    a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
+                    a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = lse * kLn2;
                 }
             }
         }

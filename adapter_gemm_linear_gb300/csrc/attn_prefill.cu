@@ -26,7 +26,7 @@
 //  - warp 12 issues the products; warp 13 hands out the items, and warp 14
 //    looks up the pages and scales of the key tiles, four tiles ahead.
 //  - q is f16 times a power of two per row (exact for bf16), P is f16 (11
-//    bits) with the page's scale of V in its exponent, as in attn_decode.cu; a
+//    bits) with the page's scale of V in its exponent (attn_split.cuh); a
 //    row's sums are rescaled only when its maximum grew by 2^14.
 //  - Tensor Memory: S_A, S_B (128 columns each, P over the first 64), O_A, O_B.
 // The key tiles of all items form one line that the CTAs share equally
@@ -76,20 +76,16 @@ constexpr int kFromStart = 1, kToEnd = 2;
 
 // A key tile of the CTA's line: where its 16-key pieces are, and their scales.
 struct KeyTile {
-    // Of each piece K's scale, and log2 and reciprocal of V's.  A piece whose V
-    // is zero (scale 0) takes those of a neighbour: any would do, and that one
-    // keeps the exponents together.
+    // Of each piece K's scale, and V's relative to the reference vr (attn_split.cuh)
+    // in log2, and what takes it out again; of a V that is zero the least.
     float4 scales[kSubs];
     int64_t at[kSubs];    // offset in k_pages; < 0: past the end or not there, zeros
     int64_t at_v[kSubs];  // and in v_pages
     int32_t key0, len;    // first key, the sequence's length; key0 < 0: no more tiles
     int32_t off, n, head, row_tile;  // of an item's first tile: its queries (n = 0 in its other tiles)
-    // The item's first tile with a V that is not zero, if tiles before it took
-    // log2 vs = 0: what their sums are multiplied by (in log2 and as a factor)
-    int32_t rebase;
-    float rebase_lv, rebase_iv;
-    int32_t edge;  // some row of the item does not see some key
-    int32_t pad[2];
+    float vr, step;  // the reference; log2 of how much it grew with this tile, 0 if it did not (or is the first)
+    int32_t edge;    // some row of the item does not see some key
+    int32_t pad[3];
 };
 static_assert(sizeof(KeyTile) % 16 == 0, "scales are read as 16-byte pieces");
 
@@ -491,6 +487,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             return it.tile1 >= 0 && (X == 0 || it.n * a.group - it.row_tile * kRows > kHalf);
         };
 
+        auto rescale = [&](uint32_t at, float f) {  // O, the thread's row
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(at + 16 * i, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st_32x32b_x16(at + 16 * i, o);
+            }
+        };
+
         Item it;
         get_item(it);
         while (it.tile1 >= 0) {
@@ -508,7 +515,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             // keys that every row of the item sees
             const int32_t all_hi = a.causal ? it.len - it.n + it.row_tile * kRows / a.group + 1 : it.len;
             const int32_t all_lo = a.window > 0 ? it.len - it.n + (it.row_tile * kRows + rows - 1) / a.group - a.window + 1 : 0;
-            float m = -INFINITY, l = 0.0f, cr = 0.0f;
+            float m = -INFINITY, l = 0.0f, cr = 0.0f, vr = 1.0f;
             for (int32_t t = it.tile0; t < it.tile1; ++t, ++n_tile, ++n_own) {
                 wait(&sm.tile_full[n_tile % kTileRing], (n_tile / kTileRing) & 1u, 55);
                 wait(&sm.s_full[X], n_own & 1u, 51 + X);
@@ -529,9 +536,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     }
                     tmem_st_wait();
                 }
-                if (__builtin_expect(tile.rebase, 0)) {
-                    m += tile.rebase_lv;
-                    l *= tile.rebase_iv;
+                vr = tile.vr;
+                if (__builtin_expect(tile.step > 0.0f, 0)) {  // (not an item's first tile)
+                    const float lower = reference_shift(tile.step, l);
+                    m -= lower;
+                    l *= ex2(lower);
+                    rescale(to, ex2(lower - tile.step));
                 }
                 // Two halves of 64 keys, one after the other, each with the row's
                 // maximum so far: the product with the first half's V runs while
@@ -578,14 +588,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                                 wait(&sm.half_done[X], n_own & 1u, 57);
                                 tc_fence_after_sync();
                             }
-#pragma unroll 1
-                            for (int i = 0; i < D / 16; ++i) {
-                                uint32_t o[16];
-                                tmem_ld_32x32b_x16(to + 16 * i, o);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st_32x32b_x16(to + 16 * i, o);
-                            }
+                            rescale(to, f);
                         }
                     }
                     const float mu = m == -INFINITY ? 0.0f : m;
@@ -621,7 +624,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             const bool whole = (it.flags & (kFromStart | kToEnd)) == (kFromStart | kToEnd);
             float *part = partial_at(a, blockIdx.x, it.flags & kFromStart ? 1 : 0, kRows, D);
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out.p) + static_cast<int64_t>(it.off + qi) * a.out.row + qh * a.out.head;
-            const float inv = 1.0f / l;
+            // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
+            const float inv = whole || !(l == 0.0f) ? 1.0f / l : 0.0f, lse = m + log2f(l);
             const bool hidden = FMT == LORA_KV_E4M3 && *static_cast<volatile int32_t *>(&sm.nan_item[n_item % kItemRing]) == static_cast<int32_t>(n_item);
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
@@ -635,13 +639,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     for (int e = 0; e < 32; ++e)
                         if (nan >> e & 1u) o[e] = 0x7FFFFFFFu;
                 }
+                // (one after the other: 1 / l times vr may leave fp32's normal range)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv * vr);
                 if (whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 16) {
                         uint32_t h[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
                             h[k] = *reinterpret_cast<const uint32_t *>(&two);
                         }
                         store_32(dst + 32 * i + e, h);
@@ -657,10 +664,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             tc_fence_before_sync();
             if (rt < rows) {
                 if (!whole) {
-                    part[kRows * D + rt] = m;
-                    part[kRows * D + kRows + rt] = l;
+                    part[kRows * D + rt] = lse;
                 } else if (a.lse) {
-                    a.lse[static_cast<int64_t>(it.off + qi) * a.q_heads + qh] = (m + log2f(l)) * kLn2;
+                    a.lse[static_cast<int64_t>(it.off + qi) * a.q_heads + qh] = lse * kLn2;
                 }
             }
             if (!whole && (it.flags & kFromStart) && threadIdx.x == 0)
@@ -1016,8 +1022,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 if (lane == 0) mbar_arrive(&sm.item_empty[e]);
                 ++n_item;
                 // four tiles at a time: lane = (tile, piece)
-                float lv_last = 0.0f, iv_last = 1.0f;
-                bool seen = false;  // a piece whose V is not zero
+                float vr = 0.0f, ref = 0.0f;  // the reference scale of V and its log2; none yet
                 for (int32_t t0 = tile0; t0 < max(tile1, tile0 + 1); t0 += 4) {
                     const int32_t t = t0 + (lane >> 3), key = t * kKeys + sub * kKvTile;
                     int64_t at = -1;
@@ -1031,17 +1036,31 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         }
                     }
                     __syncwarp();
-                    const uint32_t some = __ballot_sync(0xffffffffu, vs > 0.0f);
-                    // a piece without takes the last one's before it, or else the first of its own tile
-                    const uint32_t before = some & (0xFFFFFFFFu >> (31 - lane)), own = some & (0xFFu << (lane & 24));
-                    const int from = before ? 31 - __clz(before) : own && !seen ? __ffs(own) - 1 : -1;
-                    float lv = vs > 0.0f ? log2f(vs) : 0.0f, iv = vs > 0.0f ? 1.0f / vs : 1.0f;
-                    const float lv_from = __shfl_sync(0xffffffffu, lv, max(from, 0));
-                    const float iv_from = __shfl_sync(0xffffffffu, iv, max(from, 0));
-                    lv = from >= 0 ? lv_from : lv_last;
-                    iv = from >= 0 ? iv_from : iv_last;
-                    // the tile in which the item's first such piece is
-                    const bool first = !seen && some && ((__ffs(some) - 1) >> 3) == (lane >> 3) && t > tile0;
+                    // the reference in force in each tile: the largest scale of the
+                    // first tile that has one, and again where that is far larger
+                    float top = vs > 0.0f ? vs : 0.0f;
+#pragma unroll
+                    for (int o = 1; o < kSubs; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    float vr_own = 0.0f, ref_own = 0.0f, step = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float vq = __shfl_sync(0xffffffffu, top, q * kSubs), lq = log2f(vq);
+                        const bool mine = (lane >> 3) == q;
+                        if (vq > 0.0f && (vr == 0.0f || lq - ref > kSpread)) {
+                            if (mine && vr > 0.0f) step = lq - ref;
+                            vr = vq;
+                            ref = lq;
+                        }
+                        if (mine) {
+                            vr_own = vr;
+                            ref_own = ref;
+                        }
+                    }
+                    float lv = -kSpread, iv = kSpreadFactor;
+                    if (vs > 0.0f && log2f(vs) - ref_own >= -kSpread) {
+                        lv = log2f(vs) - ref_own;
+                        iv = vr_own / vs;
+                    }
                     for (int q = 0; q < 4 && t0 + q < max(tile1, tile0 + 1); ++q) {
                         const uint32_t r = n_tile % kTileRing;
                         wait(&sm.tile_empty[r], ((n_tile / kTileRing) & 1u) ^ 1u, 91);
@@ -1057,19 +1076,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                                 sm.tiles[r].head = head;
                                 sm.tiles[r].row_tile = row_tile;
                                 sm.tiles[r].edge = t * kKeys < all_lo || t * kKeys + kKeys > all_hi;
-                                sm.tiles[r].rebase = first;
-                                sm.tiles[r].rebase_lv = lv;
-                                sm.tiles[r].rebase_iv = iv;
+                                sm.tiles[r].vr = vr_own > 0.0f ? vr_own : 1.0f;
+                                sm.tiles[r].step = step;
                             }
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.tile_full[r]);
                         ++n_tile;
-                    }
-                    if (some) {
-                        lv_last = __shfl_sync(0xffffffffu, lv, 31 - __clz(some));
-                        iv_last = __shfl_sync(0xffffffffu, iv, 31 - __clz(some));
-                        seen = true;
                     }
                 }
                 if (tile1 < 0) break;

@@ -19,8 +19,9 @@ struct alignas(16) JoinEntry {
     int32_t pad[3];
 };
 
-// Floats of one partial result: [rows][D] sums, then the rows' maximum (log2 units) and sum.
-__host__ __device__ constexpr size_t partial_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
+// Floats of one partial result: [rows][D] outputs over the keys of the part
+// alone, then the rows' log2 of the sum of 2^score over them.
+__host__ __device__ constexpr size_t partial_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 1); }
 
 __host__ __device__ constexpr size_t split_workspace_bytes(int ctas, int rows, int D) {
     return static_cast<size_t>(ctas) * (partial_floats(rows, D) * 2 * sizeof(float) + sizeof(JoinEntry));
@@ -40,6 +41,26 @@ constexpr float kLog2e = 1.4426950408889634f;
 // below 2^14, well inside f16.  (With 8 one key tile in two of a long prompt
 // whose pages differ in scale waited for some warp's rescaling.)
 constexpr float kGrow = 14.0f;
+
+// The scales of V's pages, as the exponents of the probabilities take them: in
+// log2 relative to a reference, the scale vr of a page that the row's sums
+// began with (or a later page's, see below), and within +-kSpread of it.
+//     p' = 2^(s + rel - m),  o = sum p' code,  l = sum p' 2^-rel = sum 2^(s - m),  out = o vr / l
+// so that neither l nor p' leaves fp32's range wherever the scales lie in theirs
+// (2^-120 .. 2^121): with n keys l is between 2^-kSpread and n 2^(kGrow + kSpread).
+// A page smaller than 2^-kSpread of the reference counts as that much, or as
+// zero: what it is off by is 2^-kSpread of the row's largest V, below every other
+// rounding here.  A page that is larger than 2^kSpread of it becomes the reference:
+// with d = log2 of the step, o *= 2^(lower - d), m -= lower, l *= 2^lower, where
+// lower = d (o stays) unless l would then pass 2^kMostSum.
+constexpr float kSpread = 40.0f;
+constexpr float kSpreadFactor = 1099511627776.0f;  // 2^kSpread
+constexpr float kMostSum = 60.0f;
+
+// The `lower` above, for a row whose l is `sum`.
+__device__ __forceinline__ float reference_shift(float d, float sum) {
+    return fminf(fminf(d, 100.0f), fmaxf(kMostSum - log2f(sum), 0.0f));
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -79,6 +100,9 @@ __device__ __forceinline__ void add_scaled(float4 &v, float &L, float f, const f
 // The kernel also gives the rows of padding and skipped sequences their zeros,
 // and records the malformed ones.
 constexpr int kJoinThreads = 256;
+// log2 by which the partial results' weights are lowered, so that the sum over
+// them stays in range whatever V's is
+constexpr float kPartialShift = 12.0f;
 
 template <typename T, int D, int ROWS, int G>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnView a, int32_t ctas,
@@ -104,12 +128,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int32_t lane = threadIdx.x % PER_ROW, group = threadIdx.x / PER_ROW % G, r0 = threadIdx.x / (PER_ROW * G);
     const int32_t rt = blockIdx.y * BLOCK_ROWS + r0, c = lane * 4;
     if (e.last_cta < 0 || blockIdx.y * BLOCK_ROWS >= e.rows) return;
-    // the group's partial results in order
+    // the group's partial results in order, of which each has weight 2^m
     constexpr int AT_ONCE = 8;
     float M = -INFINITY, L = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int32_t k0 = blockIdx.x + group; rt < e.rows && k0 <= e.last_cta; k0 += AT_ONCE * G) {
-        float m[AT_ONCE], l[AT_ONCE];
+        float m[AT_ONCE];
         float4 x[AT_ONCE];
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
@@ -118,7 +142,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             m[i] = -INFINITY;
             if (k <= e.last_cta) {
                 m[i] = __ldg(p + slot_rows * D + rt);
-                l[i] = __ldg(p + slot_rows * D + slot_rows + rt);
                 x[i] = __ldg(reinterpret_cast<const float4 *>(p + rt * D + c));
             }
         }
@@ -133,7 +156,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
             if (k0 + i * G > e.last_cta) break;
-            add_scaled(v, L, ex2(m[i] - mu), x[i], l[i]);
+            add_scaled(v, L, ex2(m[i] - mu - kPartialShift), x[i], 1.0f);
         }
     }
     if constexpr (G > 1) {
@@ -156,7 +179,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int32_t row = e.row + rt;
     const int32_t qi = row / a.group, qh = e.head * a.group + row % a.group;
     store4(static_cast<T *>(a.out.p) + static_cast<int64_t>(e.off + qi) * a.out.row + qh * a.out.head + c, v, 1.0f / L);
-    if (a.lse && c == 0) a.lse[static_cast<int64_t>(e.off + qi) * a.q_heads + qh] = (M + log2f(L)) * kLn2;
+    if (a.lse && c == 0) a.lse[static_cast<int64_t>(e.off + qi) * a.q_heads + qh] = (M + kPartialShift + log2f(L)) * kLn2;
 }
 
 // Opts a kernel in to `bytes` of shared memory, once per device and context (`ctx`: what has been done).

@@ -86,3 +86,47 @@ def test_a_nan_row_first_in_its_page_reaches_attention(dtype, n):
         out = cache.attention(q, tb, dev(lens), of, max_queries=n)
         assert bool(torch.isnan(out[:, :4]).all()) and bool(torch.isfinite(out[:, 4:]).all())
     assert status() == 0
+
+
+# ---------------------------------------------------------------- scales of V at both ends of their range
+
+def v_scales(kind, i, count, rng):
+    """Of page i of `count` of a sequence, in log2."""
+    if kind == "least":
+        return -120.0
+    if kind == "largest":
+        return 108.0
+    if kind == "least, then ordinary":
+        return -120.0 if i < count // 2 else -6.0
+    if kind == "ordinary, then least":
+        return -6.0 if i < count // 2 else -120.0
+    if kind == "rising":
+        return -120.0 + 200.0 * i / count
+    if kind == "falling":
+        return 80.0 - 200.0 * i / count
+    if kind == "zeros, then least":
+        return -np.inf if i < count // 3 else -120.0
+    return rng.choice([-120.0, -np.inf, -60.0, -20.0, 0.0, 30.0, 75.0])  # "any"
+
+
+KINDS = ["least", "largest", "least, then ordinary", "ordinary, then least", "rising", "falling", "zeros, then least", "any"]
+
+
+@pytest.mark.parametrize("k_growth", [1.0, 40.0, 0.02])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype,fmt,n,before,page,D", [
+    ("bf16", "int8", 1, 900, 16, 128), ("bf16", "e4m3", 2, 900, 32, 64), ("fp32", "int8", 2, 600, 16, 64),
+    ("fp32", "e4m3", 1, 6000, 64, 128), ("bf16", "int8", 48, 700, 16, 128), ("bf16", "e4m3", 200, 4000, 64, 64),
+])
+def test_attention_with_v_scales_anywhere(kind, k_growth, dtype, fmt, n, before, page, D):
+    """Scales from 2^-120 up, scores that grow or shrink along the sequence: the softmax's sum stays itself (lse), and so does the result."""
+    rng, cache, table, lens, offs = setup(before + n, [n, 3], [before, 40], page, fmt, 2, D)
+    for s in range(2):
+        pages = [int(p) for p in table[s] if p >= 0]
+        for i, p in enumerate(pages):
+            scale = float(np.exp2(np.float32(v_scales(kind, i, len(pages), rng))))
+            cache.v_scales[p] = scale
+            if scale == 0.0:
+                cache.v_pages[p] = 0
+            cache.k_scales[p] *= k_growth ** (i / len(pages))
+    check_attention(cache, rng, dtype, 8, [n, 3], [before, 40], table, lens, offs, q_width=1.0 if k_growth > 1 else 3.0)
