@@ -36,8 +36,8 @@
 //    column tiles of the MMA whose sums are added: 22 significant bits.
 //  - The page's scale of V is folded into the exponent, relative to a reference
 //    scale vr (attn_split.cuh): p' = 2^(s + log2 (vs / vr) - m), o sums p' codes,
-//    l sums p' vr / vs.  p' <= 2^14 whatever the scales, so f16 holds it.  m
-//    follows the maximum only when that grows by 2^14, so the sums are rarely
+//    l sums p' vr / vs.  p' <= 2^kGrow whatever the scales, so f16 holds it.  m
+//    follows the maximum only when p' would pass that, so the sums are rarely
 //    rescaled.
 // Measured, with the join: 256 sequences of about 4096 tokens, 64 heads on 8 of
 // 128, int8: 318 us, 5.8 TB/s (0.86 of a copy's rate; SMs that reach the memory
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 for (int u = 0; u < RT; ++u)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float mn = fmaxf(m[u][i], mx[u][i]);
+                        const float mn = fmaxf(m[u][i], mx[u][i] - kStartDecode);
                         const float f = m[u][i] == -INFINITY ? 0.0f : ex2(m[u][i] - mn);
                         m[u][i] = mn;
                         l[u][i] *= f;

@@ -27,7 +27,7 @@
 //    looks up the pages and scales of the key tiles, four tiles ahead.
 //  - q is f16 times a power of two per row (exact for bf16), P is f16 (11
 //    bits) with the page's scale of V in its exponent (attn_split.cuh); a
-//    row's sums are rescaled only when its maximum grew by 2^14.
+//    row's sums are rescaled only when a p' would leave f16.
 //  - Tensor Memory: S_A, S_B (128 columns each, P over the first 64), O_A, O_B.
 // The key tiles of all items form one line that the CTAs share equally
 // (attn_split.cuh), so causal and ragged work is level to one tile.
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     }
                     const bool grow = mx > m + kGrow;
                     if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
-                        const float mn = grow ? mx : m;
+                        const float mn = grow ? mx - kStartPrefill : m;
                         const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn);
                         m = mn;
                         l *= f;
@@ -593,6 +593,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     }
                     const float mu = m == -INFINITY ? 0.0f : m;
                     uint32_t pk[32];
+                    // (first the half's own sum: l, which may be far larger than each
+                    // of the terms of a long tail, is rounded once for 64 keys)
+                    float half = 0.0f;
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         const uint64_t c2 = pack2(c[v], c[v]), d2 = pack2(d[v] - mu, d[v] - mu);
@@ -609,8 +612,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         }
                         float x, y;
                         unpack2(sum, x, y);
-                        l = fmaf(x + y, tile.scales[4 * h + v].z, l);
+                        half = fmaf(x + y, tile.scales[4 * h + v].z, half);
                     }
+                    l += half;
                     tmem_st_32x32b_x32(ts + 32 * h, pk);
                     tmem_st_wait();
                     tc_fence_before_sync();

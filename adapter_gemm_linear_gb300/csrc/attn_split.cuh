@@ -37,10 +37,16 @@ __device__ __forceinline__ float *partial_at(const AttnView &a, int32_t cta, int
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-// log2 growth of a row's maximum that rescales its sums: probabilities stay
-// below 2^14, well inside f16.  (With 8 one key tile in two of a long prompt
-// whose pages differ in scale waited for some warp's rescaling.)
-constexpr float kGrow = 14.0f;
+// Where in f16's range the probabilities p' lie that enter the second product: a
+// row's sums are (re)scaled so that the largest so far is 2^start, and again
+// when one would pass 2^kGrow (below f16's largest, 65504).  What lies below
+// 2^-14 has steps of 2^-24, so the largest p' are started high: a p' is off by
+// 2^-25 at most, 2^-(25 + start) of the row's largest, which a long flat tail behind a
+// dominant key adds up.  In the decode kernel the start costs nothing (0, 4
+// and 8 within 1% of each other).  The prompt kernel waits for each rescaling of
+// a row of 128: 16 prompts take 210, 213, 227 and 242 us with starts of 0,
+// 4, 6 and 8, the long chunk 824, 835, 844 and 848.
+constexpr float kStartDecode = 8.0f, kStartPrefill = 4.0f, kGrow = 15.9f;
 
 // The scales of V's pages, as the exponents of the probabilities take them: in
 // log2 relative to a reference, the scale vr of a page that the row's sums

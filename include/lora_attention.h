@@ -182,8 +182,15 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * Rows outside every sequence are not written.
  * max_queries bounds the rows of one sequence (it and max_pages choose the kernel); a
  * sequence with more rows is recorded (SEGMENTS) and skipped.
- * Precision: products with the codes exact, fp32 sums; probabilities enter
- * the second product with 11 significant bits for bf16 calls, 22 for fp32.
+ * Precision: products with the codes exact, fp32 sums.  A probability p_j
+ * enters the second product, times its page's scale of V, with 11 significant
+ * bits for bf16 calls and 22 for fp32 ones, but not with less than a fixed
+ * step: with P the row's largest p_j * (page's scale of V), each is off by at
+ * most 2^-29 P (bf16), 2^-33 P (bf16, where the call takes the kernel for few
+ * queries) or 2^-44 P (fp32) beyond that.  Over n keys this adds up to n 2^-29 P times
+ * the largest code, which stays below bf16's own rounding of the largest values
+ * up to a million keys.  V of pages whose scale is below 2^-40 of the largest
+ * that a query sees may count as zero or as that much.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (num_q_heads /
  * num_heads over 64; num_q_heads not a multiple; rows * num_q_heads of 2^31
  * or more), WORKSPACE, CUDA.

@@ -130,3 +130,49 @@ def test_attention_with_v_scales_anywhere(kind, k_growth, dtype, fmt, n, before,
                 cache.v_pages[p] = 0
             cache.k_scales[p] *= k_growth ** (i / len(pages))
     check_attention(cache, rng, dtype, 8, [n, 3], [before, 40], table, lens, offs, q_width=1.0 if k_growth > 1 else 3.0)
+
+
+# ---------------------------------------------------------------- probabilities far below the largest
+
+def sink_and_tail(fmt, n, before, page, D, below, H=1):
+    """A first key whose score is `below` (log2) above all others', which are equal; V of the first is zero but in dimension 0."""
+    rng, cache, table, lens, offs = setup(int(before + below), [n], [before], page, fmt, H, D)
+    kp = torch.zeros((cache.num_pages, H, page, D), dtype=torch.float32)
+    first = int(table[0][0])
+    kp[first, :, 0, 0] = 96.0
+    vp = torch.from_numpy(rng.integers(4, 8, (cache.num_pages, H, page, D)).astype(np.float32) * 16)  # codes of both formats
+    vp[first, :, 0] = 0.0
+    vp[first, :, 0, 0] = 96.0
+    tiles = page // 16
+    cache.k_pages.copy_(kp.view(-1, H, tiles, 16, D // 64, 64).transpose(3, 4).to(cache.k_pages.dtype))
+    cache.v_pages.copy_(vp.view(-1, H, tiles, 4, 4, D // 4, 4).permute(0, 1, 2, 5, 3, 6, 4).to(cache.v_pages.dtype))
+    cache.k_scales.fill_(0.25)
+    cache.v_scales.fill_(0.125)
+    return cache, table, lens, offs
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("below", [20.4, 23.4, 26.4])
+@pytest.mark.parametrize("dtype,n,before,page,D,start,seqs", [
+    ("bf16", 1, 4000, 16, 128, 33, 1), ("bf16", 3, 30000, 64, 64, 33, 1), ("bf16", 20, 131072, 128, 64, 29, 1),
+    ("bf16", 1, 4000, 16, 128, 33, 64), ("fp32", 2, 2000, 32, 64, 44, 64), ("bf16", 40, 4000, 16, 128, 29, 20),
+    ("bf16", 20, 32768, 128, 64, 29, 20),
+])
+def test_a_long_tail_behind_a_dominant_key(fmt, below, dtype, n, before, page, D, start, seqs):
+    """What many small probabilities add up to: off by their 11 (22) bits and by 2^-start of the largest each, no more.
+    `seqs` sequences of the same pages (few CTAs an item: the tail is summed where the dominant key is)."""
+    H = 1 if seqs == 1 else 8
+    cache, table, lens, offs = sink_and_tail(fmt, n, before, page, D, below, H)
+    q = torch.zeros((seqs * n, 4 * H, D), dtype=DT[dtype], device=DEV)
+    q[..., 0] = 1.0
+    scale = float(np.float32(below * np.log(2.0) / 24.0))
+    out, lse = cache.attention(q, dev(np.repeat(table, seqs, 0)), dev(np.repeat(lens, seqs)),
+                               dev(np.arange(seqs + 1, dtype=np.int32) * n), scale=scale, max_queries=n, return_lse=True)
+    want, wl, _, score = R.attention(R.Paged(cache), q[:n].double().cpu().numpy(), table, lens, offs, scale)
+    rest = 2.0 ** -20 * (score + 16)
+    small = max(lens) * 2.0 ** -start * 112 * 0.125  # (the largest code is 112, the largest p is 1)
+    tol = np.abs(want) * ((2.0 ** -8 + 2.0 ** -11 if dtype == "bf16" else 2.0 ** -23 + 2.0 ** -21) + rest[..., None]) + small
+    err = np.abs(out.double().cpu().numpy().reshape(seqs, n, 4 * H, D) - want)
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of its tolerance, {np.max(err / np.abs(want)):.3g} of the result"
+    assert np.all(np.abs(lse.double().cpu().numpy().reshape(seqs, n, 4 * H) - wl) <= rest)
+    assert status() == 0
