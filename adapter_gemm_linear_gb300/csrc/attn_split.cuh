@@ -103,6 +103,9 @@ __device__ __forceinline__ void add_scaled(float4 &v, float &L, float f, const f
 // what bounds the kernel is their latency.  (Both kernels for one sequence of
 // 2000 tokens, 32 heads on 8, each of these in 16 CTAs: 14.3 us with G = 4,
 // 18.4 with 1, 16.4 with 8.)  Every sum's order is fixed.
+// The kernel may begin while the one before still writes what it joins, so after
+// its wait it reads through the L2 and never by the read-only path, which is
+// for data that nobody writes while a kernel runs.
 // The kernel also gives the rows of padding and skipped sequences their zeros,
 // and records the malformed ones.
 constexpr int kJoinThreads = 256;
@@ -147,8 +150,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             const float *p = partial_at(a, k, k == static_cast<int32_t>(blockIdx.x) ? 1 : 0, slot_rows, D);
             m[i] = -INFINITY;
             if (k <= e.last_cta) {
-                m[i] = __ldg(p + slot_rows * D + rt);
-                x[i] = __ldg(reinterpret_cast<const float4 *>(p + rt * D + c));
+                m[i] = __ldcg(p + slot_rows * D + rt);
+                x[i] = __ldcg(reinterpret_cast<const float4 *>(p + rt * D + c));
             }
         }
         float mn = M;

@@ -176,3 +176,19 @@ def test_a_long_tail_behind_a_dominant_key(fmt, below, dtype, n, before, page, D
     assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of its tolerance, {np.max(err / np.abs(want)):.3g} of the result"
     assert np.all(np.abs(lse.double().cpu().numpy().reshape(seqs, n, 4 * H) - wl) <= rest)
     assert status() == 0
+
+
+# ---------------------------------------------------------------- calls one after the other in one workspace
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 1), ("fp32", 2), ("bf16", 64)])
+def test_calls_that_share_a_workspace(dtype, n):
+    """The join starts beside the kernel whose partial results it reads: with other values in the same places before, each call's are its own."""
+    rng, cache, table, lens, offs = setup(7 + n, [n], [9000], 64, "int8", 2, 128)
+    args = dev(table), dev(lens), dev(offs)
+    qs = [draw(rng, (n, 16, 128), dtype, w)[0] for w in (1.0, 3.0, 0.2, 5.0)]
+    want = [cache.attention(q, *args, max_queries=n) for q in qs]
+    workspace = torch.full((1 << 27,), 0x7F, dtype=torch.uint8, device=DEV)
+    got = [cache.attention(qs[i % 4], *args, max_queries=n, workspace=workspace) for i in range(40)]
+    for i, out in enumerate(got):
+        assert torch.equal(out, want[i % 4]), i
+    assert status() == 0
