@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             for (int32_t t = it.tile0; t < it.tile1; ++t, ++n_tile, ++n_own) {
                 wait(&sm.tile_full[n_tile % kTileRing], (n_tile / kTileRing) & 1u, 55);
                 wait(&sm.s_full[X], n_own & 1u, 51 + X);
+                __syncwarp();  // (lanes may leave a wait apart; what follows is for the whole warp at once)
                 tc_fence_after_sync();
                 if (t == it.tile0) cr = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + sm.q_exponent[(n_item - 1) & 1u][rt]) << 23);
                 const KeyTile &tile = sm.tiles[n_tile % kTileRing];
@@ -586,6 +587,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             // s_full, of this one's first half when half_done says so
                             if (h > 0) {
                                 wait(&sm.half_done[X], n_own & 1u, 57);
+                                __syncwarp();
                                 tc_fence_after_sync();
                             }
                             rescale(to, f);
@@ -623,6 +625,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 }
             }
             wait(&sm.o_done[X], n_part & 1u, 53 + X);
+            __syncwarp();
             ++n_part;
             tc_fence_after_sync();
             const bool whole = (it.flags & (kFromStart | kToEnd)) == (kFromStart | kToEnd);
@@ -636,34 +639,36 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(to + 32 * i, o);
                 tmem_ld_wait(o);
-                if (rt >= rows) continue;
-                if (FMT == LORA_KV_E4M3 && __builtin_expect(hidden, 0)) {
-                    const uint32_t nan = nan_dims<D>(b, it.seq, it.head, it.tile0, it.tile1, all_lo, all_hi, kmin, kmax, 32 * i);
+                if (rt < rows) {
+                    if (FMT == LORA_KV_E4M3 && __builtin_expect(hidden, 0)) {
+                        const uint32_t nan = nan_dims<D>(b, it.seq, it.head, it.tile0, it.tile1, all_lo, all_hi, kmin, kmax, 32 * i);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (nan >> e & 1u) o[e] = 0x7FFFFFFFu;
-                }
-                // (one after the other: 1 / l times vr may leave fp32's normal range)
+                        for (int e = 0; e < 32; ++e)
+                            if (nan >> e & 1u) o[e] = 0x7FFFFFFFu;
+                    }
+                    // (one after the other: 1 / l times vr may leave fp32's normal range)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv * vr);
-                if (whole) {
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv * vr);
+                    if (whole) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 16) {
-                        uint32_t h[8];
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t h[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
-                            h[k] = *reinterpret_cast<const uint32_t *>(&two);
+                            for (int k = 0; k < 8; ++k) {
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
+                                h[k] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            store_32(dst + 32 * i + e, h);
                         }
-                        store_32(dst + 32 * i + e, h);
-                    }
-                } else {
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        const uint32_t w[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
-                        store_32(part + rt * D + 32 * i + e, w);
+                        for (int e = 0; e < 32; e += 8) {
+                            const uint32_t w[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                            store_32(part + rt * D + 32 * i + e, w);
+                        }
                     }
                 }
+                __syncwarp();  // before the next load, which takes the whole warp
             }
             tc_fence_before_sync();
             if (rt < rows) {

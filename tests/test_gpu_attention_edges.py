@@ -192,3 +192,26 @@ def test_calls_that_share_a_workspace(dtype, n):
     for i, out in enumerate(got):
         assert torch.equal(out, want[i % 4]), i
     assert status() == 0
+
+
+# ---------------------------------------------------------------- row tiles that end inside a warp
+
+@pytest.mark.parametrize("fmt,D", [("int8", 128), ("e4m3", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("n,G", [(17, 1), (33, 1), (9, 5), (127, 1), (43, 3), (130, 1), (37, 7), (255, 1), (259, 1), (20, 13)])
+def test_attention_row_tiles_that_end_inside_a_warp(n, G, fmt, D):
+    """The prompt kernel with 1 to 255 rows in its last tile, whole items and split ones, and NaN in V that only some rows see."""
+    news, befores = [n, n, 1], [0, 2000, 300]
+    rng, cache, table, lens, offs = setup(n * G, news, befores, 16, fmt, 1, D)
+    check_attention(cache, rng, "bf16", G, news, befores, table, lens, offs)
+    if fmt == "e4m3":
+        q, _ = draw(rng, (int(offs[-1]), G, D), "bf16")
+        args = q, dev(table), dev(lens), dev(offs)
+        clean = cache.attention(*args, max_queries=n)
+        t, d = n - n // 3 - 1, D - 5  # a token of the first sequence, whose later queries see it
+        page = cache.v_pages[int(table[0][t // 16])].view(torch.uint8)
+        page[0, 0, d // 4, t % 16 // 4, d % 4, t % 4] = 0x7F
+        out = cache.attention(*args, max_queries=n)
+        want = torch.zeros_like(out, dtype=torch.bool)
+        want[t:n, :, d] = True
+        assert torch.equal(torch.isnan(out), want) and torch.equal(out[~want], clean[~want])
+    assert status() == 0
