@@ -378,8 +378,9 @@ def linear_forward(x: torch.Tensor, projections, row_adapter=None, seg_offsets=N
 
 
 def arm_test_wait_timeout(limit_ns: int) -> None:
-    """lora_test_arm_wait_timeout: the next forward's split-K counter waits
-    expect an arrival that never comes and give up after ``limit_ns``."""
+    """lora_test_arm_wait_timeout: the next forward's split-K counter waits (or
+    the next attention call's waits for its tiles) expect an arrival that never
+    comes and give up after ``limit_ns``."""
     _check(_lib.lib().lora_test_arm_wait_timeout(int(limit_ns)), "lora_test_arm_wait_timeout")
 
 

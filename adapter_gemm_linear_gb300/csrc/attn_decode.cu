@@ -218,7 +218,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 
     // ---- the plan: where this CTA's range of units begins
     if (threadIdx.x < kBatches) {
-        mbar_init(&sm.full[threadIdx.x], 1);
+        mbar_init(&sm.full[threadIdx.x], a.test_wait_ns ? 2 : 1);
         mbar_init(&sm.empty[threadIdx.x], kWarps);
         fence_mbar_init();
     }
@@ -262,9 +262,10 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     __syncthreads();
     Walk<ROWS> walk(a, w0, w1, sm.seq, sm.base);
     volatile int32_t *dead = &sm.dead;
+    const uint64_t limit = a.test_wait_ns ? a.test_wait_ns : kWaitNs;
 
     auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t site) {
-        if (*dead || mbar_wait_bounded(bar, parity, kWaitNs)) return;
+        if (*dead || mbar_wait_bounded(bar, parity, limit)) return;
         record_error(b.status, kDevTimeout, site);
         *dead = 1;
     };
@@ -311,10 +312,11 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             }
             __syncwarp();
             wait(&sm.empty[n % kBatches], ((n / kBatches) & 1u) ^ 1u, 40);
+            // (what the consumers may still read is left alone; they see `dead` when they look for more)
+            if (__any_sync(0xffffffffu, *dead)) break;
             sm.info[n % kBatches][lane] = x;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.full[n % kBatches]);
-            if (*dead) break;
         }
         return;
     }

@@ -103,6 +103,7 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
     v->window = a->window;
     v->max_queries = a->max_queries;
     v->workspace = static_cast<unsigned char *>(a->workspace);
+    v->test_wait_ns = 0;
     return LORA_OK;
 }
 
@@ -227,6 +228,7 @@ lora_status_t lora_kv_attention(const lora_kv_cache_t *cache, const lora_kv_batc
     if (!v.workspace || args->workspace_bytes < need) return LORA_ERR_WORKSPACE;
     if (!aligned(v.workspace, 16)) return LORA_ERR_ALIGNMENT;
     cudaError_t e = lora::device_status_ptr(&v.kv.status);
+    v.test_wait_ns = lora::take_test_wait_limit();
     if (e == cudaSuccess)
         e = many_queries(v, args->dtype)
                 ? lora::launch_attn_prefill(v, cache->format, cache->head_dim, as_stream(stream))

@@ -46,6 +46,9 @@ struct AttnView {
     float scale;
     int32_t causal, window, max_queries;
     unsigned char *workspace;
+    // lora_test_arm_wait_timeout: 0, or the time limit of this call's waits, of
+    // which some then expect one arrival more than there is
+    uint64_t test_wait_ns;
 };
 
 cudaError_t launch_rope(const RopeView &v, lora_dtype_t dtype, cudaStream_t stream);

@@ -218,14 +218,14 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 }
 
 // Wait for a phase of an mbarrier, bounded by the SM's clock (cheaper to read
-// than the global timer).
-__device__ __forceinline__ bool wait_clocks(uint64_t *bar, uint32_t parity) {
+// than the global timer), or until another wait has run out (`dead`).
+__device__ __forceinline__ bool wait_clocks(uint64_t *bar, uint32_t parity, long long limit, const volatile int32_t *dead) {
     const long long t0 = clock64();
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-        if (clock64() - t0 > kWaitClocks) return false;
+        if (*dead || clock64() - t0 > limit) return false;
     }
 }
 
@@ -373,11 +373,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const KvView &b = a.kv;
     JoinEntry *joins = join_entries(a, gridDim.x, kRows, D);
-    volatile int32_t *dead = &sm.dead;  // where a wait ran out (0: none did); then nobody waits any more
+    // where a wait ran out (0: none did); then nobody waits any more, no entry of
+    // the rings is written again, and every role ends when it looks for more
+    volatile int32_t *dead = &sm.dead;
+    const long long limit = a.test_wait_ns ? 2 * static_cast<long long>(a.test_wait_ns) : kWaitClocks;  // (2 GHz)
 
     auto wait = [&](uint64_t *bar, uint32_t parity, int32_t site) {
-        if (!mbar_try_wait(bar, parity) && !*dead && !wait_clocks(bar, parity)) *dead = site;
+        if (!mbar_try_wait(bar, parity) && !wait_clocks(bar, parity, limit, dead) && !*dead) *dead = site;
     };
+    auto any_dead = [&] { return __any_sync(0xffffffffu, *dead != 0) != 0; };  // the same for the whole warp
 
     // the joining kernel may come in as soon as there is room beside CTAs that
     // run or have none of the work; it waits for this one's end before it reads
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.k_full[i], 4);
             mbar_init(&sm.k_empty[i], 1);
-            mbar_init(&sm.v_full[i], 4);
+            mbar_init(&sm.v_full[i], a.test_wait_ns ? 5 : 4);
             mbar_init(&sm.v_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_ready[i][0], 4);
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             const uint32_t e = n_item % kItemRing;
             wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 50);
             it = sm.items[e];
-            if (*dead) it.tile1 = -1;
+            if (any_dead()) it.tile1 = -1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.item_empty[e]);
             ++n_item;
@@ -698,7 +702,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         auto look = [&](Tile &x, uint32_t n) {
             const uint32_t e = n % kTileRing;
             wait(&sm.tile_full[e], (n / kTileRing) & 1u, 60);
-            x.key0 = *dead ? -1 : sm.tiles[e].key0;
+            x.key0 = any_dead() ? -1 : sm.tiles[e].key0;
             x.len = sm.tiles[e].len;
             x.at[0] = sm.tiles[e].at[2 * wq];
             x.at[1] = sm.tiles[e].at[2 * wq + 1];
@@ -914,7 +918,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 const uint32_t nx = sm.items[e].n * a.group - sm.items[e].row_tile * kRows > kHalf ? 2 : 1;  // tile B may be empty
                 __syncwarp();
                 if (elect_one()) mbar_arrive(&sm.item_empty[e]);
-                if (stop || *dead) break;
+                if (any_dead() || stop) break;
                 wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
 #pragma unroll 1
                 for (uint32_t X = 0; X < nx; ++X) {
@@ -932,6 +936,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     const uint32_t st1 = (n_tile + 1) & 1u, ph1 = ((n_tile + 1) >> 1) & 1u;
                     const bool more = j + 1 < nt;
                     wait(&sm.v_full[st], ph, 74);
+                    if (any_dead()) break;  // no products of what may not be there
 #pragma unroll 1
                     for (uint32_t X = 0; X < nx; ++X) {
 #pragma unroll 1
@@ -961,14 +966,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             }
             // nothing of this thread's may be in flight when Tensor Memory is freed
             commit(&sm.drain);
-            wait_clocks(&sm.drain, 0);
+            const int32_t alone = 0;
+            wait_clocks(&sm.drain, 0, kWaitClocks, &alone);
         } else if (warp == 13) {
             // ============================================ the items
             uint32_t n_item = 0;
             auto publish = [&](const Item &it) {
                 const uint32_t e = n_item % kItemRing;
                 wait(&sm.item_empty[e], ((n_item / kItemRing) & 1u) ^ 1u, 80);
-                if (lane == 0) {
+                if (!any_dead() && lane == 0) {
                     sm.items[e] = it;
                     mbar_arrive(&sm.item_full[e]);
                 }
@@ -997,7 +1003,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     it.last_cta = static_cast<int32_t>(((w + (units - skip)) * ctas - 1) / total);
                     if (it.tile1 > it.tile0) publish(it);
                     w += take;
-                    if (w >= w1 || *dead) break;
+                    if (any_dead() || w >= w1) break;
                     skip = 0;
                     if (++it.row_tile == count) {
                         it.row_tile = 0;
@@ -1021,7 +1027,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 const uint32_t e = n_item % kItemRing;
                 wait(&sm.item_full[e], (n_item / kItemRing) & 1u, 90);
                 const int32_t seq = sm.items[e].seq, head = sm.items[e].head, len = sm.items[e].len;
-                const int32_t tile0 = sm.items[e].tile0, tile1 = *dead ? -1 : sm.items[e].tile1;
+                if (any_dead()) break;
+                const int32_t tile0 = sm.items[e].tile0, tile1 = sm.items[e].tile1;
                 const int32_t off = sm.items[e].off, n = sm.items[e].n, row_tile = sm.items[e].row_tile;
                 // keys that every row of the item sees
                 const int32_t all_hi = a.causal ? len - n + row_tile * kRows / a.group + 1 : len;
@@ -1073,6 +1080,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     for (int q = 0; q < 4 && t0 + q < max(tile1, tile0 + 1); ++q) {
                         const uint32_t r = n_tile % kTileRing;
                         wait(&sm.tile_empty[r], ((n_tile / kTileRing) & 1u) ^ 1u, 91);
+                        if (any_dead()) break;
                         if ((lane >> 3) == q) {
                             sm.tiles[r].scales[sub] = make_float4(ks, lv, iv, 0.0f);
                             sm.tiles[r].at[sub] = at;

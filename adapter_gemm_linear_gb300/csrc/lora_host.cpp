@@ -18,6 +18,8 @@ static thread_local int32_t g_last_cuda_error = 0;  // behind this thread's last
 
 void lora::count_launches(int n) { g_kernel_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }
 
+uint64_t lora::take_test_wait_limit() { return g_test_wait_limit_ns.exchange(0); }
+
 void lora::set_last_cuda_error(int32_t code) { g_last_cuda_error = code; }
 
 using lora::align_up;
@@ -605,7 +607,7 @@ static lora_status_t linear_forward(const lora_forward_args_t *args, void *strea
     plan.counters = reinterpret_cast<int32_t *>(base + ws.counter_off);
     plan.n_counters = static_cast<int32_t>((ws.total - ws.counter_off) / sizeof(int32_t));
     cudaStream_t st = as_stream(stream);
-    plan.test_wait_limit_ns = g_test_wait_limit_ns.exchange(0);
+    plan.test_wait_limit_ns = lora::take_test_wait_limit();
     plan.seg_offsets = plan.seg_adapter = nullptr;
     plan.num_segs = 0;
     plan.rows_in_plan = false;

@@ -171,6 +171,9 @@ struct ForwardPlan {
 // The code lora_last_cuda_error() reports for the calling thread.
 void set_last_cuda_error(int32_t code);
 
+// The limit that lora_test_arm_wait_timeout armed, taken by the call that asks (0: none).
+uint64_t take_test_wait_limit();
+
 // Count of kernels launched by the library (lora_kernel_launches).
 void count_launches(int n);
 

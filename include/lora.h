@@ -383,11 +383,16 @@ lora_status_t lora_get_device_status(void *stream, int32_t *detail);
 
 /*
  * Testing hook for the failure path of the kernels' bounded waits (no
- * counterpart in the pages).  Arms the next lora_linear_forward call on any
- * thread: in that call every split-K tile-counter wait of the tensor-core
- * GEMM (small M), and every wait of the large-M two-SM GEMM for a token
- * tile's LoRA intermediate, waits for one arrival more than the launch makes,
- * giving up after limit_ns (1 ms .. 2 s) instead of the normal 2 s.  The
+ * counterpart in the pages).  Arms the next lora_linear_forward or
+ * lora_kv_attention call on any thread.  In a forward every split-K
+ * tile-counter wait of the tensor-core GEMM (small M), and every wait of the
+ * large-M two-SM GEMM for a token tile's LoRA intermediate, waits for one
+ * arrival more than the launch makes, giving up after limit_ns (1 ms .. 2 s)
+ * instead of the normal 2 s; in an attention call the waits for looked-up
+ * pages (few queries) or for converted values (prompts) do, and all others
+ * have the same limit.  An attention call whose waits ran out records
+ * LORA_ERR_DEVICE_TIMEOUT, leaves `out`, `lse` and the workspace undefined,
+ * writes nothing else, releases its tensor memory and ends.  In a forward the
  * waits then run out: the GEMM records LORA_ERR_DEVICE_TIMEOUT in the status
  * word, writes no output for the tiles it could not finish, releases its
  * tensor memory and ends normally (after its other bounded waits, up to a

@@ -215,3 +215,34 @@ def test_attention_row_tiles_that_end_inside_a_warp(n, G, fmt, D):
         want[t:n, :, d] = True
         assert torch.equal(torch.isnan(out), want) and torch.equal(out[~want], clean[~want])
     assert status() == 0
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("fmt,dtype,n,before,D", [
+    ("int8", "bf16", 1, 900, 128), ("e4m3", "fp32", 3, 3000, 64),                               # the kernel for few queries
+    ("int8", "bf16", 60, 100, 128), ("e4m3", "bf16", 300, 5000, 64), ("int8", "bf16", 17, 40000, 128),  # and for prompts
+])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(fmt, dtype, n, before, D):
+    """With an arrival fewer than its waits expect, a call ends by itself after their limit and says so; nothing outside its
+    outputs is written, and the same call after it gives the same bits as before."""
+    from adapter_gemm_linear_gb300 import arm_test_wait_timeout, device_status
+    rng, cache, table, lens, offs = setup(n + D, [n, 2], [before, 70], 32, fmt, 2, D)
+    T = int(offs[-1])
+    q, _ = draw(rng, (T, 8, D), dtype)
+    args = dev(table), dev(lens), dev(offs)
+    want = cache.attention(q, *args, max_queries=n + 1, return_lse=True)
+    held = [t.clone() for t in (cache.k_pages, cache.v_pages, cache.k_scales, cache.v_scales, q)]
+    out = torch.full((T + 8, 8, D), 7.0, dtype=q.dtype, device=DEV)
+    status()
+    for limit in (5_000_000, 20_000_000):
+        arm_test_wait_timeout(limit)
+        cache.attention(q, *args, max_queries=n + 1, out=out[4:T + 4])
+        st, site = device_status()
+        assert st == 10 and 40 <= site <= 91, (st, site)
+        assert bool((out[:4] == 7).all()) and bool((out[T + 4:] == 7).all())
+        for t, h in zip((cache.k_pages, cache.v_pages, cache.k_scales, cache.v_scales, q), held):
+            assert torch.equal(t.view(torch.uint8), h.view(torch.uint8))
+        again = cache.attention(q, *args, max_queries=n + 1, return_lse=True)
+        assert status() == 0
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
