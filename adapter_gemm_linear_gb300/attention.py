@@ -108,7 +108,9 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: tor
     ``inverse`` turns the other way: the gradient of the call, or its undoing.
     ``stream``: launch there instead of on the current stream."""
     device, shape = q.get_device(), q.shape
-    if stream is not None or (device >= 0 and device != _current_device()):
+    if device < 0:
+        raise ValueError(f"q must be on a CUDA device, not on {q.device}")
+    if stream is not None or device != _current_device():
         return _elsewhere(rope, device, stream, (q, k, cos, sin, positions), axes=axes, interleaved=interleaved,
                           inverse=inverse, q_out=q_out, k_out=k_out)
     if len(shape) != 3:
