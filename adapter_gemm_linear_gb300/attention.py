@@ -178,17 +178,21 @@ class KvCache:
         if device is None:
             device = k_pages.device if k_pages is not None else "cuda"
         device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"a KvCache is on a CUDA device, not on {device}")
         tiles = (self.num_pages, self.num_heads, self.page_tokens // LORA_BLOCK_ROWS)
 
         def tensor(t, shape, dt, name):
             if t is None:
                 return torch.zeros(shape, dtype=dt, device=device)
-            if t.shape != shape or t.dtype != dt or not t.is_contiguous() or t.device.type != device.type:
+            if t.shape != shape or t.dtype != dt or not t.is_contiguous() or t.device.type != "cuda" or \
+                    (device.index is not None and t.device != device):
                 raise ValueError(f"{name} must be contiguous {dt} {tuple(shape)} on {device}")
             return t
 
         D = self.head_dim
         self.k_pages = tensor(k_pages, tiles + (D // 64, LORA_BLOCK_ROWS, 64), dtype, "k_pages")
+        device = self.k_pages.device  # ("cuda" names none: the other buffers are of k_pages' own)
         self.v_pages = tensor(v_pages, tiles + (D // 4, 4, 4, 4), dtype, "v_pages")
         self.k_scales = tensor(k_scales, tiles[:2], torch.float32, "k_scales")
         self.v_scales = tensor(v_scales, tiles[:2], torch.float32, "v_scales")

@@ -13,3 +13,45 @@ def test_rope_refuses_tensors_of_the_host():
         rope(x, None, table, table, pos)
     with pytest.raises(ValueError, match="CUDA"):
         rope(x, x, table, table, pos, q_out=x, k_out=x)
+
+
+def test_a_cache_of_the_host_is_refused():
+    with pytest.raises(ValueError, match="CUDA"):
+        KvCache(4, 2, 64, 16, "int8", device="cpu")
+    pages = torch.zeros((4, 2, 1, 1, 16, 64), dtype=torch.int8)
+    with pytest.raises(ValueError, match="CUDA"):
+        KvCache(4, 2, 64, 16, "int8", k_pages=pages)
+
+
+class Where:
+    """A tensor, as far as KvCache looks at one, of a device that need not be there."""
+
+    def __init__(self, device, shape, dtype):
+        self.device, self.shape, self.dtype = torch.device(device), torch.Size(shape), dtype
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.device.index
+
+    def data_ptr(self):
+        return 0x10000
+
+
+def test_the_four_buffers_of_a_cache_are_of_one_device():
+    def buffers(*devices):
+        return {name: Where(d, shape, dt) for name, d, shape, dt in zip(
+            ("k_pages", "v_pages", "k_scales", "v_scales"), devices,
+            ((4, 2, 1, 1, 16, 64), (4, 2, 1, 16, 4, 4, 4), (4, 2), (4, 2)),
+            (torch.int8, torch.int8, torch.float32, torch.float32))}
+
+    KvCache(4, 2, 64, 16, "int8", **buffers("cuda:0", "cuda:0", "cuda:0", "cuda:0"))
+    KvCache(4, 2, 64, 16, "int8", device="cuda", **buffers("cuda:1", "cuda:1", "cuda:1", "cuda:1"))
+    for i in range(1, 4):
+        devices = ["cuda:0"] * 4
+        devices[i] = "cuda:1"
+        with pytest.raises(ValueError, match="cuda:0"):
+            KvCache(4, 2, 64, 16, "int8", **buffers(*devices))
+    with pytest.raises(ValueError):
+        KvCache(4, 2, 64, 16, "int8", device="cuda:1", **buffers(*["cuda:0"] * 4))
