@@ -77,6 +77,8 @@ def _elsewhere(f, device: int, stream: Optional[torch.cuda.Stream], args, **kw):
     if stream is None:
         with torch.cuda.device(device):
             return f(*args, **kw)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on device {device}")
     with torch.cuda.stream(stream):
         result = f(*args, **kw)
     for t in list(args) + list(kw.values()):

@@ -55,3 +55,16 @@ def test_the_four_buffers_of_a_cache_are_of_one_device():
             KvCache(4, 2, 64, 16, "int8", **buffers(*devices))
     with pytest.raises(ValueError):
         KvCache(4, 2, 64, 16, "int8", device="cuda:1", **buffers(*["cuda:0"] * 4))
+
+
+class Stream:
+    def __init__(self, device):
+        self.device = torch.device(device)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """(Such a call used to run again without the stream.)"""
+    ran = []
+    with pytest.raises(ValueError, match="cuda:1"):
+        attention._elsewhere(lambda *a, **kw: ran.append(1), 0, Stream("cuda:1"), ())
+    assert not ran
