@@ -320,6 +320,8 @@ class KvCache:
                 if need:
                     self._workspace[key] = need
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        elif workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {self.device}")
         _call(L.lora_kv_attention(self._ref, batch, _ATTENTION_ARGS.pack(
             *head, workspace.data_ptr(), workspace.numel() * workspace.element_size()), _current_stream(device)),
             "lora_kv_attention")

@@ -246,3 +246,16 @@ def test_waits_that_run_out_are_reported_and_the_next_call_is_right(fmt, dtype, 
         again = cache.attention(q, *args, max_queries=n + 1, return_lse=True)
         assert status() == 0
         assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+# ---------------------------------------------------------------- the binding
+
+def test_a_workspace_that_the_kernels_cannot_use_is_refused():
+    cache = KvCache(4, 2, 128, 16, "int8")
+    tb, ln = torch.zeros((2, 2), dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    q = torch.zeros((2, 2, 128), device=DEV)
+    for bad in (torch.empty(1 << 27, dtype=torch.uint8), torch.empty((1 << 27, 2), dtype=torch.uint8, device=DEV)[:, 0]):
+        with pytest.raises(ValueError):
+            cache.attention(q, tb, ln, workspace=bad)
+    assert bool((cache.attention(q, tb, ln, workspace=torch.empty(1 << 25, device=DEV)) == 0).all())
+    assert status() == 0
