@@ -43,6 +43,23 @@ __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
+// Every bit of the low four, twice.
+__device__ __forceinline__ uint32_t twice(uint32_t b) {
+    return (b & 1u) * 3u | (b >> 1 & 1u) * 12u | (b >> 2 & 1u) * 48u | (b >> 3 & 1u) * 192u;
+}
+
+// The VE values in `a`, with those of `b` where `from_b` has their bit.
+template <int VE>
+__device__ __forceinline__ uint4 replace(const uint4 &a, const uint4 &b, uint32_t from_b) {
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m[i] = VE == 4 ? (from_b >> i & 1u) * 0xFFFFFFFFu
+                       : (from_b >> 2 * i & 1u) * 0xFFFFu | (from_b >> (2 * i + 1) & 1u) * 0xFFFF0000u;
+    return make_uint4((a.x & ~m[0]) | (b.x & m[0]), (a.y & ~m[1]) | (b.y & m[1]), (a.z & ~m[2]) | (b.z & m[2]),
+                      (a.w & ~m[3]) | (b.w & m[3]));
+}
+
 // Thread (x, y, z): chunk x (a head's row is read in whole lines), head group
 // y, row z of the block.  Group j has heads j, j + groups, ..., of which HPT are
 // in work at once.
@@ -60,6 +77,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads) rope_kernel(const __grid_cons
     const int32_t d1 = !turn ? d0 : a.interleaved ? d0 + VE : d0 + a.rot_dim / 2;
 
     float cs[VE], sn[VE];
+    uint32_t out_of_range = 0;  // a bit a pair: these stay as they are
     if (turn) {
         const int32_t half = a.rot_dim / 2;
         auto position = [&](int32_t axis) {  // < 0: out of range
@@ -79,20 +97,15 @@ __global__ void __launch_bounds__(kRopeMaxThreads) rope_kernel(const __grid_cons
                 cs[e] = x.x; cs[e + 1] = x.y; cs[e + 2] = x.z; cs[e + 3] = x.w;
                 sn[e] = y.x; sn[e + 1] = y.y; sn[e + 2] = y.z; sn[e + 3] = y.w;
             }
-            if (p < 0) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    cs[e] = 1.0f;
-                    sn[e] = 0.0f;
-                }
-            }
+            if (p < 0) out_of_range = (1u << VE) - 1u;
         } else {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 const int32_t p = position(a.pair_axis[c * VE + e]);
                 const int64_t at = static_cast<int64_t>(max(p, 0)) * half + c * VE + e;
-                cs[e] = p < 0 ? 1.0f : __ldg(a.cos_table + at);
-                sn[e] = p < 0 ? 0.0f : __ldg(a.sin_table + at);
+                cs[e] = __ldg(a.cos_table + at);
+                sn[e] = __ldg(a.sin_table + at);
+                if (p < 0) out_of_range |= 1u << e;
             }
         }
         if (a.inverse) {
@@ -141,8 +154,14 @@ __global__ void __launch_bounds__(kRopeMaxThreads) rope_kernel(const __grid_cons
                     w[e] = v[e] * cs[e] + u[e] * sn[e];
                 }
             }
-            *reinterpret_cast<uint4 *>(dst + d0) = pack(y);
-            *reinterpret_cast<uint4 *>(dst + d1) = pack(w);
+            uint4 py = pack(y), pw = pack(w);
+            if (__builtin_expect(out_of_range != 0, 0)) {
+                // (not by a cosine of 1: the other value of a pair may be infinite or NaN)
+                py = replace<VE>(py, x[i][0], a.interleaved ? twice(out_of_range) : out_of_range);
+                pw = replace<VE>(pw, x[i][1], a.interleaved ? twice(out_of_range >> (VE / 2)) : out_of_range);
+            }
+            *reinterpret_cast<uint4 *>(dst + d0) = py;
+            *reinterpret_cast<uint4 *>(dst + d1) = pw;
         }
     }
 }

@@ -259,3 +259,31 @@ def test_a_workspace_that_the_kernels_cannot_use_is_refused():
             cache.attention(q, tb, ln, workspace=bad)
     assert bool((cache.attention(q, tb, ln, workspace=torch.empty(1 << 25, device=DEV)) == 0).all())
     assert status() == 0
+
+
+# ---------------------------------------------------------------- rotary positions out of range
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("axes,interleaved,rows", [(1, False, 4), (3, True, 4), (2, False, 4000)])
+def test_pairs_of_positions_out_of_range_stay_as_they_are(dtype, axes, interleaved, rows):
+    """To the bit, infinities, NaN and -0 among them; the other pairs of the row are turned as ever."""
+    from adapter_gemm_linear_gb300 import device_status, rope, rope_tables
+    rng = np.random.default_rng(axes)
+    q, _ = draw(rng, (rows, 5, 64), dtype)
+    q[1, :, ::3], q[1, :, 1::3], q[1, 2] = float("nan"), float("inf"), -0.0
+    cos, sin = rope_tables(50, 64, device=DEV)
+    pos = rng.integers(0, 50, (axes, rows)).astype(np.int32)
+    ax = [int(a) for a in rng.integers(0, axes, 32)]
+    good, _ = rope(q, None, cos, sin, dev(pos), axes=ax, interleaved=interleaved)
+    pos[axes - 1, 1:] = 50
+    pos[axes - 1, 2:] = -3
+    status()
+    out, _ = rope(q, None, cos, sin, dev(pos), axes=ax, interleaved=interleaved)
+    st, row = device_status()
+    assert st == 11 and 1 <= row < rows
+    pairs = torch.tensor(ax) == axes - 1
+    stays = (pairs.repeat_interleave(2) if interleaved else pairs.repeat(2)).to(DEV)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(out.view(bits)[1:, :, stays], q.view(bits)[1:, :, stays])
+    assert torch.equal(out.view(bits)[1:, :, ~stays], good.view(bits)[1:, :, ~stays])
+    assert torch.equal(out.view(bits)[0], good.view(bits)[0])
