@@ -318,6 +318,8 @@ class KvCache:
             if need is None:
                 need = L.lora_kv_attention_workspace_bytes(self._ref, batch, _ATTENTION_ARGS.pack(*head, 0, 0))
                 if need:
+                    if len(self._workspace) >= 256:  # (ever new numbers of rows)
+                        self._workspace.clear()
                     self._workspace[key] = need
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
         elif workspace.get_device() != device or not workspace.is_contiguous():

@@ -287,3 +287,15 @@ def test_pairs_of_positions_out_of_range_stay_as_they_are(dtype, axes, interleav
     assert torch.equal(out.view(bits)[1:, :, stays], q.view(bits)[1:, :, stays])
     assert torch.equal(out.view(bits)[1:, :, ~stays], good.view(bits)[1:, :, ~stays])
     assert torch.equal(out.view(bits)[0], good.view(bits)[0])
+
+
+def test_a_cache_keeps_no_growing_record_of_its_calls():
+    """A server's calls have ever new numbers of rows: what the handle remembers of them stays bounded."""
+    cache = KvCache(4, 1, 64, 16, "int8")
+    tb, ln = torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    q = torch.zeros((700, 1, 64), device=DEV)
+    for rows in range(1, 701):
+        offs = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+        cache.attention(q[:rows], tb, ln, offs, max_queries=1)
+    held = sum(len(x) for x in vars(cache).values() if isinstance(x, (dict, list, set)))
+    assert held <= 256 and status() == 0
