@@ -44,6 +44,7 @@
 #include "attn_device.cuh"
 #include "attn_internal.h"
 #include "attn_split.cuh"
+#include "attn_sums.h"
 #include "sm100_ptx.cuh"
 
 namespace lora {
@@ -231,30 +232,6 @@ __device__ __forceinline__ bool wait_clocks(uint64_t *bar, uint32_t parity, long
 
 // ---------------------------------------------------------------- the line of work
 
-// sum of floor((a i + b) / m) over 0 <= i < n (the Euclid-like recursion);
-// every a n + b on the way fits 32 bits, as rows * group does.
-__device__ __noinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    long long ans = 0;
-    while (n > 0) {
-        if (a >= m) {
-            ans += static_cast<long long>(a / m) * (static_cast<long long>(n) * (n - 1) / 2);
-            a %= m;
-        }
-        if (b >= m) {
-            ans += static_cast<long long>(b / m) * n;
-            b %= m;
-        }
-        const uint32_t y = a * n + b;
-        if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const uint32_t t = m;
-        m = a;
-        a = t;
-    }
-    return ans;
-}
-
 // A sequence's row tiles: tile i covers rows [256 i, 256 i + 256) of n *
 // group.  (The host refuses calls with 2^31 rows * group or more.)
 struct RowTiles {
@@ -282,7 +259,7 @@ struct RowTiles {
         long long sum;
         if (causal) {
             const long long c = (kRows - 1 + static_cast<long long>(group) * (first + kKeys)) >> 7;
-            sum = floor_sum(min(i, count - 1), group, 2, static_cast<uint32_t>(c));
+            sum = sum_of_floors(min(i, count - 1), group, static_cast<uint32_t>(c));
             if (i == count) sum += hi(count - 1);
         } else {
             sum = static_cast<long long>(i) * hi(0);
@@ -291,7 +268,7 @@ struct RowTiles {
             const long long x = static_cast<long long>(group) * (first - window + 1);
             const int32_t e = static_cast<int32_t>(x >> 7);  // floor, of negative numbers too
             const int32_t i0 = e >= 0 ? 0 : (1 - e) / 2;
-            if (i > i0) sum -= floor_sum(i - i0, group, 2, 2 * i0 + e);
+            if (i > i0) sum -= sum_of_floors(i - i0, group, 2 * i0 + e);
         }
         return sum + static_cast<long long>(i) * kItemUnits;
     }
