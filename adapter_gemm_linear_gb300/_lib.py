@@ -132,6 +132,8 @@ SIGNATURES = [
 
 KV_INT8 = 0
 KV_E4M3 = 1
+KV_GROW_LEAST = 0
+KV_GROW_DOUBLING = 1
 ROPE_MAX_PAIRS = 256
 
 
@@ -173,6 +175,7 @@ class KvCacheDesc(ctypes.Structure):
         ("num_heads", ctypes.c_int32),
         ("head_dim", ctypes.c_int32),
         ("page_tokens", ctypes.c_int32),
+        ("growth", ctypes.c_int32),
         ("k_pages", ctypes.c_void_p),
         ("v_pages", ctypes.c_void_p),
         ("k_scales", ctypes.c_void_p),

@@ -26,6 +26,7 @@ from . import _lib
 from ._lib import LORA_BLOCK_ROWS
 from .api import LoraError, lora_dtype
 
+_GROWTHS = {"least": _lib.KV_GROW_LEAST, "doubling": _lib.KV_GROW_DOUBLING}
 _FORMATS = {"int8": (_lib.KV_INT8, torch.int8), "e4m3": (_lib.KV_E4M3, torch.float8_e4m3fn)}
 
 # A decode step makes these calls once per layer with a few microseconds of
@@ -165,16 +166,24 @@ class KvCache:
     head, are torch tensors, allocated here unless given.  Which pages a
     sequence owns is the caller's business (block tables); a page's older
     content does not matter once its first token is written anew.
+
+    ``growth``: how an int8 page's scale grows when a later token does not
+    fit.  "least" takes the least scale that holds it, the finest steps for
+    prompts written at once, but each growth rounds the page's older codes again;
+    "doubling" takes the least power of two of its first one, which keeps
+    pages that are filled token by token within one step.  (e4m3 rescales exactly.)
     """
 
     def __init__(self, num_pages: int, num_heads: int, head_dim: int, page_tokens: int = LORA_BLOCK_ROWS,
                  fmt: str = "int8", device=None, k_pages: Optional[torch.Tensor] = None,
                  v_pages: Optional[torch.Tensor] = None, k_scales: Optional[torch.Tensor] = None,
-                 v_scales: Optional[torch.Tensor] = None):
+                 v_scales: Optional[torch.Tensor] = None, growth: str = "least"):
+        if growth not in _GROWTHS:
+            raise ValueError(f"unknown growth {growth!r}; use 'least' or 'doubling'")
         if fmt not in _FORMATS:
             raise ValueError(f"unknown format {fmt!r}; use 'int8' or 'e4m3'")
         code, dtype = _FORMATS[fmt]
-        self.fmt = fmt
+        self.fmt, self.growth = fmt, growth
         self.num_pages, self.num_heads = int(num_pages), int(num_heads)
         self.head_dim, self.page_tokens = int(head_dim), int(page_tokens)
         if device is None:
@@ -201,7 +210,7 @@ class KvCache:
         self.device = self.k_pages.device
         self._device = self.k_pages.get_device()
         self._workspace = {}  # bytes of an attention call's workspace, by what they depend on
-        self._desc = _lib.KvCacheDesc(code, self.num_pages, self.num_heads, D, self.page_tokens,
+        self._desc = _lib.KvCacheDesc(code, self.num_pages, self.num_heads, D, self.page_tokens, _GROWTHS[growth],
                                       self.k_pages.data_ptr(), self.v_pages.data_ptr(), self.k_scales.data_ptr(),
                                       self.v_scales.data_ptr())
         self._ref = ctypes.byref(self._desc)

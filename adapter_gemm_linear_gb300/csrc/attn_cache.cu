@@ -44,6 +44,13 @@ __device__ __forceinline__ float scale_for(float a) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// s0 times the least power of two that makes it `least` at least (both normal, s0 below it).
+__device__ __forceinline__ float doubled_to(float s0, float least) {
+    const uint32_t a = __float_as_uint(s0), b = __float_as_uint(least);
+    const float s = __uint_as_float((a & 0x7FFFFFu) | (b & 0x7F800000u));  // with the exponent of `least`
+    return s < least ? 2.0f * s : s;
+}
+
 // Adding it rounds a float below 2^22 to an integer (ties to even), whose low
 // byte is the sum's: one add where a rounding and a conversion instruction
 // would take eight times as long each.
@@ -239,7 +246,9 @@ __device__ __forceinline__ void append_page(const KvView &b, const HeadsView &x,
         for (int32_t w = 0; w < unit_warps; ++w) amax = fmaxf(amax, unit_amax[w]);
         __syncthreads();
     }
-    const float s = fmaxf(old_s, scale_for<FMT>(amax));
+    const float least = scale_for<FMT>(amax);
+    float s = fmaxf(old_s, least);
+    if (FMT == LORA_KV_INT8 && b.growth == LORA_KV_GROW_DOUBLING && old_s > 0.0f && least > old_s) s = doubled_to(old_s, least);
     const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
     const float ratio = s > 0.0f ? __fdiv_rn(old_s, s) : 0.0f;
     __syncwarp();  // every lane has read the old scale

@@ -43,6 +43,7 @@ lora_status_t check_cache(const lora_kv_cache_t *c) {
     if (c->head_dim != 64 && c->head_dim != 128) return LORA_ERR_UNSUPPORTED;
     if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
         return LORA_ERR_UNSUPPORTED;
+    if (c->growth != LORA_KV_GROW_LEAST && c->growth != LORA_KV_GROW_DOUBLING) return LORA_ERR_UNSUPPORTED;
     if (!c->k_pages || !c->v_pages || !c->k_scales || !c->v_scales) return LORA_ERR_INVALID_ARG;
     if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16))
         return LORA_ERR_ALIGNMENT;
@@ -74,6 +75,7 @@ lora_status_t check_batch(const lora_kv_cache_t *c, const lora_kv_batch_t *b, lo
     v->num_seqs = b->num_seqs;
     v->rows = b->rows;
     v->max_pages = b->max_pages;
+    v->growth = c->growth;
     v->status = nullptr;
     return LORA_OK;
 }

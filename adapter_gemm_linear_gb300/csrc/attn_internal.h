@@ -19,6 +19,7 @@ struct KvView {
     const int32_t *seq_lens, *offsets, *table;
     int32_t num_pages, heads, page_tokens, page_shift;  // page_tokens = 1 << page_shift
     int32_t num_seqs, rows, max_pages;
+    int32_t growth;  // lora_kv_growth_t
     unsigned long long *status;
 };
 

@@ -45,7 +45,8 @@ class AdaptedAttention:
                 pool.load(slot, A, B, alpha=2.0 * rank)
                 self.adapters[p, slot] = (A, B, 2.0)
             self.pools[p] = pool
-        self.cache = KvCache(num_pages, kv_heads, head_dim, page_tokens, fmt, device=device)
+        # (decoding fills pages token by token: int8 scales grow by doubling)
+        self.cache = KvCache(num_pages, kv_heads, head_dim, page_tokens, fmt, device=device, growth="doubling")
         self.cos, self.sin = rope_tables(max_pos, head_dim, device=device)
 
     def project(self, x, names, row_adapter):

@@ -86,6 +86,12 @@ typedef enum lora_kv_format {
     LORA_KV_E4M3 = 1  /* 8-bit floating point (4 exponent, 3 mantissa bits), power-of-two scale */
 } lora_kv_format_t;
 
+/* How an int8 page's scale grows when a later token does not fit (e4m3 scales are powers of two either way). */
+typedef enum lora_kv_growth {
+    LORA_KV_GROW_LEAST = 0,   /* to the least that holds it: the finest steps for pages written at once */
+    LORA_KV_GROW_DOUBLING = 1 /* by the least power of two that holds it: for pages filled token by token */
+} lora_kv_growth_t;
+
 /*
  * One layer's cache.  A page holds page_tokens consecutive tokens of one
  * sequence; a value is code * scale, with one fp32 scale per page and head,
@@ -105,6 +111,7 @@ typedef struct lora_kv_cache {
     int32_t num_heads;    /* key/value heads, >= 1 */
     int32_t head_dim;     /* 64 or 128 */
     int32_t page_tokens;  /* 16, 32, 64 or 128 */
+    int32_t growth;       /* a lora_kv_growth_t */
     void *k_pages, *v_pages;    /* device; num_pages*num_heads*page_tokens*head_dim bytes each */
     float *k_scales, *v_scales; /* device [num_pages][num_heads] */
 } lora_kv_cache_t;
@@ -143,11 +150,19 @@ typedef struct lora_kv_batch {
  *   int8:  s = max(s0, a / 127), a / 127 taken as 2^-120 at least if a > 0;
  *          code = x / s rounded to nearest even, within [-127, 127];
  *          older codes of the page become code * (s0 / s), rounded so too.
+ *          With LORA_KV_GROW_DOUBLING and s0 > 0, s = s0 * 2^k with the least
+ *          such k >= 0 that gives s >= a / 127.
  *   e4m3:  s = max(s0, the least power of two with a <= 448 s, 2^-120 at
  *          least if a > 0); code = x / s rounded to nearest even; older codes
  *          are rescaled by s0 / s, exactly unless they fall below the
  *          format's least normal.
- * All of it in fp32.  Infinities take the largest code, NaN code 0 in int8
+ * All of it in fp32.  Every growth of an int8 page's scale rounds its older
+ * codes once more: after g growths a value may be off by (g + 1) / 2 steps of
+ * the page's scale, and where the magnitudes of a page grow little by little g may
+ * be as large as its number of tokens (128 tokens that grow by 0.5% each: 42 of
+ * 127 steps).  With LORA_KV_GROW_DOUBLING the roundings halve each other: it is
+ * off by less than one step, of a scale less than twice the least.  e4m3 codes
+ * are rescaled exactly.  Infinities take the largest code, NaN code 0 in int8
  * and NaN in e4m3; neither moves the scale of its neighbours, but where the
  * call's new values have no finite one but zeros, an infinity or NaN among them
  * counts as the least a > 0 (s is 2^-120 at least), so that it has a code.  A

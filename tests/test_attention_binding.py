@@ -68,3 +68,19 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError, match="cuda:1"):
         attention._elsewhere(lambda *a, **kw: ran.append(1), 0, Stream("cuda:1"), ())
     assert not ran
+
+
+def test_growth_of_a_cache_is_checked():
+    import ctypes
+
+    from adapter_gemm_linear_gb300 import _lib, build
+    build()
+    with pytest.raises(ValueError, match="growth"):
+        KvCache(4, 2, 64, 16, "int8", growth="most")
+    # the field lies where the structure had four unused bytes
+    assert _lib.KvCacheDesc.growth.offset == 20 and _lib.KvCacheDesc.k_pages.offset == 24 and ctypes.sizeof(_lib.KvCacheDesc) == 56
+    heads, batch = _lib.Heads(None, 256, 128), _lib.KvBatch(0, 0, None, None, None, 1)
+    for growth, status in ((0, "LORA_OK"), (1, "LORA_OK"), (2, "LORA_ERR_UNSUPPORTED"), (-1, "LORA_ERR_UNSUPPORTED")):
+        desc = _lib.KvCacheDesc(0, 4, 2, 128, 16, growth, 0x10000, 0x10000, 0x10000, 0x10000)
+        got = _lib.lib().lora_kv_append(ctypes.byref(desc), ctypes.byref(batch), 0, ctypes.byref(heads), ctypes.byref(heads), None)
+        assert got == _lib.STATUS[status]

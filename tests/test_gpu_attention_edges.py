@@ -299,3 +299,85 @@ def test_a_cache_keeps_no_growing_record_of_its_calls():
         cache.attention(q[:rows], tb, ln, offs, max_queries=1)
     held = sum(len(x) for x in vars(cache).values() if isinstance(x, (dict, list, set)))
     assert held <= 256 and status() == 0
+
+
+# ---------------------------------------------------------------- int8 pages filled token by token
+
+def slowly(kind, tokens, D, rng):
+    x = rng.normal(size=(tokens, 1, D))
+    if kind == "growing":  # magnitudes 0.5% larger every token
+        x = np.broadcast_to(x[:1], x.shape) * 1.005 ** np.arange(tokens)[:, None, None]
+    elif kind == "turning":  # a large channel that turns slowly, as a low-frequency rotary pair does
+        x[:, 0, 5] = 20 * np.cos(0.01 * np.arange(tokens) - 1.28)
+    elif kind == "jumping":
+        x = x * np.exp2(rng.integers(-60, 60, tokens))[:, None, None]
+    return x
+
+
+@pytest.mark.parametrize("kind", ["normal", "growing", "turning", "jumping"])
+@pytest.mark.parametrize("dtype,D,page", [("bf16", 128, 128), ("fp32", 64, 32), ("bf16", 64, 16)])
+def test_doubling_keeps_a_page_filled_token_by_token_within_a_step(kind, dtype, D, page):
+    """Off by less than a step of the page's scale, which is less than twice the least one; and to the bit the definition's codes."""
+    rng = np.random.default_rng(D + page)
+    tokens = page + page // 2
+    x = torch.from_numpy(slowly(kind, tokens, D, rng).astype(np.float32)).to(DT[dtype])
+    cache = KvCache(2, 1, D, page, "int8", growth="doubling")
+    table = dev(np.array([[1, 0]], np.int32))
+    codes, scales = np.zeros((2, page, D), np.float32), np.zeros(2, np.float32)
+    for t in range(tokens):
+        row = x[t:t + 1].to(DEV)
+        cache.append(row, row, table, dev(np.array([t + 1], np.int32)))
+        p, i, v = t // page, t % page, x[t, 0].float().numpy()
+        least = max(np.float32(np.abs(v).max()) / np.float32(127), np.float32(2.0 ** -120))
+        s = scales[p]
+        if i == 0:
+            s = least
+        while s < least:
+            s = np.float32(2 * s)
+        codes[p, :i] = np.rint(codes[p, :i] * np.float32(scales[p] / s)) if i else codes[p, :i]
+        codes[p, i] = np.clip(np.rint(v / s), -127, 127)
+        scales[p] = s
+    assert np.array_equal(cache.k_scales.cpu().numpy()[[1, 0], 0], scales) and torch.equal(cache.k_scales, cache.v_scales)
+    assert np.array_equal(R.unpack_k(cache.k_pages)[[1, 0], 0], codes) and np.array_equal(R.unpack_v(cache.v_pages)[[1, 0], 0], codes)
+    got = cache.gather(table, dev(np.array([tokens], np.int32)), dev(np.array([0, tokens], np.int32)), rows=tokens, dtype=torch.float32)
+    want = x.double().numpy()[:, 0]
+    for y in got:
+        err = np.abs(y.double().cpu().numpy()[:, 0] - want)
+        for p in range(2):
+            here = slice(p * page, min(tokens, (p + 1) * page))
+            assert np.all(err[here] <= float(scales[p]) * (1 + 2.0 ** -20))
+            assert float(scales[p]) < 2 * np.abs(want[here]).max() / 127 * (1 + 2.0 ** -22)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("kind", ["normal", "growing", "turning"])
+def test_the_least_scale_is_off_by_half_a_step_for_each_growth(kind):
+    """The bound that the header gives for the default: (growths + 1) / 2 steps."""
+    rng = np.random.default_rng(7)
+    x = slowly(kind, 64, 64, rng).astype(np.float32)
+    cache = KvCache(1, 1, 64, 64, "int8")
+    table, growths, last = dev(np.zeros((1, 1), np.int32)), 0, 0.0
+    for t in range(64):
+        row = torch.from_numpy(x[t:t + 1]).to(DEV)
+        cache.append(row, row, table, dev(np.array([t + 1], np.int32)))
+        s = float(cache.k_scales[0, 0])
+        growths += t > 0 and s > last
+        last = s
+    k, _ = cache.gather(table, dev(np.array([64], np.int32)), dev(np.array([0, 64], np.int32)), rows=64, dtype=torch.float32)
+    assert float((k.cpu().double() - torch.from_numpy(x).double()).abs().max()) <= last * (growths + 1) / 2 * (1 + 2.0 ** -20)
+
+
+def test_doubling_changes_nothing_where_no_scale_grows():
+    """Whole pages at once, and e4m3: the same codes and scales with either growth."""
+    for fmt, steps in (("int8", [96]), ("e4m3", [1] * 20 + [30, 46])):
+        rng = np.random.default_rng(3)
+        x, _ = draw(rng, (96, 2, 128), "bf16", 4.0)
+        a, b = (KvCache(3, 2, 128, 32, fmt, growth=g) for g in ("least", "doubling"))
+        table = dev(np.array([[2, 0, 1]], np.int32))
+        for cache in (a, b):
+            at = 0
+            for n in steps:
+                cache.append(x[at:at + n], x[at:at + n], table, dev(np.array([at + n], np.int32)), dev(np.array([0, n], np.int32)))
+                at += n
+        for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
+            assert torch.equal(getattr(a, name).view(torch.uint8), getattr(b, name).view(torch.uint8))
