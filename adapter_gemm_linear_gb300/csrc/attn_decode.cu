@@ -80,14 +80,15 @@ template <int D, int NT>
 __host__ __device__ constexpr int ctas_per_sm() { return D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3); }
 
 // What the looking-up warp says of a tile: where its codes are (in k_pages and
-// in v_pages; < 0: not there, zeros), and K's scale, V's, its log2 and reciprocal.
+// in v_pages; < 0: not there, zeros), K's scale, V's relative to the reference vr
+// (attn_split.cuh) in log2, and what takes it out again; of a V that is zero the least.
 struct alignas(16) TileInfo {
-    float ks, vs, lv, ivs;
+    float ks, lv, ivs, vr;
     int64_t at;
     int64_t pad;
 };
 constexpr int64_t kNoTile = -1, kEndOfLine = -2;
-constexpr float kNoReference = -1e30f;  // below every page's log2 scale
+constexpr int64_t kZeroV = 1;  // added to `at` (a multiple of 1024): V is zero whatever its codes
 
 constexpr int kBatch = 32, kBatches = 8;  // tiles looked up at once, and ahead
 
@@ -99,7 +100,7 @@ struct DecodeSmem {
     uint4 codes[kWarps][kDepth][2][kPieces][32];     // [.., K or V, piece, lane]
     float o[kWarps][8 * NT][D + 4];                  // merge: padded against bank conflicts
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    float vr[kWarps];
+    float vr[2];  // the reference scale of V of the item (by its parity)
     TileInfo info[kBatches][kBatch];
     uint64_t full[kBatches], empty[kBatches];
     long long warp_sum[kWarps + 1];
@@ -275,9 +276,11 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         const int tile_shift = b.page_shift - 4;  // tiles of a page, as a shift
         int32_t next = 0, end = 0;  // the item's tiles that are not given out
         bool more = true;
+        float vr = 1.0f, ref = 0.0f;  // of the item: the reference scale of V and its log2
         // (past the last tile the consumers still look for as many as they fetch ahead)
         for (int32_t n = 0, past = 0; past < kWarps * Smem::kDepth; ++n) {
             int32_t seq = -1, head = 0, t = 0;
+            float own_vr = 1.0f, own_ref = 0.0f;
             for (int fill = 0; fill < kBatch;) {
                 if (next == end) {
                     more = more && walk.next();
@@ -287,17 +290,40 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     }
                     next = walk.tile0;
                     end = walk.tile1;
+                    // the largest scale of the item's pages in this CTA (their
+                    // reads, eight a lane in flight, are hidden but for the first item's)
+                    const int32_t p0 = next >> tile_shift, p1 = (end - 1) >> tile_shift;
+                    float top = 0.0f;
+                    for (int32_t at = p0 + lane; at <= p1; at += 32 * 8) {
+                        int32_t page[8];
+                        float vs[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            page[k] = at + 32 * k <= p1 ? b.table[static_cast<int64_t>(walk.s) * b.max_pages + at + 32 * k] : -1;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            vs[k] = page[k] >= 0 && page[k] < b.num_pages
+                                ? __ldg(b.v_scales + static_cast<int64_t>(page[k]) * b.heads + walk.head) : 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) top = fmaxf(top, vs[k]);
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    vr = top > 0.0f ? top : 1.0f;
+                    ref = log2f(vr);
                 }
                 const int take = min(kBatch - fill, end - next);
                 if (lane >= fill && lane < fill + take) {
                     seq = walk.s;
                     head = walk.head;
                     t = next + lane - fill;
+                    own_vr = vr;
+                    own_ref = ref;
                 }
                 fill += take;
                 next += take;
             }
-            TileInfo x = {0.0f, 0.0f, -INFINITY, INFINITY, kEndOfLine, 0};
+            TileInfo x = {0.0f, -kSpread, kSpreadFactor, own_vr, kEndOfLine, 0};
             if (seq >= 0) {
                 const int32_t page = read_page(b, seq, t >> tile_shift);
                 x.at = kNoTile;
@@ -305,9 +331,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     x.at = tile_offset<D>(b, page, head, t & ((1 << tile_shift) - 1));
                     const int64_t sc = static_cast<int64_t>(page) * b.heads + head;
                     x.ks = __ldg(b.k_scales + sc);
-                    x.vs = __ldg(b.v_scales + sc);
-                    x.lv = log2f(x.vs);
-                    x.ivs = 1.0f / x.vs;
+                    const float vs = __ldg(b.v_scales + sc), lv = log2f(vs) - own_ref;
+                    if (!(vs > 0.0f)) x.at += kZeroV;
+                    else if (lv >= -kSpread) {
+                        x.lv = lv;
+                        x.ivs = own_vr / vs;
+                    }
                 }
             }
             __syncwarp();
@@ -327,17 +356,17 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     // after the transposition a thread holds p of tokens 4 tig .. 4 tig + 3
     const int tok = 4 * (g >> 1) + (g & 1);
     auto fetch_k = [&](int64_t at, uint32_t slot) {
-        const uint8_t *src = b.k_pages + max(at, int64_t{0}) + tok * 64 + tig * 16;
+        const uint8_t *src = b.k_pages + (max(at, int64_t{0}) & ~kZeroV) + tok * 64 + tig * 16;
 #pragma unroll
         for (int i = 0; i < Smem::kPieces; ++i)  // [64 dimensions][token or that + 2]
             if (at != kEndOfLine) copy16(&sm.codes[warp][slot][0][i][lane], src + (i >> 1) * (kKvTile * 64) + (i & 1) * 128, at >= 0);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto fetch_v = [&](int64_t at, uint32_t slot) {
-        const uint8_t *src = b.v_pages + max(at, int64_t{0}) + g * 64 + tig * 16;
+        const uint8_t *src = b.v_pages + (max(at, int64_t{0}) & ~kZeroV) + g * 64 + tig * 16;
 #pragma unroll
         for (int i = 0; i < Smem::kPieces; ++i)
-            if (at != kEndOfLine) copy16(&sm.codes[warp][slot][1][i][lane], src + i * 512, at >= 0);
+            if (at != kEndOfLine) copy16(&sm.codes[warp][slot][1][i][lane], src + i * 512, at >= 0 && !(at & kZeroV));
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // where tile i of the CTA's line is; waits for its batch if it is the warp's first of it
@@ -355,6 +384,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     uint32_t taken = 0;  // tiles the warp has used
     uint32_t i0 = 0;
     bool merged = false;  // whether the merge buffer may still be read by others
+    uint32_t n_item = 0;
     while (walk.next()) {
         const SeqRows &r = walk.work.r;
         const int32_t rows = min(ROWS, r.n * a.group - walk.row_tile * ROWS);
@@ -425,43 +455,16 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 m[u][i] = -INFINITY;
                 l[u][i] = 0.0f;
             }
-        float vr = 1.0f, ref = kNoReference;  // the reference scale of V and its log2 (attn_split.cuh)
 
         const int32_t count = walk.tile1 - walk.tile0;
         // this warp's tiles: those whose running number is the warp's modulo kWarps
-        for (int32_t j = (warp - static_cast<int32_t>(i0 % kWarps) + kWarps) % kWarps; j < count; j += kWarps) {
+        const int32_t j0 = (warp - static_cast<int32_t>(i0 % kWarps) + kWarps) % kWarps;
+        if (j0 == 0 && lane == 0) sm.vr[n_item & 1] = sm.info[i0 / kBatch % kBatches][i0 % kBatch].vr;
+        for (int32_t j = j0; j < count; j += kWarps) {
             const uint32_t i = i0 + j, slot = taken++ % Smem::kDepth;
             const int32_t key0 = (walk.tile0 + j) * kKvTile;
             const TileInfo &info = sm.info[i / kBatch % kBatches][i % kBatch];
-            const float ks = info.ks;
-            if (__builtin_expect(info.lv - ref > kSpread, 0)) {  // a new reference, the first or a far larger one
-                if (ref != kNoReference) {
-                    const float step = info.lv - ref;
-#pragma unroll
-                    for (int u = 0; u < RT; ++u)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float sum = l[u][e];
-                            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-                            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                            const float lower = reference_shift(step, sum), f = ex2(lower - step);
-                            m[u][e] -= lower;
-                            l[u][e] *= ex2(lower);
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                o[u][k][e] *= f;
-                                o[u][k][e + 2] *= f;
-                                if (SPLIT) {
-                                    o[NT - 1][k][e] *= f;
-                                    o[NT - 1][k][e + 2] *= f;
-                                }
-                            }
-                        }
-                }
-                ref = info.lv;
-                vr = info.vs;
-            }
+            const float ks = info.ks, lv = info.lv, ivs = info.ivs;
             const int64_t ahead = look(i + Smem::kDepth * kWarps);
             float s[NT][4];
 #pragma unroll
@@ -481,9 +484,6 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 }
             }
             fetch_k(ahead, slot);
-            // V's scale relative to the reference, in log2, and what takes it
-            // out again; of a V that is zero the least
-            const float lv = fmaxf(info.lv - ref, -kSpread), ivs = fminf(vr * info.ivs, kSpreadFactor);
             // scores in log2 units, with V's scale
             float z[RT][4];  // [2 * token half + row]
 #pragma unroll
@@ -550,10 +550,6 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     pf[NT - 1][0] = transpose_8x8(pack_rest(p[0], p[1], h0));
                     pf[NT - 1][1] = transpose_8x8(pack_rest(p[2], p[3], h1));
                 }
-            }
-            if (lv <= -kSpread) {  // V = 0 whatever its codes, or nothing beside the reference
-#pragma unroll
-                for (int u = 0; u < NT; ++u) pf[u][0] = pf[u][1] = 0u;
             }
             // codes of V past the sequence's end are whatever was there; in
             // int8 p = 0 removes them, in e4m3 they may be NaN
@@ -651,7 +647,6 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     *reinterpret_cast<float4 *>(&sm.o[warp][rt][32 * jj + 4 * g]) = v;
                 }
             }
-        if (lane == 0) sm.vr[warp] = vr;
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
         const bool whole = walk.from_start && walk.to_end;
         // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
@@ -664,7 +659,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
         const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
         if (rt < rows) {
-            float M = -INFINITY, L = 0.0f, f[kWarps], scale[kWarps];
+            float M = -INFINITY, L = 0.0f, f[kWarps];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][rt]);
             const float mu = M == -INFINITY ? 0.0f : M;
@@ -672,12 +667,9 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             for (int w = 0; w < kWarps; ++w) {
                 f[w] = ex2(sm.m[w][rt] - mu);
                 L = fmaf(sm.l[w][rt], f[w], L);
-                scale[w] = sm.vr[w];
             }
             // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
-            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) f[w] *= inv;
+            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f, scale = sm.vr[n_item & 1];
             const int32_t row = walk.row_tile * ROWS + rt;
             const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
             T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head;
@@ -687,15 +679,16 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][rt][c]);
-                    v.x = fmaf(x.x * f[w], scale[w], v.x);
-                    v.y = fmaf(x.y * f[w], scale[w], v.y);
-                    v.z = fmaf(x.z * f[w], scale[w], v.z);
-                    v.w = fmaf(x.w * f[w], scale[w], v.w);
+                    v.x = fmaf(x.x, f[w], v.x);
+                    v.y = fmaf(x.y, f[w], v.y);
+                    v.z = fmaf(x.z, f[w], v.z);
+                    v.w = fmaf(x.w, f[w], v.w);
                 }
+                v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);  // (inv * scale may leave fp32's range)
                 if (whole) {
-                    store4(dst + c, v, 1.0f);
+                    store4(dst + c, v, scale);
                 } else {
-                    *reinterpret_cast<float4 *>(part + rt * D + c) = v;
+                    store4(part + rt * D + c, v, scale);
                 }
             }
             if (c0 == 0) {
@@ -707,6 +700,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 }
             }
         }
+        ++n_item;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
