@@ -276,7 +276,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         const int tile_shift = b.page_shift - 4;  // tiles of a page, as a shift
         int32_t next = 0, end = 0;  // the item's tiles that are not given out
         bool more = true;
-        float vr = 1.0f, ref = 0.0f;  // of the item: the reference scale of V and its log2
+        float vr = 1.0f, ref = 0.0f;  // of the item: the reference scale of V (v_reference) and its log2
         // (past the last tile the consumers still look for as many as they fetch ahead)
         for (int32_t n = 0, past = 0; past < kWarps * Smem::kDepth; ++n) {
             int32_t seq = -1, head = 0, t = 0;
@@ -290,27 +290,9 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     }
                     next = walk.tile0;
                     end = walk.tile1;
-                    // the largest scale of the item's pages in this CTA (their
-                    // reads, eight a lane in flight, are hidden but for the first item's)
-                    const int32_t p0 = next >> tile_shift, p1 = (end - 1) >> tile_shift;
-                    float top = 0.0f;
-                    for (int32_t at = p0 + lane; at <= p1; at += 32 * 8) {
-                        int32_t page[8];
-                        float vs[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            page[k] = at + 32 * k <= p1 ? b.table[static_cast<int64_t>(walk.s) * b.max_pages + at + 32 * k] : -1;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            vs[k] = page[k] >= 0 && page[k] < b.num_pages
-                                ? __ldg(b.v_scales + static_cast<int64_t>(page[k]) * b.heads + walk.head) : 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) top = fmaxf(top, vs[k]);
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    vr = top > 0.0f ? top : 1.0f;
-                    ref = log2f(vr);
+                    // (the reads are hidden but for the first item's)
+                    vr = v_reference(b, walk.s, walk.head, next, end);
+                    ref = log2f(fabsf(vr));
                 }
                 const int take = min(kBatch - fill, end - next);
                 if (lane >= fill && lane < fill + take) {
@@ -335,7 +317,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     if (!(vs > 0.0f)) x.at += kZeroV;
                     else if (lv >= -kSpread) {
                         x.lv = lv;
-                        x.ivs = own_vr / vs;
+                        x.ivs = fabsf(own_vr) / vs;
                     }
                 }
             }
@@ -658,7 +640,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         }
         constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
         const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
-        if (rt < rows) {
+        const float scale = sm.vr[n_item & 1];
+        if (__builtin_expect(scale < 0.0f, 0)) {
+            for (int r0 = warp; r0 < rows; r0 += kWarps)
+                plain_row<T, D, FMT>(a, walk.s, walk.head, r.off, r.n, r.len, walk.row_tile * ROWS + r0, walk.tile0 * kKvTile,
+                                     min(walk.tile1 * kKvTile, r.len), whole ? nullptr : part + r0 * D, part + kSlotRows * D + r0);
+        } else if (rt < rows) {
             float M = -INFINITY, L = 0.0f, f[kWarps];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][rt]);
@@ -669,7 +656,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 L = fmaf(sm.l[w][rt], f[w], L);
             }
             // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
-            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f, scale = sm.vr[n_item & 1];
+            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f;
             const int32_t row = walk.row_tile * ROWS + rt;
             const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
             T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head;

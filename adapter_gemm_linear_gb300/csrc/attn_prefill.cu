@@ -72,6 +72,7 @@ struct Item {
     int32_t off, n, len;
     int32_t tile0, tile1;  // key tiles of this CTA; tile1 < 0: no more items
     int32_t flags;
+    float vr;  // v_reference of the key tiles
 };
 constexpr int kFromStart = 1, kToEnd = 2;
 
@@ -84,9 +85,8 @@ struct KeyTile {
     int64_t at_v[kSubs];  // and in v_pages
     int32_t key0, len;    // first key, the sequence's length; key0 < 0: no more tiles
     int32_t off, n, head, row_tile;  // of an item's first tile: its queries (n = 0 in its other tiles)
-    float vr, step;  // the reference; log2 of how much it grew with this tile, 0 if it did not (or is the first)
-    int32_t edge;    // some row of the item does not see some key
-    int32_t pad[3];
+    float vr;      // the item's v_reference
+    int32_t edge;  // some row of the item does not see some key
 };
 static_assert(sizeof(KeyTile) % 16 == 0, "scales are read as 16-byte pieces");
 
@@ -355,9 +355,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     volatile int32_t *dead = &sm.dead;
     const long long limit = a.test_wait_ns ? 2 * static_cast<long long>(a.test_wait_ns) : kWaitClocks;  // (2 GHz)
 
-    auto wait = [&](uint64_t *bar, uint32_t parity, int32_t site) {
-        if (!mbar_try_wait(bar, parity) && !wait_clocks(bar, parity, limit, dead) && !*dead) *dead = site;
+    auto wait = [&](uint64_t *bar, uint32_t parity, int32_t site) {  // whether the phase is complete
+        if (mbar_try_wait(bar, parity) || wait_clocks(bar, parity, limit, dead)) return true;
+        if (!*dead) *dead = site;
+        return false;
     };
+    auto all = [](bool yes) { return __all_sync(0xffffffffu, yes) != 0; };
     auto any_dead = [&] { return __any_sync(0xffffffffu, *dead != 0) != 0; };  // the same for the whole warp
 
     // the joining kernel may come in as soon as there is room beside CTAs that
@@ -468,17 +471,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             return it.tile1 >= 0 && (X == 0 || it.n * a.group - it.row_tile * kRows > kHalf);
         };
 
-        auto rescale = [&](uint32_t at, float f) {  // O, the thread's row
-#pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(at + 16 * i, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st_32x32b_x16(at + 16 * i, o);
-            }
-        };
-
         Item it;
         get_item(it);
         while (it.tile1 >= 0) {
@@ -497,13 +489,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             const int32_t all_hi = a.causal ? it.len - it.n + it.row_tile * kRows / a.group + 1 : it.len;
             const int32_t all_lo = a.window > 0 ? it.len - it.n + (it.row_tile * kRows + rows - 1) / a.group - a.window + 1 : 0;
             float m = -INFINITY, l = 0.0f, cr = 0.0f, vr = 1.0f;
+            float top = -INFINITY;  // where vr < 0: l is the sum of 2^(s - top), top the largest score
             for (int32_t t = it.tile0; t < it.tile1; ++t, ++n_tile, ++n_own) {
                 wait(&sm.tile_full[n_tile % kTileRing], (n_tile / kTileRing) & 1u, 55);
                 wait(&sm.s_full[X], n_own & 1u, 51 + X);
                 __syncwarp();  // (lanes may leave a wait apart; what follows is for the whole warp at once)
                 tc_fence_after_sync();
-                if (t == it.tile0) cr = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + sm.q_exponent[(n_item - 1) & 1u][rt]) << 23);
                 const KeyTile &tile = sm.tiles[n_tile % kTileRing];
+                if (t == it.tile0) {
+                    cr = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + sm.q_exponent[(n_item - 1) & 1u][rt]) << 23);
+                    vr = tile.vr;
+                }
                 const int32_t key0 = t * kKeys;
                 if (__builtin_expect(key0 < all_lo || key0 + kKeys > all_hi, 0)) {
                     // keys that the row does not see: -inf, in place
@@ -518,12 +514,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     }
                     tmem_st_wait();
                 }
-                vr = tile.vr;
-                if (__builtin_expect(tile.step > 0.0f, 0)) {  // (not an item's first tile)
-                    const float lower = reference_shift(tile.step, l);
-                    m -= lower;
-                    l *= ex2(lower);
-                    rescale(to, ex2(lower - tile.step));
+                if (__builtin_expect(vr < 0.0f, 0)) {
+                    // V's scales are so far apart that the probabilities with them
+                    // in their exponents do not give l: from the scores alone
+#pragma unroll 1
+                    for (int i = 0; i < kSubs; ++i) {
+                        uint32_t x[16];
+                        tmem_ld_32x32b_x16(ts + 16 * i, x);
+                        const float f = fmaxf(tile.scales[i].x * cr, 1e-37f);
+                        float most = top, sum = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) most = fmaxf(most, __uint_as_float(x[e]) * f);
+                        const float from = most == -INFINITY ? 0.0f : most;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sum += ex2(fmaf(__uint_as_float(x[e]), f, -from));
+                        l = fmaf(l, ex2(top - from), sum);
+                        top = most;
+                    }
                 }
                 // Two halves of 64 keys, one after the other, each with the row's
                 // maximum so far: the product with the first half's V runs while
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         const float mn = grow ? mx - kStartPrefill : m;
                         const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn);
                         m = mn;
-                        l *= f;
+                        if (vr > 0.0f) l *= f;
                         if (t > it.tile0 || h > 0) {
                             // the products so far are complete: of earlier tiles since
                             // s_full, of this one's first half when half_done says so
@@ -571,7 +578,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                                 __syncwarp();
                                 tc_fence_after_sync();
                             }
-                            rescale(to, f);
+#pragma unroll 1
+                            for (int i = 0; i < D / 16; ++i) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(to + 16 * i, o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st_32x32b_x16(to + 16 * i, o);
+                            }
                         }
                     }
                     const float mu = m == -INFINITY ? 0.0f : m;
@@ -613,7 +627,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             float *part = partial_at(a, blockIdx.x, it.flags & kFromStart ? 1 : 0, kRows, D);
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out.p) + static_cast<int64_t>(it.off + qi) * a.out.row + qh * a.out.head;
             // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
-            const float inv = whole || !(l == 0.0f) ? 1.0f / l : 0.0f, lse = m + log2f(l);
+            float inv = whole || !(l == 0.0f) ? 1.0f / l : 0.0f, lse = m + log2f(l);
+            if (__builtin_expect(vr < 0.0f, 0)) {
+                // out = o 2^(m - top) |vr| / l, the power in two halves; m <= top, as no V is above vr
+                const float half = top == -INFINITY ? 0.0f : ex2(0.5f * (m - top));
+                lse = top + log2f(l);
+                inv *= half;
+                vr *= -half;
+            }
             const bool hidden = FMT == LORA_KV_E4M3 && *static_cast<volatile int32_t *>(&sm.nan_item[n_item % kItemRing]) == static_cast<int32_t>(n_item);
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
@@ -678,8 +699,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         Tile cur, nxt;
         auto look = [&](Tile &x, uint32_t n) {
             const uint32_t e = n % kTileRing;
-            wait(&sm.tile_full[e], (n / kTileRing) & 1u, 60);
-            x.key0 = any_dead() ? -1 : sm.tiles[e].key0;
+            x.key0 = all(wait(&sm.tile_full[e], (n / kTileRing) & 1u, 60)) ? sm.tiles[e].key0 : -1;
             x.len = sm.tiles[e].len;
             x.at[0] = sm.tiles[e].at[2 * wq];
             x.at[1] = sm.tiles[e].at[2 * wq + 1];
@@ -912,8 +932,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     const uint32_t st = n_tile & 1u, ph = (n_tile >> 1) & 1u;
                     const uint32_t st1 = (n_tile + 1) & 1u, ph1 = ((n_tile + 1) >> 1) & 1u;
                     const bool more = j + 1 < nt;
-                    wait(&sm.v_full[st], ph, 74);
-                    if (any_dead()) break;  // no products of what may not be there
+                    if (!all(wait(&sm.v_full[st], ph, 74))) break;  // no products of what may not be there
 #pragma unroll 1
                     for (uint32_t X = 0; X < nx; ++X) {
 #pragma unroll 1
@@ -978,7 +997,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     it.tile1 = lo + skip + take - kItemUnits;
                     it.flags = (it.tile0 == lo ? kFromStart : 0) | (it.tile1 == hi ? kToEnd : 0);
                     it.last_cta = static_cast<int32_t>(((w + (units - skip)) * ctas - 1) / total);
-                    if (it.tile1 > it.tile0) publish(it);
+                    if (it.tile1 > it.tile0) {
+                        // (items ahead of their use: its reads are hidden but for the first item's)
+                        it.vr = v_reference(b, it.seq, it.head, it.tile0 * kSubs, min(it.tile1 * kSubs, (it.len + kKvTile - 1) / kKvTile));
+                        publish(it);
+                    }
                     w += take;
                     if (any_dead() || w >= w1) break;
                     skip = 0;
@@ -994,6 +1017,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             }
             it.tile0 = 0;
             it.tile1 = -1;
+            it.vr = 1.0f;
             publish(it);
         }
         if (warp == 14) {
@@ -1006,6 +1030,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 const int32_t seq = sm.items[e].seq, head = sm.items[e].head, len = sm.items[e].len;
                 if (any_dead()) break;
                 const int32_t tile0 = sm.items[e].tile0, tile1 = sm.items[e].tile1;
+                const float vr = sm.items[e].vr;
                 const int32_t off = sm.items[e].off, n = sm.items[e].n, row_tile = sm.items[e].row_tile;
                 // keys that every row of the item sees
                 const int32_t all_hi = a.causal ? len - n + row_tile * kRows / a.group + 1 : len;
@@ -1015,7 +1040,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 if (lane == 0) mbar_arrive(&sm.item_empty[e]);
                 ++n_item;
                 // four tiles at a time: lane = (tile, piece)
-                float vr = 0.0f, ref = 0.0f;  // the reference scale of V and its log2; none yet
+                const float ref = log2f(fabsf(vr));
                 for (int32_t t0 = tile0; t0 < max(tile1, tile0 + 1); t0 += 4) {
                     const int32_t t = t0 + (lane >> 3), key = t * kKeys + sub * kKvTile;
                     int64_t at = -1;
@@ -1029,31 +1054,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         }
                     }
                     __syncwarp();
-                    // the reference in force in each tile: the largest scale of the
-                    // first tile that has one, and again where that is far larger
-                    float top = vs > 0.0f ? vs : 0.0f;
-#pragma unroll
-                    for (int o = 1; o < kSubs; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    float vr_own = 0.0f, ref_own = 0.0f, step = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float vq = __shfl_sync(0xffffffffu, top, q * kSubs), lq = log2f(vq);
-                        const bool mine = (lane >> 3) == q;
-                        if (vq > 0.0f && (vr == 0.0f || lq - ref > kSpread)) {
-                            if (mine && vr > 0.0f) step = lq - ref;
-                            vr = vq;
-                            ref = lq;
-                        }
-                        if (mine) {
-                            vr_own = vr;
-                            ref_own = ref;
-                        }
-                    }
-                    float lv = -kSpread, iv = kSpreadFactor;
-                    if (vs > 0.0f && log2f(vs) - ref_own >= -kSpread) {
-                        lv = log2f(vs) - ref_own;
-                        iv = vr_own / vs;
-                    }
+                    // (with scales too far apart l is not taken from these: iv = 0)
+                    const float rel = vs > 0.0f ? log2f(vs) - ref : -INFINITY;
+                    const float lv = fmaxf(rel, vr < 0.0f ? -400.0f : -kSpread);
+                    const float iv = vr < 0.0f ? 0.0f : rel >= -kSpread ? vr / vs : kSpreadFactor;
                     for (int q = 0; q < 4 && t0 + q < max(tile1, tile0 + 1); ++q) {
                         const uint32_t r = n_tile % kTileRing;
                         wait(&sm.tile_empty[r], ((n_tile / kTileRing) & 1u) ^ 1u, 91);
@@ -1070,8 +1074,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                                 sm.tiles[r].head = head;
                                 sm.tiles[r].row_tile = row_tile;
                                 sm.tiles[r].edge = t * kKeys < all_lo || t * kKeys + kKeys > all_hi;
-                                sm.tiles[r].vr = vr_own > 0.0f ? vr_own : 1.0f;
-                                sm.tiles[r].step = step;
+                                sm.tiles[r].vr = vr;
                             }
                         }
                         __syncwarp();

@@ -49,26 +49,50 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kStartDecode = 8.0f, kStartPrefill = 4.0f, kGrow = 15.9f;
 
 // The scales of V's pages, as the exponents of the probabilities take them: in
-// log2 relative to a reference vr, and within +-kSpread of it.
+// log2 relative to a reference vr, the largest of an item's pages in the CTA.
 //     p' = 2^(s + rel - m),  o = sum p' code,  l = sum p' 2^-rel = sum 2^(s - m),  out = o vr / l
-// so that neither l nor p' leaves fp32's range wherever the scales lie in theirs
-// (2^-120 .. 2^121): with n keys l is between 2^-kSpread and n 2^(kGrow + kSpread).
-// A page smaller than 2^-kSpread of the reference counts as that much, or as
-// zero: what it is off by is 2^-kSpread of the row's largest V, below every other
-// rounding here.
-// The decode kernel's reference is the largest scale of an item's pages in the
-// CTA, looked up beforehand.  The prompt kernel's is that of the first key tile that has
-// one, until a tile's is larger than 2^kSpread of it: with d = log2 of that step, o *= 2^(lower -
-// d), m -= lower, l *= 2^lower, where lower = d (o stays) unless l would then
-// pass 2^kMostSum.  (In the decode kernel that change, once in the tile loop, cost
-// calls of 9 to 16 query rows 5 to 14%.)
-constexpr float kSpread = 40.0f;
-constexpr float kSpreadFactor = 1099511627776.0f;  // 2^kSpread
-constexpr float kMostSum = 60.0f;
+// While rel is within [-kSpread, 0] neither l nor p' leaves fp32's range: with n
+// keys l is below n 2^(kGrow + kSpread), and no p' that counts is flushed.  The
+// scales themselves may be anything from 2^-120 to 2^121, and a row may see any of
+// an item's pages.  Where an item's scales are further apart, l has to be taken
+// from the scores alone: the prompt kernel does that in its tile loop (rel is then
+// not held within anything), the decode kernel computes the item by plain_row, and
+// what its tile loop gives, with rel held at -kSpread, is not used.  (With a
+// reference that begins with the first page's and is changed in the tile loops where
+// a later one's is too large, calls of 9 to 16 query rows took 5 to 14% longer
+// and long prompts 2%; and rows that do not see the large page lost their V.)
+constexpr float kSpread = 80.0f;
+constexpr float kSpreadFactor = 1.2089258196146292e24f;  // 2^kSpread
 
-// The `lower` above, for a row whose l is `sum`.
-__device__ __forceinline__ float reference_shift(float d, float sum) {
-    return fminf(fminf(d, 100.0f), fmaxf(kMostSum - log2f(sum), 0.0f));
+// The reference for the 16-token tiles [tile0, tile1) of a sequence, by a whole
+// warp, eight reads a lane in flight: 1 where no scale is above 0, and negative
+// where they are too far apart.
+__device__ __forceinline__ float v_reference(const KvView &b, int32_t seq, int32_t head, int32_t tile0, int32_t tile1) {
+    const int shift = b.page_shift - 4;  // tiles of a page
+    const int32_t p1 = (tile1 - 1) >> shift;
+    float top = 0.0f, low = INFINITY;
+    for (int32_t at = (tile0 >> shift) + (threadIdx.x & 31); tile0 < tile1 && at <= p1; at += 32 * 8) {
+        int32_t page[8];
+        float vs[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            page[k] = at + 32 * k <= p1 ? b.table[static_cast<int64_t>(seq) * b.max_pages + at + 32 * k] : -1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            vs[k] = page[k] >= 0 && page[k] < b.num_pages ? __ldg(b.v_scales + static_cast<int64_t>(page[k]) * b.heads + head) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            top = fmaxf(top, vs[k]);
+            low = vs[k] > 0.0f ? fminf(low, vs[k]) : low;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    if (!(top > 0.0f)) return 1.0f;
+    return log2f(top) - log2f(low) <= kSpread - 1.0f ? top : -top;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -89,6 +113,97 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v, float 
 __device__ __forceinline__ void copy16(void *smem_dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(smem_dst)), "l"(src), "r"(there ? 16 : 0)
                  : "memory");
+}
+
+// One query row of (sequence, key/value head) over its keys in [key0, key1), for
+// items whose V scales are too far apart for the kernels' sums: a whole warp, four
+// dimensions a lane, four tokens a step, in fp32 and with V relative to the largest
+// scale that the row itself sees.  Writes the row's output and lse, or its
+// partial result.  (Slow: some microseconds for 100 keys.)
+template <typename T, int D, int FMT>
+__device__ __noinline__ void plain_row(const AttnView &a, int32_t seq, int32_t head, int32_t off, int32_t n, int32_t len,
+                                       int32_t row, int32_t key0, int32_t key1, float *part, float *part_lse) {
+    const KvView &b = a.kv;
+    const int lane = threadIdx.x & 31, c = 4 * lane;
+    const int32_t qi = row / a.group, qh = head * a.group + row % a.group, pos = len - n + qi;
+    const int32_t lo = max(key0, a.window > 0 ? max(0, pos - a.window + 1) : 0), hi = min(key1, a.causal ? pos + 1 : len);
+    auto page_of = [&](int32_t key) {
+        const int32_t page = b.table[static_cast<int64_t>(seq) * b.max_pages + (key >> b.page_shift)];
+        return page >= 0 && page < b.num_pages ? page : -1;
+    };
+    float q[4] = {0.0f, 0.0f, 0.0f, 0.0f}, amax = 0.0f;
+    if (c < D) {
+        const T *src = static_cast<const T *>(a.q.p) + static_cast<int64_t>(off + qi) * a.q.row + qh * a.q.head + c;
+        for (int d = 0; d < 4; ++d) q[d] = to_float(src[d]);
+    }
+    for (int d = 0; d < 4; ++d) amax = fmaxf(amax, fabsf(q[d]));
+    float top = 0.0f;
+    for (int32_t key = (lo >> b.page_shift << b.page_shift) + (lane << b.page_shift); key < hi; key += 32 << b.page_shift) {
+        const int32_t page = page_of(key);
+        if (page >= 0) top = fmaxf(top, b.v_scales[static_cast<int64_t>(page) * b.heads + head]);
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    if (!(top > 0.0f)) top = 1.0f;
+    // as the kernels do: the row's largest to [2^13, 2^14)
+    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+    e = amax < INFINITY ? max(e, -126) : 0;
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const float up = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    for (int d = 0; d < 4; ++d) q[d] *= down;
+    float M = -INFINITY, L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int32_t k4 = lo & ~3; k4 < hi; k4 += 4) {
+        const int32_t page = page_of(k4), t0 = k4 & (kKvTile - 1);
+        float ks = 0.0f, vs = 0.0f, s[4], v[4][4];
+        uint32_t kw[4] = {0u, 0u, 0u, 0u};
+        uint4 vw = make_uint4(0u, 0u, 0u, 0u);
+        if (page >= 0) {
+            ks = b.k_scales[static_cast<int64_t>(page) * b.heads + head];
+            vs = b.v_scales[static_cast<int64_t>(page) * b.heads + head];
+            const int64_t at = tile_offset<D>(b, page, head, (k4 & (b.page_tokens - 1)) / kKvTile);
+            if (c < D) {
+                for (int t = 0; t < 4; ++t)
+                    kw[t] = *reinterpret_cast<const uint32_t *>(b.k_pages + at + c / 64 * (kKvTile * 64) + (t0 + t) * 64 + c % 64);
+                if (vs > 0.0f) vw = *reinterpret_cast<const uint4 *>(b.v_pages + at + lane * 64 + t0 * 4);
+            }
+        }
+        float mn = M;
+        for (int t = 0; t < 4; ++t) {
+            float k[4];
+            codes_to_float<FMT>(kw[t], k);
+            float dot = q[0] * k[0] + q[1] * k[1] + (q[2] * k[2] + q[3] * k[3]);
+            for (int i = 16; i > 0; i >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
+            s[t] = k4 + t >= lo && k4 + t < hi ? dot * (ks * up) : -INFINITY;
+            mn = fmaxf(mn, s[t]);
+        }
+        codes_to_float<FMT>(vw.x, v[0]);
+        codes_to_float<FMT>(vw.y, v[1]);
+        codes_to_float<FMT>(vw.z, v[2]);
+        codes_to_float<FMT>(vw.w, v[3]);
+        const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(M - mu), rel = vs > 0.0f ? vs / top : 0.0f;
+        float sum = 0.0f, add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < 4; ++t) {
+            if (k4 + t < lo || k4 + t >= hi) continue;  // (whose codes may be NaN)
+            const float w = ex2(s[t] - mu);
+            sum += w;
+            for (int d = 0; d < 4; ++d) add[d] = fmaf(w, v[d][t], add[d]);
+        }
+        M = mn;
+        L = fmaf(L, f, sum);
+        for (int d = 0; d < 4; ++d) o[d] = fmaf(add[d], rel, o[d] * f);
+    }
+    const float inv = part == nullptr || !(L == 0.0f) ? 1.0f / L : 0.0f, lse = M + log2f(L);
+    const float4 y = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    if (c < D) {
+        if (part) store4(part + c, y, top);
+        else store4(static_cast<T *>(a.out.p) + static_cast<int64_t>(off + qi) * a.out.row + qh * a.out.head + c, y, top);
+    }
+    if (lane == 0) {
+        if (part) *part_lse = lse;
+        else if (a.lse) a.lse[static_cast<int64_t>(off + qi) * a.q_heads + qh] = lse * kLn2;
+    }
 }
 
 __device__ __forceinline__ void add_scaled(float4 &v, float &L, float f, const float4 &x, float l) {

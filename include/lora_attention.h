@@ -204,8 +204,9 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * most 2^-29 P (bf16), 2^-33 P (bf16, where the call takes the kernel for few
  * queries) or 2^-44 P (fp32) beyond that.  Over n keys this adds up to n 2^-29 P times
  * the largest code, which stays below bf16's own rounding of the largest values
- * up to a million keys.  V of pages whose scale is below 2^-40 of the largest
- * that a query sees may count as zero or as that much.
+ * up to a million keys.  Values that a query does not see have no part in this.
+ * (Pages whose V scales differ by more than 2^79 within a sequence and head cost
+ * time: twice as much for prompts, some ten times for few queries.)
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (num_q_heads /
  * num_heads over 64; num_q_heads not a multiple; rows * num_q_heads of 2^31
  * or more), WORKSPACE, CUDA.

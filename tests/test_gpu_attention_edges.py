@@ -381,3 +381,41 @@ def test_doubling_changes_nothing_where_no_scale_grows():
                 at += n
         for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
             assert torch.equal(getattr(a, name).view(torch.uint8), getattr(b, name).view(torch.uint8))
+
+
+@pytest.mark.parametrize("where", ["last page", "last page and least", "first page, out of the window"])
+@pytest.mark.parametrize("huge", [40.0, 100.0, 119.0])
+@pytest.mark.parametrize("dtype,fmt,n,before,page,D", [
+    ("bf16", "int8", 5, 3000, 16, 128), ("fp32", "e4m3", 40, 300, 32, 64), ("bf16", "e4m3", 20, 20, 16, 64),
+    ("bf16", "int8", 100, 700, 16, 128), ("bf16", "e4m3", 300, 4000, 32, 64), ("bf16", "int8", 150, 0, 16, 64),
+])
+def test_rows_are_untouched_by_scales_they_do_not_see(where, huge, dtype, fmt, n, before, page, D):
+    """A later token's V, or one before the window, however large: each row's tolerance is by the V that it sees."""
+    rng, cache, table, lens, offs = setup(before + n + page, [n], [before], page, fmt, 2, D)
+    L, G, window = before + n, 4, 0
+    pages = [int(p) for p in table[0] if p >= 0]
+    if where.startswith("last"):
+        cache.v_scales[pages[-1]] = float(2.0 ** huge)
+        if where.endswith("least"):
+            cache.v_scales[pages[:-1]] *= 2.0 ** -110
+    else:
+        cache.v_scales[pages[0]] = float(2.0 ** huge)
+        window = L - page - n // 2  # the later rows do not see the first page
+        if window < 1:
+            window = 7
+    ref = R.Paged(cache)
+    q, qd = draw(rng, (n, 2 * G, D), dtype, 1.5)
+    out, lse = cache.attention(q, dev(table), dev(lens), dev(offs), window=window, return_lse=True, max_queries=n)
+    scale = np.float32(D ** -0.5).astype(np.float64)
+    want, wl, spread, score = R.attention(ref, qd, table, lens, offs, scale, True, window)
+    top = np.abs(ref.v).max((2, 3)) * ref.vs.astype(np.float64)  # of page and head
+    vmax = np.zeros((n, 2 * G))
+    for i in range(n):
+        pos = before + i
+        seen = pages[(max(0, pos - window + 1) if window else 0) // page:pos // page + 1]
+        vmax[i] = np.repeat(top[seen].max(0), G)
+    tol, ltol = bounds(dtype, want, wl, spread, score, L, vmax)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err <= tol), f"worst {np.nanmax(err / tol):.3g} of its tolerance"
+    assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= ltol)
+    assert status() == 0
