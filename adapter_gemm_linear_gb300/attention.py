@@ -256,6 +256,8 @@ class KvCache:
         """lora_kv_gather: the rows' keys and values, dequantised -> (k, v)
         [rows, num_heads, head_dim], new tensors of ``dtype`` unless given.
         ``rows`` (needed with offsets and no k_out) is offsets' last value.
+        Rows of padding (length 0), of skipped sequences and of none are not
+        written: in new tensors they hold whatever the memory held.
         ``stream``: launch there instead of on the current stream."""
         device = self._device
         if stream is not None or device != _current_device():
@@ -292,8 +294,12 @@ class KvCache:
         softmax's sum).  The rows' own tokens must be in the cache.
 
         ``max_queries`` bounds the rows of one sequence (default: 1 without
-        offsets, else all rows); ``window`` > 0 limits a query to the last
-        ``window`` positions up to its own; ``scale`` defaults to head_dim^-0.5.
+        offsets, else all rows).  It and the block table's width, as a bound on
+        the lengths, choose the kernel for bf16 queries: a table much wider than
+        its longest sequence needs costs short calls of several queries some
+        time, and the same call with another width may differ in its last bits.
+        ``window`` > 0 limits a query to the last ``window`` positions up to its
+        own; ``scale`` defaults to head_dim^-0.5.
         ``stream``: launch there instead of on the current stream."""
         shape, device = q.shape, self._device
         if stream is not None or device != _current_device():

@@ -6,16 +6,20 @@
 //
 // Append: one warp takes one 16-token tile of one (page, head) of K or V; the
 // warps of a page share the page's largest magnitude through shared memory, and
-// hold their rows as they were read until the scale is known.  Codes that are
+// hold their rows as they were read until the scale is known (with heads of 128
+// in 80 registers some of them in local memory: 140 bytes a thread in bf16, 500 in
+// fp32).  Codes that are
 // there already are only touched where the page's scale grows (or, in V's
 // tiles, where they share a 16-byte piece with a new token).
 // What bounds it is the chain of dependent reads (the sequence, its page, the
-// rows), which as many warps as possible have to cover, and the instructions a
-// value (about ten): magnitudes are compared two at a time, and an int8 code
-// takes one fused multiply-add that rounds and one that checks.  8192 tokens of
-// 8 heads of 128 take 22 us (50 MB), one token of each of 256 sequences 15.5.
-// With 128 registers a thread instead of 80: 24 and 16.4; with the rows read
-// twice by rolled code that rounds with conversion instructions: 31.5 and 18.4.
+// rows), which as many warps as possible have to cover, and the instructions: 23
+// a value and lane, of which an int8 code's rounding takes two fused
+// multiply-adds, and magnitudes are compared two at a time.  8192 tokens of 8
+// heads of 128 take 22 us (50 MB; 11.9 million instructions, 10 us of issue
+// slots, 55% of them used), one token of each of 256 sequences 15.5 (50%).  With
+// 128 registers a thread instead of 80: 24 and 16.4; with the rows read twice by
+// rolled code that rounds with conversion instructions: 31.5 and 18.4.  In fp32, in
+// a graph with the reading back, 54 us for 31.
 #include <cuda_runtime.h>
 
 #include "attn_device.cuh"

@@ -40,12 +40,16 @@
 //    follows the maximum only when p' would pass that, so the sums are rarely
 //    rescaled.
 // Measured, with the join: 256 sequences of about 4096 tokens, 64 heads on 8 of
-// 128, int8: 318 us, 5.8 TB/s (0.86 of a copy's rate; SMs that reach the memory
-// less well end last).  4 sequences of 131072, e4m3: 183 us, 5.9 TB/s.  One of
-// 2000, 32 heads on 8: 14.3 us, of which the reads that depend on one another
-// (length, page, scale, codes) and two launches take most.  64 sequences of 4 new
-// tokens in a window of 1024, heads of 64: 51 us, where the instructions of a
-// tile (460 for 2 KB of codes) bound it, not the 61 MB.
+// 128, int8: 317 us, 5.8 TB/s (0.86 of a copy's rate; SMs that reach the memory
+// less well end last).  4 sequences of 131072, e4m3: 184 us, 5.9 TB/s.  One of
+// 2000, 32 heads on 8: 14.3 us (9.7 + 4.5; 10.5 in a graph), of which the reads that
+// depend on one another (length, page, scale, codes) and two launches take most.
+// 64 sequences of 4 new tokens in a window of 1024, heads of 64: 53 us, where the
+// instructions of a tile (480 for 2 KB of codes, 43% of the issue slots) bound it,
+// not the 61 MB.  16 rows a key head, 64 sequences of 4096 tokens, heads of 128: 133
+// us in a graph (8 rows: 99, fp32 118; the codes take 79).  fp32 prompts take this
+// kernel too, eight rows a pass over all keys: 512 tokens of 32 heads on 8, 81 us
+// (bf16 30), on 4096 more 458 (55).
 #include <cuda_runtime.h>
 #include <math.h>
 

@@ -113,12 +113,14 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
 // heads that share a key/value head) at a time, the tensor-core kernel of
 // attn_prefill.cu on 256, and is faster as soon as the first would take more
 // than one pass: 64 sequences of 4096 tokens, 8 heads of 128, with 16 rows
-// 141 against 190 us, with 32 rows 258 against 192 us.  But it takes some 20 us
-// to get going, so where the tables have no room for more than eight of the
-// first's units of work an SM (16 rows x 128 keys), those are done sooner: 128
-// queries of 32 heads on 8 on their own keys (512 units) 18.4 against 26.6 us,
-// 64 on 1064 (1152 units) 28.7 against 30.7, 178 x 2 heads on 7673 (1440
-// units) 38.9 against 34.8, 4 x 128 queries (2048 units) 49 against 28.7.
+// 133 against 186 us, with 32 rows 244 against 187 us (in a graph, as what
+// follows).  But it takes some 20 us to get going, so where the tables have no
+// room for more than eight of the first's units of work an SM (16 rows x 128
+// keys), those are done sooner: 128 queries of 32 heads on 8 on their own keys
+// (512 units) 13.6 against 20.9 us, 64 on 1064 (1152 units) 25.1 against 25.0, 178
+// x 2 heads on 7673 (1440 units) 28.5 against 28.8, 4 x 128 queries (2048 units)
+// 43.5 against 22.0.  (What the tables have room for is all that the host knows of
+// the lengths: a wider table of the same sequences may take the other kernel.)
 bool many_queries(const lora::AttnView &v, lora_dtype_t dtype) {
     const int64_t rows = static_cast<int64_t>(v.max_queries) * v.group;  // of a sequence, at most
     if (dtype != LORA_BF16 || rows <= 16) return false;

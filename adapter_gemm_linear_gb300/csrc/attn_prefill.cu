@@ -32,12 +32,16 @@
 // The key tiles of all items form one line that the CTAs share equally
 // (attn_split.cuh), so causal and ragged work is level to one tile.
 // Measured, with the join: 2048 queries x 34816 keys, 32 heads on 8 of 128, int8:
-// 797 us, 1.42 PFLOP/s (0.73 of the measured bf16 product): the softmax's and
-// the conversions' instructions take the issue slots that are left, 1.75 us for
-// a key tile whose products take 1.1.  16 causal prompts, 8192 tokens, 64 heads
-// on 8: 208 us, 0.58 PFLOP/s of what the mask leaves: an item has some four
-// key tiles there, and costs about four more (its queries' conversion, the
-// masked tile, the results' way out).
+// 795 us in a graph (830-843 one by one), 1.43 PFLOP/s (0.74 of the measured bf16
+// product): 1.75 us for a key tile whose products take 1.1.  The tensor pipes are
+// busy for 51% of the time and 52% of the issue slots are used, so neither bounds
+// it alone, but the roles' waits for one another.  With 32 query rows, a quarter
+// of tile A and none of B, a key tile takes as long (64 x 4 queries of 64 heads on 8
+// on 4096 keys: 187 us, whose codes take 79): it is the converting warps or A's
+// own chain that the others wait for.  16 causal prompts, 8192 tokens, 64 heads on 8:
+// 212-217 us (207 in a graph), 0.56 PFLOP/s of what the mask leaves: an item has
+// some four key tiles there, and costs about four more (its queries' conversion, the
+// masked tile, the results' way out); pipes 31%, issue slots 50%.
 #include <cuda_runtime.h>
 #include <math.h>
 

@@ -44,8 +44,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 2^-25 at most, 2^-(25 + start) of the row's largest, which a long flat tail behind a
 // dominant key adds up.  In the decode kernel the start costs nothing (0, 4
 // and 8 within 1% of each other).  The prompt kernel waits for each rescaling of
-// a row of 128: 16 prompts take 210, 213, 227 and 242 us with starts of 0,
-// 4, 6 and 8, the long chunk 824, 835, 844 and 848.
+// a row of 128: 16 prompts take 210, 213, 227 and 242 us with starts of 0, 4, 6
+// and 8, the long chunk 824, 835, 844 and 848, and 2048 queries on 6048 keys whose
+// e4m3 scales differ by powers of two 157 and 176 with 0 and 4.
 constexpr float kStartDecode = 8.0f, kStartPrefill = 4.0f, kGrow = 15.9f;
 
 // The scales of V's pages, as the exponents of the probabilities take them: in
@@ -218,9 +219,11 @@ __device__ __forceinline__ void add_scaled(float4 &v, float &L, float f, const f
 // and goes on in the next ones, block row y some of its rows.  The partial
 // results of a row go to G groups of threads in turn, which take up to eight at
 // a time, so that all loads of an item in up to 8 G CTAs are in flight together:
-// what bounds the kernel is their latency.  (Both kernels for one sequence of
-// 2000 tokens, 32 heads on 8, each of these in 16 CTAs: 14.3 us with G = 4,
-// 18.4 with 1, 16.4 with 8.)  Every sum's order is fixed.
+// what bounds the kernel is their latency.  (Both kernels in a graph, with G = 1,
+// 2, 4 and 8: one sequence of 2000 tokens, 32 heads on 8, 11.1, 10.5, 10.5 and 12.1
+// us; of 4096, 64 heads on 8, 14.7, 13.0, 12.7 and 13.7; but 64 x 4 queries in a
+// window of 1024, whose items span two CTAs, 42.6, 43.7, 45.7 and 49.7.)  Every
+// sum's order is fixed.
 // The kernel may begin while the one before still writes what it joins, so after
 // its wait it reads through the L2 and never by the read-only path, which is
 // for data that nobody writes while a kernel runs.
