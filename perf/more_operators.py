@@ -242,7 +242,7 @@ def prepare(case, seed):
         st["max_queries"] = max(n)
     if own:  # the cache handle over these buffers, which a program makes once
         from adapter_gemm_linear_gb300 import KvCache
-        st["cache"] = KvCache(pages, H, D, page_tokens=P, fmt="int4", k_pages=st["k_pages"],
+        st["cache"] = KvCache(pages, H, D, page_tokens=P, fmt="uint4", k_pages=st["k_pages"],
                               v_pages=st["v_pages"], k_scales=st["k_scales"], v_scales=st["v_scales"])
     return st
 
