@@ -27,5 +27,5 @@ from .api import (  # noqa: F401
     status_string,
     arm_test_wait_timeout,
 )
-from .attention import KvCache, kv_pages_bytes, rope, rope_tables  # noqa: F401
+from .attention import KvCache, kv_pages_bytes, norm_rope, norm_rope_backward, rope, rope_tables  # noqa: F401
 from .build import build  # noqa: F401

@@ -168,6 +168,28 @@ class RopeArgs(ctypes.Structure):
     ]
 
 
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("rope", RopeArgs),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("weight_dtype", ctypes.c_int),
+        ("unit_offset", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class NormRopeGrads(ctypes.Structure):
+    _fields_ = [
+        ("dq", Heads),
+        ("dk", Heads),
+        ("dq_weight", ctypes.c_void_p),
+        ("dk_weight", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class KvCacheDesc(ctypes.Structure):
     _fields_ = [
         ("format", ctypes.c_int),
@@ -217,6 +239,9 @@ _ROWS_ARGS = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, c
 # (name, restype, argtypes) of every entry point declared in include/lora_attention.h
 ATTENTION_SIGNATURES = [
     ("lora_rope", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    ("lora_norm_rope", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    ("lora_norm_rope_backward_workspace_bytes", ctypes.c_size_t, [ctypes.c_void_p]),
+    ("lora_norm_rope_backward", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     ("lora_kv_pages_bytes", ctypes.c_size_t, [ctypes.c_int32] * 4),
     ("lora_kv_append", ctypes.c_int, _ROWS_ARGS),
     ("lora_kv_gather", ctypes.c_int, _ROWS_ARGS),

@@ -34,10 +34,14 @@ _FORMATS = {"int8": (_lib.KV_INT8, torch.int8), "e4m3": (_lib.KV_E4M3, torch.flo
 # in one go (ctypes takes a microsecond for every few fields it sets) and the
 # stream is asked for as a bare handle.
 _ROPE_ARGS = struct.Struct("@6i PqqPqqPqqPqq PPiiPPii")
+_NORM_ARGS = struct.Struct("@PPiifi")  # (what follows the lora_rope_args_t)
+_NORM_GRADS = struct.Struct("@PqqPqqPPPN")
 _BATCH = struct.Struct("@iiPPPi0P")
 _HEADS = struct.Struct("@Pqq")
 _ATTENTION_ARGS = struct.Struct("@iiPqqPqqPfiiiPN")
 assert _ROPE_ARGS.size == ctypes.sizeof(_lib.RopeArgs) and _BATCH.size == ctypes.sizeof(_lib.KvBatch)
+assert _ROPE_ARGS.size + _NORM_ARGS.size == ctypes.sizeof(_lib.NormRopeArgs)
+assert _NORM_GRADS.size == ctypes.sizeof(_lib.NormRopeGrads)
 assert _HEADS.size == ctypes.sizeof(_lib.Heads) and _ATTENTION_ARGS.size == ctypes.sizeof(_lib.AttentionArgs)
 
 _DTYPES = {torch.bfloat16: _lib.LORA_BF16, torch.float32: _lib.LORA_FP32}
@@ -110,12 +114,20 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: tor
     width), with ``axes[i]`` the axis of pair i (default: axis 0).
     ``inverse`` turns the other way: the gradient of the call, or its undoing.
     ``stream``: launch there instead of on the current stream."""
-    device, shape = q.get_device(), q.shape
+    device = q.get_device()
     if device < 0:
         raise ValueError(f"q must be on a CUDA device, not on {q.device}")
     if stream is not None or device != _current_device():
         return _elsewhere(rope, device, stream, (q, k, cos, sin, positions), axes=axes, interleaved=interleaved,
                           inverse=inverse, q_out=q_out, k_out=k_out)
+    args, q_out, k_out, _keep = _rope_args(q, k, cos, sin, positions, axes, interleaved, inverse, q_out, k_out, device)
+    _call(_lib.lib().lora_rope(args, _current_stream(device)), "lora_rope")
+    return q_out, k_out
+
+
+def _rope_args(q, k, cos, sin, positions, axes, interleaved, inverse, q_out, k_out, device):
+    """(lora_rope_args_t as bytes, q_out, k_out, what has to live until the call)"""
+    shape = q.shape
     if len(shape) != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
     rows, q_heads, D = shape
@@ -144,13 +156,86 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: tor
         kh, koh = _heads(k, "k", device), _heads(k_out, "k_out", device)
     pair_axis = None if axes is None else bytes(axes)
     axis_ptr = 0 if axes is None else ctypes.cast(pair_axis, ctypes.c_void_p).value
-    args = _ROPE_ARGS.pack(
+    return _ROPE_ARGS.pack(
         _dtype(q.dtype), rows, D, 2 * table[1], q_heads, k_heads, *_heads(q, "q", device),
         *_heads(q_out, "q_out", device), *kh, *koh, cos.data_ptr(), sin.data_ptr(), table[0],
         1 if positions.dim() == 1 else positions.shape[0], _index(positions, "positions", device), axis_ptr,
-        interleaved, inverse)
-    _call(_lib.lib().lora_rope(args, _current_stream(device)), "lora_rope")
-    return q_out, k_out if k is not None else None
+        interleaved, inverse), q_out, k_out if k is not None else None, pair_axis
+
+
+def _norm_args(q, k, q_weight, k_weight, eps, unit_offset, device):
+    """The rest of lora_norm_rope_args_t as bytes."""
+    w = [t for t in (q_weight, k_weight if k is not None else None) if t is not None]
+    for t in w:
+        if t.shape != q.shape[2:] or t.dtype != w[0].dtype or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"q_weight and k_weight must be contiguous [{q.shape[2]}] of one dtype on device {device}")
+    return _NORM_ARGS.pack(0 if q_weight is None else q_weight.data_ptr(),
+                           0 if k_weight is None or k is None else k_weight.data_ptr(),
+                           _dtype(w[0].dtype) if w else _lib.LORA_FP32, unit_offset, eps, 0)
+
+
+def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+              k_weight: Optional[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor,
+              eps: float = 1e-6, unit_offset: bool = False, axes: Optional[Sequence[int]] = None,
+              interleaved: bool = False, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """lora_norm_rope: every head of q and k (or None) divided by the root of
+    its mean square + ``eps``, times its weight, and turned by its row's
+    position, in one pass -> (q_out, k_out), new tensors unless given
+    (``q_out=q`` works in place).
+
+    ``q_weight``, ``k_weight``: [head_dim], bfloat16 or float32, or None for
+    none; with ``unit_offset`` they are taken as 1 + weight.  The others: as
+    rope.  head_dim up to 256."""
+    device = q.get_device()
+    if device < 0:
+        raise ValueError(f"q must be on a CUDA device, not on {q.device}")
+    if stream is not None or device != _current_device():
+        return _elsewhere(norm_rope, device, stream, (q, k, q_weight, k_weight, cos, sin, positions), eps=eps,
+                          unit_offset=unit_offset, axes=axes, interleaved=interleaved, q_out=q_out, k_out=k_out)
+    args, q_out, k_out, _keep = _rope_args(q, k, cos, sin, positions, axes, interleaved, False, q_out, k_out, device)
+    args += _norm_args(q, k, q_weight, k_weight, eps, unit_offset, device)
+    _call(_lib.lib().lora_norm_rope(args, _current_stream(device)), "lora_norm_rope")
+    return q_out, k_out
+
+
+def norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
+                       q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], cos: torch.Tensor,
+                       sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6, unit_offset: bool = False,
+                       axes: Optional[Sequence[int]] = None, interleaved: bool = False,
+                       q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """lora_norm_rope_backward: from the gradients dq, dk of norm_rope's outputs
+    -> (gradient of q, of k, of q_weight, of k_weight).  The other arguments are
+    norm_rope's, but q_out and k_out, where the gradients of q and k go
+    (``q_out=dq`` works in place).  Those of the weights are float32 [head_dim];
+    None for what was None."""
+    device = q.get_device()
+    if device < 0:
+        raise ValueError(f"q must be on a CUDA device, not on {q.device}")
+    if stream is not None or device != _current_device():
+        return _elsewhere(norm_rope_backward, device, stream, (dq, dk, q, k, q_weight, k_weight, cos, sin, positions),
+                          eps=eps, unit_offset=unit_offset, axes=axes, interleaved=interleaved, q_out=q_out,
+                          k_out=k_out, workspace=workspace)
+    args, q_out, k_out, _keep = _rope_args(q, k, cos, sin, positions, axes, interleaved, False, q_out, k_out, device)
+    args += _norm_args(q, k, q_weight, k_weight, eps, unit_offset, device)
+    if dq.shape != q.shape or dq.dtype != q.dtype:
+        raise ValueError("dq must have q's shape and dtype")
+    if (dk is None) != (k is None) or (k is not None and (dk.shape != k.shape or dk.dtype != k.dtype)):
+        raise ValueError("dk must have k's shape and dtype")
+    L = _lib.lib()
+    weights = [None if w is None else torch.empty(q.shape[2:], dtype=torch.float32, device=q.device)
+               for w in (q_weight, k_weight if k is not None else None)]
+    if workspace is None:
+        need = L.lora_norm_rope_backward_workspace_bytes(args) if any(w is not None for w in weights) else 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {q.device}")
+    grads = _NORM_GRADS.pack(*_heads(dq, "dq", device), *((0, 0, 0) if dk is None else _heads(dk, "dk", device)),
+                             *(0 if w is None else w.data_ptr() for w in weights), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size())
+    _call(L.lora_norm_rope_backward(args, grads, _current_stream(device)), "lora_norm_rope_backward")
+    return q_out, k_out, weights[0], weights[1]
 
 
 def kv_pages_bytes(num_pages: int, num_heads: int, head_dim: int, page_tokens: int) -> int:

@@ -11,6 +11,7 @@
 namespace {
 
 constexpr int32_t kMaxKvHeads = 4096;  // keeps every grid dimension in range
+constexpr int32_t kMaxNormDim = 256;   // of a head that lora_norm_rope normalises: two chunks a lane at most
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -82,6 +83,69 @@ lora_status_t check_batch(const lora_kv_cache_t *c, const lora_kv_batch_t *b, lo
 
 bool valid_dtype(lora_dtype_t t) { return t == LORA_BF16 || t == LORA_FP32; }
 
+lora_status_t check_rope(const lora_rope_args_t *a, lora::RopeView *out) {
+    if (!a) return LORA_ERR_INVALID_ARG;
+    if (!valid_dtype(a->dtype)) return LORA_ERR_DTYPE;
+    if (a->rows < 0 || a->head_dim <= 0 || a->num_q_heads <= 0 || a->num_k_heads < 0 || a->max_pos <= 0)
+        return LORA_ERR_INVALID_ARG;
+    if (a->num_axes < 1 || a->num_axes > LORA_ROPE_MAX_AXES) return LORA_ERR_INVALID_ARG;
+    if (a->rot_dim < 16 || a->rot_dim > a->head_dim || a->rot_dim > 2 * LORA_ROPE_MAX_PAIRS)
+        return LORA_ERR_INVALID_ARG;
+    if (a->head_dim % 8 || a->rot_dim % 16) return LORA_ERR_ALIGNMENT;
+    if (a->head_dim > 1024) return LORA_ERR_UNSUPPORTED;
+    lora::RopeView &v = *out;
+    lora_status_t s = check_heads(&a->q, a->dtype, a->rows, &v.q);
+    if (s == LORA_OK) s = check_heads(&a->q_out, a->dtype, a->rows, &v.q_out);
+    if (s == LORA_OK) s = check_heads(&a->k, a->dtype, a->num_k_heads ? a->rows : 0, &v.k);
+    if (s == LORA_OK) s = check_heads(&a->k_out, a->dtype, a->num_k_heads ? a->rows : 0, &v.k_out);
+    if (s != LORA_OK) return s;
+    if (a->rows > 0) {
+        if (!a->cos_table || !a->sin_table || !a->positions) return LORA_ERR_INVALID_ARG;
+        if (!aligned(a->cos_table, 16) || !aligned(a->sin_table, 16) || !aligned(a->positions, 4))
+            return LORA_ERR_ALIGNMENT;
+    }
+    memset(v.pair_axis, 0, sizeof(v.pair_axis));
+    for (int32_t i = 0; a->pair_axis && i < a->rot_dim / 2; ++i) {
+        if (a->pair_axis[i] >= a->num_axes) return LORA_ERR_INVALID_ARG;
+        v.pair_axis[i] = a->pair_axis[i];
+    }
+    v.cos_table = a->cos_table;
+    v.sin_table = a->sin_table;
+    v.positions = a->positions;
+    v.rows = a->rows;
+    v.head_dim = a->head_dim;
+    v.rot_dim = a->rot_dim;
+    v.q_heads = a->num_q_heads;
+    v.k_heads = a->num_k_heads;
+    v.max_pos = a->max_pos;
+    v.num_axes = a->num_axes;
+    v.interleaved = a->interleaved != 0;
+    v.inverse = a->inverse != 0;
+    v.status = nullptr;
+    return LORA_OK;
+}
+
+lora_status_t check_norm_rope(const lora_norm_rope_args_t *a, lora::NormRopeView *v) {
+    if (!a) return LORA_ERR_INVALID_ARG;
+    const lora_status_t s = check_rope(&a->rope, &v->rope);
+    if (s != LORA_OK) return s;
+    if (a->rope.inverse) return LORA_ERR_UNSUPPORTED;
+    if (a->rope.head_dim > kMaxNormDim) return LORA_ERR_UNSUPPORTED;
+    if (!valid_dtype(a->weight_dtype)) return LORA_ERR_DTYPE;
+    if (!(a->eps > 0.0f) || !isfinite(a->eps)) return LORA_ERR_INVALID_ARG;
+    const uintptr_t size = a->weight_dtype == LORA_FP32 ? 4 : 2;
+    if (!aligned(a->q_weight, size) || !aligned(a->k_weight, size)) return LORA_ERR_ALIGNMENT;
+    v->dq = v->dk = lora::HeadsView{nullptr, 0, 0};
+    v->q_weight = a->q_weight;
+    v->k_weight = a->k_weight;
+    v->partial = nullptr;
+    v->eps = a->eps;
+    v->weight_fp32 = a->weight_dtype == LORA_FP32;
+    v->unit_offset = a->unit_offset != 0;
+    v->q_groups = v->k_groups = 0;
+    return LORA_OK;
+}
+
 lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b, const lora_kv_attention_args_t *a,
                               lora::AttnView *v) {
     lora_status_t s = check_batch(c, b, &v->kv);
@@ -139,46 +203,51 @@ size_t workspace_bytes(const lora::AttnView &v, int head_dim, lora_dtype_t dtype
 extern "C" {
 
 lora_status_t lora_rope(const lora_rope_args_t *a, void *stream) {
-    if (!a) return LORA_ERR_INVALID_ARG;
-    if (!valid_dtype(a->dtype)) return LORA_ERR_DTYPE;
-    if (a->rows < 0 || a->head_dim <= 0 || a->num_q_heads <= 0 || a->num_k_heads < 0 || a->max_pos <= 0)
-        return LORA_ERR_INVALID_ARG;
-    if (a->num_axes < 1 || a->num_axes > LORA_ROPE_MAX_AXES) return LORA_ERR_INVALID_ARG;
-    if (a->rot_dim < 16 || a->rot_dim > a->head_dim || a->rot_dim > 2 * LORA_ROPE_MAX_PAIRS)
-        return LORA_ERR_INVALID_ARG;
-    if (a->head_dim % 8 || a->rot_dim % 16) return LORA_ERR_ALIGNMENT;
-    if (a->head_dim > 1024) return LORA_ERR_UNSUPPORTED;
     lora::RopeView v;
-    lora_status_t s = check_heads(&a->q, a->dtype, a->rows, &v.q);
-    if (s == LORA_OK) s = check_heads(&a->q_out, a->dtype, a->rows, &v.q_out);
-    if (s == LORA_OK) s = check_heads(&a->k, a->dtype, a->num_k_heads ? a->rows : 0, &v.k);
-    if (s == LORA_OK) s = check_heads(&a->k_out, a->dtype, a->num_k_heads ? a->rows : 0, &v.k_out);
-    if (s != LORA_OK) return s;
-    if (a->rows > 0) {
-        if (!a->cos_table || !a->sin_table || !a->positions) return LORA_ERR_INVALID_ARG;
-        if (!aligned(a->cos_table, 16) || !aligned(a->sin_table, 16) || !aligned(a->positions, 4))
-            return LORA_ERR_ALIGNMENT;
-    }
-    memset(v.pair_axis, 0, sizeof(v.pair_axis));
-    for (int32_t i = 0; a->pair_axis && i < a->rot_dim / 2; ++i) {
-        if (a->pair_axis[i] >= a->num_axes) return LORA_ERR_INVALID_ARG;
-        v.pair_axis[i] = a->pair_axis[i];
-    }
-    v.cos_table = a->cos_table;
-    v.sin_table = a->sin_table;
-    v.positions = a->positions;
-    v.rows = a->rows;
-    v.head_dim = a->head_dim;
-    v.rot_dim = a->rot_dim;
-    v.q_heads = a->num_q_heads;
-    v.k_heads = a->num_k_heads;
-    v.max_pos = a->max_pos;
-    v.num_axes = a->num_axes;
-    v.interleaved = a->interleaved != 0;
-    v.inverse = a->inverse != 0;
-    if (a->rows == 0) return LORA_OK;
+    const lora_status_t s = check_rope(a, &v);
+    if (s != LORA_OK || a->rows == 0) return s;
     cudaError_t e = lora::device_status_ptr(&v.status);
     if (e == cudaSuccess) e = lora::launch_rope(v, a->dtype, as_stream(stream));
+    return e == cudaSuccess ? LORA_OK : fail(e);
+}
+
+lora_status_t lora_norm_rope(const lora_norm_rope_args_t *a, void *stream) {
+    lora::NormRopeView v;
+    const lora_status_t s = check_norm_rope(a, &v);
+    if (s != LORA_OK || a->rope.rows == 0) return s;
+    cudaError_t e = lora::device_status_ptr(&v.rope.status);
+    if (e == cudaSuccess) e = lora::launch_norm_rope(v, a->rope.dtype, as_stream(stream));
+    return e == cudaSuccess ? LORA_OK : fail(e);
+}
+
+size_t lora_norm_rope_backward_workspace_bytes(const lora_norm_rope_args_t *a) {
+    lora::NormRopeView v;
+    return check_norm_rope(a, &v) == LORA_OK ? lora::norm_rope_workspace_bytes(a->rope.head_dim) : 0;
+}
+
+lora_status_t lora_norm_rope_backward(const lora_norm_rope_args_t *a, const lora_norm_rope_grads_t *g, void *stream) {
+    lora::NormRopeView v;
+    lora_status_t s = check_norm_rope(a, &v);
+    if (s != LORA_OK) return s;
+    if (!g) return LORA_ERR_INVALID_ARG;
+    s = check_heads(&g->dq, a->rope.dtype, a->rope.rows, &v.dq);
+    if (s == LORA_OK) s = check_heads(&g->dk, a->rope.dtype, a->rope.num_k_heads ? a->rope.rows : 0, &v.dk);
+    if (s != LORA_OK) return s;
+    if (!aligned(g->dq_weight, 4) || !aligned(g->dk_weight, 4)) return LORA_ERR_ALIGNMENT;
+    cudaStream_t st = as_stream(stream);
+    if (a->rope.rows == 0) {  // sums of nothing
+        const size_t bytes = sizeof(float) * a->rope.head_dim;
+        cudaError_t e = g->dq_weight ? cudaMemsetAsync(g->dq_weight, 0, bytes, st) : cudaSuccess;
+        if (e == cudaSuccess && g->dk_weight) e = cudaMemsetAsync(g->dk_weight, 0, bytes, st);
+        return e == cudaSuccess ? LORA_OK : fail(e);
+    }
+    if (g->dq_weight || g->dk_weight) {
+        if (!g->workspace || g->workspace_bytes < lora::norm_rope_workspace_bytes(a->rope.head_dim)) return LORA_ERR_WORKSPACE;
+        if (!aligned(g->workspace, 16)) return LORA_ERR_ALIGNMENT;
+        v.partial = static_cast<float *>(g->workspace);
+    }
+    cudaError_t e = lora::device_status_ptr(&v.rope.status);
+    if (e == cudaSuccess) e = lora::launch_norm_rope_backward(v, a->rope.dtype, g->dq_weight, g->dk_weight, st);
     return e == cudaSuccess ? LORA_OK : fail(e);
 }
 

@@ -39,6 +39,16 @@ struct RopeView {
     uint8_t chunk_axis[LORA_ROPE_MAX_PAIRS / 4];  // of a thread's pairs, or LORA_ROPE_MAX_AXES where they differ
 };
 
+struct NormRopeView {
+    RopeView rope;  // (of the gradient: q and k the inputs, q_out and k_out their gradients)
+    HeadsView dq, dk;
+    const void *q_weight, *k_weight;
+    float *partial;  // of the weights' gradients: [blocks][q or k][head_dim]; null: not wanted
+    float eps;
+    int32_t weight_fp32, unit_offset;
+    int32_t q_groups, k_groups;  // of a block, per row
+};
+
 struct AttnView {
     KvView kv;
     HeadsView q, out;
@@ -53,6 +63,10 @@ struct AttnView {
 };
 
 cudaError_t launch_rope(const RopeView &v, lora_dtype_t dtype, cudaStream_t stream);
+size_t norm_rope_workspace_bytes(int head_dim);
+cudaError_t launch_norm_rope(const NormRopeView &v, lora_dtype_t dtype, cudaStream_t stream);
+cudaError_t launch_norm_rope_backward(const NormRopeView &v, lora_dtype_t dtype, float *dq_weight, float *dk_weight,
+                                      cudaStream_t stream);
 cudaError_t launch_kv_append(const KvView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,
                              const HeadsView &k, const HeadsView &val, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,

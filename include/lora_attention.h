@@ -77,6 +77,54 @@ typedef struct lora_rope_args {
 
 lora_status_t lora_rope(const lora_rope_args_t *args, void *stream);
 
+/*
+ * Norms of q and k for each head, and the rotary positions, in one pass: with W =
+ * w, or 1 + w if unit_offset, a head x of head_dim = D values becomes
+ *
+ *     n_d = x_d W_d / sqrt(sum_d x_d^2 / D + eps),   y = n turned as by lora_rope
+ *
+ * (dimensions past rot_dim are normalised, not turned).  Each value is read and
+ * written once.  Arithmetic in fp32, squares and their sum included, one
+ * rounding to the dtype at the end.  A weight of NULL stands for W = 1.
+ * An output may be its own input (same pointer and strides); other overlaps are
+ * not allowed.  Errors: as lora_rope, and UNSUPPORTED for head_dim over 256 or
+ * `inverse`; a position out of range leaves its pairs unturned (normalised).
+ */
+typedef struct lora_norm_rope_args {
+    lora_rope_args_t rope;    /* its `inverse` is 0 */
+    const void *q_weight;     /* device [head_dim] of weight_dtype, or NULL */
+    const void *k_weight;
+    lora_dtype_t weight_dtype;
+    int32_t unit_offset;
+    float eps;                /* > 0, finite */
+} lora_norm_rope_args_t;
+
+lora_status_t lora_norm_rope(const lora_norm_rope_args_t *args, void *stream);
+
+/*
+ * The gradient of that call.  args as given to it, with q and k its inputs, and
+ * q_out and k_out where their gradients go; dq and dk: the gradients of its outputs.
+ * With h = dy turned back, r = 1 / sqrt(mean(x^2) + eps) and a = h W:
+ *
+ *     dx = r (a - x r^2 mean(a x)),   dw = sum over rows and heads of h x r
+ *
+ * in fp32; dx is rounded once to the dtype, dw is fp32, its sums' order fixed by
+ * the sizes and the device's number of SMs.  A gradient may take the place of dy, or of
+ * the input (same pointer and strides).  With rows = 0 the weights' gradients are set to 0.
+ */
+typedef struct lora_norm_rope_grads {
+    lora_heads_t dq, dk;      /* like q and k */
+    float *dq_weight;         /* device [head_dim], 4-byte aligned; NULL: not wanted */
+    float *dk_weight;
+    void *workspace;          /* device, >= lora_norm_rope_backward_workspace_bytes, if a weight's gradient is wanted */
+    size_t workspace_bytes;
+} lora_norm_rope_grads_t;
+
+/* Scratch bytes on the current device; it keeps nothing between calls.  0 if the arguments are invalid. */
+size_t lora_norm_rope_backward_workspace_bytes(const lora_norm_rope_args_t *args);
+
+lora_status_t lora_norm_rope_backward(const lora_norm_rope_args_t *args, const lora_norm_rope_grads_t *grads, void *stream);
+
 /* ---------------------------------------------------------------------- */
 /* The 8-bit paged key/value cache                                         */
 /* ---------------------------------------------------------------------- */
