@@ -133,8 +133,7 @@ lora_status_t check_norm_rope(const lora_norm_rope_args_t *a, lora::NormRopeView
     if (a->rope.head_dim > kMaxNormDim) return LORA_ERR_UNSUPPORTED;
     if (!valid_dtype(a->weight_dtype)) return LORA_ERR_DTYPE;
     if (!(a->eps > 0.0f) || !isfinite(a->eps)) return LORA_ERR_INVALID_ARG;
-    const uintptr_t size = a->weight_dtype == LORA_FP32 ? 4 : 2;
-    if (!aligned(a->q_weight, size) || !aligned(a->k_weight, size)) return LORA_ERR_ALIGNMENT;
+    if (!aligned(a->q_weight, 16) || !aligned(a->k_weight, 16)) return LORA_ERR_ALIGNMENT;
     v->dq = v->dk = lora::HeadsView{nullptr, 0, 0};
     v->q_weight = a->q_weight;
     v->k_weight = a->k_weight;
