@@ -6,8 +6,9 @@ done by liblora.so (C ABI in include/lora.h, CUDA kernels for sm_103a); this
 package only binds it to PyTorch tensors and streams.
 
 What stands between the adapted q/k/v and o projections of a decoder layer
-(include/lora_attention.h): rotary positions (rope), an 8-bit paged key/value
-cache (KvCache.append, KvCache.gather) and attention over it
+(include/lora_attention.h): rotary positions (rope), with norms of queries and
+keys in the same pass (norm_rope, norm_rope_backward), a paged key/value cache of
+8 or 4 bits (KvCache.append, KvCache.gather) and attention over it
 (KvCache.attention).
 """
 
@@ -27,5 +28,5 @@ from .api import (  # noqa: F401
     status_string,
     arm_test_wait_timeout,
 )
-from .attention import KvCache, kv_pages_bytes, norm_rope, norm_rope_backward, rope, rope_tables  # noqa: F401
+from .attention import KvCache, kv_pages_bytes, kv_scales_bytes, norm_rope, norm_rope_backward, rope, rope_tables  # noqa: F401
 from .build import build  # noqa: F401

@@ -132,6 +132,7 @@ SIGNATURES = [
 
 KV_INT8 = 0
 KV_E4M3 = 1
+KV_UINT4 = 4
 KV_GROW_LEAST = 0
 KV_GROW_DOUBLING = 1
 ROPE_MAX_PAIRS = 256
@@ -243,6 +244,8 @@ ATTENTION_SIGNATURES = [
     ("lora_norm_rope_backward_workspace_bytes", ctypes.c_size_t, [ctypes.c_void_p]),
     ("lora_norm_rope_backward", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     ("lora_kv_pages_bytes", ctypes.c_size_t, [ctypes.c_int32] * 4),
+    ("lora_kv_codes_bytes", ctypes.c_size_t, [ctypes.c_int] + [ctypes.c_int32] * 4),
+    ("lora_kv_scales_bytes", ctypes.c_size_t, [ctypes.c_int] + [ctypes.c_int32] * 4),
     ("lora_kv_append", ctypes.c_int, _ROWS_ARGS),
     ("lora_kv_gather", ctypes.c_int, _ROWS_ARGS),
     ("lora_kv_attention_workspace_bytes", ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),

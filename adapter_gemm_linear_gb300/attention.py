@@ -1,5 +1,6 @@
-"""PyTorch-facing binding of include/lora_attention.h: rotary positions, the
-8-bit paged key/value cache and attention over it.
+"""PyTorch-facing binding of include/lora_attention.h: rotary positions, with
+norms of queries and keys or without, the paged key/value cache of 8 or 4 bits,
+and attention over it.
 
 As in api.py, the functions only marshal arguments: torch allocates device
 memory and provides the stream, the C library does the work, and an argument
@@ -27,7 +28,8 @@ from ._lib import LORA_BLOCK_ROWS
 from .api import LoraError, lora_dtype
 
 _GROWTHS = {"least": _lib.KV_GROW_LEAST, "doubling": _lib.KV_GROW_DOUBLING}
-_FORMATS = {"int8": (_lib.KV_INT8, torch.int8), "e4m3": (_lib.KV_E4M3, torch.float8_e4m3fn)}
+_FORMATS = {"int8": (_lib.KV_INT8, torch.int8), "e4m3": (_lib.KV_E4M3, torch.float8_e4m3fn),
+            "uint4": (_lib.KV_UINT4, torch.uint8)}
 
 # A decode step makes these calls once per layer with a few microseconds of
 # work each, so the argument structures of include/lora_attention.h are packed
@@ -238,17 +240,29 @@ def norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Te
     return q_out, k_out, weights[0], weights[1]
 
 
-def kv_pages_bytes(num_pages: int, num_heads: int, head_dim: int, page_tokens: int) -> int:
-    """lora_kv_pages_bytes: device bytes of a cache's K codes (as many again for V)."""
-    return int(_lib.lib().lora_kv_pages_bytes(num_pages, num_heads, head_dim, page_tokens))
+def kv_pages_bytes(num_pages: int, num_heads: int, head_dim: int, page_tokens: int, fmt: str = "int8") -> int:
+    """lora_kv_codes_bytes: device bytes of a cache's K codes (as many again for V)."""
+    return int(_lib.lib().lora_kv_codes_bytes(_format(fmt)[0], num_pages, num_heads, head_dim, page_tokens))
+
+
+def kv_scales_bytes(num_pages: int, num_heads: int, head_dim: int, page_tokens: int, fmt: str = "int8") -> int:
+    """lora_kv_scales_bytes: device bytes of a cache's K scales (as many again for V)."""
+    return int(_lib.lib().lora_kv_scales_bytes(_format(fmt)[0], num_pages, num_heads, head_dim, page_tokens))
+
+
+def _format(fmt: str):
+    if fmt not in _FORMATS:
+        raise ValueError(f"unknown format {fmt!r}; use 'int8', 'e4m3' or 'uint4'")
+    return _FORMATS[fmt]
 
 
 class KvCache:
-    """One layer's 8-bit paged key/value cache (lora_kv_cache_t).
+    """One layer's paged key/value cache (lora_kv_cache_t).
 
-    ``fmt`` "int8" or "e4m3"; head_dim 64 or 128; pages of 16, 32, 64 or 128
-    tokens.  The codes (k_pages, v_pages) and the scales, one per page and
-    head, are torch tensors, allocated here unless given.  Which pages a
+    ``fmt`` "int8", "e4m3" or "uint4"; head_dim 64 or 128; pages of 16, 32, 64 or
+    128 tokens.  The codes (k_pages, v_pages) and the scales, one per page and
+    head, or for "uint4" a scale and a least value (float16) per token and 64
+    dimensions, are torch tensors, allocated here unless given.  Which pages a
     sequence owns is the caller's business (block tables); a page's older
     content does not matter once its first token is written anew.
 
@@ -256,7 +270,8 @@ class KvCache:
     fit.  "least" takes the least scale that holds it, the finest steps for
     prompts written at once, but each growth rounds the page's older codes again;
     "doubling" takes the least power of two of its first one, which keeps
-    pages that are filled token by token within one step.  (e4m3 rescales exactly.)
+    pages that are filled token by token within one step.  (e4m3 rescales exactly,
+    and uint4 has a scale for each token.)
     """
 
     def __init__(self, num_pages: int, num_heads: int, head_dim: int, page_tokens: int = LORA_BLOCK_ROWS,
@@ -265,9 +280,7 @@ class KvCache:
                  v_scales: Optional[torch.Tensor] = None, growth: str = "least"):
         if growth not in _GROWTHS:
             raise ValueError(f"unknown growth {growth!r}; use 'least' or 'doubling'")
-        if fmt not in _FORMATS:
-            raise ValueError(f"unknown format {fmt!r}; use 'int8' or 'e4m3'")
-        code, dtype = _FORMATS[fmt]
+        code, dtype = _format(fmt)
         self.fmt, self.growth = fmt, growth
         self.num_pages, self.num_heads = int(num_pages), int(num_heads)
         self.head_dim, self.page_tokens = int(head_dim), int(page_tokens)
@@ -287,11 +300,15 @@ class KvCache:
             return t
 
         D = self.head_dim
-        self.k_pages = tensor(k_pages, tiles + (D // 64, LORA_BLOCK_ROWS, 64), dtype, "k_pages")
+        k_tile, v_tile, scales, scale_dtype = (D // 64, LORA_BLOCK_ROWS, 64), (D // 4, 4, 4, 4), tiles[:2], torch.float32
+        if fmt == "uint4":
+            k_tile = v_tile = (D // 64, 32, 16)
+            scales, scale_dtype = tiles + (D // 64, LORA_BLOCK_ROWS, 2), torch.float16
+        self.k_pages = tensor(k_pages, tiles + k_tile, dtype, "k_pages")
         device = self.k_pages.device  # ("cuda" names none: the other buffers are of k_pages' own)
-        self.v_pages = tensor(v_pages, tiles + (D // 4, 4, 4, 4), dtype, "v_pages")
-        self.k_scales = tensor(k_scales, tiles[:2], torch.float32, "k_scales")
-        self.v_scales = tensor(v_scales, tiles[:2], torch.float32, "v_scales")
+        self.v_pages = tensor(v_pages, tiles + v_tile, dtype, "v_pages")
+        self.k_scales = tensor(k_scales, scales, scale_dtype, "k_scales")
+        self.v_scales = tensor(v_scales, scales, scale_dtype, "v_scales")
         self.device = self.k_pages.device
         self._device = self.k_pages.get_device()
         self._workspace = {}  # bytes of an attention call's workspace, by what they depend on

@@ -38,7 +38,7 @@ lora_status_t check_heads(const lora_heads_t *h, lora_dtype_t dtype, int32_t row
 
 lora_status_t check_cache(const lora_kv_cache_t *c) {
     if (!c) return LORA_ERR_INVALID_ARG;
-    if (c->format != LORA_KV_INT8 && c->format != LORA_KV_E4M3) return LORA_ERR_UNSUPPORTED;
+    if (c->format != LORA_KV_INT8 && c->format != LORA_KV_E4M3 && c->format != LORA_KV_UINT4) return LORA_ERR_UNSUPPORTED;
     if (c->num_pages <= 0 || c->num_heads <= 0) return LORA_ERR_INVALID_ARG;
     if (c->num_heads > kMaxKvHeads) return LORA_ERR_UNSUPPORTED;
     if (c->head_dim != 64 && c->head_dim != 128) return LORA_ERR_UNSUPPORTED;
@@ -64,8 +64,8 @@ lora_status_t check_batch(const lora_kv_cache_t *c, const lora_kv_batch_t *b, lo
     }
     v->k_pages = static_cast<uint8_t *>(c->k_pages);
     v->v_pages = static_cast<uint8_t *>(c->v_pages);
-    v->k_scales = c->k_scales;
-    v->v_scales = c->v_scales;
+    v->k_scales = static_cast<float *>(c->k_scales);
+    v->v_scales = static_cast<float *>(c->v_scales);
     v->seq_lens = b->seq_lens;
     v->offsets = b->offsets;
     v->table = b->block_table;
@@ -150,6 +150,7 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
     lora_status_t s = check_batch(c, b, &v->kv);
     if (s != LORA_OK) return s;
     if (!a) return LORA_ERR_INVALID_ARG;
+    if (c->format == LORA_KV_UINT4) return LORA_ERR_UNSUPPORTED;
     if (!valid_dtype(a->dtype)) return LORA_ERR_DTYPE;
     if (a->num_q_heads <= 0 || a->window < 0 || a->max_queries <= 0) return LORA_ERR_INVALID_ARG;
     if (!(a->scale > 0.0f) || !isfinite(a->scale)) return LORA_ERR_INVALID_ARG;
@@ -255,6 +256,17 @@ size_t lora_kv_pages_bytes(int32_t num_pages, int32_t num_heads, int32_t head_di
     return static_cast<size_t>(num_pages) * num_heads * head_dim * page_tokens;
 }
 
+size_t lora_kv_codes_bytes(lora_kv_format_t format, int32_t num_pages, int32_t num_heads, int32_t head_dim, int32_t page_tokens) {
+    const size_t n = lora_kv_pages_bytes(num_pages, num_heads, head_dim, page_tokens);
+    return format == LORA_KV_UINT4 ? n / 2 : format == LORA_KV_INT8 || format == LORA_KV_E4M3 ? n : 0;
+}
+
+size_t lora_kv_scales_bytes(lora_kv_format_t format, int32_t num_pages, int32_t num_heads, int32_t head_dim, int32_t page_tokens) {
+    const size_t n = lora_kv_codes_bytes(format, num_pages, num_heads, head_dim, page_tokens);
+    if (n == 0) return 0;
+    return format == LORA_KV_UINT4 ? n / 8 : static_cast<size_t>(num_pages) * num_heads * sizeof(float);
+}
+
 static lora_status_t rows_call(bool append, const lora_kv_cache_t *cache, const lora_kv_batch_t *batch,
                                lora_dtype_t dtype, const lora_heads_t *k, const lora_heads_t *v, void *stream) {
     lora::KvView view;
@@ -267,7 +279,9 @@ static lora_status_t rows_call(bool append, const lora_kv_cache_t *cache, const 
     if (s != LORA_OK) return s;
     if (batch->rows == 0 || batch->num_seqs == 0) return LORA_OK;
     cudaError_t e = lora::device_status_ptr(&view.status);
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && cache->format == LORA_KV_UINT4)
+        e = (append ? lora::launch_kv_append4 : lora::launch_kv_gather4)(view, cache->head_dim, dtype, kh, vh, as_stream(stream));
+    else if (e == cudaSuccess)
         e = (append ? lora::launch_kv_append : lora::launch_kv_gather)(view, cache->format, cache->head_dim, dtype, kh,
                                                                        vh, as_stream(stream));
     return e == cudaSuccess ? LORA_OK : fail(e);

@@ -15,7 +15,7 @@ constexpr int kMaxGroup = 64;             // query heads that share a key/value 
 // Kernel view of a cache and of the call's rows.
 struct KvView {
     uint8_t *k_pages, *v_pages;
-    float *k_scales, *v_scales;
+    float *k_scales, *v_scales;  // (LORA_KV_UINT4: f16 pairs, see attn_uint4.cuh)
     const int32_t *seq_lens, *offsets, *table;
     int32_t num_pages, heads, page_tokens, page_shift;  // page_tokens = 1 << page_shift
     int32_t num_seqs, rows, max_pages;
@@ -71,6 +71,11 @@ cudaError_t launch_kv_append(const KvView &v, lora_kv_format_t fmt, int head_dim
                              const HeadsView &k, const HeadsView &val, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,
                              const HeadsView &k, const HeadsView &val, cudaStream_t stream);
+// The same for LORA_KV_UINT4 (attn_cache4.cu).
+cudaError_t launch_kv_append4(const KvView &v, int head_dim, lora_dtype_t dtype, const HeadsView &k, const HeadsView &val,
+                              cudaStream_t stream);
+cudaError_t launch_kv_gather4(const KvView &v, int head_dim, lora_dtype_t dtype, const HeadsView &k, const HeadsView &val,
+                              cudaStream_t stream);
 // Few query rows a sequence, and every fp32 call (attn_decode.cu).
 size_t decode_workspace_bytes(int head_dim);
 cudaError_t launch_attn_decode(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,

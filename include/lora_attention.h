@@ -1,7 +1,8 @@
 /*
  * lora_attention.h — C ABI of what stands between the adapted q/k/v
- * projections (lora.h) and the adapted o projection: rotary positions, an
- * 8-bit paged key/value cache, and attention over it.
+ * projections (lora.h) and the adapted o projection: rotary positions, with
+ * norms of queries and keys or without, a paged key/value cache of 8 or 4 bits,
+ * and attention over it.
  *
  * The conventions of lora.h hold for every entry point: plain C, the caller
  * owns all device memory, work is ordered on `stream`, device pointers are
@@ -126,12 +127,13 @@ size_t lora_norm_rope_backward_workspace_bytes(const lora_norm_rope_args_t *args
 lora_status_t lora_norm_rope_backward(const lora_norm_rope_args_t *args, const lora_norm_rope_grads_t *grads, void *stream);
 
 /* ---------------------------------------------------------------------- */
-/* The 8-bit paged key/value cache                                         */
+/* The paged key/value cache, of 8 or 4 bits                                */
 /* ---------------------------------------------------------------------- */
 
 typedef enum lora_kv_format {
     LORA_KV_INT8 = 0, /* int8 in [-127, 127], scale = largest magnitude / 127 */
-    LORA_KV_E4M3 = 1  /* 8-bit floating point (4 exponent, 3 mantissa bits), power-of-two scale */
+    LORA_KV_E4M3 = 1, /* 8-bit floating point (4 exponent, 3 mantissa bits), power-of-two scale */
+    LORA_KV_UINT4 = 4 /* 4 bits, 0 to 15, with an f16 scale and least value for each 64 dimensions of a token */
 } lora_kv_format_t;
 
 /* How an int8 page's scale grows when a later token does not fit (e4m3 scales are powers of two either way). */
@@ -152,6 +154,19 @@ typedef enum lora_kv_growth {
  * so that one 16-byte load of a K tile is a piece of a token's row, one of a
  * V tile four tokens of four dimensions: what a thread of the attention
  * kernels' matrix instructions takes of each, without a transposition.
+ *
+ * LORA_KV_UINT4: a value is code * scale + least, with an f16 scale and least
+ * value for each 64 dimensions of a token and head (0.5625 bytes a value):
+ *
+ *   k_pages, v_pages    uint8 [num_pages][num_heads][page_tokens/16][head_dim/64][32 pieces][16]
+ *   k_scales, v_scales  f16 [num_pages][num_heads][page_tokens/16][head_dim/64][16 tokens][scale, least]
+ *
+ * K: piece 4g + q holds dimensions 16q .. 16q + 15 of token t = 4(g/2) + g%2 of the
+ * tile (its first 8 bytes) and of token t + 2; each four bytes eight dimensions: 0 and 2,
+ * 4 and 6, 1 and 3, 5 and 7, the first in the low half of the byte.  V: piece 4g + q holds
+ * tokens 4q .. 4q + 3; its j-th four bytes dimension d = 4g + 32(j/2) + 2(j%2) in the low
+ * halves and d + 1 in the high ones, of tokens 4q, 4q + 2, 4q + 1, 4q + 3.  Scales are
+ * finite; those of tokens that are not written yet may be anything.
  */
 typedef struct lora_kv_cache {
     lora_kv_format_t format;
@@ -159,13 +174,17 @@ typedef struct lora_kv_cache {
     int32_t num_heads;    /* key/value heads, >= 1 */
     int32_t head_dim;     /* 64 or 128 */
     int32_t page_tokens;  /* 16, 32, 64 or 128 */
-    int32_t growth;       /* a lora_kv_growth_t */
-    void *k_pages, *v_pages;    /* device; num_pages*num_heads*page_tokens*head_dim bytes each */
-    float *k_scales, *v_scales; /* device [num_pages][num_heads] */
+    int32_t growth;       /* a lora_kv_growth_t; LORA_KV_UINT4 has no use for it */
+    void *k_pages, *v_pages;    /* device; lora_kv_codes_bytes each */
+    void *k_scales, *v_scales;  /* device; float [num_pages][num_heads], or as above */
 } lora_kv_cache_t;
 
-/* Device bytes of k_pages (and of v_pages); 0 on bad input. */
+/* Device bytes of an 8-bit cache's k_pages (and of v_pages); 0 on bad input. */
 size_t lora_kv_pages_bytes(int32_t num_pages, int32_t num_heads, int32_t head_dim, int32_t page_tokens);
+
+/* Device bytes of k_pages and of k_scales (and as many for v) in any format; 0 on bad input. */
+size_t lora_kv_codes_bytes(lora_kv_format_t format, int32_t num_pages, int32_t num_heads, int32_t head_dim, int32_t page_tokens);
+size_t lora_kv_scales_bytes(lora_kv_format_t format, int32_t num_pages, int32_t num_heads, int32_t head_dim, int32_t page_tokens);
 
 /*
  * Which rows of a call belong to which sequence: rows offsets[s] up to
@@ -216,6 +235,13 @@ typedef struct lora_kv_batch {
  * counts as the least a > 0 (s is 2^-120 at least), so that it has a code.  A
  * page with no value but zeros has scale 0.  Pages are not shared: no two
  * sequences of a call may write the same page.
+ *   uint4: for each 64 dimensions of a token and head, with NaN counted as 0,
+ *          finite values cut to [-2^15, 2^15], and lo, hi the least and the largest
+ *          finite one (0, 0 if there is none):
+ *          least = lo and scale = (hi - lo) / 15, each rounded to f16 (nearest even);
+ *          code = (x - least) / scale rounded to nearest even, within [0, 15]; infinities
+ *          take the end codes; with scale 0 every code is 0.
+ *          In fp32 but for the two roundings.  Older tokens are not touched.
  * k, v: the rows' [num_heads][head_dim] in `dtype`.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (head_dim, page_tokens
  * or format), CUDA.
@@ -224,7 +250,7 @@ lora_status_t lora_kv_append(const lora_kv_cache_t *cache, const lora_kv_batch_t
                              const lora_heads_t *k, const lora_heads_t *v, void *stream);
 
 /*
- * Read the rows' keys and values back: code * scale, rounded once to
+ * Read the rows' keys and values back: code * scale (+ least), rounded once to
  * `dtype`.  With n = seq_lens a sequence is read whole.  Rows of padding or
  * skipped sequences are not written.  Errors: as lora_kv_append.
  */
@@ -255,6 +281,12 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * up to a million keys.  Values that a query does not see have no part in this.
  * (Pages whose V scales differ by more than 2^79 within a sequence and head cost
  * time: twice as much for prompts, some ten times for few queries.)
+ * LORA_KV_UINT4: scale * code + least enters the products as its parts, exactly
+ * and in fp32, where the call takes the kernel for few queries (and in every fp32
+ * call); there each p_j times the token's scale is off by at most 2^-33 of the
+ * row's largest such product (bf16), 2^-44 (fp32), beyond its 11 or 22 bits.  Where
+ * it takes the one for many, values enter rounded to f16 (11 bits), and V's least
+ * step beyond p's 11 bits is 2^-29 of the row's largest p.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (num_q_heads /
  * num_heads over 64; num_q_heads not a multiple; rows * num_q_heads of 2^31
  * or more), WORKSPACE, CUDA.
