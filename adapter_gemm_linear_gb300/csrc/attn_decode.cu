@@ -53,21 +53,14 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include "attn_device.cuh"
+#include "attn_few.cuh"
 #include "attn_internal.h"
-#include "attn_split.cuh"
-#include "sm100_ptx.cuh"
 
 namespace lora {
 
 namespace {
 
 using namespace sm100;
-
-constexpr int kChunkTiles = 8;                     // tiles of a unit of work (128 tokens)
-constexpr int kSlotRows = 16;                      // rows a partial result has place for
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLoScale = 2048.0f;                // 2^11: the lo parts of fp32 operands
 
 // Query rows of an item, with NT column tiles of eight; fp32 takes two for the parts of eight rows.
 template <typename T, int NT>
@@ -94,8 +87,6 @@ struct alignas(16) TileInfo {
 constexpr int64_t kNoTile = -1, kEndOfLine = -2;
 constexpr int64_t kZeroV = 1;  // added to `at` (a multiple of 1024): V is zero whatever its codes
 
-constexpr int kBatch = 32, kBatches = 8;  // tiles looked up at once, and ahead
-
 template <int D, int NT>
 struct DecodeSmem {
     static constexpr int kWarps = consumers<D, NT>();
@@ -111,95 +102,6 @@ struct DecodeSmem {
     long long base;  // first unit of the sequence the CTA begins in
     int32_t seq;
     int32_t dead;    // a wait ran out: nobody waits any more
-};
-
-__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// The lo parts of two values whose f16 roundings are `hi`, times 2^11.
-__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
-    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    return pack_f16((a - h.x) * kLoScale, (b - h.y) * kLoScale);
-}
-
-// An 8 x 8 matrix of f16 (a thread: row lane / 4, columns 2 (lane % 4) and the next) transposed.
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-
-// A sequence's work: `chunks` units for each of heads x row_tiles items, over tiles [t0, t1).
-struct SeqWork {
-    SeqRows r;
-    int32_t t0, t1, chunks, row_tiles;
-    long long units;
-};
-
-template <int ROWS>
-__device__ __forceinline__ SeqWork seq_work(const AttnView &a, int32_t s) {
-    SeqWork w;
-    w.r = read_seq(a.kv, s, false);
-    if (w.r.n > a.max_queries) w.r.n = 0;
-    w.t0 = w.t1 = w.chunks = w.row_tiles = 0;
-    if (w.r.n > 0) {
-        const int32_t first = w.r.len - w.r.n;
-        const int32_t begin = a.window > 0 ? max(0, first - a.window + 1) : 0;
-        w.t0 = begin / kKvTile;
-        w.t1 = (w.r.len + kKvTile - 1) / kKvTile;
-        w.chunks = (w.t1 - w.t0 + kChunkTiles - 1) / kChunkTiles;
-        w.row_tiles = (w.r.n * a.group + ROWS - 1) / ROWS;
-    }
-    w.units = static_cast<long long>(w.chunks) * w.row_tiles * a.kv.heads;
-    return w;
-}
-
-// One CTA's walk over its units [w, end): item by item.
-template <int ROWS>
-struct Walk {
-    const AttnView &a;
-    long long w, end, base;
-    int32_t s;
-    SeqWork work;
-    // the current item
-    int32_t head, row_tile, tile0, tile1;  // tiles of this CTA
-    bool from_start, to_end;               // whether the item begins / ends in this CTA
-    long long item_end;                    // unit after the item's last
-
-    __device__ __forceinline__ Walk(const AttnView &v, long long w0, long long w1, int32_t seq, long long seq_base)
-        : a(v), w(w0), end(w1), base(seq_base), s(seq) {
-        if (w < end) work = seq_work<ROWS>(a, s);
-    }
-
-    __device__ __forceinline__ bool next() {
-        if (w >= end) return false;
-        while (w >= base + work.units) {
-            base += work.units;
-            work = seq_work<ROWS>(a, ++s);
-        }
-        const long long local = w - base;
-        const long long item = local / work.chunks;
-        const int32_t c = static_cast<int32_t>(local - item * work.chunks);
-        head = static_cast<int32_t>(item / work.row_tiles);
-        row_tile = static_cast<int32_t>(item - static_cast<long long>(head) * work.row_tiles);
-        const int32_t c1 = static_cast<int32_t>(min(static_cast<long long>(work.chunks), c + (end - w)));
-        tile0 = work.t0 + c * kChunkTiles;
-        tile1 = min(work.t1, work.t0 + c1 * kChunkTiles);
-        from_start = c == 0;
-        to_end = c1 == work.chunks;
-        item_end = base + (item + 1) * work.chunks;
-        w += c1 - c;
-        return true;
-    }
 };
 
 // The query rows [row_tile * tile_rows, ...) of (sequence, key/value head): row r is query r / group of the
@@ -221,51 +123,18 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     // run or have none of the work; it waits for this one's end before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- the plan: where this CTA's range of units begins
     if (threadIdx.x < kBatches) {
         mbar_init(&sm.full[threadIdx.x], a.test_wait_ns ? 2 : 1);
         mbar_init(&sm.empty[threadIdx.x], kWarps);
         fence_mbar_init();
     }
-    const int32_t per = (b.num_seqs + kThreads - 1) / kThreads;
-    const int32_t s0 = min(b.num_seqs, static_cast<int32_t>(threadIdx.x) * per), s1 = min(b.num_seqs, s0 + per);
-    long long mine = 0;
-    for (int32_t s = s0; s < s1; ++s) mine += seq_work<ROWS>(a, s).units;
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) sm.warp_sum[warp] = upto;
     if (threadIdx.x == 0) {
         sm.dead = 0;
         joins[blockIdx.x].last_cta = -1;
     }
-    __syncthreads();
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) upto += sm.warp_sum[w];
-        total += sm.warp_sum[w];
-    }
-    // as many CTAs as there are units at most, so that none between two of an item is without work
-    const long long ctas = min(total, static_cast<long long>(gridDim.x));
-    const long long w0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
-    const long long w1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
-    if (w0 < w1 && upto - mine <= w0 && w0 < upto) {
-        long long at = upto - mine;
-        int32_t s = s0;
-        for (;; ++s) {
-            const long long u = seq_work<ROWS>(a, s).units;
-            if (w0 < at + u) break;
-            at += u;
-        }
-        sm.seq = s;
-        sm.base = at;
-    }
-    __syncthreads();
-    Walk<ROWS> walk(a, w0, w1, sm.seq, sm.base);
+    const Range range = plan_line<ROWS, kThreads>(a, sm.warp_sum, &sm.seq, &sm.base);
+    const long long total = range.total, ctas = range.ctas;
+    Walk<ROWS> walk(a, range.w0, range.w1, sm.seq, sm.base);
     volatile int32_t *dead = &sm.dead;
     const uint64_t limit = a.test_wait_ns ? a.test_wait_ns : kWaitNs;
 

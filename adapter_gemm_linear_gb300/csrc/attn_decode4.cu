@@ -1,0 +1,623 @@
+// Attention over the 4-bit paged cache (LORA_KV_UINT4) for few queries a sequence,
+// and for every fp32 call.  The line of work, the persistent CTAs, the warps' ring of
+// asynchronous copies and the join are those of attn_decode.cu; what is different:
+//
+//  - With s and m a token's scale and least value in 64 dimensions, c its codes,
+//        q.k = sum over blocks of  s (q.c) + m sum(q),
+//        o   = sum_j (p_j s_j) c_j + sum_j p_j m_j,
+//    so the matrix instructions take codes, and scales and least values enter in
+//    fp32.  A word of codes becomes four operand registers by four ANDs and a
+//    shift (attn_uint4.cuh): f16 subnormals, whose 2^-24 and 2^-20 come out of the
+//    score's factor, of q (second pairs of a word by 1/16) and of the results.
+//  - p' = p s enters as f16 times a factor fr of the row, a power of two that is
+//    lowered (with the row's sums) when a p' would leave f16's range, and first set
+//    so that the row's largest p' is in [2^8, 2^9); p itself is relative to a maximum
+//    that is raised when a score passes it by kSlack.  Both are looked at lane by
+//    lane; only a raise takes shuffles.
+//  - A warp takes TS tiles a step, of one column tile of rows two: a step's
+//    fixed instructions (waits, looks, the checks) are shared by 32 tokens.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "attn_few.cuh"
+#include "attn_internal.h"
+#include "attn_uint4.cuh"
+
+namespace lora {
+
+namespace {
+
+using namespace sm100;
+
+template <typename T, int NT>
+__host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? 4 * NT : 8 * NT; }
+
+template <int D, int NT>
+__host__ __device__ constexpr int consumers() { return D == 128 && NT == 2 ? 5 : 4; }
+template <int D, int NT>
+__host__ __device__ constexpr int ctas_per_sm() { return D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3); }
+
+constexpr int64_t kNoTile = -1, kEndOfLine = -2;  // zeros; nothing any more
+constexpr float kSlack = 8.0f;                    // log2 by which a score may pass the row's maximum so far
+constexpr int kTopExponent = 8;                   // a row's largest p' begins in [2^8, 2^9)
+constexpr float kMostFactor = 1.152921504606847e18f;  // 2^60: fr of rows without a scale so far
+
+template <int D, int NT>
+struct Decode4Smem {
+    static constexpr int kWarps = consumers<D, NT>();
+    static constexpr int H = D / kBlockDims;
+    static constexpr int TS = NT == 1 ? 2 : 1;                      // tiles of a step
+    static constexpr int kDepth = NT == 1 ? (D == 128 ? 3 : 4) : 5;  // steps a warp fetches ahead
+    static constexpr int kMeta = TS * 2 * H * 4;                    // 16-byte pieces of a step's scales
+    uint4 codes[kWarps][kDepth][2][TS * H][32];                     // [.., K or V, (tile, block), lane]
+    uint4 meta[kWarps][kDepth][kMeta];                              // [.., (tile, K or V, block, four tokens)]
+    float o[kWarps][8 * NT][D + 4];                                 // merge: padded against bank conflicts
+    float m[kWarps][8 * NT], l[kWarps][8 * NT];
+    int64_t info[kBatches][kBatch];                                 // tile_index, kNoTile or kEndOfLine
+    uint64_t full[kBatches], empty[kBatches];
+    long long warp_sum[kWarps + 1];
+    long long base;  // first unit of the sequence the CTA begins in
+    int32_t seq;
+    int32_t dead;    // a wait ran out: nobody waits any more
+};
+
+// The query rows [row_tile * tile_rows, ...) of (sequence, key/value head): row r is query r / group of the
+// sequence, query head head * group + r % group.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, NT>()) attn_decode4_kernel(const __grid_constant__ AttnView a) {
+    extern __shared__ __align__(128) unsigned char raw[];
+    using Smem = Decode4Smem<D, NT>;
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    constexpr bool SPLIT = sizeof(T) == 4;  // fp32: operands in two f16 parts
+    constexpr int ROWS = tile_rows<T, NT>();
+    constexpr int kWarps = Smem::kWarps, kThreads = (kWarps + 1) * 32;
+    constexpr int RT = SPLIT ? 1 : NT;  // column tiles of rows
+    constexpr int H = Smem::H, TS = Smem::TS, kDepth = Smem::kDepth;
+    constexpr int kSteps = kBatch / TS;  // of a batch of looked-up tiles
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const KvView &b = a.kv;
+    JoinEntry *joins = join_entries(a, gridDim.x, kSlotRows, D);
+
+    // the joining kernel may come in as soon as there is room beside CTAs that
+    // run or have none of the work; it waits for this one's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (threadIdx.x < kBatches) {
+        mbar_init(&sm.full[threadIdx.x], a.test_wait_ns ? 2 : 1);
+        mbar_init(&sm.empty[threadIdx.x], kWarps);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) {
+        sm.dead = 0;
+        joins[blockIdx.x].last_cta = -1;
+    }
+    const Range range = plan_line<ROWS, kThreads>(a, sm.warp_sum, &sm.seq, &sm.base);
+    Walk<ROWS> walk(a, range.w0, range.w1, sm.seq, sm.base);
+    volatile int32_t *dead = &sm.dead;
+    const uint64_t limit = a.test_wait_ns ? a.test_wait_ns : kWaitNs;
+
+    auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t site) {
+        if (*dead || mbar_wait_bounded(bar, parity, limit)) return;
+        record_error(b.status, kDevTimeout, site);
+        *dead = 1;
+    };
+
+    if (warp == kWarps) {
+        // ---- places of the CTA's tiles, 32 at a time, a lane each; an item's are rounded up to whole steps
+        const int tile_shift = b.page_shift - 4;  // tiles of a page, as a shift
+        int32_t next = 0, end = 0, last = 0;      // the item's tiles that are not given out: up to `last`, rounded up `end`
+        bool more = true;
+        // (past the last tile the consumers still look for as many as they fetch ahead)
+        for (int32_t n = 0, past = 0; past < kWarps * kDepth * TS; ++n) {
+            int32_t seq = -1, head = 0, t = 0;
+            for (int fill = 0; fill < kBatch;) {
+                if (next == end) {
+                    more = more && walk.next();
+                    if (!more) {
+                        past += kBatch - fill;
+                        break;
+                    }
+                    next = walk.tile0;
+                    last = walk.tile1;
+                    end = next + (last - next + TS - 1) / TS * TS;
+                }
+                const int take = min(kBatch - fill, end - next);
+                if (lane >= fill && lane < fill + take) {
+                    t = next + lane - fill;
+                    seq = t < last ? walk.s : -2;
+                    head = walk.head;
+                }
+                fill += take;
+                next += take;
+            }
+            int64_t at = seq == -1 ? kEndOfLine : kNoTile;
+            if (seq >= 0) {
+                const int32_t page = read_page(b, seq, t >> tile_shift);
+                if (page >= 0) at = tile_index(b, page, head, t & ((1 << tile_shift) - 1));
+            }
+            __syncwarp();
+            wait(&sm.empty[n % kBatches], ((n / kBatches) & 1u) ^ 1u, 45);
+            // (what the consumers may still read is left alone; they see `dead` when they look for more)
+            if (__any_sync(0xffffffffu, *dead)) break;
+            sm.info[n % kBatches][lane] = at;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[n % kBatches]);
+        }
+        return;
+    }
+
+    // ---- consumers
+    const int g = lane >> 2, tig = lane & 3;
+    const int tok = k_token(g);  // S^T: rows g and g + 8 are tokens tok and tok + 2 of a tile
+    auto fetched = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    auto fetch_k = [&](const int64_t (&at)[TS], uint32_t slot) {
+#pragma unroll
+        for (int i = 0; i < TS * H; ++i) {
+            const int64_t tile = at[i / H];
+            if (tile != kEndOfLine)
+                copy16(&sm.codes[warp][slot][0][i][lane], b.k_pages + (max(tile, int64_t{0}) * H + i % H) * kBlockBytes + lane * 16, tile >= 0);
+        }
+        if (lane < Smem::kMeta) {  // (scales too)
+            const int64_t tile = TS == 2 && lane >= 8 * H ? at[TS - 1] : at[0];
+            const float *from = lane / (4 * H) % 2 ? b.v_scales : b.k_scales;
+            if (tile != kEndOfLine)
+                copy16(&sm.meta[warp][slot][lane], from + (max(tile, int64_t{0}) * (H * kKvTile) + lane % (4 * H) * 4), tile >= 0);
+        }
+        fetched();
+    };
+    auto fetch_v = [&](const int64_t (&at)[TS], uint32_t slot) {
+#pragma unroll
+        for (int i = 0; i < TS * H; ++i) {
+            const int64_t tile = at[i / H];
+            if (tile != kEndOfLine)
+                copy16(&sm.codes[warp][slot][1][i][lane], b.v_pages + (max(tile, int64_t{0}) * H + i % H) * kBlockBytes + lane * 16, tile >= 0);
+        }
+        fetched();
+    };
+    // where the tiles of the line's step i are; waits for their batch if it is the warp's
+    // first of it, and gives the batch back after the last
+    auto look = [&](uint32_t i, int64_t (&at)[TS]) {
+        const uint32_t n = i / kSteps, k = i % kSteps;
+        if (k < kWarps) wait(&sm.full[n % kBatches], (n / kBatches) & 1u, 46);
+        const bool gone = *dead;
+#pragma unroll
+        for (int j = 0; j < TS; ++j) at[j] = gone ? kEndOfLine : sm.info[n % kBatches][k * TS + j];
+        if (k >= kSteps - kWarps) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[n % kBatches]);
+        }
+    };
+    auto landed = [] { asm volatile("cp.async.wait_group %0;" ::"n"(2 * kDepth - 1) : "memory"); };
+    for (uint32_t d = 0; d < kDepth; ++d) {
+        int64_t at[TS];
+        look(warp + d * kWarps, at);
+        fetch_k(at, d);
+        fetch_v(at, d);
+    }
+    uint32_t taken = 0;  // steps the warp has used
+    uint32_t i0 = 0;     // steps of the items before
+    bool merged = false;  // whether the merge buffer may still be read by others
+    while (walk.next()) {
+        const SeqRows &r = walk.work.r;
+        const int32_t rows = min(ROWS, r.n * a.group - walk.row_tile * ROWS);
+        const int32_t key_end = min(walk.tile1 * kKvTile, r.len);
+        // q as B fragments: column g of tile u is row 8 u + g, dimensions 64 h + 16 tig +
+        // 4 j + 0..3 in k-step (h, j), the last two by 1/16
+        uint32_t qf[NT][D / 16][2];
+        // of the rows 8 u + 2 tig + i that the thread's scores belong to: the score
+        // scale in log2 units times 2^24, the blocks' sums of q times 2^-24, and the keys seen
+        float cr[RT][2], qs[RT][2][H];
+        int32_t kmin[RT][2], kmax[RT][2];
+#pragma unroll
+        for (int u = 0; u < RT; ++u) {
+            const int32_t row = walk.row_tile * ROWS + min(8 * u + g, rows - 1);  // rows past the last repeat it
+            const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
+            const T *src = static_cast<const T *>(a.q.p) + static_cast<int64_t>(r.off + qi) * a.q.row + qh * a.q.head;
+            float x[D / 4];
+            float amax = 0.0f;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int e = 0; e < 16; e += VecTraits<T>::kElems)
+                    VecTraits<T>::load(src + 64 * h + 16 * tig + e, x + 16 * h + e);
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) amax = fmaxf(amax, fabsf(x[e]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // a power of two that brings the row's largest to [2^13, 2^14): f16 keeps
+            // every value down to 2^-24 of it; not finite: left as it is
+            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+            e = amax < INFINITY ? max(e, -126) : 0;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            const float up = fminf(a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * kCode0, 3e38f);
+            const int32_t pos = r.len - r.n + qi;
+            const int32_t hi = min(a.causal ? pos + 1 : r.len, key_end), lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            float sum[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                sum[h] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[h] += x[16 * h + i] * down;
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+                sum[h] *= 1.0f / kCode0;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // from the lanes of row 8 u + 2 tig + i
+                cr[u][i] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * i);
+                kmax[u][i] = __shfl_sync(0xffffffffu, hi, 8 * tig + 4 * i);
+                kmin[u][i] = __shfl_sync(0xffffffffu, lo, 8 * tig + 4 * i);
+#pragma unroll
+                for (int h = 0; h < H; ++h) qs[u][i][h] = __shfl_sync(0xffffffffu, sum[h], 8 * tig + 4 * i);
+            }
+            const float down2 = down * (kCode1 / kCode0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const float *v = x + 4 * k;
+                qf[u][k][0] = pack_f16(v[0] * down, v[1] * down);
+                qf[u][k][1] = pack_f16(v[2] * down2, v[3] * down2);
+                if (SPLIT) {
+                    qf[NT - 1][k][0] = pack_rest(v[0] * down, v[1] * down, qf[0][k][0]);
+                    qf[NT - 1][k][1] = pack_rest(v[2] * down2, v[3] * down2, qf[0][k][1]);
+                }
+            }
+        }
+        // keys that every row of the item sees: steps within need no mask
+        const int32_t pos0 = r.len - r.n + walk.row_tile * ROWS / a.group;
+        const int32_t pos1 = r.len - r.n + (walk.row_tile * ROWS + rows - 1) / a.group;
+        const int32_t all_hi = min(a.causal ? pos0 + 1 : r.len, key_end);
+        const int32_t all_lo = a.window > 0 ? max(0, pos1 - a.window + 1) : 0;
+
+        // o^T, in units of 2^-24 / fr (rows d = 4 (g + 8 (k / 2)) + 2 (k % 2)) and 2^-20 / fr
+        // (d + 1), columns 2 tig and the next; om: what the least values add, in 1 / fr
+        float o[NT][D / 16][4];
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) o[u][k][0] = o[u][k][1] = o[u][k][2] = o[u][k][3] = 0.0f;
+        float m[RT][2], l[RT][2], fr[RT][2], om[RT][2][H];
+#pragma unroll
+        for (int u = 0; u < RT; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[u][i] = -INFINITY;
+                l[u][i] = 0.0f;
+                fr[u][i] = kMostFactor;
+#pragma unroll
+                for (int h = 0; h < H; ++h) om[u][i][h] = 0.0f;
+            }
+        auto rescale = [&](int u, int i, float f) {  // the row's o and om
+#pragma unroll
+            for (int h = 0; h < H; ++h) om[u][i][h] *= f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                o[u][k][i] *= f;
+                o[u][k][i + 2] *= f;
+                if (SPLIT) {
+                    o[NT - 1][k][i] *= f;
+                    o[NT - 1][k][i + 2] *= f;
+                }
+            }
+        };
+
+        const int32_t steps = (walk.tile1 - walk.tile0 + TS - 1) / TS;
+        // this warp's steps: those whose running number is the warp's modulo kWarps
+        const int32_t j0 = (warp - static_cast<int32_t>(i0 % kWarps) + kWarps) % kWarps;
+        for (int32_t st = j0; st < steps; st += kWarps) {
+            const uint32_t slot = taken++ % kDepth;
+            const int32_t key0 = (walk.tile0 + st * TS) * kKvTile;
+            int64_t ahead[TS];
+            look(i0 + st + kDepth * kWarps, ahead);
+            landed();
+            __syncwarp();  // every lane's copies of scales
+            // scale and least value of tokens tok and tok + 2
+            uint32_t kmeta[TS][2][H], vmeta[TS][2][H];
+            const uint32_t *meta = reinterpret_cast<const uint32_t *>(sm.meta[warp][slot]);
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        kmeta[j][t][h] = meta[(j * 2 * H + h) * kKvTile + tok + 2 * t];
+                        vmeta[j][t][h] = meta[(j * 2 * H + H + h) * kKvTile + tok + 2 * t];
+                    }
+            float s[TS][H][NT][4];
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) s[j][h][u][0] = s[j][h][u][1] = s[j][h][u][2] = s[j][h][u][3] = 0.0f;
+                    const uint4 w = sm.codes[warp][slot][0][j * H + h][lane];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t x[4], y[4];
+                        nibble_pairs(k == 0 ? w.x : w.y, x);
+                        nibble_pairs(k == 0 ? w.z : w.w, y);
+                        const uint32_t f0[4] = {x[0], y[0], x[1], y[1]}, f1[4] = {x[2], y[2], x[3], y[3]};
+#pragma unroll
+                        for (int u = 0; u < NT; ++u) {
+                            mma_16816_f16(s[j][h][u], f0, qf[u][4 * h + 2 * k][0], qf[u][4 * h + 2 * k][1]);
+                            mma_16816_f16(s[j][h][u], f1, qf[u][4 * h + 2 * k + 1][0], qf[u][4 * h + 2 * k + 1][1]);
+                        }
+                    }
+                }
+            __syncwarp();  // the scales have been read
+            fetch_k(ahead, slot);
+            // scores in log2 units
+            float z[TS][RT][4];  // [2 * token half + row]
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int u = 0; u < RT; ++u) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            const float2 ks = f16_pair(kmeta[j][e >> 1][h]);
+                            const float dot = SPLIT ? fmaf(s[j][h][NT - 1][e], 1.0f / kLoScale, s[j][h][0][e]) : s[j][h][u][e];
+                            sum = fmaf(ks.x, dot, fmaf(ks.y, qs[u][e & 1][h], sum));
+                        }
+                        z[j][u][e] = sum * cr[u][e & 1];
+                    }
+                }
+            if (key0 < all_lo || key0 + TS * kKvTile > all_hi) {  // some row does not see some key
+#pragma unroll
+                for (int j = 0; j < TS; ++j) {
+#pragma unroll
+                    for (int u = 0; u < RT; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int32_t key = key0 + j * kKvTile + tok + (e & 2);
+                            if (key < kmin[u][e & 1] || key >= kmax[u][e & 1]) z[j][u][e] = -INFINITY;
+                        }
+                    // scales of V past the sequence's end are whatever was there, and 0 * NaN is not 0
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            if (key0 + j * kKvTile + tok + 2 * t >= key_end) vmeta[j][t][h] = 0;
+                }
+            }
+            bool grow = false;
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int u = 0; u < RT; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) grow = grow || z[j][u][e] > m[u][e & 1] + kSlack;  // (also from m = -inf)
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int u = 0; u < RT; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float mx = m[u][i];
+#pragma unroll
+                        for (int j = 0; j < TS; ++j) mx = fmaxf(mx, fmaxf(z[j][u][i], z[j][u][i + 2]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float f = m[u][i] == -INFINITY ? 0.0f : ex2(m[u][i] - mx);
+                        m[u][i] = mx;
+                        l[u][i] *= f;
+                        rescale(u, i, f);
+                    }
+            }
+            // probabilities, and l
+#pragma unroll
+            for (int u = 0; u < RT; ++u) {
+                const float m0 = m[u][0] == -INFINITY ? 0.0f : m[u][0], m1 = m[u][1] == -INFINITY ? 0.0f : m[u][1];
+#pragma unroll
+                for (int j = 0; j < TS; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        z[j][u][e] = ex2(z[j][u][e] - (e & 1 ? m1 : m0));
+                        l[u][e & 1] += z[j][u][e];
+                    }
+                }
+            }
+            // p' = p s fr, rows side by side: [.., token half]
+            uint32_t ph[TS][H][NT][2];
+            auto scaled = [&] {
+                uint32_t over = 0;  // the largest of the hi parts: infinite where fr is too large
+#pragma unroll
+                for (int j = 0; j < TS; ++j)
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const float vs = f16_pair(vmeta[j][t][h]).x;
+#pragma unroll
+                            for (int u = 0; u < RT; ++u) {
+                                const float x = z[j][u][2 * t] * fr[u][0] * vs, y = z[j][u][2 * t + 1] * fr[u][1] * vs;
+                                const uint32_t hi = pack_f16(x, y);
+                                ph[j][h][u][t] = hi;
+                                if (SPLIT) ph[j][h][NT - 1][t] = pack_rest(x, y, hi);
+                                const __half2 most = __hmax2(*reinterpret_cast<const __half2 *>(&over), *reinterpret_cast<const __half2 *>(&hi));
+                                over = *reinterpret_cast<const uint32_t *>(&most);
+                            }
+                        }
+                return ((over + 0x04000400u) & 0x80008000u) != 0;  // (7C00 in either half)
+            };
+            if (__any_sync(0xffffffffu, scaled())) {
+#pragma unroll
+                for (int u = 0; u < RT; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float most = 0.0f;  // of p s
+#pragma unroll
+                        for (int j = 0; j < TS; ++j)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                for (int h = 0; h < H; ++h) most = fmaxf(most, z[j][u][2 * t + i] * f16_pair(vmeta[j][t][h]).x);
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 4));
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+                        // 2^(8 - exponent of most), where that is less than what there is
+                        const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
+                        const float least = __uint_as_float(static_cast<uint32_t>(127 + min(max(kTopExponent - e, -60), 60)) << 23);
+                        const float f = fminf(least, fr[u][i]);
+                        if (f < fr[u][i]) rescale(u, i, f / fr[u][i]);
+                        fr[u][i] = f;
+                    }
+                scaled();
+            }
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int u = 0; u < RT; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            om[u][e & 1][h] = fmaf(z[j][u][e] * fr[u][e & 1], f16_pair(vmeta[j][e >> 1][h]).y, om[u][e & 1][h]);
+            landed();
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    uint32_t pf[NT][2];  // p'^T as B fragments
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        pf[u][0] = transpose_8x8(ph[j][h][u][0]);
+                        pf[u][1] = transpose_8x8(ph[j][h][u][1]);
+                    }
+                    const uint4 w = sm.codes[warp][slot][1][j * H + h][lane];
+                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t f[4];
+                        nibble_pairs(ws[k], f);
+#pragma unroll
+                        for (int u = 0; u < NT; ++u) mma_16816_f16(o[u][4 * h + k], f, pf[u][0], pf[u][1]);
+                    }
+                }
+            fetch_v(ahead, slot);
+        }
+        i0 += steps;
+
+        // ---- merge the warps
+        if (merged) asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // the buffer has been read
+        merged = true;
+#pragma unroll
+        for (int u = 0; u < RT; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                auto over_lanes = [](float x) {
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+                };
+                const float sum = over_lanes(l[u][i]), un = 1.0f / fr[u][i];
+                float least[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) least[h] = over_lanes(om[u][i][h]);
+                const int rt = 8 * u + 2 * tig + i;
+                if (rt >= rows) continue;
+                if (g == 0) {
+                    sm.m[warp][rt] = m[u][i];
+                    sm.l[warp][rt] = sum;
+                }
+#pragma unroll
+                for (int jj = 0; jj < D / 32; ++jj) {
+                    float4 v = make_float4(o[u][2 * jj][i], o[u][2 * jj][i + 2], o[u][2 * jj + 1][i], o[u][2 * jj + 1][i + 2]);
+                    if (SPLIT) {
+                        v.x = fmaf(o[NT - 1][2 * jj][i], 1.0f / kLoScale, v.x);
+                        v.y = fmaf(o[NT - 1][2 * jj][i + 2], 1.0f / kLoScale, v.y);
+                        v.z = fmaf(o[NT - 1][2 * jj + 1][i], 1.0f / kLoScale, v.z);
+                        v.w = fmaf(o[NT - 1][2 * jj + 1][i + 2], 1.0f / kLoScale, v.w);
+                    }
+                    const float add = least[jj / 2];
+                    *reinterpret_cast<float4 *>(&sm.o[warp][rt][32 * jj + 4 * g]) =
+                        make_float4(fmaf(v.x, kCode0, add) * un, fmaf(v.y, kCode1, add) * un, fmaf(v.z, kCode0, add) * un,
+                                    fmaf(v.w, kCode1, add) * un);
+                }
+            }
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        const bool whole = walk.from_start && walk.to_end;
+        // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
+        float *part = partial_at(a, blockIdx.x, walk.from_start ? 1 : 0, kSlotRows, D);
+        if (!whole && walk.from_start && threadIdx.x == 0) {
+            const long long lastu = walk.item_end - 1;
+            joins[blockIdx.x] = JoinEntry{static_cast<int32_t>(((lastu + 1) * range.ctas - 1) / range.total), walk.head, r.off,
+                                          walk.row_tile * ROWS, rows, {}};
+        }
+        constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
+        const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
+        if (rt < rows) {
+            float M = -INFINITY, L = 0.0f, f[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][rt]);
+            const float mu = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                f[w] = ex2(sm.m[w][rt] - mu);
+                L = fmaf(sm.l[w][rt], f[w], L);
+            }
+            // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
+            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f;
+            const int32_t row = walk.row_tile * ROWS + rt;
+            const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
+            T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head;
+#pragma unroll
+            for (int c = c0 * 4; c < D; c += PER_ROW * 4) {
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][rt][c]);
+                    v.x = fmaf(x.x, f[w], v.x);
+                    v.y = fmaf(x.y, f[w], v.y);
+                    v.z = fmaf(x.z, f[w], v.z);
+                    v.w = fmaf(x.w, f[w], v.w);
+                }
+                if (whole) store4(dst + c, v, inv);
+                else store4(part + rt * D + c, v, inv);
+            }
+            if (c0 == 0) {
+                const float lse = M + log2f(L);
+                if (!whole) {
+                    part[kSlotRows * D + rt] = lse;
+                } else if (a.lse) {
+                    a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = lse * kLn2;
+                }
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int D, int NT>
+cudaError_t decode4_tiles(const AttnView &v, cudaStream_t stream) {
+    static uint64_t ctx[128] = {};
+    constexpr int smem = static_cast<int>(sizeof(Decode4Smem<D, NT>));
+    static_assert((smem + 1024) * ctas_per_sm<D, NT>() <= 228 * 1024, "the shared memory of an SM");
+    cudaError_t e = allow_smem(attn_decode4_kernel<T, D, NT>, smem, ctx);
+    if (e != cudaSuccess) return e;
+    const int grid = device_sm_count() * ctas_per_sm<D, NT>();
+    attn_decode4_kernel<T, D, NT><<<grid, (consumers<D, NT>() + 1) * 32, smem, stream>>>(v);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_join<T, D, tile_rows<T, NT>(), 4>(v, grid, kSlotRows, stream);
+    count_launches(2);
+    return e;
+}
+
+template <typename T, int D>
+cudaError_t decode4_typed(const AttnView &v, cudaStream_t stream) {
+    if constexpr (sizeof(T) == 4) return decode4_tiles<T, D, 2>(v, stream);
+    // one column tile of eight rows where that is all that any sequence has
+    else if (static_cast<int64_t>(v.max_queries) * v.group <= 8) return decode4_tiles<T, D, 1>(v, stream);
+    else return decode4_tiles<T, D, 2>(v, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode4(const AttnView &v, int head_dim, lora_dtype_t dtype, cudaStream_t stream) {
+    if (dtype == LORA_FP32) return head_dim == 64 ? decode4_typed<float, 64>(v, stream) : decode4_typed<float, 128>(v, stream);
+    return head_dim == 64 ? decode4_typed<__nv_bfloat16, 64>(v, stream) : decode4_typed<__nv_bfloat16, 128>(v, stream);
+}
+
+}  // namespace lora

@@ -81,6 +81,9 @@ size_t decode_workspace_bytes(int head_dim);
 cudaError_t launch_attn_decode(const AttnView &v, lora_kv_format_t fmt, int head_dim, lora_dtype_t dtype,
                                cudaStream_t stream);
 
+// The same over LORA_KV_UINT4 (attn_decode4.cu), with the same workspace.
+cudaError_t launch_attn_decode4(const AttnView &v, int head_dim, lora_dtype_t dtype, cudaStream_t stream);
+
 // Many query rows a sequence, bf16 (attn_prefill.cu).
 size_t prefill_workspace_bytes(int head_dim);
 cudaError_t launch_attn_prefill(const AttnView &v, lora_kv_format_t fmt, int head_dim, cudaStream_t stream);

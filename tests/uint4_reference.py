@@ -108,3 +108,52 @@ def random_cache(rng, cache, spread=0.3, size=1.0):
         s = np.stack((0.3 * z, z * (-2.3 + 0.4 * rng.normal(size=z.shape))), -1)
         s[..., 0][rng.random(z.shape) < 0.02] = 0
         t.copy_(torch.from_numpy(s.astype(np.float16)))
+
+
+def attention(ref: Paged4, q, table, lens, offs, scale, causal=True, window=0, rounded=False):
+    """q: float64 [rows, Hq, D] -> (out, lse, spread, score, vmax): the exact result, and per row and head what error
+    bounds need: the largest over dimensions of sum p |v|, the largest of scale * sum |q k|, and the largest |v| that
+    it sees.  In them |v| stands for |scale code| + |least|, the parts that the products take.  `rounded`: K's and V's
+    values rounded to f16 first, and |v| theirs."""
+    T, Hq, D = q.shape
+    G = Hq // ref.H
+    vals, mags = {}, {}
+    for name in ("k", "v"):
+        s = getattr(ref, name + "s").astype(np.float64).repeat(64, 3)
+        with np.errstate(invalid="ignore"):
+            parts = getattr(ref, name) * s[..., 0], s[..., 1]
+            vals[name] = parts[0] + parts[1]
+            mags[name] = np.abs(parts[0]) + np.abs(parts[1])
+            if rounded:
+                vals[name] = vals[name].astype(np.float16).astype(np.float64)
+                mags[name] = np.abs(vals[name])
+    out, lse = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf)
+    spread, score, vmax = np.zeros((T, Hq)), np.zeros((T, Hq)), np.zeros((T, Hq))
+    for s in range(len(lens)):
+        n, L = offs[s + 1] - offs[s], lens[s]
+        if L == 0 or n == 0:
+            continue
+
+        def tokens(x):
+            j = np.arange(L)
+            return np.stack([x[table[s][i // ref.P], :, i % ref.P] if 0 <= table[s][i // ref.P] < x.shape[0] else
+                             np.zeros((ref.H, D)) for i in j])
+
+        k, v, km, vm = (tokens(x) for x in (vals["k"], vals["v"], mags["k"], mags["v"]))
+        pos, j = np.arange(L - n, L)[:, None], np.arange(L)[None, :]
+        ok = np.ones((n, L), bool) if not causal else j <= pos
+        if window:
+            ok = ok & (j > pos - window)
+        rows = slice(offs[s], offs[s + 1])
+        for h in range(Hq):
+            qs, hk = q[rows, h], h // G
+            z = np.where(ok, qs @ k[:, hk].T * scale, -np.inf)
+            m = z.max(1, keepdims=True)
+            p = np.exp(z - m)
+            l = p.sum(1, keepdims=True)
+            out[rows, h] = p @ v[:, hk] / l
+            lse[rows, h] = (m + np.log(l))[:, 0]
+            spread[rows, h] = (p @ vm[:, hk] / l).max(1)
+            score[rows, h] = np.where(ok, np.abs(qs) @ km[:, hk].T * scale, 0.0).max(1)
+            vmax[rows, h] = np.where(ok, vm[:, hk].max(1)[None], 0.0).max(1)
+    return out, lse, spread, score, vmax
