@@ -83,7 +83,7 @@ struct Scale {
 
     __device__ __forceinline__ Scale(float lo, float hi) {
         if (!(lo <= hi)) lo = hi = 0.0f;  // no finite value
-        stored = __halves2half2(__float2half_rn(__fdiv_rn(hi - lo, 15.0f)), __float2half_rn(lo));
+        stored = __halves2half2(__float2half_rn((hi - lo) * (1.0f / 15.0f)), __float2half_rn(lo));
         s = __low2float(stored);
         m = __high2float(stored);
         inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;

@@ -8,7 +8,11 @@
 //    so the matrix instructions take codes, and scales and least values enter in
 //    fp32.  A word of codes becomes four operand registers by four ANDs and a
 //    shift (attn_uint4.cuh): f16 subnormals, whose 2^-24 and 2^-20 come out of the
-//    score's factor, of q (second pairs of a word by 1/16) and of the results.
+//    score's factor, of q (second pairs of a word by 1/16) and of the results.  In fp32
+//    calls they are f16 values of code - 8 instead (one instruction more a pair): the
+//    matrix instructions' sums cut off what is below their last bit, which adds up
+//    where all codes are positive and most of the sum goes out again with the least
+//    values (5e-5 of the result, with code - 8 3e-7).
 //  - p' = p s enters as f16 times a factor fr of the row, a power of two that is
 //    lowered (with the row's sums) when a p' would leave f16's range, and first set
 //    so that the row's largest p' is in [2^8, 2^9); p itself is relative to a maximum
@@ -74,6 +78,18 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     constexpr int RT = SPLIT ? 1 : NT;  // column tiles of rows
     constexpr int H = Smem::H, TS = Smem::TS, kDepth = Smem::kDepth;
     constexpr int kSteps = kBatch / TS;  // of a batch of looked-up tiles
+    // what the products with codes are units of: first and second pairs of a word
+    constexpr float kUnit0 = SPLIT ? 1.0f : 1.0f / kCode0, kUnit1 = SPLIT ? 1.0f : 1.0f / kCode1;
+    auto pairs = [](uint32_t w, uint32_t (&f)[4]) {
+        if constexpr (SPLIT) nibbles_less<8>(w, f);
+        else nibble_pairs(w, f);
+    };
+    // a token's scale and least value (for code 8 in fp32 calls)
+    auto scale_of = [](uint32_t meta) {
+        float2 x = f16_pair(meta);
+        if constexpr (SPLIT) x.y = fmaf(8.0f, x.x, x.y);
+        return x;
+    };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView &b = a.kv;
     JoinEntry *joins = join_entries(a, gridDim.x, kSlotRows, D);
@@ -202,10 +218,10 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         const int32_t rows = min(ROWS, r.n * a.group - walk.row_tile * ROWS);
         const int32_t key_end = min(walk.tile1 * kKvTile, r.len);
         // q as B fragments: column g of tile u is row 8 u + g, dimensions 64 h + 16 tig +
-        // 4 j + 0..3 in k-step (h, j), the last two by 1/16
+        // 4 j + 0..3 in k-step (h, j), the last two by kUnit0 / kUnit1
         uint32_t qf[NT][D / 16][2];
         // of the rows 8 u + 2 tig + i that the thread's scores belong to: the score
-        // scale in log2 units times 2^24, the blocks' sums of q times 2^-24, and the keys seen
+        // scale in log2 units over kUnit0, the blocks' sums of q times kUnit0, and the keys seen
         float cr[RT][2], qs[RT][2][H];
         int32_t kmin[RT][2], kmax[RT][2];
 #pragma unroll
@@ -229,7 +245,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
             e = amax < INFINITY ? max(e, -126) : 0;
             const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            const float up = fminf(a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * kCode0, 3e38f);
+            const float up = fminf(a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (1.0f / kUnit0), 3e38f);
             const int32_t pos = r.len - r.n + qi;
             const int32_t hi = min(a.causal ? pos + 1 : r.len, key_end), lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
             float sum[H];
@@ -240,7 +256,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 for (int i = 0; i < 16; ++i) sum[h] += x[16 * h + i] * down;
                 sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
                 sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
-                sum[h] *= 1.0f / kCode0;
+                sum[h] *= kUnit0;
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // from the lanes of row 8 u + 2 tig + i
@@ -250,7 +266,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                 for (int h = 0; h < H; ++h) qs[u][i][h] = __shfl_sync(0xffffffffu, sum[h], 8 * tig + 4 * i);
             }
-            const float down2 = down * (kCode1 / kCode0);
+            const float down2 = down * (kUnit0 / kUnit1);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const float *v = x + 4 * k;
@@ -268,7 +284,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         const int32_t all_hi = min(a.causal ? pos0 + 1 : r.len, key_end);
         const int32_t all_lo = a.window > 0 ? max(0, pos1 - a.window + 1) : 0;
 
-        // o^T, in units of 2^-24 / fr (rows d = 4 (g + 8 (k / 2)) + 2 (k % 2)) and 2^-20 / fr
+        // o^T, in units of kUnit0 / fr (rows d = 4 (g + 8 (k / 2)) + 2 (k % 2)) and kUnit1 / fr
         // (d + 1), columns 2 tig and the next; om: what the least values add, in 1 / fr
         float o[NT][D / 16][4];
 #pragma unroll
@@ -333,8 +349,8 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t x[4], y[4];
-                        nibble_pairs(k == 0 ? w.x : w.y, x);
-                        nibble_pairs(k == 0 ? w.z : w.w, y);
+                        pairs(k == 0 ? w.x : w.y, x);
+                        pairs(k == 0 ? w.z : w.w, y);
                         const uint32_t f0[4] = {x[0], y[0], x[1], y[1]}, f1[4] = {x[2], y[2], x[3], y[3]};
 #pragma unroll
                         for (int u = 0; u < NT; ++u) {
@@ -356,7 +372,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                         float sum = 0.0f;
 #pragma unroll
                         for (int h = 0; h < H; ++h) {
-                            const float2 ks = f16_pair(kmeta[j][e >> 1][h]);
+                            const float2 ks = scale_of(kmeta[j][e >> 1][h]);
                             const float dot = SPLIT ? fmaf(s[j][h][NT - 1][e], 1.0f / kLoScale, s[j][h][0][e]) : s[j][h][u][e];
                             sum = fmaf(ks.x, dot, fmaf(ks.y, qs[u][e & 1][h], sum));
                         }
@@ -473,7 +489,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int h = 0; h < H; ++h)
-                            om[u][e & 1][h] = fmaf(z[j][u][e] * fr[u][e & 1], f16_pair(vmeta[j][e >> 1][h]).y, om[u][e & 1][h]);
+                            om[u][e & 1][h] = fmaf(z[j][u][e] * fr[u][e & 1], scale_of(vmeta[j][e >> 1][h]).y, om[u][e & 1][h]);
             landed();
 #pragma unroll
             for (int j = 0; j < TS; ++j)
@@ -490,7 +506,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t f[4];
-                        nibble_pairs(ws[k], f);
+                        pairs(ws[k], f);
 #pragma unroll
                         for (int u = 0; u < NT; ++u) mma_16816_f16(o[u][4 * h + k], f, pf[u][0], pf[u][1]);
                     }
@@ -532,8 +548,8 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     }
                     const float add = least[jj / 2];
                     *reinterpret_cast<float4 *>(&sm.o[warp][rt][32 * jj + 4 * g]) =
-                        make_float4(fmaf(v.x, kCode0, add) * un, fmaf(v.y, kCode1, add) * un, fmaf(v.z, kCode0, add) * un,
-                                    fmaf(v.w, kCode1, add) * un);
+                        make_float4(fmaf(v.x, 1.0f / kUnit0, add) * un, fmaf(v.y, 1.0f / kUnit1, add) * un,
+                                    fmaf(v.z, 1.0f / kUnit0, add) * un, fmaf(v.w, 1.0f / kUnit1, add) * un);
                 }
             }
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");

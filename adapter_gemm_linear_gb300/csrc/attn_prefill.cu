@@ -49,6 +49,7 @@
 #include "attn_internal.h"
 #include "attn_split.cuh"
 #include "attn_sums.h"
+#include "attn_uint4.cuh"
 #include "sm100_ptx.cuh"
 
 namespace lora {
@@ -85,7 +86,8 @@ struct KeyTile {
     // Of each piece K's scale, and V's relative to the reference vr (attn_split.cuh)
     // in log2, and what takes it out again; of a V that is zero the least.
     float4 scales[kSubs];
-    int64_t at[kSubs];    // offset in k_pages; < 0: past the end or not there, zeros
+    // (of the 4-bit cache 1, 0 and 1)
+    int64_t at[kSubs];    // offset in k_pages (of the 4-bit cache its tile_index); < 0: past the end or not there, zeros
     int64_t at_v[kSubs];  // and in v_pages
     int32_t key0, len;    // first key, the sequence's length; key0 < 0: no more tiles
     int32_t off, n, head, row_tile;  // of an item's first tile: its queries (n = 0 in its other tiles)
@@ -94,14 +96,29 @@ struct KeyTile {
 };
 static_assert(sizeof(KeyTile) % 16 == 0, "scales are read as 16-byte pieces");
 
+// The codes on their way: 16-byte pieces of the converting threads, of K and of V, each read by
+// the thread that fetched it.
+template <int D, int FMT>
+struct Codes {
+    uint4 codes[2][2 * D / 32][128];
+};
+// Of the 4-bit cache half as many, and in the other half: its scales, by the tile's parity
+// (of a warp's two 16-key pieces K's and V's, [64 dimensions][key](scale, least) in f16),
+// and sixteen more columns of K and of Q_A and Q_B (32 bytes a row, 32-byte swizzle).
 template <int D>
-struct PrefillSmem {
+struct Codes<D, LORA_KV_UINT4> {
+    static constexpr int H = D / kBlockDims;
+    uint4 codes[2][D / 32][128];
+    uint32_t meta[2][4][2 * 2 * H * kKvTile];  // [parity][warp]
+    alignas(1024) uint8_t kx[kKeys * 32];
+    uint8_t qx[2][kHalf * 32];
+};
+
+template <int D, int FMT>
+struct PrefillSmem : Codes<D, FMT> {
     alignas(1024) uint8_t q[2][kHalf * D * 2];
     uint8_t k[2][kKeys * D * 2];
     uint8_t v[2][kKeys * D * 2];
-    // codes on their way, of K and of V: 16-byte pieces of the converting
-    // threads, each read by the thread that fetched it
-    uint4 codes[2][2 * D / 32][128];
     alignas(16) KeyTile tiles[kTileRing];
     int8_t q_exponent[2][2 * kHalf];  // of an item's rows, by the item's parity: q is 2^this times what is in q
     Item items[kItemRing];
@@ -295,8 +312,8 @@ __device__ __forceinline__ long long seq_units(const AttnView &a, int32_t s) {
 //
 // Tensor Memory columns: S_A 0, S_B 128 (P over their first 64), O_A 256, O_B 384.
 
-template <int D>
-__device__ __forceinline__ void issue_scores(PrefillSmem<D> &sm, uint32_t X, uint32_t stage) {
+template <int D, int FMT>
+__device__ __forceinline__ void issue_scores(PrefillSmem<D, FMT> &sm, uint32_t X, uint32_t stage) {
     const uint64_t q = desc_kmajor_sw128(smem_u32(sm.q[0])) + X * (sizeof(sm.q[0]) >> 4);
     const uint64_t k = desc_kmajor_sw128(smem_u32(sm.k[0])) + stage * (sizeof(sm.k[0]) >> 4);
 #pragma unroll
@@ -306,9 +323,26 @@ __device__ __forceinline__ void issue_scores(PrefillSmem<D> &sm, uint32_t X, uin
     }
 }
 
-// Half h of the keys.
+// Of the 4-bit cache: K's value s code + m = (code - 8) s_a + (code - 8) s_b + (m + 8 s), s_a
+// the upper seven bits of s and s_b the rest, so that both products are f16 values
+// exactly: two tiles.  The last term is one column for all dimensions of a block,
+// against the sum of q over them, which has two f16 parts: m and 8 s twice each.
 template <int D>
-__device__ __forceinline__ void issue_values(PrefillSmem<D> &sm, uint32_t X, uint32_t stage, uint32_t h, bool accumulate) {
+__device__ __forceinline__ void issue_scores(PrefillSmem<D, LORA_KV_UINT4> &sm, uint32_t X) {
+    const uint64_t q = desc_kmajor_sw128(smem_u32(sm.q[0])) + X * (sizeof(sm.q[0]) >> 4);
+    const uint64_t k = desc_kmajor_sw128(smem_u32(sm.k[0]));
+    const uint64_t qx = desc_kmajor_sw32(smem_u32(sm.qx[0])) + X * (sizeof(sm.qx[0]) >> 4);
+    mma_bf16_f32(X * 128, qx, desc_kmajor_sw32(smem_u32(sm.kx)), idesc_f16_f32(kHalf, kKeys), 0);
+#pragma unroll
+    for (int i = 0; i < 2 * (D / 16); ++i) {
+        const uint32_t at = (i % (D / 16) / 4) * (kHalf * 128 >> 4) + (i % 4) * 2;
+        mma_bf16_f32(X * 128, q + at, k + at + i / (D / 16) * (sizeof(sm.k[0]) >> 4), idesc_f16_f32(kHalf, kKeys), 1);
+    }
+}
+
+// Half h of the keys.
+template <int D, int FMT>
+__device__ __forceinline__ void issue_values(PrefillSmem<D, FMT> &sm, uint32_t X, uint32_t stage, uint32_t h, bool accumulate) {
     const uint64_t v = desc_kmajor_sw128(smem_u32(sm.v[0])) + stage * (sizeof(sm.v[0]) >> 4) + h * (D * 128 >> 4);
 #pragma unroll
     for (int i = 0; i < kKeys / 32; ++i)
@@ -346,7 +380,9 @@ __device__ __noinline__ uint32_t nan_dims(const KvView &b, int32_t seq, int32_t 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __grid_constant__ AttnView a) {
     extern __shared__ __align__(1024) unsigned char raw[];
-    PrefillSmem<D> &sm = *reinterpret_cast<PrefillSmem<D> *>(raw);
+    PrefillSmem<D, FMT> &sm = *reinterpret_cast<PrefillSmem<D, FMT> *>(raw);
+    constexpr bool U4 = FMT == LORA_KV_UINT4;
+    constexpr int H = D / kBlockDims;
     constexpr uint32_t kRowAtom = kHalf * 128;    // bytes of one atom of 128 rows
     constexpr uint32_t kVAtom = D * 128;          // bytes of 64 keys of V
     // (the same for the warp, which the compiler cannot know of threadIdx.x / 32:
@@ -691,7 +727,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     } else if (warp < 12) {
         // ================================================ codes to f16 tiles
         const int wq = warp - 8;  // the warp's 32 keys of a tile
-        constexpr int NL = 2 * D / 32;  // 16-byte pieces a lane holds of K (or V)
+        constexpr int NL = U4 ? D / 32 : 2 * D / 32;  // 16-byte pieces a lane holds of K (or V)
         uint32_t n_tile = 0;
         const int cc = lane & 3, dpar = (lane >> 2) & 1, dq = lane >> 3;
         // of one tile: its first key, the length, and where the warp's two 16-key pieces are
@@ -718,11 +754,24 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         // the thread's piece i of a tile; zeros where there is no page
         auto fetch_k = [&](const Tile &x, int i) {
             const int64_t at = i < NL / 2 ? x.at[0] : x.at[1];
-            copy16(kc + 128 * i, b.k_pages + max(at, int64_t{0}) + 16 * (lane + 32 * (i % (NL / 2))), at >= 0);
+            if constexpr (U4) copy16(kc + 128 * i, b.k_pages + (max(at, int64_t{0}) * H + i % H) * kBlockBytes + lane * 16, at >= 0);
+            else copy16(kc + 128 * i, b.k_pages + max(at, int64_t{0}) + 16 * (lane + 32 * (i % (NL / 2))), at >= 0);
         };
         auto fetch_v = [&](const Tile &x, int i) {
-            copy16(vc + 128 * i, b.v_pages + max(x.at_v, int64_t{0}) + (dq * 2 + dpar) * 64 + (cc & 1) * 32 + (i >> 1) * 512 + (i & 1) * 16,
+            if constexpr (U4)  // tokens 8 cc .. 8 cc + 7 of the warp's, four a piece
+                copy16(vc + 128 * i, b.v_pages + (max(x.at_v, int64_t{0}) * H + (i >> 1)) * kBlockBytes + (lane >> 2) * 64 + (cc & 1) * 32 + (i & 1) * 16,
+                       x.at_v >= 0);
+            else copy16(vc + 128 * i, b.v_pages + max(x.at_v, int64_t{0}) + (dq * 2 + dpar) * 64 + (cc & 1) * 32 + (i >> 1) * 512 + (i & 1) * 16,
                    x.at_v >= 0);
+        };
+        // The 4-bit cache's scales of the warp's keys, of tile n (lanes read what others fetched).
+        auto fetch_scales = [&](const Tile &x, uint32_t n) {
+            if constexpr (U4) {
+                if (lane >= 16 * H) return;
+                const int64_t at = lane < 8 * H ? x.at[0] : x.at[1];
+                const float *from = lane / (4 * H) % 2 ? b.v_scales : b.k_scales;
+                copy16(&sm.meta[n & 1][wq][lane * 4], from + (max(at, int64_t{0}) * (H * kKvTile) + lane % (4 * H) * 4), at >= 0);
+            }
         };
         auto fetched = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
         // Where the thread's pieces go (all but constants).  K: piece i is of key
@@ -733,6 +782,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
         const uint32_t k_at = (wq * 32 + kr) * 128, k_c0 = ((2 * kp) ^ kr) << 4, k_c1 = ((2 * kp + 1) ^ kr) << 4;
         const uint32_t v_at = (wq >> 1) * kVAtom + (8 * dq + 4 * dpar) * 128, v_c = ((wq & 1) * 4 + cc) ^ (4 * dpar);
         auto landed = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };  // all groups but the newest
+        // Row r of the sixteen more columns: eight values, and zeros.
+        auto extra = [&](uint8_t *tile, int r, const uint32_t (&w)[4]) {
+            uint4 *const at = reinterpret_cast<uint4 *>(tile + r * 32);
+            at[r >> 2 & 1] = make_uint4(w[0], w[1], w[2], w[3]);
+            at[~r >> 2 & 1] = make_uint4(0u, 0u, 0u, 0u);
+        };
         // An item's Q_A and Q_B, the warp's 32 rows of each: copied to their
         // places as bf16, several rows at a time and 16 bytes a lane ...
         uint32_t n_q = 0, n_qb = 0;
@@ -763,7 +818,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             fetched();
         };
         // ... and turned in place into f16 times a power of two per row (its
-        // largest value in [2^13, 2^14)), a row a lane.
+        // largest value in [2^13, 2^14); with the 4-bit cache [2^7, 2^8), so that
+        // the sums of 64 are f16 values too), a row a lane.
         auto convert_q = [&](int X) {
             __syncwarp();  // every lane's copies
             float amax = 0.0f;
@@ -775,10 +831,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 for (int k = 0; k < 4; ++k)
                     amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
             }
-            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13;
+            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - (U4 ? 7 : 13);
             e = amax < INFINITY ? max(e, -126) : 0;
             const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
             sm.q_exponent[n_q & 1u][X * kHalf + wq * 32 + lane] = static_cast<int8_t>(e);
+            float sum = 0.0f;
+            uint32_t sums[4] = {0u, 0u, 0u, 0u};  // of 64 dimensions, in two parts, twice
 #pragma unroll 2
             for (int i = 0; i < D / 8; ++i) {
                 uint4 *at = q_place(X, lane, i);
@@ -786,16 +844,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                 uint32_t h[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    h[k] = pack_h2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+                for (int k = 0; k < 4; ++k) {
+                    const float x0 = __uint_as_float(w[k] << 16) * down, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * down;
+                    h[k] = pack_h2(x0, x1);
+                    sum += x0 + x1;
+                }
                 *at = make_uint4(h[0], h[1], h[2], h[3]);
+                if constexpr (U4) {
+                    if (i % 8 == 7) {
+                        const float hi = __half2float(__float2half_rn(sum));
+                        sums[2 * (i / 8)] = sums[2 * (i / 8) + 1] = pack_h2(hi, sum - hi);
+                        sum = 0.0f;
+                    }
+                }
             }
+            if constexpr (U4) extra(sm.qx[X], wq * 32 + lane, sums);
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_full[X]);
         };
         look(cur, 0);
         for (int i = 0; cur.key0 >= 0 && i < NL; ++i) fetch_k(cur, i);
+        if (cur.key0 >= 0) fetch_scales(cur, 0);
         fetched();
         for (int i = 0; cur.key0 >= 0 && i < NL; ++i) fetch_v(cur, i);
         fetched();
@@ -804,9 +874,46 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             look(nxt, n_tile + 1);
             const bool more = nxt.key0 >= 0;
             // K: row = key, 16 dimensions of one key a piece
-            wait(&sm.k_empty[stage], ph ^ 1u, 61);
+            wait(&sm.k_empty[U4 ? 0 : stage], (U4 ? stage : ph) ^ 1u, 61);
             landed();
             uint8_t *kdst = sm.k[stage] + k_at;
+            if constexpr (U4) {
+                __syncwarp();  // every lane's copies
+                if (more) fetch_scales(nxt, n_tile + 1);
+                const uint32_t *const sc = sm.meta[n_tile & 1][wq];
+                uint32_t w[4] = {0u, 0u, 0u, 0u};  // a key a lane: least values, and 8 scales
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const uint32_t y = sc[(lane / kKvTile * 2 * H + h) * kKvTile + lane % kKvTile];
+                    w[2 * h] = __byte_perm(y, y, 0x3232);
+                    w[2 * h + 1] = times(__byte_perm(y, y, 0x1010), 0x48004800u);
+                }
+                extra(sm.kx, wq * 32 + lane, w);
+                // a piece: 16 dimensions of keys `tok` and tok + 2 of 16
+                const int tok = k_token(kr);
+                uint8_t *const row = sm.k[0] + (wq * 32 + tok) * 128;
+                const int x7 = tok & 7;
+#pragma unroll 2
+                for (int i = 0; i < NL; ++i) {
+                    const uint4 r = kc[128 * i];
+                    if (more) fetch_k(nxt, i);
+                    const uint32_t c[4] = {r.x, r.y, r.z, r.w};
+                    uint8_t *const dst = row + (i / H) * (kKvTile * 128) + i % H * kRowAtom;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t y = sc[(i / H * 2 * H + i % H) * kKvTile + tok + 2 * t], s2 = __byte_perm(y, y, 0x1010);
+                        const uint32_t sa = s2 & 0xFFF0FFF0u, sb = less(s2, sa);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t f[4];
+                            nibbles_less<8>(c[2 * t + k], f);
+                            uint4 *const to = reinterpret_cast<uint4 *>(dst + t * 256 + (((2 * kp + k) ^ (x7 + 2 * t)) << 4));
+                            to[0] = make_uint4(times(f[0], sa), times(f[1], sa), times(f[2], sa), times(f[3], sa));
+                            to[sizeof(sm.k[0]) / 16] = make_uint4(times(f[0], sb), times(f[1], sb), times(f[2], sb), times(f[3], sb));
+                        }
+                    }
+                }
+            } else {
 #pragma unroll 2
             for (int i = 0; i < NL; ++i) {
                 const uint4 r = kc[128 * i];
@@ -820,10 +927,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 *reinterpret_cast<uint4 *>(dst + k_c0) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(dst + k_c1) = make_uint4(w[4], w[5], w[6], w[7]);
             }
+            }
             fetched();
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.k_full[stage]);
+            if (lane == 0) mbar_arrive(&sm.k_full[U4 ? 0 : stage]);
             const bool first = cur.n > 0;  // tile of an item: its queries, on their way while V is converted
             if (first) fetch_q(cur, 0);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
@@ -831,6 +939,48 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             wait(&sm.v_empty[stage], ph ^ 1u, 62);
             if (first) asm volatile("cp.async.wait_group 2;" ::: "memory");
             else landed();
+            if constexpr (U4) {
+                // keys past the end: scale and least value 0 (what is there may be NaN)
+                const int have = cur.len - (cur.key0 + wq * 32 + cc * 8);
+                const uint32_t *const sc = sm.meta[n_tile & 1][wq];
+#pragma unroll 1
+                for (int h = 0; h < H; ++h) {
+                    const uint4 *y = reinterpret_cast<const uint4 *>(sc + ((cc >> 1) * 2 * H + H + h) * kKvTile + (cc & 1) * 8);
+                    const uint4 ya = y[0], yb = y[1];
+                    uint32_t s2[4] = {__byte_perm(ya.x, ya.y, 0x5410), __byte_perm(ya.z, ya.w, 0x5410), __byte_perm(yb.x, yb.y, 0x5410),
+                                      __byte_perm(yb.z, yb.w, 0x5410)};
+                    uint32_t m2[4] = {__byte_perm(ya.x, ya.y, 0x7632), __byte_perm(ya.z, ya.w, 0x7632), __byte_perm(yb.x, yb.y, 0x7632),
+                                      __byte_perm(yb.z, yb.w, 0x7632)};
+                    if (__builtin_expect(have < 8, 0)) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t there = (2 * k < have ? 0xFFFFu : 0u) | (2 * k + 1 < have ? 0xFFFF0000u : 0u);
+                            s2[k] &= there;
+                            m2[k] &= there;
+                        }
+                    }
+                    const uint4 ra = vc[128 * (2 * h)], rb = vc[128 * (2 * h + 1)];
+                    if (more) {
+                        fetch_v(nxt, 2 * h);
+                        fetch_v(nxt, 2 * h + 1);
+                    }
+                    const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+                    uint8_t *const to = sm.v[stage] + (wq >> 1) * kVAtom + h * (kBlockDims * 128);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t fa[4], fb[4];
+                        nibbles_less<0>(wa[j], fa);
+                        nibbles_less<0>(wb[j], fb);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {  // dimensions d and d + 1: of keys 0, 1 and 2, 3
+                            const int d = 4 * kr + 32 * (j >> 1) + 2 * (j & 1) + k;
+                            *reinterpret_cast<uint4 *>(to + d * 128 + ((((wq & 1) * 4 + cc) ^ (d & 7)) << 4)) =
+                                make_uint4(times_and(fa[k], s2[0], m2[0]), times_and(fa[2 + k], s2[1], m2[1]), times_and(fb[k], s2[2], m2[2]),
+                                           times_and(fb[2 + k], s2[3], m2[3]));
+                        }
+                    }
+                }
+            } else {
             uint32_t keep[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -875,6 +1025,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     *reinterpret_cast<uint4 *>(vdst + e * 128 + ((v_c ^ e) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            }
             fetched();
             fence_proxy_async_shared();
             __syncwarp();
@@ -907,7 +1058,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             // (Tensor Memory begins at column 0: the CTA has all of it)
             auto scores = [&](uint32_t X, uint32_t stage) {
                 if (elect_one()) {
-                    issue_scores(sm, X, stage);
+                    if constexpr (U4) issue_scores(sm, X);
+                    else issue_scores(sm, X, stage);
                     mma_commit(&sm.s_full[X]);
                 }
                 __syncwarp();
@@ -920,7 +1072,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 __syncwarp();
                 if (elect_one()) mbar_arrive(&sm.item_empty[e]);
                 if (any_dead() || stop) break;
-                wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
+                wait(&sm.k_full[U4 ? 0u : n_tile & 1u], (U4 ? n_tile : n_tile >> 1) & 1u, 72);
 #pragma unroll 1
                 for (uint32_t X = 0; X < nx; ++X) {
                     wait(&sm.q_full[X], (X ? n_qb : n_item) & 1u, 71);
@@ -930,7 +1082,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 }
                 ++n_item;
                 n_qb += nx - 1;
-                commit(&sm.k_empty[n_tile & 1u]);
+                commit(&sm.k_empty[U4 ? 0u : n_tile & 1u]);
 #pragma unroll 1
                 for (int32_t j = 0; j < nt; ++j, ++n_tile) {
                     const uint32_t st = n_tile & 1u, ph = (n_tile >> 1) & 1u;
@@ -950,7 +1102,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             __syncwarp();
                         }
                         if (more) {
-                            if (X == 0) wait(&sm.k_full[st1], ph1, 76);
+                            if (X == 0) wait(&sm.k_full[U4 ? 0u : st1], U4 ? st1 : ph1, 76);
                             tc_fence_after_sync();
                             scores(X, st1);
                             if (j + 2 == nt) commit(&sm.q_empty[X]);
@@ -961,7 +1113,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     n_b += nx - 1;
                     commit(&sm.v_empty[st]);
                     commit(&sm.tile_empty[n_tile % kTileRing]);  // (the softmax has read its scales)
-                    if (more) commit(&sm.k_empty[st1]);
+                    if (more) commit(&sm.k_empty[U4 ? 0u : st1]);
                 }
             }
             // nothing of this thread's may be in flight when Tensor Memory is freed
@@ -1003,7 +1155,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     it.last_cta = static_cast<int32_t>(((w + (units - skip)) * ctas - 1) / total);
                     if (it.tile1 > it.tile0) {
                         // (items ahead of their use: its reads are hidden but for the first item's)
-                        it.vr = v_reference(b, it.seq, it.head, it.tile0 * kSubs, min(it.tile1 * kSubs, (it.len + kKvTile - 1) / kKvTile));
+                        it.vr = FMT == LORA_KV_UINT4
+                                    ? 1.0f  // (its values come whole)
+                                    : v_reference(b, it.seq, it.head, it.tile0 * kSubs, min(it.tile1 * kSubs, (it.len + kKvTile - 1) / kKvTile));
                         publish(it);
                     }
                     w += take;
@@ -1051,7 +1205,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     float ks = 0.0f, vs = 0.0f;
                     if (t < tile1 && key < len) {
                         const int32_t page = read_page(b, seq, key >> b.page_shift);
-                        if (page >= 0) {
+                        if (page >= 0 && FMT == LORA_KV_UINT4) {
+                            at = tile_index(b, page, head, (key & (b.page_tokens - 1)) / kKvTile);
+                        } else if (page >= 0) {
                             at = tile_offset<D>(b, page, head, (key & (b.page_tokens - 1)) / kKvTile);
                             ks = __ldg(b.k_scales + static_cast<int64_t>(page) * b.heads + head);
                             vs = __ldg(b.v_scales + static_cast<int64_t>(page) * b.heads + head);
@@ -1067,9 +1223,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                         wait(&sm.tile_empty[r], ((n_tile / kTileRing) & 1u) ^ 1u, 91);
                         if (any_dead()) break;
                         if ((lane >> 3) == q) {
-                            sm.tiles[r].scales[sub] = make_float4(ks, lv, iv, 0.0f);
+                            sm.tiles[r].scales[sub] = FMT == LORA_KV_UINT4 ? make_float4(1.0f, 0.0f, 1.0f, 0.0f) : make_float4(ks, lv, iv, 0.0f);
                             sm.tiles[r].at[sub] = at;
-                            sm.tiles[r].at_v[sub] = vs > 0.0f ? at : -1;
+                            sm.tiles[r].at_v[sub] = FMT == LORA_KV_UINT4 || vs > 0.0f ? at : -1;
                             if (sub == 0) {
                                 sm.tiles[r].key0 = tile1 < 0 ? -1 : t * kKeys;
                                 sm.tiles[r].len = len;
@@ -1104,7 +1260,7 @@ template <int D, int FMT>
 cudaError_t prefill_typed(const AttnView &v, cudaStream_t stream) {
     static uint64_t ctx[128] = {};
     // more than half of an SM's shared memory even for D = 64: a CTA takes all of its Tensor Memory
-    constexpr int smem = static_cast<int>(sizeof(PrefillSmem<D>) > 128 * 1024 ? sizeof(PrefillSmem<D>) : 128 * 1024);
+    constexpr int smem = static_cast<int>(sizeof(PrefillSmem<D, FMT>) > 128 * 1024 ? sizeof(PrefillSmem<D, FMT>) : 128 * 1024);
     static_assert(smem <= 227 * 1024, "the shared memory of one CTA");
     cudaError_t e = allow_smem(attn_prefill_kernel<D, FMT>, smem, ctx);
     if (e != cudaSuccess) return e;
@@ -1123,8 +1279,12 @@ size_t prefill_workspace_bytes(int head_dim) { return split_workspace_bytes(devi
 
 cudaError_t launch_attn_prefill(const AttnView &v, lora_kv_format_t fmt, int head_dim, cudaStream_t stream) {
     if (head_dim == 64)
-        return fmt == LORA_KV_INT8 ? prefill_typed<64, LORA_KV_INT8>(v, stream) : prefill_typed<64, LORA_KV_E4M3>(v, stream);
-    return fmt == LORA_KV_INT8 ? prefill_typed<128, LORA_KV_INT8>(v, stream) : prefill_typed<128, LORA_KV_E4M3>(v, stream);
+        return fmt == LORA_KV_INT8   ? prefill_typed<64, LORA_KV_INT8>(v, stream)
+               : fmt == LORA_KV_E4M3 ? prefill_typed<64, LORA_KV_E4M3>(v, stream)
+                                     : prefill_typed<64, LORA_KV_UINT4>(v, stream);
+    return fmt == LORA_KV_INT8   ? prefill_typed<128, LORA_KV_INT8>(v, stream)
+           : fmt == LORA_KV_E4M3 ? prefill_typed<128, LORA_KV_E4M3>(v, stream)
+                                 : prefill_typed<128, LORA_KV_UINT4>(v, stream);
 }
 
 }  // namespace lora

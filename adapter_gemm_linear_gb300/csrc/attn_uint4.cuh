@@ -41,6 +41,35 @@ __device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t (&f)[4]) {
     f[3] = h & kNibbles1;
 }
 
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {  // pairs of f16
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t times_and(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                              *reinterpret_cast<const __half2 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The eight codes of a word of the 4-bit cache, less LESS, as f16 pairs in the order of
+// nibble_pairs: a nibble in the low bits of 1024's f16 is 1024 + code, four bits up 1024 + 16 code.
+template <int LESS>
+__device__ __forceinline__ void nibbles_less(uint32_t w, uint32_t (&f)[4]) {
+    constexpr uint32_t k1024 = LESS ? 0x64086408u : 0x64006400u, k64 = LESS ? 0xD480D480u : 0xD400D400u;  // 1024, -64, and LESS
+    static_assert(LESS == 0 || LESS == 8, "the constants");
+    uint32_t x[4];
+    nibble_pairs(w, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t y = x[i] | 0x64006400u;
+        f[i] = i & 1 ? times_and(y, 0x2C002C00u, k64) : less(y, k1024);  // (2C00: 1/16)
+    }
+}
+
 __device__ __forceinline__ float2 f16_pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
 }  // namespace lora

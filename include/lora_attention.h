@@ -166,7 +166,8 @@ typedef enum lora_kv_growth {
  * 4 and 6, 1 and 3, 5 and 7, the first in the low half of the byte.  V: piece 4g + q holds
  * tokens 4q .. 4q + 3; its j-th four bytes dimension d = 4g + 32(j/2) + 2(j%2) in the low
  * halves and d + 1 in the high ones, of tokens 4q, 4q + 2, 4q + 1, 4q + 3.  Scales are
- * finite; those of tokens that are not written yet may be anything.
+ * not negative, and values within f16's range (an append's are within 2^15, about);
+ * what tokens that are not written yet have may be anything.
  */
 typedef struct lora_kv_cache {
     lora_kv_format_t format;
@@ -238,7 +239,7 @@ typedef struct lora_kv_batch {
  *   uint4: for each 64 dimensions of a token and head, with NaN counted as 0,
  *          finite values cut to [-2^15, 2^15], and lo, hi the least and the largest
  *          finite one (0, 0 if there is none):
- *          least = lo and scale = (hi - lo) / 15, each rounded to f16 (nearest even);
+ *          least = lo and scale = (hi - lo) * fp32(1/15), each rounded to f16 (nearest even);
  *          code = (x - least) / scale rounded to nearest even, within [0, 15]; infinities
  *          take the end codes; with scale 0 every code is 0.
  *          In fp32 but for the two roundings.  Older tokens are not touched.
@@ -281,12 +282,13 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * up to a million keys.  Values that a query does not see have no part in this.
  * (Pages whose V scales differ by more than 2^79 within a sequence and head cost
  * time: twice as much for prompts, some ten times for few queries.)
- * LORA_KV_UINT4: scale * code + least enters the products as its parts, exactly
- * and in fp32, where the call takes the kernel for few queries (and in every fp32
- * call); there each p_j times the token's scale is off by at most 2^-33 of the
- * row's largest such product (bf16), 2^-44 (fp32), beyond its 11 or 22 bits.  Where
- * it takes the one for many, values enter rounded to f16 (11 bits), and V's least
- * step beyond p's 11 bits is 2^-29 of the row's largest p.
+ * LORA_KV_UINT4: K's codes enter the first product exactly, its scales and least
+ * values in fp32.  So do V's in every fp32 call, and where a bf16 call takes the
+ * kernel for few queries: there each p_j times the token's scale has 22 and 11 bits,
+ * and is off by at most 2^-44 and 2^-33 of the row's largest such product beyond
+ * that.  Where a bf16 call takes the one for many, V's values enter rounded to
+ * f16 (11 bits), and a p_j is off by at most 2^-29 of the row's largest beyond
+ * its 11 bits.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (num_q_heads /
  * num_heads over 64; num_q_heads not a multiple; rows * num_q_heads of 2^31
  * or more), WORKSPACE, CUDA.

@@ -4,8 +4,8 @@ Tolerances as derived at the head of test_gpu_attention.py, with |v| = |scale co
 products apart), per row:
     bf16: 2^-8 |o| + A (2^-11 + 2^-20 (S + 16)) + n 2^-25 V;  fp32: 2^-23 |o| + A (2^-21 + 2^-20 (S + 16)) + n 2^-36 V;
     lse: 2^-20 (S + 16).
-(p' = p scale has 11 or 22 bits; the least values' sums are fp32.)  Where a call takes the kernel for many queries, K and V
-enter rounded to f16: the restatement rounds them so too, and |v| is that value's."""
+(p' = p scale has 11 or 22 bits; the least values' sums are fp32.)  Where a call takes the kernel for many queries, V
+enters rounded to f16: the restatement rounds it so too, and |v| is that value's."""
 
 import numpy as np
 import pytest
@@ -32,7 +32,6 @@ def setup(seed, news, befores, page, H, D, **kw):
 
 def many_queries(dtype, rows, T, G, H, table, page, max_queries):
     """Which kernel: the rule of the library's host side."""
-    return False
     n = max_queries * G
     if dtype != "bf16" or n <= 16:
         return False
@@ -178,7 +177,8 @@ KINDS = ["zeros", "zero first", "least", "largest", "rising", "falling", "any", 
 @pytest.mark.parametrize("dtype,n,before,page,D", [("bf16", 1, 900, 16, 128), ("bf16", 2, 900, 32, 64), ("fp32", 2, 600, 16, 64),
                                                   ("fp32", 1, 6000, 64, 128), ("bf16", 48, 700, 16, 128), ("bf16", 200, 4000, 64, 64)])
 def test_scales_of_v_anywhere(kind, dtype, n, before, page, D):
-    """V's scales from 2^-24 to 2^12, in any order, and none; each row's tolerance by the V that it sees."""
+    """V's scales from 2^-24 to 2^12, in any order, and none (values within f16's range, as the format has them); each row's
+    tolerance by the V that it sees."""
     rng, cache, table, lens, offs = setup(before + n, [n, 3], [before, 40], page, 2, D)
     sc = np.zeros(tuple(cache.v_scales.shape), np.float64)
     for s in range(2):
@@ -187,7 +187,7 @@ def test_scales_of_v_anywhere(kind, dtype, n, before, page, D):
             e = {"zeros": -np.inf, "zero first": -np.inf if j < L // 2 else -3, "least": -24, "largest": 12,
                  "rising": -24 + 36 * j / L, "falling": 12 - 36 * j / L, "any": rng.choice([-24, -np.inf, -12, -2, 5, 12]),
                  "huge at the end": 12 if j >= L - n else -20, "least values alone": -np.inf}[kind]
-            least = rng.normal() * 2.0 ** e if np.isfinite(e) else 0.0
+            least = -(7.5 + 1.5 * np.clip(rng.normal(), -2, 2)) * 2.0 ** e if np.isfinite(e) else 0.0
             if kind == "least values alone":
                 least = rng.normal() * 100
             at = sc[int(table[s][j // page]), :, j % page // 16, :, j % 16]

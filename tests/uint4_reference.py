@@ -69,7 +69,7 @@ def quantise(x):
     none = ~fin.any(-1)
     lo, hi = np.where(none, np.float32(0), lo), np.where(none, np.float32(0), hi)
     m = lo.astype(np.float16)
-    s = ((hi - lo) / np.float32(15)).astype(np.float16)
+    s = ((hi - lo) * np.float32(1 / 15)).astype(np.float16)
     s32, m32 = s.astype(np.float32)[..., None], m.astype(np.float32)[..., None]
     with np.errstate(divide="ignore", invalid="ignore"):
         q = np.rint((x - m32) / s32)
@@ -113,7 +113,7 @@ def random_cache(rng, cache, spread=0.3, size=1.0):
 def attention(ref: Paged4, q, table, lens, offs, scale, causal=True, window=0, rounded=False):
     """q: float64 [rows, Hq, D] -> (out, lse, spread, score, vmax): the exact result, and per row and head what error
     bounds need: the largest over dimensions of sum p |v|, the largest of scale * sum |q k|, and the largest |v| that
-    it sees.  In them |v| stands for |scale code| + |least|, the parts that the products take.  `rounded`: K's and V's
+    it sees.  In them |k| and |v| stand for |scale code| + |least|, the parts that the products take.  `rounded`: V's
     values rounded to f16 first, and |v| theirs."""
     T, Hq, D = q.shape
     G = Hq // ref.H
@@ -124,7 +124,7 @@ def attention(ref: Paged4, q, table, lens, offs, scale, causal=True, window=0, r
             parts = getattr(ref, name) * s[..., 0], s[..., 1]
             vals[name] = parts[0] + parts[1]
             mags[name] = np.abs(parts[0]) + np.abs(parts[1])
-            if rounded:
+            if rounded and name == "v":
                 vals[name] = vals[name].astype(np.float16).astype(np.float64)
                 mags[name] = np.abs(vals[name])
     out, lse = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf)
