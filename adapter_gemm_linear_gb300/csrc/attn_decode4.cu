@@ -165,30 +165,23 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     // ---- consumers
     const int g = lane >> 2, tig = lane & 3;
     const int tok = k_token(g);  // S^T: rows g and g + 8 are tokens tok and tok + 2 of a tile
-    auto fetched = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    auto fetch_k = [&](const int64_t (&at)[TS], uint32_t slot) {
+    auto fetch = [&](const int64_t (&at)[TS], uint32_t slot) {
 #pragma unroll
-        for (int i = 0; i < TS * H; ++i) {
-            const int64_t tile = at[i / H];
-            if (tile != kEndOfLine)
-                copy16(&sm.codes[warp][slot][0][i][lane], b.k_pages + (max(tile, int64_t{0}) * H + i % H) * kBlockBytes + lane * 16, tile >= 0);
+        for (int j = 0; j < TS; ++j) {
+            if (at[j] == kEndOfLine) continue;
+            const int64_t byte = max(at[j], int64_t{0}) * (H * kBlockBytes) + lane * 16;
+#pragma unroll
+            for (int h = 0; h < H; ++h) copy16(&sm.codes[warp][slot][0][j * H + h][lane], b.k_pages + byte + h * kBlockBytes, at[j] >= 0);
+#pragma unroll
+            for (int h = 0; h < H; ++h) copy16(&sm.codes[warp][slot][1][j * H + h][lane], b.v_pages + byte + h * kBlockBytes, at[j] >= 0);
         }
-        if (lane < Smem::kMeta) {  // (scales too)
+        if (lane < Smem::kMeta) {
             const int64_t tile = TS == 2 && lane >= 8 * H ? at[TS - 1] : at[0];
             const float *from = lane / (4 * H) % 2 ? b.v_scales : b.k_scales;
             if (tile != kEndOfLine)
                 copy16(&sm.meta[warp][slot][lane], from + (max(tile, int64_t{0}) * (H * kKvTile) + lane % (4 * H) * 4), tile >= 0);
         }
-        fetched();
-    };
-    auto fetch_v = [&](const int64_t (&at)[TS], uint32_t slot) {
-#pragma unroll
-        for (int i = 0; i < TS * H; ++i) {
-            const int64_t tile = at[i / H];
-            if (tile != kEndOfLine)
-                copy16(&sm.codes[warp][slot][1][i][lane], b.v_pages + (max(tile, int64_t{0}) * H + i % H) * kBlockBytes + lane * 16, tile >= 0);
-        }
-        fetched();
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // where the tiles of the line's step i are; waits for their batch if it is the warp's
     // first of it, and gives the batch back after the last
@@ -203,12 +196,11 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             if (lane == 0) mbar_arrive(&sm.empty[n % kBatches]);
         }
     };
-    auto landed = [] { asm volatile("cp.async.wait_group %0;" ::"n"(2 * kDepth - 1) : "memory"); };
+    auto landed = [] { asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory"); };
     for (uint32_t d = 0; d < kDepth; ++d) {
         int64_t at[TS];
         look(warp + d * kWarps, at);
-        fetch_k(at, d);
-        fetch_v(at, d);
+        fetch(at, d);
     }
     uint32_t taken = 0;  // steps the warp has used
     uint32_t i0 = 0;     // steps of the items before
@@ -322,22 +314,11 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         for (int32_t st = j0; st < steps; st += kWarps) {
             const uint32_t slot = taken++ % kDepth;
             const int32_t key0 = (walk.tile0 + st * TS) * kKvTile;
-            int64_t ahead[TS];
-            look(i0 + st + kDepth * kWarps, ahead);
             landed();
             __syncwarp();  // every lane's copies of scales
-            // scale and least value of tokens tok and tok + 2
-            uint32_t kmeta[TS][2][H], vmeta[TS][2][H];
-            const uint32_t *meta = reinterpret_cast<const uint32_t *>(sm.meta[warp][slot]);
-#pragma unroll
-            for (int j = 0; j < TS; ++j)
-#pragma unroll
-                for (int h = 0; h < H; ++h)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        kmeta[j][t][h] = meta[(j * 2 * H + h) * kKvTile + tok + 2 * t];
-                        vmeta[j][t][h] = meta[(j * 2 * H + H + h) * kKvTile + tok + 2 * t];
-                    }
+            // scale and least value of token tok + 2 t, of K (v = 0) or V
+            const uint32_t *meta = reinterpret_cast<const uint32_t *>(sm.meta[warp][slot]) + tok;
+            auto meta_of = [&](int v, int j, int t, int h) { return meta[(j * 2 * H + v * H + h) * kKvTile + 2 * t]; };
             float s[TS][H][NT][4];
 #pragma unroll
             for (int j = 0; j < TS; ++j)
@@ -359,26 +340,32 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                         }
                     }
                 }
-            __syncwarp();  // the scales have been read
-            fetch_k(ahead, slot);
             // scores in log2 units
             float z[TS][RT][4];  // [2 * token half + row]
 #pragma unroll
             for (int j = 0; j < TS; ++j)
 #pragma unroll
-                for (int u = 0; u < RT; ++u) {
+                for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float sum = 0.0f;
+                    for (int h = 0; h < H; ++h) {
+                        const float2 ks = scale_of(meta_of(0, j, t, h));
 #pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            const float2 ks = scale_of(kmeta[j][e >> 1][h]);
-                            const float dot = SPLIT ? fmaf(s[j][h][NT - 1][e], 1.0f / kLoScale, s[j][h][0][e]) : s[j][h][u][e];
-                            sum = fmaf(ks.x, dot, fmaf(ks.y, qs[u][e & 1][h], sum));
-                        }
-                        z[j][u][e] = sum * cr[u][e & 1];
+                        for (int u = 0; u < RT; ++u)
+#pragma unroll
+                            for (int e = 2 * t; e < 2 * t + 2; ++e) {
+                                const float dot = SPLIT ? fmaf(s[j][h][NT - 1][e], 1.0f / kLoScale, s[j][h][0][e]) : s[j][h][u][e];
+                                const float sum = fmaf(ks.x, dot, h == 0 ? ks.y * qs[u][e & 1][0] : fmaf(ks.y, qs[u][e & 1][h], z[j][u][e]));
+                                z[j][u][e] = h == H - 1 ? sum * cr[u][e & 1] : sum;
+                            }
                     }
                 }
+            uint32_t vmeta[TS][2][H];
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int h = 0; h < H; ++h) vmeta[j][t][h] = meta_of(1, j, t, h);
             if (key0 < all_lo || key0 + TS * kKvTile > all_hi) {  // some row does not see some key
 #pragma unroll
                 for (int j = 0; j < TS; ++j) {
@@ -490,7 +477,6 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                         for (int h = 0; h < H; ++h)
                             om[u][e & 1][h] = fmaf(z[j][u][e] * fr[u][e & 1], scale_of(vmeta[j][e >> 1][h]).y, om[u][e & 1][h]);
-            landed();
 #pragma unroll
             for (int j = 0; j < TS; ++j)
 #pragma unroll
@@ -511,7 +497,10 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                         for (int u = 0; u < NT; ++u) mma_16816_f16(o[u][4 * h + k], f, pf[u][0], pf[u][1]);
                     }
                 }
-            fetch_v(ahead, slot);
+            __syncwarp();  // every lane has read the scales
+            int64_t ahead[TS];
+            look(i0 + st + kDepth * kWarps, ahead);
+            fetch(ahead, slot);
         }
         i0 += steps;
 
