@@ -26,6 +26,7 @@
 #include "attn_few.cuh"
 #include "attn_internal.h"
 #include "attn_uint4.cuh"
+#include "f32x2.cuh"
 
 namespace lora {
 
@@ -214,7 +215,8 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         uint32_t qf[NT][D / 16][2];
         // of the rows 8 u + 2 tig + i that the thread's scores belong to: the score
         // scale in log2 units over kUnit0, the blocks' sums of q times kUnit0, and the keys seen
-        float cr[RT][2], qs[RT][2][H];
+        // (pairs: of rows 2 tig and the next)
+        F2 cr[RT], qs[RT][H];
         int32_t kmin[RT][2], kmax[RT][2];
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
@@ -250,13 +252,15 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
                 sum[h] *= kUnit0;
             }
+            // from the lanes of rows 8 u + 2 tig and the next
+            auto of_rows = [&](float x) { return two(__shfl_sync(0xffffffffu, x, 8 * tig), __shfl_sync(0xffffffffu, x, 8 * tig + 4)); };
+            cr[u] = of_rows(up);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {  // from the lanes of row 8 u + 2 tig + i
-                cr[u][i] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * i);
+            for (int h = 0; h < H; ++h) qs[u][h] = of_rows(sum[h]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 kmax[u][i] = __shfl_sync(0xffffffffu, hi, 8 * tig + 4 * i);
                 kmin[u][i] = __shfl_sync(0xffffffffu, lo, 8 * tig + 4 * i);
-#pragma unroll
-                for (int h = 0; h < H; ++h) qs[u][i][h] = __shfl_sync(0xffffffffu, sum[h], 8 * tig + 4 * i);
             }
             const float down2 = down * (kUnit0 / kUnit1);
 #pragma unroll
@@ -283,29 +287,27 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) o[u][k][0] = o[u][k][1] = o[u][k][2] = o[u][k][3] = 0.0f;
-        float m[RT][2], l[RT][2], fr[RT][2], om[RT][2][H];
+        float m[RT][2];
+        F2 less[RT], l[RT], fr[RT], om[RT][H];  // less: -m, 0 for -inf
 #pragma unroll
-        for (int u = 0; u < RT; ++u)
+        for (int u = 0; u < RT; ++u) {
+            m[u][0] = m[u][1] = -INFINITY;
+            less[u] = l[u] = two(0.0f, 0.0f);
+            fr[u] = two(kMostFactor, kMostFactor);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                m[u][i] = -INFINITY;
-                l[u][i] = 0.0f;
-                fr[u][i] = kMostFactor;
+            for (int h = 0; h < H; ++h) om[u][h] = two(0.0f, 0.0f);
+        }
+        auto rescale = [&](int u, F2 f) {  // the rows' o and om
 #pragma unroll
-                for (int h = 0; h < H; ++h) om[u][i][h] = 0.0f;
-            }
-        auto rescale = [&](int u, int i, float f) {  // the row's o and om
+            for (int h = 0; h < H; ++h) om[u][h] = mul(om[u][h], f);
+            const float2 x = apart(f);
 #pragma unroll
-            for (int h = 0; h < H; ++h) om[u][i][h] *= f;
+            for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                o[u][k][i] *= f;
-                o[u][k][i + 2] *= f;
-                if (SPLIT) {
-                    o[NT - 1][k][i] *= f;
-                    o[NT - 1][k][i + 2] *= f;
+                for (int e = 0; e < 4; ++e) {
+                    o[u][k][e] *= e & 1 ? x.y : x.x;
+                    if (SPLIT) o[NT - 1][k][e] *= e & 1 ? x.y : x.x;
                 }
-            }
         };
 
         const int32_t steps = (walk.tile1 - walk.tile0 + TS - 1) / TS;
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     }
                 }
             // scores in log2 units
-            float z[TS][RT][4];  // [2 * token half + row]
+            F2 z[TS][RT][2];  // [token half]
 #pragma unroll
             for (int j = 0; j < TS; ++j)
 #pragma unroll
@@ -349,15 +351,17 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         const float2 ks = scale_of(meta_of(0, j, t, h));
+                        const F2 scale = two(ks.x, ks.x), least = two(ks.y, ks.y);
 #pragma unroll
-                        for (int u = 0; u < RT; ++u)
-#pragma unroll
-                            for (int e = 2 * t; e < 2 * t + 2; ++e) {
-                                const float dot = SPLIT ? fmaf(s[j][h][NT - 1][e], 1.0f / kLoScale, s[j][h][0][e]) : s[j][h][u][e];
-                                const float sum = fmaf(ks.x, dot, h == 0 ? ks.y * qs[u][e & 1][0] : fmaf(ks.y, qs[u][e & 1][h], z[j][u][e]));
-                                z[j][u][e] = h == H - 1 ? sum * cr[u][e & 1] : sum;
-                            }
+                        for (int u = 0; u < RT; ++u) {
+                            F2 dot = two(s[j][h][u][2 * t], s[j][h][u][2 * t + 1]);
+                            if (SPLIT)
+                                dot = fma(two(s[j][h][NT - 1][2 * t], s[j][h][NT - 1][2 * t + 1]), two(1.0f / kLoScale, 1.0f / kLoScale), dot);
+                            z[j][u][t] = fma(scale, dot, h == 0 ? mul(least, qs[u][0]) : fma(least, qs[u][h], z[j][u][t]));
+                        }
                     }
+#pragma unroll
+                    for (int u = 0; u < RT; ++u) z[j][u][t] = mul(z[j][u][t], cr[u]);
                 }
             uint32_t vmeta[TS][2][H];
 #pragma unroll
@@ -372,9 +376,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                     for (int u = 0; u < RT; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int32_t key = key0 + j * kKvTile + tok + (e & 2);
-                            if (key < kmin[u][e & 1] || key >= kmax[u][e & 1]) z[j][u][e] = -INFINITY;
+                        for (int t = 0; t < 2; ++t) {
+                            const int32_t key = key0 + j * kKvTile + tok + 2 * t;
+                            float2 x = apart(z[j][u][t]);
+                            if (key < kmin[u][0] || key >= kmax[u][0]) x.x = -INFINITY;
+                            if (key < kmin[u][1] || key >= kmax[u][1]) x.y = -INFINITY;
+                            z[j][u][t] = two(x.x, x.y);
                         }
                     // scales of V past the sequence's end are whatever was there, and 0 * NaN is not 0
 #pragma unroll
@@ -384,43 +391,49 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                             if (key0 + j * kKvTile + tok + 2 * t >= key_end) vmeta[j][t][h] = 0;
                 }
             }
+            float2 top[RT];  // the lane's largest scores
             bool grow = false;
 #pragma unroll
-            for (int j = 0; j < TS; ++j)
+            for (int u = 0; u < RT; ++u) {
+                top[u] = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-                for (int u = 0; u < RT; ++u)
+                for (int j = 0; j < TS; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) grow = grow || z[j][u][e] > m[u][e & 1] + kSlack;  // (also from m = -inf)
+                    for (int t = 0; t < 2; ++t) {
+                        const float2 x = apart(z[j][u][t]);
+                        top[u] = make_float2(fmaxf(top[u].x, x.x), fmaxf(top[u].y, x.y));
+                    }
+                grow = grow || top[u].x > m[u][0] + kSlack || top[u].y > m[u][1] + kSlack;  // (also from m = -inf)
+            }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int u = 0; u < RT; ++u)
+                for (int u = 0; u < RT; ++u) {
+                    float f[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float mx = m[u][i];
-#pragma unroll
-                        for (int j = 0; j < TS; ++j) mx = fmaxf(mx, fmaxf(z[j][u][i], z[j][u][i + 2]));
+                        float mx = fmaxf(m[u][i], i ? top[u].y : top[u].x);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float f = m[u][i] == -INFINITY ? 0.0f : ex2(m[u][i] - mx);
+                        f[i] = m[u][i] == -INFINITY ? 0.0f : ex2(m[u][i] - mx);
                         m[u][i] = mx;
-                        l[u][i] *= f;
-                        rescale(u, i, f);
                     }
+                    less[u] = two(m[u][0] == -INFINITY ? 0.0f : -m[u][0], m[u][1] == -INFINITY ? 0.0f : -m[u][1]);
+                    l[u] = mul(l[u], two(f[0], f[1]));
+                    rescale(u, two(f[0], f[1]));
+                }
             }
             // probabilities, and l
 #pragma unroll
-            for (int u = 0; u < RT; ++u) {
-                const float m0 = m[u][0] == -INFINITY ? 0.0f : m[u][0], m1 = m[u][1] == -INFINITY ? 0.0f : m[u][1];
+            for (int u = 0; u < RT; ++u)
 #pragma unroll
-                for (int j = 0; j < TS; ++j) {
+                for (int j = 0; j < TS; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        z[j][u][e] = ex2(z[j][u][e] - (e & 1 ? m1 : m0));
-                        l[u][e & 1] += z[j][u][e];
+                    for (int t = 0; t < 2; ++t) {
+                        const float2 x = apart(add(z[j][u][t], less[u]));
+                        z[j][u][t] = two(ex2(x.x), ex2(x.y));
+                        l[u] = add(l[u], z[j][u][t]);
                     }
-                }
-            }
             // p' = p s fr, rows side by side: [.., token half]
             uint32_t ph[TS][H][NT][2];
             auto scaled = [&] {
@@ -434,10 +447,10 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                             const float vs = f16_pair(vmeta[j][t][h]).x;
 #pragma unroll
                             for (int u = 0; u < RT; ++u) {
-                                const float x = z[j][u][2 * t] * fr[u][0] * vs, y = z[j][u][2 * t + 1] * fr[u][1] * vs;
-                                const uint32_t hi = pack_f16(x, y);
+                                const float2 x = apart(mul(mul(z[j][u][t], fr[u]), two(vs, vs)));
+                                const uint32_t hi = pack_f16(x.x, x.y);
                                 ph[j][h][u][t] = hi;
-                                if (SPLIT) ph[j][h][NT - 1][t] = pack_rest(x, y, hi);
+                                if (SPLIT) ph[j][h][NT - 1][t] = pack_rest(x.x, x.y, hi);
                                 const __half2 most = __hmax2(*reinterpret_cast<const __half2 *>(&over), *reinterpret_cast<const __half2 *>(&hi));
                                 over = *reinterpret_cast<const uint32_t *>(&most);
                             }
@@ -446,26 +459,33 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             };
             if (__any_sync(0xffffffffu, scaled())) {
 #pragma unroll
-                for (int u = 0; u < RT; ++u)
+                for (int u = 0; u < RT; ++u) {
+                    float2 most = make_float2(0.0f, 0.0f);  // of p s
+#pragma unroll
+                    for (int j = 0; j < TS; ++j)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int h = 0; h < H; ++h) {
+                                const float2 x = apart(z[j][u][t]);
+                                const float vs = f16_pair(vmeta[j][t][h]).x;
+                                most = make_float2(fmaxf(most.x, x.x * vs), fmaxf(most.y, x.y * vs));
+                            }
+                    const float2 was = apart(fr[u]);
+                    float now[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float most = 0.0f;  // of p s
-#pragma unroll
-                        for (int j = 0; j < TS; ++j)
-#pragma unroll
-                            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                                for (int h = 0; h < H; ++h) most = fmaxf(most, z[j][u][2 * t + i] * f16_pair(vmeta[j][t][h]).x);
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 4));
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
-                        // 2^(8 - exponent of most), where that is less than what there is
-                        const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
-                        const float least = __uint_as_float(static_cast<uint32_t>(127 + min(max(kTopExponent - e, -60), 60)) << 23);
-                        const float f = fminf(least, fr[u][i]);
-                        if (f < fr[u][i]) rescale(u, i, f / fr[u][i]);
-                        fr[u][i] = f;
+                        float x = i ? most.y : most.x;
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        // 2^(8 - exponent of the largest), where that is less than what there is
+                        const int e = static_cast<int>(__float_as_uint(x) >> 23) - 127;
+                        now[i] = fminf(__uint_as_float(static_cast<uint32_t>(127 + min(max(kTopExponent - e, -60), 60)) << 23), i ? was.y : was.x);
                     }
+                    rescale(u, two(now[0] / was.x, now[1] / was.y));
+                    fr[u] = two(now[0], now[1]);
+                }
                 scaled();
             }
 #pragma unroll
@@ -473,10 +493,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
 #pragma unroll
                 for (int u = 0; u < RT; ++u)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int h = 0; h < H; ++h)
-                            om[u][e & 1][h] = fmaf(z[j][u][e] * fr[u][e & 1], scale_of(vmeta[j][e >> 1][h]).y, om[u][e & 1][h]);
+                        for (int h = 0; h < H; ++h) {
+                            const float vm = scale_of(vmeta[j][t][h]).y;
+                            om[u][h] = fma(mul(z[j][u][t], fr[u]), two(vm, vm), om[u][h]);
+                        }
 #pragma unroll
             for (int j = 0; j < TS; ++j)
 #pragma unroll
@@ -516,10 +538,11 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     x += __shfl_xor_sync(0xffffffffu, x, 8);
                     return x + __shfl_xor_sync(0xffffffffu, x, 16);
                 };
-                const float sum = over_lanes(l[u][i]), un = 1.0f / fr[u][i];
+                auto row_of = [&](F2 x) { return i ? apart(x).y : apart(x).x; };
+                const float sum = over_lanes(row_of(l[u])), un = 1.0f / row_of(fr[u]);
                 float least[H];
 #pragma unroll
-                for (int h = 0; h < H; ++h) least[h] = over_lanes(om[u][i][h]);
+                for (int h = 0; h < H; ++h) least[h] = over_lanes(row_of(om[u][h]));
                 const int rt = 8 * u + 2 * tig + i;
                 if (rt >= rows) continue;
                 if (g == 0) {

@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_rope.cuh"
+#include "f32x2.cuh"
 
 namespace lora {
 
@@ -24,35 +25,6 @@ constexpr int kNormMaxThreads = 512;
 constexpr int kNormThreads = 128;  // of a block, about
 constexpr int kNormHeads = 4;      // of a group, where there is much work
 constexpr int kGradCtas = 3;       // blocks of the gradient, per SM: what 128 registers a thread leave room for
-
-// Two fp32 values at once.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 two(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 apart(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 swapped(F2 a) {
-    const float2 x = apart(a);
-    return two(x.y, x.x);
-}
 
 template <typename T>
 __device__ __forceinline__ void unpack2(const uint4 &q, F2 (&v)[VecTraits<T>::kElems / 2]) {
