@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_uint4.cuh"
+#include "f32x2.cuh"
 
 namespace lora {
 
@@ -19,183 +20,221 @@ namespace {
 constexpr float kLargest = 32768.0f;   // magnitudes held
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds a float below 2^22 to an integer, ties to even
 
-// N values as they are read, in fp32.
-template <int N>
-__device__ __forceinline__ void load_values(const __nv_bfloat16 *p, float *v) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        uint2 x;
-        if (N >= 8) {
-            if (i % 8) continue;
-            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p + i));
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[i + 2 * k] = __uint_as_float(w[k] << 16);
-                v[i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-            }
-        } else {
-            x = __ldg(reinterpret_cast<const uint2 *>(p + i));
-            v[i] = __uint_as_float(x.x << 16); v[i + 1] = __uint_as_float(x.x & 0xFFFF0000u);
-            v[i + 2] = __uint_as_float(x.y << 16); v[i + 3] = __uint_as_float(x.y & 0xFFFF0000u);
-        }
-    }
+// Least and largest of values, NaN if one of them is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
-template <int N>
-__device__ __forceinline__ void load_values(const float *p, float *v) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(p + i));
-        v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
-    }
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// Least and largest of N values (+inf and -inf where none counts): NaN is turned into
-// 0, what is beyond kLargest cut; infinities stay, and do not count.
+// N values as they are read.
+template <typename T, int N>
+struct Raw {
+    static constexpr int kWords = N * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) {
+            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
+            w[i] = y.x; w[i + 1] = y.y; w[i + 2] = y.z; w[i + 3] = y.w;
+        }
+    }
+    // as pairs in fp32, and the least and the largest of them (NaN if one of them is)
+    __device__ __forceinline__ void values(F2 (&v)[N / 2], float &lo, float &hi) const {
+        if constexpr (sizeof(T) == 2) {
+            __nv_bfloat162 l, h;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+                l = i == 0 ? x : __hmin2_nan(l, x);
+                h = i == 0 ? x : __hmax2_nan(h, x);
+                v[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            }
+            lo = min_nan(__low2float(l), __high2float(l));
+            hi = max_nan(__low2float(h), __high2float(h));
+        } else {
+            lo = hi = __uint_as_float(w[0]);
+#pragma unroll
+            for (int i = 1; i < kWords; ++i) {
+                lo = min_nan(lo, __uint_as_float(w[i]));
+                hi = max_nan(hi, __uint_as_float(w[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) v[i] = two(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        }
+    }
+};
+
+// Values of which some are not finite or beyond kLargest: NaN turned into 0, finite ones
+// cut, and the least and largest of the finite (+inf and -inf if there is none).
+__device__ __noinline__ void clean(float *v, int n, float *bounds) {
+    float lo = INFINITY, hi = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        float x = v[i];
+        if (!(x == x)) x = 0.0f;
+        if (fabsf(x) < INFINITY) {
+            x = fminf(fmaxf(x, -kLargest), kLargest);
+            lo = fminf(lo, x);
+            hi = fmaxf(hi, x);
+        }
+        v[i] = x;
+    }
+    bounds[0] = lo;
+    bounds[1] = hi;
+}
+// Codes by the quotients themselves.
+__device__ __noinline__ void near_codes(float *v, int n, float s, float m) {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) v[i] = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(v[i] - m, s)), 0.0f), 15.0f) : 0.0f;
+}
 template <int N>
-__device__ __forceinline__ void bounds(float *v, float &lo, float &hi) {
-    uint32_t most = 0;
-    lo = INFINITY;
-    hi = -INFINITY;
+__device__ __forceinline__ void to_array(const F2 (&v)[N], float (&x)[2 * N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        lo = fminf(lo, v[i]);
-        hi = fmaxf(hi, v[i]);
+        const float2 y = apart(v[i]);
+        x[2 * i] = y.x;
+        x[2 * i + 1] = y.y;
     }
-    if (__builtin_expect(most > __float_as_uint(kLargest), 0)) {
-        lo = INFINITY;
-        hi = -INFINITY;
+}
+template <int N>
+__device__ __forceinline__ void from_array(F2 (&v)[N], const float (&x)[2 * N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (!(v[i] == v[i])) v[i] = 0.0f;
-            if (fabsf(v[i]) == INFINITY) continue;
-            v[i] = fminf(fmaxf(v[i], -kLargest), kLargest);
-            lo = fminf(lo, v[i]);
-            hi = fmaxf(hi, v[i]);
-        }
+    for (int i = 0; i < N; ++i) v[i] = two(x[2 * i], x[2 * i + 1]);
+}
+
+template <int N>
+__device__ __forceinline__ void bounds_of(F2 (&v)[N], float &lo, float &hi) {
+    if (__builtin_expect(!(lo >= -kLargest && hi <= kLargest), 0)) {
+        float x[2 * N], b[2];
+        to_array(v, x);
+        clean(x, 2 * N, b);
+        from_array(v, x);
+        lo = b[0];
+        hi = b[1];
     }
 }
 
 struct Scale {
     __half2 stored;  // (scale, least)
     float s, m, inv;
+    bool plain;      // every code is within [0, 15] without being cut to it
 
+    // from the least and largest of all 64
     __device__ __forceinline__ Scale(float lo, float hi) {
         if (!(lo <= hi)) lo = hi = 0.0f;  // no finite value
         stored = __halves2half2(__float2half_rn((hi - lo) * (1.0f / 15.0f)), __float2half_rn(lo));
         s = __low2float(stored);
         m = __high2float(stored);
-        inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+        plain = s == 0.0f || ((lo - m) * inv > -0.49f && (hi - m) * inv < 15.49f);
     }
-    // A value's code, as the low bits of a float that is kRound + code.
-    __device__ __forceinline__ uint32_t code(float x) const {
-        const float d = x - m;
-        // d * inv is within 2e-6 of d / s where it is below 15, so both round
-        // alike unless it lies nearer than that to a half: there the quotient decides
-        float t = fminf(fmaxf(d * inv, 0.0f), 15.0f);
-        float r = t + kRound;
-        if (__builtin_expect(fabsf(t - (r - kRound)) > 0.4999f, 0)) r = fminf(fmaxf(rintf(__fdiv_rn(d, s)), 0.0f), 15.0f) + kRound;
-        return s > 0.0f ? __float_as_uint(r) : __float_as_uint(kRound);
+    // The codes of the lane's values, negative.
+    template <int N>
+    __device__ __forceinline__ void codes(const F2 (&v)[N], F2 (&q)[N]) const {
+        // (x - m) * inv is within 2e-6 of (x - m) / s where it is below 16, so both round
+        // alike unless it lies nearer than that to a half: there, and where a value
+        // is not within the codes' range, the quotients decide
+        const F2 less = two(-m, -m), i2 = two(inv, inv), round = two(kRound, kRound), minus = two(-1.0f, -1.0f);
+        float off = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const F2 d = add(v[i], less);
+            q[i] = fma(fma(d, i2, round), minus, round);
+            const float2 e = apart(fma(d, i2, q[i]));
+            off = max_nan(off, max_nan(fabsf(e.x), fabsf(e.y)));
+        }
+        if (__builtin_expect(!(plain && off < 0.49999f), 0)) {
+            float x[2 * N];
+            to_array(v, x);
+            near_codes(x, 2 * N, s, m);
+            from_array(q, x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) q[i] = mul(q[i], minus);
+        }
     }
 };
 
-// Codes into nibbles: sums of (kRound + code) << shift, less what the kRound make.
-struct Word {
-    uint32_t sum = 0, less = 0;
-    __device__ __forceinline__ void add(uint32_t code, int nibble) {
-        sum += code << (4 * nibble);
-        less += __float_as_uint(kRound) << (4 * nibble);
-    }
-    __device__ __forceinline__ uint32_t bits() const { return sum - less; }
-};
+constexpr float kBits = 8388608.0f;  // 2^23: the low bits of a float that is this and an integer are the integer's
 
-// A warp's tile of K: new tokens [lo, hi) (positions) of the tile that begins at t0.
+// A warp's tile: new tokens [lo, hi) (positions) of the tile that begins at t0.  A lane takes
+// 16 dimensions of a token a turn, of K and of V; V's codes change places in shared
+// memory (`stage`, 512 bytes of the warp's own), or go out byte by byte where the tile is
+// not written whole.  (In a loop, with the next turn's values on their way: the code of a
+// warp that has one token to write takes longer to fetch than to run; unrolled, 23 us for a
+// token of 256 sequences.)
 template <typename T, int D>
-__device__ __forceinline__ void append_k(const T *src, int64_t row, uint8_t *codes, __half2 *scales, int32_t t0, int32_t lo, int32_t hi,
-                                         int lane) {
+__device__ __forceinline__ void append_tile(const T *src, int64_t row, uint8_t *codes, __half2 *scales, int32_t t0, int32_t lo, int32_t hi,
+                                            bool is_v, uint8_t *stage, int lane) {
     const int g = lane >> 2, q = lane & 3;
+    constexpr int kTurns = 2 * (D / kBlockDims);
+    const bool whole = lo <= t0 && hi >= t0 + kKvTile;
+    auto token = [&](int i) { return k_token(g) + 2 * (i & 1); };
+    auto is_fresh = [&](int i) { return t0 + token(i) >= lo && t0 + token(i) < hi; };
+    auto read = [&](int i, Raw<T, 16> &x) {
+        x.zero();
+        if (is_fresh(i)) x.load(src + static_cast<int64_t>(t0 + token(i)) * row + (i >> 1) * kBlockDims + 16 * q);
+    };
+    Raw<T, 16> next;
+    read(0, next);
+#pragma unroll 1
+    for (int i = 0; i < kTurns; ++i) {
+        const Raw<T, 16> x = next;
+        if (i + 1 < kTurns) read(i + 1, next);
+        const bool fresh = is_fresh(i);
+        if (!__any_sync(0xffffffffu, fresh)) continue;
+        F2 v[8], c[8];
+        float a, z;
+        x.values(v, a, z);
+        bounds_of(v, a, z);
 #pragma unroll
-    for (int h = 0; h < D / kBlockDims; ++h) {
-        uint32_t w[2][2];
-        bool fresh[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int t = k_token(g) + 2 * k;
-            const int32_t pos = t0 + t;
-            fresh[k] = pos >= lo && pos < hi;
-            float v[16], a, z;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            if (fresh[k]) load_values<16>(src + static_cast<int64_t>(pos) * row + h * kBlockDims + 16 * q, v);
-            bounds<16>(v, a, z);
-#pragma unroll
-            for (int o = 1; o < 4; o *= 2) {
-                a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-            }
-            const Scale s(a, z);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                Word x;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x.add(s.code(v[8 * j + e]), (e >> 1) + 4 * (e & 1));
-                w[k][j] = x.bits();
-            }
-            if (q == 0 && fresh[k]) scales[h * kKvTile + t] = s.stored;
+        for (int o = 1; o < 4; o *= 2) {
+            a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
         }
-        uint4 *at = reinterpret_cast<uint4 *>(codes + h * kBlockBytes) + lane;
-        if (fresh[0] && fresh[1]) *at = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
-        else if (fresh[0]) reinterpret_cast<uint2 *>(at)[0] = make_uint2(w[0][0], w[0][1]);
-        else if (fresh[1]) reinterpret_cast<uint2 *>(at)[1] = make_uint2(w[1][0], w[1][1]);
-    }
-}
-
-template <typename T, int D>
-__device__ __forceinline__ void append_v(const T *src, int64_t row, uint8_t *codes, __half2 *scales, int32_t t0, int32_t lo, int32_t hi,
-                                         int lane) {
-    const int g = lane >> 2, q = lane & 3;
-    const int32_t first = t0 + 4 * q;
+        const Scale s(a, z);
+        s.codes(v, c);
+        const int h = i >> 1;
+        uint8_t *const block = codes + h * kBlockBytes;
+        if (q == 0 && fresh) scales[h * kKvTile + token(i)] = s.stored;
+        if (!is_v) {
+            // a word's even dimensions make its low half, the odd ones its high half
+            uint32_t w[2];
 #pragma unroll
-    for (int h = 0; h < D / kBlockDims; ++h) {
-        Word w[4];
-        __half2 stored[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const bool fresh = first + t >= lo && first + t < hi;
-            float v[8], a, z;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-            const T *p = src + static_cast<int64_t>(first + t) * row + h * kBlockDims + 4 * g;
-            if (fresh) {
-                load_values<4>(p, v);
-                load_values<4>(p + 32, v + 4);
+            for (int k = 0; k < 2; ++k) {
+                F2 sum = fma(c[4 * k], two(-1.0f, -1.0f), two(kBits, kBits));
+                sum = fma(c[4 * k + 1], two(-16.0f, -16.0f), sum);
+                sum = fma(c[4 * k + 2], two(-256.0f, -256.0f), sum);
+                sum = fma(c[4 * k + 3], two(-4096.0f, -4096.0f), sum);
+                const float2 y = apart(sum);
+                w[k] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410);
             }
-            bounds<8>(v, a, z);
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2) {
-                a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-            }
-            const Scale s(a, z);
-            stored[t] = s.stored;
-            constexpr int kByte[4] = {0, 2, 1, 3};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e >> 1].add(s.code(v[e]), 2 * kByte[t] + (e & 1));
-        }
-        uint8_t *at = codes + h * kBlockBytes + lane * 16;
-        __half2 *sc = scales + h * kKvTile + 4 * q;
-        if (first >= lo && first + 4 <= hi) {
-            *reinterpret_cast<uint4 *>(at) = make_uint4(w[0].bits(), w[1].bits(), w[2].bits(), w[3].bits());
-            if (g == 0) *reinterpret_cast<uint4 *>(sc) = *reinterpret_cast<const uint4 *>(stored);
+            if (fresh) reinterpret_cast<uint2 *>(block)[2 * lane + (i & 1)] = make_uint2(w[0], w[1]);
         } else {
+            // the byte of token t and dimensions 2 p, 2 p + 1 (p of 32): piece 4 (p % 16 / 2) + t / 4, word 2 (p /
+            // 16) + p % 2, byte 0, 2, 1, 3 by t % 4; here p = 8 q + k
+            const int t = token(i), at = (q & 1) * 256 + (t >> 2) * 16 + (q >> 1) * 8 + (t & 1) * 2 + (t >> 1 & 1);
+            if (whole && !(i & 1)) __syncwarp();  // the block before has been read
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (first + t < lo || first + t >= hi) continue;
-                const int byte = t == 1 ? 2 : t == 2 ? 1 : t;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) at[4 * j + byte] = static_cast<uint8_t>(w[j].bits() >> (8 * byte));
-                if (g == 0) sc[t] = stored[t];
+            for (int k = 0; k < 8; ++k) {
+                const float2 y = apart(c[k]);
+                const uint8_t b = static_cast<uint8_t>(__float_as_uint(fmaf(y.y, -16.0f, kBits - y.x)));
+                uint8_t *const to = (whole ? stage : block) + at + (k >> 1) * 64 + (k & 1) * 4;
+                if (fresh) *to = b;
+            }
+            if (whole && (i & 1)) {
+                __syncwarp();
+                reinterpret_cast<uint4 *>(block)[lane] = reinterpret_cast<const uint4 *>(stage)[lane];
             }
         }
     }
@@ -203,8 +242,9 @@ __device__ __forceinline__ void append_v(const T *src, int64_t row, uint8_t *cod
 
 // grid.x: pieces of the rows cut at multiples of 16 tokens; grid.y: groups of four (K or V, head).
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv_append4_kernel(const __grid_constant__ KvView b, const __grid_constant__ HeadsView k,
+__global__ void __launch_bounds__(128, 7) kv_append4_kernel(const __grid_constant__ KvView b, const __grid_constant__ HeadsView k,
                                                          const __grid_constant__ HeadsView v) {
+    __shared__ __align__(16) uint8_t stage[4][kBlockBytes];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t hv = blockIdx.y * 4 + warp;
     if (hv >= 2 * b.heads) return;
@@ -221,8 +261,7 @@ __global__ void __launch_bounds__(128) kv_append4_kernel(const __grid_constant__
         __half2 *scales = reinterpret_cast<__half2 *>(is_v ? b.v_scales : b.k_scales) + tile * (D / kBlockDims * kKvTile);
         // of position p: row r.off + p - (r.len - r.n)
         const T *src = static_cast<const T *>(x.p) + head * x.head + static_cast<int64_t>(r.off - (r.len - r.n)) * x.row;
-        if (is_v) append_v<T, D>(src, x.row, codes, scales, t0, lo, hi, lane);
-        else append_k<T, D>(src, x.row, codes, scales, t0, lo, hi, lane);
+        append_tile<T, D>(src, x.row, codes, scales, t0, lo, hi, is_v, stage[warp], lane);
     });
 }
 

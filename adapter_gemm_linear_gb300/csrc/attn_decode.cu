@@ -98,7 +98,7 @@ struct DecodeSmem {
     float vr[2];  // the reference scale of V of the item (by its parity)
     TileInfo info[kBatches][kBatch];
     uint64_t full[kBatches], empty[kBatches];
-    long long warp_sum[kWarps + 1];
+    long long warp_sum[kWarps + 1][2];
     long long base;  // first unit of the sequence the CTA begins in
     int32_t seq;
     int32_t dead;    // a wait ran out: nobody waits any more
@@ -132,9 +132,9 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         sm.dead = 0;
         joins[blockIdx.x].last_cta = -1;
     }
-    const Range range = plan_line<ROWS, kThreads>(a, sm.warp_sum, &sm.seq, &sm.base);
+    const Range range = plan_line<ROWS, kThreads, 0>(a, sm.warp_sum, &sm.seq, &sm.base);
     const long long total = range.total, ctas = range.ctas;
-    Walk<ROWS> walk(a, range.w0, range.w1, sm.seq, sm.base);
+    Walk<ROWS> walk(a, range, sm.seq, sm.base);
     volatile int32_t *dead = &sm.dead;
     const uint64_t limit = a.test_wait_ns ? a.test_wait_ns : kWaitNs;
 

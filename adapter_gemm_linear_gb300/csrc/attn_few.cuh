@@ -41,11 +41,11 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return r;
 }
 
-// A sequence's work: `chunks` units for each of heads x row_tiles items, over tiles [t0, t1).
+// A sequence's work: `items` items (heads x row_tiles) of `chunks` units each, over tiles [t0, t1).
 struct SeqWork {
     SeqRows r;
     int32_t t0, t1, chunks, row_tiles;
-    long long units;
+    long long items;
 };
 
 template <int ROWS>
@@ -62,79 +62,103 @@ __device__ __forceinline__ SeqWork seq_work(const AttnView &a, int32_t s) {
         w.chunks = (w.t1 - w.t0 + kChunkTiles - 1) / kChunkTiles;
         w.row_tiles = (w.r.n * a.group + ROWS - 1) / ROWS;
     }
-    w.units = static_cast<long long>(w.chunks) * w.row_tiles * a.kv.heads;
+    w.items = static_cast<long long>(w.row_tiles) * a.kv.heads;
     return w;
 }
 
-// One CTA's walk over its units [w, end): item by item.
+// The units that a CTA takes of the line: [w0, w1) of `total`, which `ctas` CTAs share.
+// Every item has `extra` units more than chunks, in front: what beginning and ending it costs.
+struct Range {
+    long long w0, w1, total, ctas;
+    int32_t extra;
+};
+
+// One CTA's walk over its units: item by item, those of which it has chunks.
 template <int ROWS>
 struct Walk {
     const AttnView &a;
     long long w, end, base;
-    int32_t s;
+    int32_t s, extra;
     SeqWork work;
     // the current item
     int32_t head, row_tile, tile0, tile1;  // tiles of this CTA
     bool from_start, to_end;               // whether the item begins / ends in this CTA
     long long item_end;                    // unit after the item's last
 
-    __device__ __forceinline__ Walk(const AttnView &v, long long w0, long long w1, int32_t seq, long long seq_base)
-        : a(v), w(w0), end(w1), base(seq_base), s(seq) {
+    __device__ __forceinline__ Walk(const AttnView &v, const Range &range, int32_t seq, long long seq_base)
+        : a(v), w(range.w0), end(range.w1), base(seq_base), s(seq), extra(range.extra) {
         if (w < end) work = seq_work<ROWS>(a, s);
     }
 
     __device__ __forceinline__ bool next() {
-        if (w >= end) return false;
-        while (w >= base + work.units) {
-            base += work.units;
-            work = seq_work<ROWS>(a, ++s);
+        while (w < end) {
+            while (w >= base + work.items * (work.chunks + extra)) {
+                base += work.items * (work.chunks + extra);
+                work = seq_work<ROWS>(a, ++s);
+            }
+            const int32_t units = work.chunks + extra;
+            const long long local = w - base;
+            const long long item = local / units;
+            const int32_t u = static_cast<int32_t>(local - item * units);
+            head = static_cast<int32_t>(item / work.row_tiles);
+            row_tile = static_cast<int32_t>(item - static_cast<long long>(head) * work.row_tiles);
+            const int32_t u1 = static_cast<int32_t>(min(static_cast<long long>(units), u + (end - w)));
+            const int32_t c = max(u - extra, 0);
+            tile0 = work.t0 + c * kChunkTiles;
+            tile1 = min(work.t1, work.t0 + (u1 - extra) * kChunkTiles);
+            from_start = c == 0;
+            to_end = u1 == units;
+            item_end = base + (item + 1) * units;
+            w += u1 - u;
+            if (u1 > extra) return true;
         }
-        const long long local = w - base;
-        const long long item = local / work.chunks;
-        const int32_t c = static_cast<int32_t>(local - item * work.chunks);
-        head = static_cast<int32_t>(item / work.row_tiles);
-        row_tile = static_cast<int32_t>(item - static_cast<long long>(head) * work.row_tiles);
-        const int32_t c1 = static_cast<int32_t>(min(static_cast<long long>(work.chunks), c + (end - w)));
-        tile0 = work.t0 + c * kChunkTiles;
-        tile1 = min(work.t1, work.t0 + c1 * kChunkTiles);
-        from_start = c == 0;
-        to_end = c1 == work.chunks;
-        item_end = base + (item + 1) * work.chunks;
-        w += c1 - c;
-        return true;
+        return false;
     }
-};
-
-// The units that a CTA takes of the line: [w0, w1) of `total`, which `ctas` CTAs share.
-struct Range {
-    long long w0, w1, total, ctas;
 };
 
 // The plan: where this CTA's range begins, by all of its threads (two barriers; what
 // they wrote to shared memory before is there for all after).  `seq` and `base` (shared
-// memory) become the sequence that it begins in and that sequence's first unit.
-template <int ROWS, int THREADS>
-__device__ __forceinline__ Range plan_line(const AttnView &a, long long *warp_sum, int32_t *seq, long long *base) {
+// memory) become the sequence that it begins in and that sequence's first unit.  Items
+// have EXTRA more units where there are more chunks than CTAs.
+template <int ROWS, int THREADS, int EXTRA>
+__device__ __forceinline__ Range plan_line(const AttnView &a, long long (*warp_sum)[2], int32_t *seq, long long *base) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t per = (a.kv.num_seqs + THREADS - 1) / THREADS;
     const int32_t s0 = min(a.kv.num_seqs, static_cast<int32_t>(threadIdx.x) * per), s1 = min(a.kv.num_seqs, s0 + per);
-    long long mine = 0;
-    for (int32_t s = s0; s < s1; ++s) mine += seq_work<ROWS>(a, s).units;
-    long long upto = mine;
+    long long chunks = 0, items = 0;
+    for (int32_t s = s0; s < s1; ++s) {
+        const SeqWork w = seq_work<ROWS>(a, s);
+        chunks += w.items * w.chunks;
+        items += w.items;
+    }
+    long long c_upto = chunks, i_upto = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
+        const long long c = __shfl_up_sync(0xffffffffu, c_upto, o), i = EXTRA ? __shfl_up_sync(0xffffffffu, i_upto, o) : 0;
+        if (lane >= o) {
+            c_upto += c;
+            i_upto += i;
+        }
     }
-    if (lane == 31) warp_sum[warp] = upto;
+    if (lane == 31) {
+        warp_sum[warp][0] = c_upto;
+        warp_sum[warp][1] = i_upto;
+    }
     __syncthreads();
-    Range r;
-    r.total = 0;
+    long long c_total = 0, i_total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) upto += warp_sum[w];
-        r.total += warp_sum[w];
+        if (w < warp) {
+            c_upto += warp_sum[w][0];
+            i_upto += warp_sum[w][1];
+        }
+        c_total += warp_sum[w][0];
+        i_total += warp_sum[w][1];
     }
+    Range r;
+    r.extra = EXTRA && c_total > static_cast<long long>(gridDim.x) ? EXTRA : 0;
+    r.total = c_total + r.extra * i_total;
+    const long long upto = c_upto + r.extra * i_upto, mine = chunks + r.extra * items;
     // as many CTAs as there are units at most, so that none between two of an item is without work
     r.ctas = min(r.total, static_cast<long long>(gridDim.x));
     r.w0 = blockIdx.x < r.ctas ? r.total * blockIdx.x / r.ctas : 0;
@@ -143,7 +167,8 @@ __device__ __forceinline__ Range plan_line(const AttnView &a, long long *warp_su
         long long at = upto - mine;
         int32_t s = s0;
         for (;; ++s) {
-            const long long u = seq_work<ROWS>(a, s).units;
+            const SeqWork w = seq_work<ROWS>(a, s);
+            const long long u = w.items * (w.chunks + r.extra);
             if (r.w0 < at + u) break;
             at += u;
         }
