@@ -93,8 +93,8 @@ __device__ __noinline__ void clean(float *v, int n, float *bounds) {
     bounds[0] = lo;
     bounds[1] = hi;
 }
-// Codes by the quotients themselves.
-__device__ __noinline__ void near_codes(float *v, int n, float s, float m) {
+// Codes by the quotients themselves, cut to [0, 15].
+__device__ __noinline__ void codes_cut(float *v, int n, float s, float m) {
 #pragma unroll 1
     for (int i = 0; i < n; ++i) v[i] = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(v[i] - m, s)), 0.0f), 15.0f) : 0.0f;
 }
@@ -113,9 +113,11 @@ __device__ __forceinline__ void from_array(F2 (&v)[N], const float (&x)[2 * N]) 
     for (int i = 0; i < N; ++i) v[i] = two(x[2 * i], x[2 * i + 1]);
 }
 
+// Whether that was so.
 template <int N>
-__device__ __forceinline__ void bounds_of(F2 (&v)[N], float &lo, float &hi) {
-    if (__builtin_expect(!(lo >= -kLargest && hi <= kLargest), 0)) {
+__device__ __forceinline__ bool bounds_of(F2 (&v)[N], float &lo, float &hi) {
+    const bool some = !(lo >= -kLargest && hi <= kLargest);
+    if (__builtin_expect(some, 0)) {
         float x[2 * N], b[2];
         to_array(v, x);
         clean(x, 2 * N, b);
@@ -123,6 +125,7 @@ __device__ __forceinline__ void bounds_of(F2 (&v)[N], float &lo, float &hi) {
         lo = b[0];
         hi = b[1];
     }
+    return some;
 }
 
 struct Scale {
@@ -139,25 +142,22 @@ struct Scale {
         inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
         plain = s == 0.0f || ((lo - m) * inv > -0.49f && (hi - m) * inv < 15.49f);
     }
-    // The codes of the lane's values, negative.
+    // The codes of the lane's values, negative.  (x - m) / s is rounded as a division rounds
+    // it: with inv = 1 / s correctly rounded, t = d inv and r = d - t s by one fused
+    // multiply-add, t + r inv is the correctly rounded quotient (Markstein).  Values that are
+    // not finite or not within the codes' range (`odd`) take the divisions themselves.
     template <int N>
-    __device__ __forceinline__ void codes(const F2 (&v)[N], F2 (&q)[N]) const {
-        // (x - m) * inv is within 2e-6 of (x - m) / s where it is below 16, so both round
-        // alike unless it lies nearer than that to a half: there, and where a value
-        // is not within the codes' range, the quotients decide
-        const F2 less = two(-m, -m), i2 = two(inv, inv), round = two(kRound, kRound), minus = two(-1.0f, -1.0f);
-        float off = 0.0f;
+    __device__ __forceinline__ void codes(const F2 (&v)[N], bool odd, F2 (&q)[N]) const {
+        const F2 less = two(-m, -m), i2 = two(inv, inv), s2 = two(-s, -s), round = two(kRound, kRound), minus = two(-1.0f, -1.0f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const F2 d = add(v[i], less);
-            q[i] = fma(fma(d, i2, round), minus, round);
-            const float2 e = apart(fma(d, i2, q[i]));
-            off = max_nan(off, max_nan(fabsf(e.x), fabsf(e.y)));
+            const F2 d = add(v[i], less), t = mul(d, i2);
+            q[i] = fma(add(fma(fma(t, s2, d), i2, t), round), minus, round);
         }
-        if (__builtin_expect(!(plain && off < 0.49999f), 0)) {
+        if (__builtin_expect(odd || !plain, 0)) {
             float x[2 * N];
             to_array(v, x);
-            near_codes(x, 2 * N, s, m);
+            codes_cut(x, 2 * N, s, m);
             from_array(q, x);
 #pragma unroll
             for (int i = 0; i < N; ++i) q[i] = mul(q[i], minus);
@@ -196,14 +196,14 @@ __device__ __forceinline__ void append_tile(const T *src, int64_t row, uint8_t *
         F2 v[8], c[8];
         float a, z;
         x.values(v, a, z);
-        bounds_of(v, a, z);
+        const bool odd = bounds_of(v, a, z);
 #pragma unroll
         for (int o = 1; o < 4; o *= 2) {
             a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
             z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
         }
         const Scale s(a, z);
-        s.codes(v, c);
+        s.codes(v, odd, c);
         const int h = i >> 1;
         uint8_t *const block = codes + h * kBlockBytes;
         if (q == 0 && fresh) scales[h * kKvTile + token(i)] = s.stored;
