@@ -12,6 +12,7 @@
 
 #include "attn_uint4.cuh"
 #include "f32x2.cuh"
+#include "sm100_ptx.cuh"
 
 namespace lora {
 
@@ -267,102 +268,129 @@ __global__ void __launch_bounds__(128, 7) kv_append4_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- gather
 
+// N values, 32 bytes at a time where there are so many (a K lane's piece of a row is a sector, or two).
 template <int N>
-__device__ __forceinline__ void store_values(float *p, const float *v) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
-template <int N>
-__device__ __forceinline__ void store_values(__nv_bfloat16 *p, const float *v) {
-    uint32_t w[N / 2];
+__device__ __forceinline__ void store_values(float *p, const F2 (&v)[N / 2]) {
+    uint32_t w[N];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        const float2 x = apart(v[i]);
+        w[2 * i] = __float_as_uint(x.x);
+        w[2 * i + 1] = __float_as_uint(x.y);
     }
     if constexpr (N >= 8) {
 #pragma unroll
-        for (int i = 0; i < N / 2; i += 4) reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        for (int i = 0; i < N; i += 8) sm100::store_32(p + i, *reinterpret_cast<const uint32_t(*)[8]>(w + i));
+    } else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_values(__nv_bfloat16 *p, const F2 (&v)[N / 2]) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 x = apart(v[i]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    if constexpr (N >= 16) {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 8) sm100::store_32(p + 2 * i, *reinterpret_cast<const uint32_t(*)[8]>(w + i));
     } else {
         *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
 }
 
+// A warp takes a tile of heads hv, hv + 4 gridDim.y, ... of the 2 heads (K's, then V's): the
+// more of them, the fewer times the tile's place is looked up.
 template <typename T, int D>
 __global__ void __launch_bounds__(128, 8) kv_gather4_kernel(const __grid_constant__ KvView b, const __grid_constant__ HeadsView k,
                                                             const __grid_constant__ HeadsView v) {
     constexpr int H = D / kBlockDims;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int32_t hv = blockIdx.y * 4 + warp;
-    if (hv >= 2 * b.heads) return;
-    const bool is_v = hv >= b.heads;
-    const int32_t head = is_v ? hv - b.heads : hv;
-    const HeadsView &x = is_v ? v : k;
     for_pieces(b, blockIdx.x, 4, blockIdx.y == 0 && threadIdx.x < 32,
                [&](int32_t s, const SeqRows &r, int32_t lo, int32_t hi) {
         const int32_t page = read_page(b, s, lo >> b.page_shift);
         const int32_t t0 = lo & ~(kKvTile - 1);
-        const int64_t tile = page < 0 ? 0 : tile_index(b, page, head, (t0 & (b.page_tokens - 1)) / kKvTile);
-        const uint4 *codes = reinterpret_cast<const uint4 *>((is_v ? b.v_pages : b.k_pages) + tile * (H * kBlockBytes)) + lane;
-        const __half2 *scales = reinterpret_cast<const __half2 *>(is_v ? b.v_scales : b.k_scales) + tile * (H * kKvTile);
-        T *dst = static_cast<T *>(x.p) + static_cast<int64_t>(r.off - (r.len - r.n)) * x.row + head * x.head;
-        uint4 c[H];
-        float2 sc[H][4];  // of K's two tokens, or V's four
+        const int64_t row0 = r.off - (r.len - r.n);  // of position 0
+#pragma unroll 1
+        for (int32_t hv = blockIdx.y * 4 + warp; hv < 2 * b.heads; hv += 4 * gridDim.y) {
+            const bool is_v = hv >= b.heads;
+            const int32_t head = is_v ? hv - b.heads : hv;
+            const HeadsView &x = is_v ? v : k;
+            const int64_t tile = page < 0 ? 0 : tile_index(b, page, head, (t0 & (b.page_tokens - 1)) / kKvTile);
+            const uint4 *codes = reinterpret_cast<const uint4 *>((is_v ? b.v_pages : b.k_pages) + tile * (H * kBlockBytes)) + lane;
+            const uint32_t *scales = reinterpret_cast<const uint32_t *>(is_v ? b.v_scales : b.k_scales) + tile * (H * kKvTile);
+            T *dst = static_cast<T *>(x.p) + row0 * x.row + head * x.head;
+            uint4 c[H];
+            uint32_t sc[H][4];  // of K's two tokens, or V's four
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            c[h] = codes[h * 32];
-            if (is_v) {
-                const uint4 y = *reinterpret_cast<const uint4 *>(scales + h * kKvTile + 4 * q);
-                sc[h][0] = f16_pair(y.x); sc[h][1] = f16_pair(y.y); sc[h][2] = f16_pair(y.z); sc[h][3] = f16_pair(y.w);
-            } else {
-                sc[h][0] = __half22float2(scales[h * kKvTile + k_token(g)]);
-                sc[h][1] = __half22float2(scales[h * kKvTile + k_token(g) + 2]);
+            for (int h = 0; h < H; ++h) {
+                c[h] = codes[h * 32];
+                if (is_v) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(scales + h * kKvTile + 4 * q);
+                    sc[h][0] = y.x; sc[h][1] = y.y; sc[h][2] = y.z; sc[h][3] = y.w;
+                } else {
+                    sc[h][0] = scales[h * kKvTile + k_token(g)];
+                    sc[h][1] = scales[h * kKvTile + k_token(g) + 2];
+                }
+                if (page < 0) sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0u;  // (a table entry out of range reads as zeros)
             }
-        }
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
-            // (a table entry out of range reads as zeros)
-            auto value = [&](float code, float unit, const float2 &s) { return page < 0 ? 0.0f : fmaf(code, s.x * unit, s.y); };
             if (!is_v) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int32_t pos = t0 + k_token(g) + 2 * t;
-                    float o[16];
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t f[4];
-                        nibble_pairs(w[2 * t + j], f);
+                    for (int t = 0; t < 2; ++t) {
+                        const int32_t pos = t0 + k_token(g) + 2 * t;
+                        const float2 y = f16_pair(sc[h][t]);
+                        const F2 s0 = two(y.x * kCode0, y.x * kCode0), s1 = two(y.x * kCode1, y.x * kCode1), m = two(y.y, y.y);
+                        F2 o[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 y = f16_pair(f[i]);
-                            o[8 * j + 2 * i] = value(y.x, i & 1 ? kCode1 : kCode0, sc[h][t]);
-                            o[8 * j + 2 * i + 1] = value(y.y, i & 1 ? kCode1 : kCode0, sc[h][t]);
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t f[4];
+                            nibble_pairs(t == 0 ? (j == 0 ? c[h].x : c[h].y) : (j == 0 ? c[h].z : c[h].w), f);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 code = f16_pair(f[i]);
+                                o[4 * j + i] = fma(two(code.x, code.y), i & 1 ? s1 : s0, m);
+                            }
+                        }
+                        if (pos >= lo && pos < hi) store_values<16>(dst + pos * x.row + h * kBlockDims + 16 * q, o);
+                    }
+            } else {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
+#pragma unroll
+                    for (int t = 0; t < 4; t += 2) {  // tokens t and t + 1 side by side
+                        const float2 ya = f16_pair(sc[h][t]), yb = f16_pair(sc[h][t + 1]);
+                        const F2 s0 = two(ya.x * kCode0, yb.x * kCode0), s1 = two(ya.x * kCode1, yb.x * kCode1), m = two(ya.y, yb.y);
+                        F2 z[4][2];  // [word][dimension of it]
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t y = t == 0 ? w[j] : w[j] >> 8;
+                            const float2 a = f16_pair(y & kNibbles0), e = f16_pair(y & kNibbles1);
+                            z[j][0] = fma(two(a.x, a.y), s0, m);
+                            z[j][1] = fma(two(e.x, e.y), s1, m);
+                        }
+                        const int32_t pos = t0 + 4 * q + t;
+                        T *to = dst + pos * x.row + h * kBlockDims + 4 * g;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            if (pos + u < lo || pos + u >= hi) continue;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                F2 o[2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const float2 a = apart(z[2 * half + j][0]), e = apart(z[2 * half + j][1]);
+                                    o[j] = two(u ? a.y : a.x, u ? e.y : e.x);
+                                }
+                                store_values<4>(to + u * x.row + 32 * half, o);
+                            }
                         }
                     }
-                    if (pos >= lo && pos < hi) store_values<16>(dst + static_cast<int64_t>(pos) * x.row + h * kBlockDims + 16 * q, o);
-                }
-            } else {
-                float o[4][2][4];  // [token][half of the 64][dimension]
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t f[4];
-                    nibble_pairs(w[j], f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // tokens 2 (i / 2) and the next, dimension i % 2 of the word
-                        const float2 y = f16_pair(f[i]);
-                        const int t = i & 2, d = 2 * (j & 1) + (i & 1);
-                        o[t][j >> 1][d] = value(y.x, i & 1 ? kCode1 : kCode0, sc[h][t]);
-                        o[t + 1][j >> 1][d] = value(y.y, i & 1 ? kCode1 : kCode0, sc[h][t + 1]);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int32_t pos = t0 + 4 * q + t;
-                    if (pos < lo || pos >= hi) continue;
-                    T *to = dst + static_cast<int64_t>(pos) * x.row + h * kBlockDims + 4 * g;
-                    store_values<4>(to, o[t][0]);
-                    store_values<4>(to + 32, o[t][1]);
                 }
             }
         }
@@ -389,7 +417,11 @@ cudaError_t launch_kv_gather4(const KvView &b, int head_dim, lora_dtype_t dtype,
                               cudaStream_t stream) {
     auto *kernel = dtype == LORA_FP32 ? (head_dim == 64 ? kv_gather4_kernel<float, 64> : kv_gather4_kernel<float, 128>)
                                       : (head_dim == 64 ? kv_gather4_kernel<__nv_bfloat16, 64> : kv_gather4_kernel<__nv_bfloat16, 128>);
-    kernel<<<pieces_grid(b), 128, 0, stream>>>(b, k, v);
+    // one turn a warp while that is less than the machine has room for four times over
+    dim3 grid = pieces_grid(b);
+    const unsigned enough = static_cast<unsigned>(device_sm_count()) * 8 * 4;
+    while (grid.y > 1 && static_cast<uint64_t>(grid.x) * ((grid.y + 1) / 2) >= enough) grid.y = (grid.y + 1) / 2;
+    kernel<<<grid, 128, 0, stream>>>(b, k, v);
     count_launches(1);
     return cudaGetLastError();
 }

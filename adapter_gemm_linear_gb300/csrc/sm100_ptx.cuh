@@ -361,6 +361,19 @@ __device__ __forceinline__ void bulk_wait_group_read() {
 // Wait until all of this thread's bulk groups have completed.
 __device__ __forceinline__ void bulk_wait_group_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// 32 bytes to global memory (16-byte aligned), a whole sector at once where the address is a
+// multiple of 32: where every lane writes a row of its own.
+__device__ __forceinline__ void store_32(void *p, const uint32_t (&w)[8]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // ---------------------------------------------------------------- descriptors
 
 // Shared-memory matrix descriptor of a K-major operand tile stored with the
