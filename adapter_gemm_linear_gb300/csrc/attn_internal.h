@@ -47,6 +47,7 @@ struct NormRopeView {
     float eps;
     int32_t weight_fp32, unit_offset;
     int32_t q_groups, k_groups;  // of a block, per row
+    int32_t turns, passes, per_turn;  // of a block; over a row; heads of a group and turn
 };
 
 struct AttnView {
