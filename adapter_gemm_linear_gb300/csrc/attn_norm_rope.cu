@@ -82,13 +82,15 @@ __device__ __forceinline__ uint4 pack2(const F2 (&v)[VecTraits<T>::kElems / 2]) 
 
 // What a thread has to know of its place: lane c of a group of L, the group's
 // tensor and heads h0, h0 + step, ... of it.
+// LT: L where it is known to the compiler, or 0.
+template <int LT>
 struct Group {
     bool is_k;
     int32_t c, h0, step, heads;
     uint32_t mask;  // of the group's lanes
 
     __device__ __forceinline__ Group(const NormRopeView &a) {
-        const int32_t L = blockDim.x, j = threadIdx.y;
+        const int32_t L = lanes(), j = threadIdx.y;
         c = threadIdx.x;
         is_k = j >= a.q_groups;
         h0 = is_k ? j - a.q_groups : j;
@@ -97,34 +99,40 @@ struct Group {
         const uint32_t lane = ((threadIdx.z * blockDim.y + j) * L + c) & 31u;
         mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~static_cast<uint32_t>(L - 1));
     }
+    static __device__ __forceinline__ int32_t lanes() { return LT ? LT : static_cast<int32_t>(blockDim.x); }
     __device__ __forceinline__ float sum(F2 x2) const {
         const float2 y = apart(x2);
         float x = y.x + y.y;
-        for (int32_t o = blockDim.x >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+        if constexpr (LT > 0) {
+#pragma unroll
+            for (int o = LT / 2; o > 0; o /= 2) x += __shfl_xor_sync(mask, x, o);
+        } else {
+            for (int32_t o = lanes() >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+        }
         return x;
     }
 };
 
 // A thread's chunks of a head, NC at most: chunk c, then c + L.  A chunk has two
 // pieces u and v of N value pairs; one past the rotated dimensions has no v (zeros).
-template <typename T, int NC>
+template <typename T, int NC, int LT>
 struct Chunks {
     static constexpr int VE = VecTraits<T>::kElems, N = VE / 2;
     Chunk at[NC];
     bool has[NC];
 
-    __device__ __forceinline__ Chunks(const NormRopeView &a, const Group &g) {
+    __device__ __forceinline__ Chunks(const NormRopeView &a, const Group<LT> &g) {
         const int32_t count = a.rope.rot_dim / (2 * VE) + (a.rope.head_dim - a.rope.rot_dim) / VE;
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-            const int32_t c = g.c + n * static_cast<int32_t>(blockDim.x);
+            const int32_t c = g.c + n * Group<LT>::lanes();
             has[n] = c < count;
             at[n] = chunk_at<VE>(a.rope, has[n] ? c : 0);
             at[n].turn = at[n].turn && has[n];  // (a lane without a chunk has no angles)
         }
     }
     // W of the chunks; 1 without a weight
-    __device__ __forceinline__ void weights(const NormRopeView &a, const Group &g, F2 (&w)[NC][2][N]) const {
+    __device__ __forceinline__ void weights(const NormRopeView &a, const Group<LT> &g, F2 (&w)[NC][2][N]) const {
         const void *p = g.is_k ? a.k_weight : a.q_weight;
         const float add = a.unit_offset ? 1.0f : 0.0f;
 #pragma unroll
@@ -153,11 +161,11 @@ struct Chunks {
             }
     }
     // Cosines and sines of the chunks' pairs in a row: 1 and 0 for what is not turned.
-    __device__ __forceinline__ void angles(const NormRopeView &a, const Group &g, int64_t row, float (&cs)[NC][VE], float (&sn)[NC][VE]) const {
+    __device__ __forceinline__ void angles(const NormRopeView &a, const Group<LT> &g, int64_t row, float (&cs)[NC][VE], float (&sn)[NC][VE]) const {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             uint32_t still = (1u << VE) - 1u;
-            if (at[n].turn) still = load_angles<VE>(a.rope, g.c + n * static_cast<int32_t>(blockDim.x), row, cs[n], sn[n]);
+            if (at[n].turn) still = load_angles<VE>(a.rope, g.c + n * Group<LT>::lanes(), row, cs[n], sn[n]);
             if (__builtin_expect(still == 0, 1)) continue;
 #pragma unroll
             for (int e = 0; e < VE; ++e)
@@ -219,13 +227,13 @@ __device__ __forceinline__ void turned(const F2 (&u)[N], const F2 (&v)[N], const
 }
 
 // Few rows: a group has a head or a few of one row, and no more.
-template <typename T, int NC, bool INTER>
+template <typename T, int NC, bool INTER, int LT>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const __grid_constant__ NormRopeView a) {
     constexpr int VE = VecTraits<T>::kElems, N = VE / 2;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.z + threadIdx.z;
     if (row >= a.rope.rows) return;
-    const Group g(a);
-    const Chunks<T, NC> ch(a, g);
+    const Group<LT> g(a);
+    const Chunks<T, NC, LT> ch(a, g);
     const HeadsView &in = g.is_k ? a.rope.k : a.rope.q, &out = g.is_k ? a.rope.k_out : a.rope.q_out;
     F2 A[NC][2][N], B[NC][2][N];
     const float inv_d = 1.0f / static_cast<float>(a.rope.head_dim);
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const __grid
 // heads of 128 and their gradient.)
 constexpr int kStages = 2;
 
-template <typename T, int NC, int P>
+template <typename T, int NC, int P, int LT>
 struct RowPipe {
     static constexpr int VE = VecTraits<T>::kElems;
     static constexpr int kPieces = P * NC * 2;  // 16 bytes each, of a thread and head: [tensor][chunk][piece]
@@ -276,8 +284,8 @@ struct RowPipe {
         int32_t pass;
     };
     const NormRopeView &a;
-    const Group &g;
-    const Chunks<T, NC> &ch;
+    const Group<LT> &g;
+    const Chunks<T, NC, LT> &ch;
     uint32_t ring;  // [stage][head][thread][piece]: the thread's first; pieces in an order that keeps 8 threads off each other's banks
     float *angles;  // [stage, one more][row of the block][cosines, sines][pair]
     int32_t threads, half, pos[LORA_ROPE_MAX_AXES];
@@ -287,17 +295,20 @@ struct RowPipe {
     uint32_t at;
     int32_t h, h_ahead;
     const T *src[P];
+    int64_t src_step[P];  // from a head of the thread's to its next
 
-    __device__ __forceinline__ RowPipe(const NormRopeView &v, const Group &group, const Chunks<T, NC> &c, unsigned char *smem)
+    __device__ __forceinline__ RowPipe(const NormRopeView &v, const Group<LT> &group, const Chunks<T, NC, LT> &c, const HeadsView (&in)[P], unsigned char *smem)
         : a(v), g(group), ch(c) {
-        threads = blockDim.x * blockDim.y * blockDim.z;
-        const uint32_t tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x;
+        threads = Group<LT>::lanes() * blockDim.y * blockDim.z;
+        const uint32_t tid = (threadIdx.z * blockDim.y + threadIdx.y) * Group<LT>::lanes() + threadIdx.x;
         ring = sm100::smem_u32(smem) + tid * (kPieces * 16) + (tid / (8 / kPieces) % kPieces) * 16;
         angles = reinterpret_cast<float *>(smem + row_pipe_ring_bytes(threads, a.per_turn, P * NC));
         half = a.rope.rot_dim / 2;
         fetches = threadIdx.y == 0;
         now.row = ahead.row = static_cast<int64_t>(blockIdx.x) * blockDim.z + threadIdx.z;
         now.pass = ahead.pass = 0;
+#pragma unroll
+        for (int p = 0; p < P; ++p) src_step[p] = g.step * in[p].head;
     }
     __device__ __forceinline__ void next(Turn &t) const {
         if (++t.pass < a.passes) return;
@@ -326,7 +337,7 @@ struct RowPipe {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             if (!ch.at[n].turn) continue;
-            const int32_t c = g.c + n * static_cast<int32_t>(blockDim.x), axis = a.rope.chunk_axis[c];
+            const int32_t c = g.c + n * Group<LT>::lanes(), axis = a.rope.chunk_axis[c];
             const bool one = axis < LORA_ROPE_MAX_AXES;  // the chunk's pairs follow one axis
             int32_t p = one ? position(axis, row) : 0;
 #pragma unroll 1
@@ -357,12 +368,12 @@ struct RowPipe {
 #pragma unroll
         for (int p = 0; p < P; ++p) src[p] = head_at<T>(in[p], ahead.row, h_ahead);
     }
-    __device__ __forceinline__ void next_head(const HeadsView (&in)[P]) {
+    __device__ __forceinline__ void next_head() {
         at += threads * (kPieces * 16);
         h += g.step;
         h_ahead += g.step;
 #pragma unroll
-        for (int p = 0; p < P; ++p) src[p] += g.step * in[p].head;
+        for (int p = 0; p < P; ++p) src[p] += src_step[p];
     }
     __device__ __forceinline__ uint32_t piece(int p, int n, int k) const { return at ^ (((p * NC + n) * 2 + k) * 16); }
     __device__ __forceinline__ bool here() const { return now.row < a.rope.rows && h < g.heads; }
@@ -381,7 +392,7 @@ struct RowPipe {
             read_positions(ahead.row);
             fetch_angles(ahead.row, s);
             first_head(in, s);
-            for (int32_t i = 0; i < a.per_turn; ++i, next_head(in)) fetch_head();
+            for (int32_t i = 0; i < a.per_turn; ++i, next_head()) fetch_head();
             asm volatile("cp.async.commit_group;" ::: "memory");
             next(ahead);
         }
@@ -407,7 +418,7 @@ struct RowPipe {
         unpack2<T>(y, v);
     }
     __device__ __forceinline__ void take_angles(const float *from, int n, float (&cs)[VE], float (&sn)[VE]) const {
-        const int32_t c = (g.c + n * static_cast<int32_t>(blockDim.x)) * VE;
+        const int32_t c = (g.c + n * Group<LT>::lanes()) * VE;
 #pragma unroll
         for (int e = 0; e < VE; e += 4) {
             float4 x = make_float4(1.0f, 1.0f, 1.0f, 1.0f), y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -422,14 +433,15 @@ struct RowPipe {
     __device__ __forceinline__ float *after_angles() const { return angles + (kStages + 1) * blockDim.z * 2 * half; }
 };
 
-template <typename T, int NC, bool INTER>
+template <typename T, int NC, bool INTER, int LT>
 __global__ void __launch_bounds__(kRowThreads) norm_rope_rows_kernel(const __grid_constant__ NormRopeView a) {
     constexpr int VE = VecTraits<T>::kElems, N = VE / 2;
     extern __shared__ __align__(16) unsigned char smem[];
-    const Group g(a);
-    const Chunks<T, NC> ch(a, g);
-    RowPipe<T, NC, 1> pipe(a, g, ch, smem);
+    const Group<LT> g(a);
+    const Chunks<T, NC, LT> ch(a, g);
     const HeadsView in[1] = {g.is_k ? a.rope.k : a.rope.q}, &out = g.is_k ? a.rope.k_out : a.rope.q_out;
+    RowPipe<T, NC, 1, LT> pipe(a, g, ch, in, smem);
+    const int64_t out_step = g.step * out.head;
     const float inv_d = 1.0f / static_cast<float>(a.rope.head_dim);
     pipe.begin(in);
     F2 W[NC][2][N];
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_rows_kernel(const __gri
             coefficients<VE, NC, INTER>(W, cs, sn, A, B);
         }
         T *dst = head_at<T>(out, pipe.now.row, pipe.h);
-        for (int32_t i = 0; i < a.per_turn; ++i, pipe.next_head(in), dst += g.step * out.head) {
+        for (int32_t i = 0; i < a.per_turn; ++i, pipe.next_head(), dst += out_step) {
             if (!pipe.here()) {
                 pipe.fetch_head();
                 continue;
@@ -473,14 +485,16 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_rows_kernel(const __gri
 
 // A thread adds up its chunks' gradients of the weights over all its rows and heads, a
 // block over its groups, grad_weights_kernel over the blocks: every sum's order is fixed.
-template <typename T, int NC, bool INTER>
+template <typename T, int NC, bool INTER, int LT>
 __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(const __grid_constant__ NormRopeView a) {
     constexpr int VE = VecTraits<T>::kElems, N = VE / 2;
     extern __shared__ __align__(16) unsigned char smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Group g(a);
-    const Chunks<T, NC> ch(a, g);
-    RowPipe<T, NC, 2> pipe(a, g, ch, smem);
+    const Group<LT> g(a);
+    const Chunks<T, NC, LT> ch(a, g);
+    const HeadsView in[2] = {g.is_k ? a.rope.k : a.rope.q, g.is_k ? a.dk : a.dq}, &out = g.is_k ? a.rope.k_out : a.rope.q_out;
+    RowPipe<T, NC, 2, LT> pipe(a, g, ch, in, smem);
+    const int64_t out_step = g.step * out.head;
     // the weights lie in shared memory, and angles and weights are read where they are used:
     // registers are short, and with most of the L1 taken spilled ones cost a trip to the L2
     float *const weights = pipe.after_angles() + (g.is_k ? a.rope.head_dim : 0);
@@ -495,7 +509,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(cons
                 if (ch.at[n].turn) *reinterpret_cast<F2 *>(weights + ch.at[n].d1 + 2 * i) = W[n][1][i];
             }
     }
-    const HeadsView in[2] = {g.is_k ? a.rope.k : a.rope.q, g.is_k ? a.dk : a.dq}, &out = g.is_k ? a.rope.k_out : a.rope.q_out;
     const float inv_d = 1.0f / static_cast<float>(a.rope.head_dim);
     pipe.begin(in);
     F2 dw[NC][2][N];
@@ -508,7 +521,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(cons
         pipe.first_head(in, turn % kStages);
         const float *const angles = pipe.angle_at(turn % (kStages + 1));
         T *dst = head_at<T>(out, pipe.now.row, pipe.h);
-        for (int32_t i = 0; i < a.per_turn; ++i, pipe.next_head(in), dst += g.step * out.head) {
+        for (int32_t i = 0; i < a.per_turn; ++i, pipe.next_head(), dst += out_step) {
             if (!pipe.here()) {
                 pipe.fetch_head();
                 continue;
@@ -521,7 +534,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(cons
             }
             pipe.fetch_head();
             F2 squares = two(0.0f, 0.0f), dot = two(0.0f, 0.0f);
-            const F2 minus = two(-1.0f, -1.0f);
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+#pragma unroll
+                for (int e = 0; e < N; ++e) squares = fma(u[n][e], u[n][e], fma(v[n][e], v[n][e], squares));
+            const float r = rsqrtf(fmaf(g.sum(squares), inv_d, a.eps));
+            const F2 r2 = two(r, r), minus = two(-1.0f, -1.0f);
             // y and z become g turned back, h
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
@@ -529,7 +547,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(cons
                 pipe.take_angles(angles, n, cs, sn);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    squares = fma(u[n][e], u[n][e], fma(v[n][e], v[n][e], squares));
                     const F2 y0 = y[n][e], z0 = z[n][e];
                     F2 c[2], t[2];
 #pragma unroll
@@ -542,8 +559,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(cons
                     z[n][e] = INTER ? fma(swapped(z0), t[1], mul(z0, c[1])) : fma(mul(y0, t[1]), minus, mul(z0, c[1]));
                 }
             }
-            const float r = rsqrtf(fmaf(g.sum(squares), inv_d, a.eps));
-            const F2 r2 = two(r, r);
             // their part in the weights' gradients; then a = h W
 #pragma unroll
             for (int n = 0; n < NC; ++n)
@@ -689,18 +704,20 @@ cudaError_t forward_typed(NormRopeView v, cudaStream_t stream) {
     count_launches(1);
     const bool second = sizeof(T) == 4 && s.chunks > 32;  // (a bf16 head has 31 chunks at most)
     if (!s.many) {
-        auto *kernel = norm_rope_kernel<T, 1, INTER>;
+        auto *kernel = norm_rope_kernel<T, 1, INTER, 0>;
         if constexpr (sizeof(T) == 4)
-            if (second) kernel = norm_rope_kernel<T, 2, INTER>;
+            if (second) kernel = norm_rope_kernel<T, 2, INTER, 0>;
         kernel<<<static_cast<unsigned>(s.row_tiles), s.block, 0, stream>>>(v);
         return cudaGetLastError();
     }
-    static uint64_t ctx[2][128] = {};
+    // (groups of 8 lanes, a head of 128 in bf16, in kernels of their own)
+    static uint64_t ctx[3][128] = {};
     const Rows r = plan_rows(v, s, second ? 2 : 1, kRowCtas);
-    auto *kernel = norm_rope_rows_kernel<T, 1, INTER>;
+    const int which = second ? 2 : s.block.x == 8;
+    auto *kernel = which == 1 ? norm_rope_rows_kernel<T, 1, INTER, 8> : norm_rope_rows_kernel<T, 1, INTER, 0>;
     if constexpr (sizeof(T) == 4)
-        if (second) kernel = norm_rope_rows_kernel<T, 2, INTER>;
-    const cudaError_t e = allow_smem(kernel, 227 * 1024, ctx[second]);
+        if (second) kernel = norm_rope_rows_kernel<T, 2, INTER, 0>;
+    const cudaError_t e = allow_smem(kernel, 227 * 1024, ctx[which]);
     if (e != cudaSuccess) return e;
     kernel<<<r.grid, s.block, r.smem, stream>>>(v);
     return cudaGetLastError();
@@ -711,14 +728,15 @@ cudaError_t backward_typed(NormRopeView v, float *dq_weight, float *dk_weight, c
     constexpr int VE = VecTraits<T>::kElems;
     const Shape s = plan<VE>(v, true, kRowThreads);
     if (!dq_weight && !dk_weight) v.partial = nullptr;
-    static uint64_t ctx[2][128] = {};
+    static uint64_t ctx[3][128] = {};
     const bool second = sizeof(T) == 4 && s.chunks > 32;
     const Rows r = plan_rows(v, s, second ? 4 : 2, kGradCtas);
     const int32_t grid = r.grid, D = v.rope.head_dim;
-    auto *kernel = norm_rope_backward_kernel<T, 1, INTER>;
+    const int which = second ? 2 : s.block.x == 8;
+    auto *kernel = which == 1 ? norm_rope_backward_kernel<T, 1, INTER, 8> : norm_rope_backward_kernel<T, 1, INTER, 0>;
     if constexpr (sizeof(T) == 4)
-        if (second) kernel = norm_rope_backward_kernel<T, 2, INTER>;
-    cudaError_t e = allow_smem(kernel, 227 * 1024, ctx[second]);
+        if (second) kernel = norm_rope_backward_kernel<T, 2, INTER, 0>;
+    cudaError_t e = allow_smem(kernel, 227 * 1024, ctx[which]);
     if (e != cudaSuccess) return e;
     kernel<<<grid, s.block, r.smem, stream>>>(v);
     e = cudaGetLastError();
