@@ -26,8 +26,8 @@ namespace {
 
 constexpr int kNormMaxThreads = 512, kRowThreads = 256;  // of a block, at most: for few rows, and for many
 constexpr int kNormThreads = 128;                        // and about
-constexpr int kNormHeads = 4;                            // of a group and turn, where there is much work
-constexpr int kRowCtas = 4, kGradCtas = 3;               // blocks per SM, at most
+constexpr int kNormHeads = 3;                            // of a group and turn, where there is much work
+constexpr int kRowCtas = 3, kGradCtas = 2;               // blocks per SM, at most
 
 // 16-byte pieces on their way, two stages of: threads x heads x (tensors x chunks) x 2 pieces.
 __host__ __device__ constexpr size_t row_pipe_ring_bytes(int threads, int heads, int chunks) {
@@ -673,7 +673,7 @@ Shape plan(NormRopeView &v, bool in_turns, int max_threads) {
     s.row_tiles = (static_cast<int64_t>(v.rope.rows) + s.block.z - 1) / s.block.z;
     int32_t heads = (qh + v.q_groups - 1) / v.q_groups;  // of a group, at most
     if (kh > 0) heads = std::max(heads, (kh + v.k_groups - 1) / v.k_groups);
-    const int32_t limit = s.chunks > 32 ? kNormHeads / 2 : kNormHeads;
+    const int32_t limit = s.chunks > 32 ? (kNormHeads + 1) / 2 : kNormHeads;
     v.passes = (heads + limit - 1) / limit;
     v.per_turn = (heads + v.passes - 1) / v.passes;
     return s;

@@ -313,17 +313,23 @@ __device__ __forceinline__ void issue_scores(PrefillSmem<D, FMT> &sm, uint32_t X
 // Of the 4-bit cache: K's value s code + m = (code - 8) s_a + (code - 8) s_b + (m + 8 s), s_a
 // the upper seven bits of s and s_b the rest, so that both products are f16 values
 // exactly: two tiles.  The last term is one column for all dimensions of a block,
-// against the sum of q over them, which has two f16 parts: m and 8 s twice each.
+// against the sum of q over them, which has two f16 parts: m and 8 s twice each.  There is
+// room for one stage of the two tiles; each is given back and filled anew by itself
+// (barriers 0 and 1 of k_full and k_empty), so that the first of the next keys is there
+// when the last product with the second of these ends: 2048 queries on 34816 keys XXX us
+// instead of 1189.
 template <int D>
-__device__ __forceinline__ void issue_scores(PrefillSmem<D, LORA_KV_UINT4> &sm, uint32_t X) {
+__device__ __forceinline__ void issue_scores_part(PrefillSmem<D, LORA_KV_UINT4> &sm, uint32_t X, uint32_t part) {
     const uint64_t q = desc_kmajor_sw128(smem_u32(sm.q[0])) + X * (sizeof(sm.q[0]) >> 4);
-    const uint64_t k = desc_kmajor_sw128(smem_u32(sm.k[0]));
-    const uint64_t qx = desc_kmajor_sw32(smem_u32(sm.qx[0])) + X * (sizeof(sm.qx[0]) >> 4);
-    mma_bf16_f32(X * 128, qx, desc_kmajor_sw32(smem_u32(sm.kx)), idesc_f16_f32(kHalf, kKeys), 0);
+    const uint64_t k = desc_kmajor_sw128(smem_u32(sm.k[0])) + part * (sizeof(sm.k[0]) >> 4);
+    if (part == 0) {
+        const uint64_t qx = desc_kmajor_sw32(smem_u32(sm.qx[0])) + X * (sizeof(sm.qx[0]) >> 4);
+        mma_bf16_f32(X * 128, qx, desc_kmajor_sw32(smem_u32(sm.kx)), idesc_f16_f32(kHalf, kKeys), 0);
+    }
 #pragma unroll
-    for (int i = 0; i < 2 * (D / 16); ++i) {
-        const uint32_t at = (i % (D / 16) / 4) * (kHalf * 128 >> 4) + (i % 4) * 2;
-        mma_bf16_f32(X * 128, q + at, k + at + i / (D / 16) * (sizeof(sm.k[0]) >> 4), idesc_f16_f32(kHalf, kKeys), 1);
+    for (int i = 0; i < D / 16; ++i) {
+        const uint32_t at = (i / 4) * (kHalf * 128 >> 4) + (i % 4) * 2;
+        mma_bf16_f32(X * 128, q + at, k + at, idesc_f16_f32(kHalf, kKeys), 1);
     }
 }
 
@@ -861,13 +867,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             look(nxt, n_tile + 1);
             const bool more = nxt.key0 >= 0;
             // K: row = key, 16 dimensions of one key a piece
-            wait(&sm.k_empty[U4 ? 0 : stage], (U4 ? stage : ph) ^ 1u, 61);
+            if (!U4) wait(&sm.k_empty[stage], ph ^ 1u, 61);
             landed();
             uint8_t *kdst = sm.k[stage] + k_at;
             if constexpr (U4) {
                 __syncwarp();  // every lane's copies
                 if (more) fetch_scales(nxt, n_tile + 1);
                 const uint32_t *const sc = sm.meta[n_tile & 1][wq];
+                uint4 c[NL];
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    c[i] = kc[128 * i];
+                    if (more) fetch_k(nxt, i);
+                }
+                wait(&sm.k_empty[0], stage ^ 1u, 61);
                 uint32_t w[4] = {0u, 0u, 0u, 0u};  // a key a lane: least values, and 8 scales
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
@@ -876,30 +889,35 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     w[2 * h + 1] = times(__byte_perm(y, y, 0x1010), 0x48004800u);
                 }
                 extra(sm.kx, wq * 32 + lane, w);
-                // a piece: 16 dimensions of keys `tok` and tok + 2 of 16
+                // a piece: 16 dimensions of keys `tok` and tok + 2 of 16, times the upper (part 0) or lower bits of the scale
                 const int tok = k_token(kr);
-                uint8_t *const row = sm.k[0] + (wq * 32 + tok) * 128;
                 const int x7 = tok & 7;
-#pragma unroll 2
-                for (int i = 0; i < NL; ++i) {
-                    const uint4 r = kc[128 * i];
-                    if (more) fetch_k(nxt, i);
-                    const uint32_t c[4] = {r.x, r.y, r.z, r.w};
-                    uint8_t *const dst = row + (i / H) * (kKvTile * 128) + i % H * kRowAtom;
+                auto convert_k = [&](int part) {
+                    uint8_t *const row = sm.k[part] + (wq * 32 + tok) * 128;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t y = sc[(i / H * 2 * H + i % H) * kKvTile + tok + 2 * t], s2 = __byte_perm(y, y, 0x1010);
-                        const uint32_t sa = s2 & 0xFFF0FFF0u, sb = less(s2, sa);
+                    for (int i = 0; i < NL; ++i) {
+                        const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+                        uint8_t *const dst = row + (i / H) * (kKvTile * 128) + i % H * kRowAtom;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t f[4];
-                            nibbles_less<8>(c[2 * t + k], f);
-                            uint4 *const to = reinterpret_cast<uint4 *>(dst + t * 256 + (((2 * kp + k) ^ (x7 + 2 * t)) << 4));
-                            to[0] = make_uint4(times(f[0], sa), times(f[1], sa), times(f[2], sa), times(f[3], sa));
-                            to[sizeof(sm.k[0]) / 16] = make_uint4(times(f[0], sb), times(f[1], sb), times(f[2], sb), times(f[3], sb));
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t y = sc[(i / H * 2 * H + i % H) * kKvTile + tok + 2 * t], s2 = __byte_perm(y, y, 0x1010);
+                            const uint32_t sa = s2 & 0xFFF0FFF0u, by = part == 0 ? sa : less(s2, sa);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t f[4];
+                                nibbles_less<8>(words[2 * t + k], f);
+                                *reinterpret_cast<uint4 *>(dst + t * 256 + (((2 * kp + k) ^ (x7 + 2 * t)) << 4)) =
+                                    make_uint4(times(f[0], by), times(f[1], by), times(f[2], by), times(f[3], by));
+                            }
                         }
                     }
-                }
+                };
+                convert_k(0);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.k_full[0]);
+                wait(&sm.k_empty[1], stage ^ 1u, 63);
+                convert_k(1);
             } else {
 #pragma unroll 2
             for (int i = 0; i < NL; ++i) {
@@ -918,7 +936,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             fetched();
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.k_full[U4 ? 0 : stage]);
+            if (lane == 0) mbar_arrive(&sm.k_full[U4 ? 1 : stage]);
             const bool first = cur.n > 0;  // tile of an item: its queries, on their way while V is converted
             if (first) fetch_q(cur, 0);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
@@ -1043,13 +1061,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             };
             uint32_t n_item = 0, n_tile = 0, n_b = 0, n_qb = 0;
             // (Tensor Memory begins at column 0: the CTA has all of it)
-            auto scores = [&](uint32_t X, uint32_t stage) {
-                if (elect_one()) {
-                    if constexpr (U4) issue_scores(sm, X);
-                    else issue_scores(sm, X, stage);
-                    mma_commit(&sm.s_full[X]);
+            // (of key tile n, which the first of them waits for; the last gives K back)
+            auto scores = [&](uint32_t X, uint32_t n, bool first, bool last) {
+                if constexpr (U4) {
+#pragma unroll 1
+                    for (uint32_t part = 0; part < 2; ++part) {
+                        if (first) wait(&sm.k_full[part], n & 1u, 72);
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            issue_scores_part(sm, X, part);
+                            if (part == 1) mma_commit(&sm.s_full[X]);
+                            if (last) mma_commit(&sm.k_empty[part]);
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    if (elect_one()) {
+                        issue_scores(sm, X, n & 1u);
+                        mma_commit(&sm.s_full[X]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             };
             while (true) {
                 const uint32_t e = n_item % kItemRing;
@@ -1059,17 +1091,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 __syncwarp();
                 if (elect_one()) mbar_arrive(&sm.item_empty[e]);
                 if (any_dead() || stop) break;
-                wait(&sm.k_full[U4 ? 0u : n_tile & 1u], (U4 ? n_tile : n_tile >> 1) & 1u, 72);
+                if (!U4) wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
 #pragma unroll 1
                 for (uint32_t X = 0; X < nx; ++X) {
                     wait(&sm.q_full[X], (X ? n_qb : n_item) & 1u, 71);
                     tc_fence_after_sync();
-                    scores(X, n_tile & 1u);
+                    scores(X, n_tile, X == 0, X + 1 == nx);
                     if (nt == 1) commit(&sm.q_empty[X]);
                 }
                 ++n_item;
                 n_qb += nx - 1;
-                commit(&sm.k_empty[U4 ? 0u : n_tile & 1u]);
+                if (!U4) commit(&sm.k_empty[n_tile & 1u]);
 #pragma unroll 1
                 for (int32_t j = 0; j < nt; ++j, ++n_tile) {
                     const uint32_t st = n_tile & 1u, ph = (n_tile >> 1) & 1u;
@@ -1089,9 +1121,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             __syncwarp();
                         }
                         if (more) {
-                            if (X == 0) wait(&sm.k_full[U4 ? 0u : st1], U4 ? st1 : ph1, 76);
+                            if (!U4 && X == 0) wait(&sm.k_full[st1], ph1, 76);
                             tc_fence_after_sync();
-                            scores(X, st1);
+                            scores(X, n_tile + 1, X == 0, X + 1 == nx);
                             if (j + 2 == nt) commit(&sm.q_empty[X]);
                         } else {
                             commit(&sm.o_done[X]);
@@ -1100,7 +1132,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     n_b += nx - 1;
                     commit(&sm.v_empty[st]);
                     commit(&sm.tile_empty[n_tile % kTileRing]);  // (the softmax has read its scales)
-                    if (more) commit(&sm.k_empty[U4 ? 0u : st1]);
+                    if (!U4 && more) commit(&sm.k_empty[st1]);
                 }
             }
             // nothing of this thread's may be in flight when Tensor Memory is freed
