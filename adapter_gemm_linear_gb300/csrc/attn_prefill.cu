@@ -316,7 +316,7 @@ __device__ __forceinline__ void issue_scores(PrefillSmem<D, FMT> &sm, uint32_t X
 // against the sum of q over them, which has two f16 parts: m and 8 s twice each.  There is
 // room for one stage of the two tiles; each is given back and filled anew by itself
 // (barriers 0 and 1 of k_full and k_empty), so that the first of the next keys is there
-// when the last product with the second of these ends: 2048 queries on 34816 keys XXX us
+// when the last product with the second of these ends: 2048 queries on 34816 keys 1137 us
 // instead of 1189.
 template <int D>
 __device__ __forceinline__ void issue_scores_part(PrefillSmem<D, LORA_KV_UINT4> &sm, uint32_t X, uint32_t part) {
@@ -370,11 +370,13 @@ __device__ __noinline__ uint32_t nan_dims(const KvView &b, int32_t seq, int32_t 
 
 // ---------------------------------------------------------------- kernel
 
-template <int D, int FMT>
+// PARTS (4-bit cache): K in two parts, exactly; else its values rounded to f16.
+template <int D, int FMT, bool PARTS>
 __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __grid_constant__ AttnView a) {
     extern __shared__ __align__(1024) unsigned char raw[];
     PrefillSmem<D, FMT> &sm = *reinterpret_cast<PrefillSmem<D, FMT> *>(raw);
     constexpr bool U4 = FMT == LORA_KV_UINT4;
+    static_assert(U4 || !PARTS, "parts of 4-bit values");
     constexpr int H = D / kBlockDims;
     constexpr uint32_t kRowAtom = kHalf * 128;    // bytes of one atom of 128 rows
     constexpr uint32_t kVAtom = D * 128;          // bytes of 64 keys of V
@@ -811,8 +813,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             fetched();
         };
         // ... and turned in place into f16 times a power of two per row (its
-        // largest value in [2^13, 2^14); with the 4-bit cache [2^7, 2^8), so that
-        // the sums of 64 are f16 values too), a row a lane.
+        // largest value in [2^13, 2^14); with K in parts [2^7, 2^8), so that the sums
+        // of 64 are f16 values too), a row a lane.
         auto convert_q = [&](int X) {
             __syncwarp();  // every lane's copies
             float amax = 0.0f;
@@ -824,7 +826,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 for (int k = 0; k < 4; ++k)
                     amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
             }
-            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - (U4 ? 7 : 13);
+            int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - (PARTS ? 7 : 13);
             e = amax < INFINITY ? max(e, -126) : 0;
             const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
             sm.q_exponent[n_q & 1u][X * kHalf + wq * 32 + lane] = static_cast<int8_t>(e);
@@ -843,7 +845,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     sum += x0 + x1;
                 }
                 *at = make_uint4(h[0], h[1], h[2], h[3]);
-                if constexpr (U4) {
+                if constexpr (PARTS) {
                     if (i % 8 == 7) {
                         const float hi = __half2float(__float2half_rn(sum));
                         sums[2 * (i / 8)] = sums[2 * (i / 8) + 1] = pack_h2(hi, sum - hi);
@@ -851,7 +853,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     }
                 }
             }
-            if constexpr (U4) extra(sm.qx[X], wq * 32 + lane, sums);
+            if constexpr (PARTS) extra(sm.qx[X], wq * 32 + lane, sums);
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_full[X]);
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             look(nxt, n_tile + 1);
             const bool more = nxt.key0 >= 0;
             // K: row = key, 16 dimensions of one key a piece
-            if (!U4) wait(&sm.k_empty[stage], ph ^ 1u, 61);
+            if (!PARTS) wait(&sm.k_empty[stage], ph ^ 1u, 61);
             landed();
             uint8_t *kdst = sm.k[stage] + k_at;
             if constexpr (U4) {
@@ -880,20 +882,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     c[i] = kc[128 * i];
                     if (more) fetch_k(nxt, i);
                 }
-                wait(&sm.k_empty[0], stage ^ 1u, 61);
-                uint32_t w[4] = {0u, 0u, 0u, 0u};  // a key a lane: least values, and 8 scales
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const uint32_t y = sc[(lane / kKvTile * 2 * H + h) * kKvTile + lane % kKvTile];
-                    w[2 * h] = __byte_perm(y, y, 0x3232);
-                    w[2 * h + 1] = times(__byte_perm(y, y, 0x1010), 0x48004800u);
-                }
-                extra(sm.kx, wq * 32 + lane, w);
-                // a piece: 16 dimensions of keys `tok` and tok + 2 of 16, times the upper (part 0) or lower bits of the scale
+                // a piece: 16 dimensions of keys `tok` and tok + 2 of 16; values, or (code - 8) times the upper
+                // (part 0) or lower bits of the scale
                 const int tok = k_token(kr);
                 const int x7 = tok & 7;
                 auto convert_k = [&](int part) {
-                    uint8_t *const row = sm.k[part] + (wq * 32 + tok) * 128;
+                    uint8_t *const row = sm.k[PARTS ? part : stage] + (wq * 32 + tok) * 128;
 #pragma unroll
                     for (int i = 0; i < NL; ++i) {
                         const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
@@ -901,23 +895,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const uint32_t y = sc[(i / H * 2 * H + i % H) * kKvTile + tok + 2 * t], s2 = __byte_perm(y, y, 0x1010);
-                            const uint32_t sa = s2 & 0xFFF0FFF0u, by = part == 0 ? sa : less(s2, sa);
+                            const uint32_t sa = s2 & 0xFFF0FFF0u, by = part == 0 ? sa : less(s2, sa), m2 = __byte_perm(y, y, 0x3232);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 uint32_t f[4];
-                                nibbles_less<8>(words[2 * t + k], f);
+                                nibbles_less<PARTS ? 8 : 0>(words[2 * t + k], f);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) f[e] = PARTS ? times(f[e], by) : times_and(f[e], s2, m2);
                                 *reinterpret_cast<uint4 *>(dst + t * 256 + (((2 * kp + k) ^ (x7 + 2 * t)) << 4)) =
-                                    make_uint4(times(f[0], by), times(f[1], by), times(f[2], by), times(f[3], by));
+                                    make_uint4(f[0], f[1], f[2], f[3]);
                             }
                         }
                     }
                 };
+                if constexpr (PARTS) {
+                    wait(&sm.k_empty[0], stage ^ 1u, 61);
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};  // a key a lane: least values, and 8 scales
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        const uint32_t y = sc[(lane / kKvTile * 2 * H + h) * kKvTile + lane % kKvTile];
+                        w[2 * h] = __byte_perm(y, y, 0x3232);
+                        w[2 * h + 1] = times(__byte_perm(y, y, 0x1010), 0x48004800u);
+                    }
+                    extra(sm.kx, wq * 32 + lane, w);
+                }
                 convert_k(0);
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.k_full[0]);
-                wait(&sm.k_empty[1], stage ^ 1u, 63);
-                convert_k(1);
+                if constexpr (PARTS) {
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.k_full[0]);
+                    wait(&sm.k_empty[1], stage ^ 1u, 63);
+                    convert_k(1);
+                }
             } else {
 #pragma unroll 2
             for (int i = 0; i < NL; ++i) {
@@ -936,7 +945,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             fetched();
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.k_full[U4 ? 1 : stage]);
+            if (lane == 0) mbar_arrive(&sm.k_full[PARTS ? 1 : stage]);
             const bool first = cur.n > 0;  // tile of an item: its queries, on their way while V is converted
             if (first) fetch_q(cur, 0);
             // V: row = dimension, 8 keys a piece; keys past the end are zeros
@@ -1063,7 +1072,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             // (Tensor Memory begins at column 0: the CTA has all of it)
             // (of key tile n, which the first of them waits for; the last gives K back)
             auto scores = [&](uint32_t X, uint32_t n, bool first, bool last) {
-                if constexpr (U4) {
+                if constexpr (PARTS) {
 #pragma unroll 1
                     for (uint32_t part = 0; part < 2; ++part) {
                         if (first) wait(&sm.k_full[part], n & 1u, 72);
@@ -1091,7 +1100,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 __syncwarp();
                 if (elect_one()) mbar_arrive(&sm.item_empty[e]);
                 if (any_dead() || stop) break;
-                if (!U4) wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
+                if (!PARTS) wait(&sm.k_full[n_tile & 1u], (n_tile >> 1) & 1u, 72);
 #pragma unroll 1
                 for (uint32_t X = 0; X < nx; ++X) {
                     wait(&sm.q_full[X], (X ? n_qb : n_item) & 1u, 71);
@@ -1101,7 +1110,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 }
                 ++n_item;
                 n_qb += nx - 1;
-                if (!U4) commit(&sm.k_empty[n_tile & 1u]);
+                if (!PARTS) commit(&sm.k_empty[n_tile & 1u]);
 #pragma unroll 1
                 for (int32_t j = 0; j < nt; ++j, ++n_tile) {
                     const uint32_t st = n_tile & 1u, ph = (n_tile >> 1) & 1u;
@@ -1121,7 +1130,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                             __syncwarp();
                         }
                         if (more) {
-                            if (!U4 && X == 0) wait(&sm.k_full[st1], ph1, 76);
+                            if (!PARTS && X == 0) wait(&sm.k_full[st1], ph1, 76);
                             tc_fence_after_sync();
                             scores(X, n_tile + 1, X == 0, X + 1 == nx);
                             if (j + 2 == nt) commit(&sm.q_empty[X]);
@@ -1132,7 +1141,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     n_b += nx - 1;
                     commit(&sm.v_empty[st]);
                     commit(&sm.tile_empty[n_tile % kTileRing]);  // (the softmax has read its scales)
-                    if (!U4 && more) commit(&sm.k_empty[st1]);
+                    if (!PARTS && more) commit(&sm.k_empty[st1]);
                 }
             }
             // nothing of this thread's may be in flight when Tensor Memory is freed
@@ -1275,16 +1284,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
     }
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool PARTS = false>
 cudaError_t prefill_typed(const AttnView &v, cudaStream_t stream) {
     static uint64_t ctx[128] = {};
     // more than half of an SM's shared memory even for D = 64: a CTA takes all of its Tensor Memory
     constexpr int smem = static_cast<int>(sizeof(PrefillSmem<D, FMT>) > 128 * 1024 ? sizeof(PrefillSmem<D, FMT>) : 128 * 1024);
     static_assert(smem <= 227 * 1024, "the shared memory of one CTA");
-    cudaError_t e = allow_smem(attn_prefill_kernel<D, FMT>, smem, ctx);
+    cudaError_t e = allow_smem(attn_prefill_kernel<D, FMT, PARTS>, smem, ctx);
     if (e != cudaSuccess) return e;
     const int grid = device_sm_count();
-    attn_prefill_kernel<D, FMT><<<grid, kPreThreads, smem, stream>>>(v);
+    attn_prefill_kernel<D, FMT, PARTS><<<grid, kPreThreads, smem, stream>>>(v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = launch_join<__nv_bfloat16, D, kRows, 1>(v, grid, kRows, stream);
@@ -1297,13 +1306,17 @@ cudaError_t prefill_typed(const AttnView &v, cudaStream_t stream) {
 size_t prefill_workspace_bytes(int head_dim) { return split_workspace_bytes(device_sm_count(), kRows, head_dim); }
 
 cudaError_t launch_attn_prefill(const AttnView &v, lora_kv_format_t fmt, int head_dim, cudaStream_t stream) {
+    if (fmt == LORA_KV_UINT4) {
+        // The scores' rounding shows in lse, which is fp32 (off by 1e-6 with K rounded), not in a
+        // bf16 result beside its own rounding (1.8e-3 from the exact one, 1.7e-3 with K in parts); in
+        // parts 2048 queries of 34816 keys (32 heads of 128, 8 of the cache) take 1137 us instead of 892.
+        if (v.lse)
+            return head_dim == 64 ? prefill_typed<64, LORA_KV_UINT4, true>(v, stream) : prefill_typed<128, LORA_KV_UINT4, true>(v, stream);
+        return head_dim == 64 ? prefill_typed<64, LORA_KV_UINT4>(v, stream) : prefill_typed<128, LORA_KV_UINT4>(v, stream);
+    }
     if (head_dim == 64)
-        return fmt == LORA_KV_INT8   ? prefill_typed<64, LORA_KV_INT8>(v, stream)
-               : fmt == LORA_KV_E4M3 ? prefill_typed<64, LORA_KV_E4M3>(v, stream)
-                                     : prefill_typed<64, LORA_KV_UINT4>(v, stream);
-    return fmt == LORA_KV_INT8   ? prefill_typed<128, LORA_KV_INT8>(v, stream)
-           : fmt == LORA_KV_E4M3 ? prefill_typed<128, LORA_KV_E4M3>(v, stream)
-                                 : prefill_typed<128, LORA_KV_UINT4>(v, stream);
+        return fmt == LORA_KV_INT8 ? prefill_typed<64, LORA_KV_INT8>(v, stream) : prefill_typed<64, LORA_KV_E4M3>(v, stream);
+    return fmt == LORA_KV_INT8 ? prefill_typed<128, LORA_KV_INT8>(v, stream) : prefill_typed<128, LORA_KV_E4M3>(v, stream);
 }
 
 }  // namespace lora

@@ -282,13 +282,13 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * up to a million keys.  Values that a query does not see have no part in this.
  * (Pages whose V scales differ by more than 2^79 within a sequence and head cost
  * time: twice as much for prompts, some ten times for few queries.)
- * LORA_KV_UINT4: K's codes enter the first product exactly, its scales and least
- * values in fp32.  So do V's in every fp32 call, and where a bf16 call takes the
- * kernel for few queries: there each p_j times the token's scale has 22 and 11 bits,
- * and is off by at most 2^-44 and 2^-33 of the row's largest such product beyond
- * that.  Where a bf16 call takes the one for many, V's values enter rounded to
- * f16 (11 bits), and a p_j is off by at most 2^-29 of the row's largest beyond
- * its 11 bits.
+ * LORA_KV_UINT4: in every fp32 call, and where a bf16 call takes the kernel for few
+ * queries, codes enter the products exactly, scales and least values in fp32: each p_j
+ * times the token's scale has 22 and 11 bits, and is off by at most 2^-44 and 2^-33 of
+ * the row's largest such product beyond that.  Where a bf16 call takes the one for many,
+ * V's values enter rounded to f16 (11 bits), and a p_j is off by at most 2^-29 of the
+ * row's largest beyond its 11 bits; K's values enter exactly if lse is given, else rounded
+ * to f16, so that `out` of the same call with and without lse may differ in its last bits.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (num_q_heads /
  * num_heads over 64; num_q_heads not a multiple; rows * num_q_heads of 2^31
  * or more), WORKSPACE, CUDA.

@@ -5,7 +5,7 @@ products apart), per row:
     bf16: 2^-8 |o| + A (2^-11 + 2^-20 (S + 16)) + n 2^-25 V;  fp32: 2^-23 |o| + A (2^-21 + 2^-20 (S + 16)) + n 2^-36 V;
     lse: 2^-20 (S + 16).
 (p' = p scale has 11 or 22 bits; the least values' sums are fp32.)  Where a call takes the kernel for many queries, V
-enters rounded to f16: the restatement rounds it so too, and |v| is that value's."""
+enters rounded to f16, and without lse K too: the restatement rounds them so too, and |v| is that value's."""
 
 import numpy as np
 import pytest
@@ -50,9 +50,17 @@ def check(cache, rng, dtype, Hq, news, table, lens, offs, causal=True, window=0,
     out, lse = cache.attention(q, dev(table), dev(lens), dev(offs) if use_offsets else None, causal=causal, window=window,
                                scale=scale, return_lse=True, max_queries=most)
     assert status() == 0
-    rounded = many_queries(dtype, T, T, Hq // cache.num_heads, cache.num_heads, table, cache.page_tokens, most)
+    many = many_queries(dtype, T, T, Hq // cache.num_heads, cache.num_heads, table, cache.page_tokens, most)
+    rounded = "v" if many else ""
     want, wl, spread, score, vmax = U.attention(ref, qd, table, lens, offs, np.float32(sm).astype(np.float64), causal, window, rounded)
     tol, ltol = bounds(dtype, want, wl, spread, score, max(lens), vmax)
+    if many:  # and without lse
+        alone = cache.attention(q, dev(table), dev(lens), dev(offs) if use_offsets else None, causal=causal, window=window,
+                                scale=scale, max_queries=most)
+        want2, wl2, spread2, score2, vmax2 = U.attention(ref, qd, table, lens, offs, np.float32(sm).astype(np.float64), causal, window, "kv")
+        err = np.abs(alone.double().cpu().numpy() - want2)
+        tol2 = bounds(dtype, want2, wl2, spread2, score2, max(lens), vmax2)[0]
+        assert np.all(err <= tol2), f"out without lse: worst {np.nanmax(err / np.maximum(tol2, 1e-300)):.3g} of its tolerance"
     got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
     err = np.abs(got - want)
     assert np.all(err <= tol), f"out: worst {np.nanmax(err / np.maximum(tol, 1e-300)):.3g} of its tolerance"
@@ -137,7 +145,7 @@ def test_bad_tables_read_as_zeros():
         out, lse = cache.attention(q, dev(table), dev(lens), dev(offs), max_queries=n, return_lse=True)
         st, s = device_status()
         assert st == 11 and s in (0, 1)
-        rounded = many_queries("bf16", 2 * n, 2 * n, 4, 2, table, 16, n)
+        rounded = "v" if many_queries("bf16", 2 * n, 2 * n, 4, 2, table, 16, n) else ""
         want, wl, spread, score, vmax = U.attention(U.Paged4(cache), qd, table, lens, offs, 0.125, True, 0, rounded)
         tol, ltol = bounds("bf16", want, wl, spread, score, max(lens), vmax)
         assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)

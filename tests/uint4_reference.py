@@ -110,11 +110,11 @@ def random_cache(rng, cache, spread=0.3, size=1.0):
         t.copy_(torch.from_numpy(s.astype(np.float16)))
 
 
-def attention(ref: Paged4, q, table, lens, offs, scale, causal=True, window=0, rounded=False):
+def attention(ref: Paged4, q, table, lens, offs, scale, causal=True, window=0, rounded=""):
     """q: float64 [rows, Hq, D] -> (out, lse, spread, score, vmax): the exact result, and per row and head what error
     bounds need: the largest over dimensions of sum p |v|, the largest of scale * sum |q k|, and the largest |v| that
-    it sees.  In them |k| and |v| stand for |scale code| + |least|, the parts that the products take.  `rounded`: V's
-    values rounded to f16 first, and |v| theirs."""
+    it sees.  In them |k| and |v| stand for |scale code| + |least|, the parts that the products take.  `rounded`: the
+    values of those ("v", "kv") rounded to f16 first, and |k| and |v| theirs."""
     T, Hq, D = q.shape
     G = Hq // ref.H
     vals, mags = {}, {}
@@ -124,7 +124,7 @@ def attention(ref: Paged4, q, table, lens, offs, scale, causal=True, window=0, r
             parts = getattr(ref, name) * s[..., 0], s[..., 1]
             vals[name] = parts[0] + parts[1]
             mags[name] = np.abs(parts[0]) + np.abs(parts[1])
-            if rounded and name == "v":
+            if name in rounded:
                 vals[name] = vals[name].astype(np.float16).astype(np.float64)
                 mags[name] = np.abs(vals[name])
     out, lse = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf)
