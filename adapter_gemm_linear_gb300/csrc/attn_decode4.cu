@@ -18,8 +18,14 @@
 //    so that the row's largest p' is in [2^8, 2^9); p itself is relative to a maximum
 //    that is raised when a score passes it by kSlack.  Both are looked at lane by
 //    lane; only a raise takes shuffles.
-//  - A warp takes TS tiles a step, of one column tile of rows two: a step's
-//    fixed instructions (waits, looks, the checks) are shared by 32 tokens.
+//  - A warp takes two tiles a step, whose fixed instructions (waits, looks, the checks)
+//    are shared by 32 tokens.
+// Bound by memory, half a byte a value and 1/16 of scales: 64 query heads on 8 of 128.
+// One token of each of 256 sequences of some 4096 reads 1.04 GB: 238 us in a graph (4.4 TB/s; a
+// floor of 154).  Of these some 50 are the 2048 items' beginnings and ends (their queries,
+// the merge and the results), beside which the bytes come at 5.9 TB/s.  64 sequences of 4097: 84 us, with
+// 128 query heads 122, fp32 120; 4 queries of 64 sequences, 32 heads of 64 on 8, in a window of 1024:
+// 31.8; one token of one sequence of 2000: 10.7.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -37,10 +43,15 @@ using namespace sm100;
 template <typename T, int NT>
 __host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? 4 * NT : 8 * NT; }
 
+// Registers are given out by a quarter of the SM, so what counts is the warps of a quarter: two of
+// 255 registers, three of 168 or four of 128.  Two column tiles of rows with heads of 128 need the
+// 255 (16 query rows a key head, 64 sequences of 4097, 8 key heads: 122 us, with three warps a quarter
+// and their spills 229, with one tile a step 135); else four are better, but for one column tile with
+// heads of 64 those of 15 warps (51.0 us; of 20 in four CTAs 55.9, of 16 in four 52.3).
 template <int D, int NT>
-__host__ __device__ constexpr int consumers() { return D == 128 && NT == 2 ? 5 : 4; }
+__host__ __device__ constexpr int consumers() { return D == 128 && NT == 2 ? 7 : 4; }
 template <int D, int NT>
-__host__ __device__ constexpr int ctas_per_sm() { return D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3); }
+__host__ __device__ constexpr int ctas_per_sm() { return D == 128 && NT == 2 ? 1 : 3; }
 
 constexpr int64_t kNoTile = -1, kEndOfLine = -2;  // zeros; nothing any more
 // What beginning and ending an item costs, in units of 128 keys.  Without it CTAs that
@@ -56,8 +67,8 @@ template <int D, int NT>
 struct Decode4Smem {
     static constexpr int kWarps = consumers<D, NT>();
     static constexpr int H = D / kBlockDims;
-    static constexpr int TS = NT == 1 || D == 64 ? 2 : 1;                  // tiles of a step
-    static constexpr int kDepth = NT == 1 ? (D == 128 ? 3 : 4) : D == 64 ? 3 : 5;  // steps a warp fetches ahead
+    static constexpr int TS = 2;                                    // tiles of a step
+    static constexpr int kDepth = D == 64 && NT == 1 ? 5 : 3;       // steps a warp fetches ahead
     static constexpr int kMeta = TS * 2 * H * 4;                    // 16-byte pieces of a step's scales
     uint4 codes[kWarps][kDepth][2][TS * H][32];                     // [.., K or V, (tile, block), lane]
     uint4 meta[kWarps][kDepth][kMeta];                              // [.., (tile, K or V, block, four tokens)]
@@ -182,7 +193,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             for (int h = 0; h < H; ++h) copy16(&sm.codes[warp][slot][1][j * H + h][lane], b.v_pages + byte + h * kBlockBytes, at[j] >= 0);
         }
         if (lane < Smem::kMeta) {
-            const int64_t tile = TS == 2 && lane >= 8 * H ? at[TS - 1] : at[0];
+            const int64_t tile = lane >= 8 * H ? at[1] : at[0];
             const float *from = lane / (4 * H) % 2 ? b.v_scales : b.k_scales;
             if (tile != kEndOfLine)
                 copy16(&sm.meta[warp][slot][lane], from + (max(tile, int64_t{0}) * (H * kKvTile) + lane % (4 * H) * 4), tile >= 0);
