@@ -54,6 +54,17 @@ template <int D, int NT>
 __host__ __device__ constexpr int ctas_per_sm() { return D == 128 && NT == 2 ? 1 : 3; }
 
 constexpr int64_t kNoTile = -1, kEndOfLine = -2;  // zeros; nothing any more
+constexpr int kLooks = 2;                         // batches looked up ahead
+constexpr int kItemRing = 64;
+
+// What the CTA has of an item.
+struct Item4 {
+    int32_t off, n, len;  // the sequence's queries and length; n = 0: no more items
+    int32_t head, row_tile, tile0, tile1;
+    int32_t last_cta;  // that it goes on to, kWhole, or kNotFirst: it began in another CTA
+};
+static_assert(sizeof(Item4) == 32, "two 16-byte pieces");
+constexpr int32_t kWhole = -1, kNotFirst = -2;
 // What beginning and ending an item costs, in units of 128 keys.  Without it CTAs that
 // get many short items take twice as long as the others: 4 queries of 64 sequences in a
 // window of 1024 take 50 us with 0, 36 with 1, 33.4 with 2, 31.8 with 4 and 31.3 with 6; one
@@ -74,8 +85,13 @@ struct Decode4Smem {
     uint4 meta[kWarps][kDepth][kMeta];                              // [.., (tile, K or V, block, four tokens)]
     float o[kWarps][8 * NT][D + 4];                                 // merge: padded against bank conflicts
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    int64_t info[kBatches][kBatch];                                 // tile_index, kNoTile or kEndOfLine
-    uint64_t full[kBatches], empty[kBatches];
+    int64_t info[kLooks][kBatch];                                   // tile_index, kNoTile or kEndOfLine
+    alignas(16) Item4 items[kItemRing];
+    uint64_t full[kLooks], empty[kLooks], merge_full, merge_empty;
+    // A batch's items are written when every warp has looked at its last step of the batch kLooks before, and
+    // so has used the step kDepth of its own before that: what it may still read are the item of that
+    // step and later ones, each of at least one step.
+    static_assert(1 + kLooks * (kBatch / TS) + (kDepth + 1) * kWarps <= kItemRing, "items that are still read");
     long long warp_sum[kWarps + 1][2];
     long long base;  // first unit of the sequence the CTA begins in
     int32_t seq;
@@ -109,23 +125,23 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView &b = a.kv;
-    JoinEntry *joins = join_entries(a, gridDim.x, kSlotRows, D);
-
     // the joining kernel may come in as soon as there is room beside CTAs that
     // run or have none of the work; it waits for this one's end before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (threadIdx.x < kBatches) {
+    if (threadIdx.x < kLooks) {
         mbar_init(&sm.full[threadIdx.x], a.test_wait_ns ? 2 : 1);
         mbar_init(&sm.empty[threadIdx.x], kWarps);
         fence_mbar_init();
     }
     if (threadIdx.x == 0) {
+        mbar_init(&sm.merge_full, kWarps);
+        mbar_init(&sm.merge_empty, kWarps);
+        fence_mbar_init();
         sm.dead = 0;
-        joins[blockIdx.x].last_cta = -1;
+        join_entries(a, gridDim.x, kSlotRows, D)[blockIdx.x].last_cta = -1;
     }
     const Range range = plan_line<ROWS, kThreads, kItemUnits>(a, sm.warp_sum, &sm.seq, &sm.base);
-    Walk<ROWS> walk(a, range, sm.seq, sm.base);
     volatile int32_t *dead = &sm.dead;
     const uint64_t limit = a.test_wait_ns ? a.test_wait_ns : kWaitNs;
 
@@ -136,16 +152,31 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     };
 
     if (warp == kWarps) {
-        // ---- places of the CTA's tiles, 32 at a time, a lane each; an item's are rounded up to whole steps
+        // ---- the CTA's items, and places of their tiles, 32 at a time, a lane each; an item's are rounded up to
+        // whole steps.  (The consumers' own walks took registers that they had to spill, and 5% of their time.)
+        Walk<ROWS> walk(a, range, sm.seq, sm.base);
+        uint32_t item = 0;
         const int tile_shift = b.page_shift - 4;  // tiles of a page, as a shift
         int32_t next = 0, end = 0, last = 0;      // the item's tiles that are not given out: up to `last`, rounded up `end`
         bool more = true;
         // (past the last tile the consumers still look for as many as they fetch ahead)
         for (int32_t n = 0, past = 0; past < kWarps * kDepth * TS; ++n) {
+            wait(&sm.empty[n % kLooks], ((n / kLooks) & 1u) ^ 1u, 45);
+            // (what the consumers may still read is left alone; they see `dead` when they look for more)
+            if (__any_sync(0xffffffffu, *dead)) break;
             int32_t seq = -1, head = 0, t = 0;
             for (int fill = 0; fill < kBatch;) {
                 if (next == end) {
-                    more = more && walk.next();
+                    if (more) {
+                        more = walk.next();
+                        const long long last_cta = more ? (walk.item_end * range.ctas - 1) / range.total : 0;
+                        if (lane == 0)
+                            sm.items[item % kItemRing] =
+                                !more ? Item4{}
+                                      : Item4{walk.work.r.off, walk.work.r.n, walk.work.r.len, walk.head, walk.row_tile, walk.tile0, walk.tile1,
+                                              !walk.from_start ? kNotFirst : walk.to_end ? kWhole : static_cast<int32_t>(last_cta)};
+                        ++item;
+                    }
                     if (!more) {
                         past += kBatch - fill;
                         break;
@@ -168,13 +199,9 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 const int32_t page = read_page(b, seq, t >> tile_shift);
                 if (page >= 0) at = tile_index(b, page, head, t & ((1 << tile_shift) - 1));
             }
+            sm.info[n % kLooks][lane] = at;
             __syncwarp();
-            wait(&sm.empty[n % kBatches], ((n / kBatches) & 1u) ^ 1u, 45);
-            // (what the consumers may still read is left alone; they see `dead` when they look for more)
-            if (__any_sync(0xffffffffu, *dead)) break;
-            sm.info[n % kBatches][lane] = at;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.full[n % kBatches]);
+            if (lane == 0) mbar_arrive(&sm.full[n % kLooks]);
         }
         return;
     }
@@ -204,13 +231,13 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     // first of it, and gives the batch back after the last
     auto look = [&](uint32_t i, int64_t (&at)[TS]) {
         const uint32_t n = i / kSteps, k = i % kSteps;
-        if (k < kWarps) wait(&sm.full[n % kBatches], (n / kBatches) & 1u, 46);
+        if (k < kWarps) wait(&sm.full[n % kLooks], (n / kLooks) & 1u, 46);
         const bool gone = *dead;
 #pragma unroll
-        for (int j = 0; j < TS; ++j) at[j] = gone ? kEndOfLine : sm.info[n % kBatches][k * TS + j];
+        for (int j = 0; j < TS; ++j) at[j] = gone ? kEndOfLine : sm.info[n % kLooks][k * TS + j];
         if (k >= kSteps - kWarps) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[n % kBatches]);
+            if (lane == 0) mbar_arrive(&sm.empty[n % kLooks]);
         }
     };
     auto landed = [] { asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory"); };
@@ -221,11 +248,15 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     }
     uint32_t taken = 0;  // steps the warp has used
     uint32_t i0 = 0;     // steps of the items before
-    bool merged = false;  // whether the merge buffer may still be read by others
-    while (walk.next()) {
-        const SeqRows &r = walk.work.r;
-        const int32_t rows = min(ROWS, r.n * a.group - walk.row_tile * ROWS);
-        const int32_t key_end = min(walk.tile1 * kKvTile, r.len);
+    // (the warp has looked at its next step, so the item's entry, which came with its first step's batch, is there)
+    for (uint32_t ni = 0;; ++ni) {
+        if (__any_sync(0xffffffffu, *dead)) break;
+        const int4 *const entry = reinterpret_cast<const int4 *>(&sm.items[ni % kItemRing]);
+        const int4 e0 = entry[0], e1 = entry[1];
+        const Item4 it{e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+        if (it.n == 0) break;
+        const int32_t rows = min(ROWS, it.n * a.group - it.row_tile * ROWS);
+        const int32_t key_end = min(it.tile1 * kKvTile, it.len);
         // q as B fragments: column g of tile u is row 8 u + g, dimensions 64 h + 16 tig +
         // 4 j + 0..3 in k-step (h, j), the last two by kUnit0 / kUnit1
         uint32_t qf[NT][D / 16][2];
@@ -236,9 +267,9 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         int32_t kmin[RT][2], kmax[RT][2];
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
-            const int32_t row = walk.row_tile * ROWS + min(8 * u + g, rows - 1);  // rows past the last repeat it
-            const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
-            const T *src = static_cast<const T *>(a.q.p) + static_cast<int64_t>(r.off + qi) * a.q.row + qh * a.q.head;
+            const int32_t row = it.row_tile * ROWS + min(8 * u + g, rows - 1);  // rows past the last repeat it
+            const int32_t qi = row / a.group, qh = it.head * a.group + row % a.group;
+            const T *src = static_cast<const T *>(a.q.p) + static_cast<int64_t>(it.off + qi) * a.q.row + qh * a.q.head;
             float x[D / 4];
             float amax = 0.0f;
 #pragma unroll
@@ -256,8 +287,8 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             e = amax < INFINITY ? max(e, -126) : 0;
             const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
             const float up = fminf(a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (1.0f / kUnit0), 3e38f);
-            const int32_t pos = r.len - r.n + qi;
-            const int32_t hi = min(a.causal ? pos + 1 : r.len, key_end), lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            const int32_t pos = it.len - it.n + qi;
+            const int32_t hi = min(a.causal ? pos + 1 : it.len, key_end), lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
             float sum[H];
 #pragma unroll
             for (int h = 0; h < H; ++h) {
@@ -291,9 +322,9 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             }
         }
         // keys that every row of the item sees: steps within need no mask
-        const int32_t pos0 = r.len - r.n + walk.row_tile * ROWS / a.group;
-        const int32_t pos1 = r.len - r.n + (walk.row_tile * ROWS + rows - 1) / a.group;
-        const int32_t all_hi = min(a.causal ? pos0 + 1 : r.len, key_end);
+        const int32_t pos0 = it.len - it.n + it.row_tile * ROWS / a.group;
+        const int32_t pos1 = it.len - it.n + (it.row_tile * ROWS + rows - 1) / a.group;
+        const int32_t all_hi = min(a.causal ? pos0 + 1 : it.len, key_end);
         const int32_t all_lo = a.window > 0 ? max(0, pos1 - a.window + 1) : 0;
 
         // o^T, in units of kUnit0 / fr (rows d = 4 (g + 8 (k / 2)) + 2 (k % 2)) and kUnit1 / fr
@@ -326,12 +357,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 }
         };
 
-        const int32_t steps = (walk.tile1 - walk.tile0 + TS - 1) / TS;
+        const int32_t steps = (it.tile1 - it.tile0 + TS - 1) / TS;
         // this warp's steps: those whose running number is the warp's modulo kWarps
         const int32_t j0 = (warp - static_cast<int32_t>(i0 % kWarps) + kWarps) % kWarps;
         for (int32_t st = j0; st < steps; st += kWarps) {
             const uint32_t slot = taken++ % kDepth;
-            const int32_t key0 = (walk.tile0 + st * TS) * kKvTile;
+            const int32_t key0 = (it.tile0 + st * TS) * kKvTile;
             landed();
             __syncwarp();  // every lane's copies of scales
             // scale and least value of token tok + 2 t, of K (v = 0) or V
@@ -543,8 +574,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         i0 += steps;
 
         // ---- merge the warps
-        if (merged) asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // the buffer has been read
-        merged = true;
+        wait(&sm.merge_empty, (ni & 1u) ^ 1u, 47);  // the buffer has been read
 #pragma unroll
         for (int u = 0; u < RT; ++u)
 #pragma unroll
@@ -580,15 +610,17 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                                     fmaf(v.z, 1.0f / kUnit0, add) * un, fmaf(v.w, 1.0f / kUnit1, add) * un);
                 }
             }
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        const bool whole = walk.from_start && walk.to_end;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merge_full);
+        wait(&sm.merge_full, ni & 1u, 48);
+        // (the entry again, instead of registers that would be held throughout)
+        const volatile Item4 &me = sm.items[ni % kItemRing];
+        const int32_t off = me.off, head = me.head, row0 = me.row_tile * ROWS, last_cta = me.last_cta;
+        const bool whole = last_cta == kWhole;
         // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
-        float *part = partial_at(a, blockIdx.x, walk.from_start ? 1 : 0, kSlotRows, D);
-        if (!whole && walk.from_start && threadIdx.x == 0) {
-            const long long lastu = walk.item_end - 1;
-            joins[blockIdx.x] = JoinEntry{static_cast<int32_t>(((lastu + 1) * range.ctas - 1) / range.total), walk.head, r.off,
-                                          walk.row_tile * ROWS, rows, {}};
-        }
+        float *part = partial_at(a, blockIdx.x, last_cta >= 0 ? 1 : 0, kSlotRows, D);
+        if (last_cta >= 0 && threadIdx.x == 0)
+            join_entries(a, gridDim.x, kSlotRows, D)[blockIdx.x] = JoinEntry{last_cta, head, off, row0, rows, {}};
         constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
         const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
         if (rt < rows) {
@@ -603,9 +635,9 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             }
             // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
             const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f;
-            const int32_t row = walk.row_tile * ROWS + rt;
-            const int32_t qi = row / a.group, qh = walk.head * a.group + row % a.group;
-            T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(r.off + qi) * a.out.row + qh * a.out.head;
+            const int32_t row = row0 + rt;
+            const int32_t qi = row / a.group, qh = head * a.group + row % a.group;
+            T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(off + qi) * a.out.row + qh * a.out.head;
 #pragma unroll
             for (int c = c0 * 4; c < D; c += PER_ROW * 4) {
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -625,10 +657,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 if (!whole) {
                     part[kSlotRows * D + rt] = lse;
                 } else if (a.lse) {
-                    a.lse[static_cast<int64_t>(r.off + qi) * a.q_heads + qh] = lse * kLn2;
+                    a.lse[static_cast<int64_t>(off + qi) * a.q_heads + qh] = lse * kLn2;
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merge_empty);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
