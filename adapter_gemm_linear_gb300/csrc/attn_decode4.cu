@@ -53,7 +53,7 @@ __host__ __device__ constexpr int consumers() { return D == 128 && NT == 2 ? 7 :
 template <int D, int NT>
 __host__ __device__ constexpr int ctas_per_sm() { return D == 128 && NT == 2 ? 1 : 3; }
 
-constexpr int64_t kNoTile = -1, kEndOfLine = -2;  // zeros; nothing any more
+constexpr int32_t kNoTile = -1, kEndOfLine = -2;  // zeros; nothing any more (a tile has 512 bytes and more: 31 bits number 1 TB)
 constexpr int kLooks = 2;                         // batches looked up ahead
 constexpr int kItemRing = 64;
 
@@ -79,13 +79,13 @@ struct Decode4Smem {
     static constexpr int kWarps = consumers<D, NT>();
     static constexpr int H = D / kBlockDims;
     static constexpr int TS = 2;                                    // tiles of a step
-    static constexpr int kDepth = D == 64 && NT == 1 ? 5 : 3;       // steps a warp fetches ahead
+    static constexpr int kDepth = 2;                                // steps a warp fetches ahead (of 3: 72 us instead of 71, 48.4 instead of 47)
     static constexpr int kMeta = TS * 2 * H * 4;                    // 16-byte pieces of a step's scales
     uint4 codes[kWarps][kDepth][2][TS * H][32];                     // [.., K or V, (tile, block), lane]
     uint4 meta[kWarps][kDepth][kMeta];                              // [.., (tile, K or V, block, four tokens)]
     float o[kWarps][8 * NT][D + 4];                                 // merge: padded against bank conflicts
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    int64_t info[kLooks][kBatch];                                   // tile_index, kNoTile or kEndOfLine
+    int2 info[kLooks][kBatch / 2];                                  // of a step: tile_index, kNoTile or kEndOfLine
     alignas(16) Item4 items[kItemRing];
     uint64_t full[kLooks], empty[kLooks], merge_full, merge_empty;
     // A batch's items are written when every warp has looked at its last step of the batch kLooks before, and
@@ -146,9 +146,11 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     const uint64_t limit = a.test_wait_ns ? a.test_wait_ns : kWaitNs;
 
     auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t site) {
-        if (*dead || mbar_wait_bounded(bar, parity, limit)) return;
+        if (*dead) return false;
+        if (mbar_wait_bounded(bar, parity, limit)) return true;
         record_error(b.status, kDevTimeout, site);
         *dead = 1;
+        return false;
     };
 
     if (warp == kWarps) {
@@ -194,12 +196,12 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                 fill += take;
                 next += take;
             }
-            int64_t at = seq == -1 ? kEndOfLine : kNoTile;
+            int32_t at = seq == -1 ? kEndOfLine : kNoTile;
             if (seq >= 0) {
                 const int32_t page = read_page(b, seq, t >> tile_shift);
-                if (page >= 0) at = tile_index(b, page, head, t & ((1 << tile_shift) - 1));
+                if (page >= 0) at = static_cast<int32_t>(tile_index(b, page, head, t & ((1 << tile_shift) - 1)));
             }
-            sm.info[n % kLooks][lane] = at;
+            reinterpret_cast<int32_t *>(sm.info[n % kLooks])[lane] = at;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.full[n % kLooks]);
         }
@@ -209,32 +211,33 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     // ---- consumers
     const int g = lane >> 2, tig = lane & 3;
     const int tok = k_token(g);  // S^T: rows g and g + 8 are tokens tok and tok + 2 of a tile
-    auto fetch = [&](const int64_t (&at)[TS], uint32_t slot) {
+    auto fetch = [&](const int32_t (&at)[TS], uint32_t slot) {
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             if (at[j] == kEndOfLine) continue;
-            const int64_t byte = max(at[j], int64_t{0}) * (H * kBlockBytes) + lane * 16;
+            const int64_t byte = static_cast<int64_t>(max(at[j], 0)) * (H * kBlockBytes) + lane * 16;
 #pragma unroll
             for (int h = 0; h < H; ++h) copy16(&sm.codes[warp][slot][0][j * H + h][lane], b.k_pages + byte + h * kBlockBytes, at[j] >= 0);
 #pragma unroll
             for (int h = 0; h < H; ++h) copy16(&sm.codes[warp][slot][1][j * H + h][lane], b.v_pages + byte + h * kBlockBytes, at[j] >= 0);
         }
         if (lane < Smem::kMeta) {
-            const int64_t tile = lane >= 8 * H ? at[1] : at[0];
+            const int32_t tile = lane >= 8 * H ? at[1] : at[0];
             const float *from = lane / (4 * H) % 2 ? b.v_scales : b.k_scales;
             if (tile != kEndOfLine)
-                copy16(&sm.meta[warp][slot][lane], from + (max(tile, int64_t{0}) * (H * kKvTile) + lane % (4 * H) * 4), tile >= 0);
+                copy16(&sm.meta[warp][slot][lane], from + (static_cast<int64_t>(max(tile, 0)) * (H * kKvTile) + lane % (4 * H) * 4), tile >= 0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // where the tiles of the line's step i are; waits for their batch if it is the warp's
     // first of it, and gives the batch back after the last
-    auto look = [&](uint32_t i, int64_t (&at)[TS]) {
+    bool gone = false;
+    auto look = [&](uint32_t i, int32_t (&at)[TS]) {
         const uint32_t n = i / kSteps, k = i % kSteps;
-        if (k < kWarps) wait(&sm.full[n % kLooks], (n / kLooks) & 1u, 46);
-        const bool gone = *dead;
-#pragma unroll
-        for (int j = 0; j < TS; ++j) at[j] = gone ? kEndOfLine : sm.info[n % kLooks][k * TS + j];
+        if (k < kWarps && !wait(&sm.full[n % kLooks], (n / kLooks) & 1u, 46)) gone = true;
+        const int2 x = sm.info[n % kLooks][k];
+        at[0] = gone ? kEndOfLine : x.x;
+        at[1] = gone ? kEndOfLine : x.y;
         if (k >= kSteps - kWarps) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.empty[n % kLooks]);
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     };
     auto landed = [] { asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory"); };
     for (uint32_t d = 0; d < kDepth; ++d) {
-        int64_t at[TS];
+        int32_t at[TS];
         look(warp + d * kWarps, at);
         fetch(at, d);
     }
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     }
                 }
             __syncwarp();  // every lane has read the scales
-            int64_t ahead[TS];
+            int32_t ahead[TS];
             look(i0 + st + kDepth * kWarps, ahead);
             fetch(ahead, slot);
         }
