@@ -20,12 +20,12 @@
 //    lane; only a raise takes shuffles.
 //  - A warp takes two tiles a step, whose fixed instructions (waits, looks, the checks)
 //    are shared by 32 tokens.
-// Bound by memory, half a byte a value and 1/16 of scales: 64 query heads on 8 of 128.
-// One token of each of 256 sequences of some 4096 reads 1.04 GB: 238 us in a graph (4.4 TB/s; a
-// floor of 154).  Of these some 50 are the 2048 items' beginnings and ends (their queries,
-// the merge and the results), beside which the bytes come at 5.9 TB/s.  64 sequences of 4097: 84 us, with
-// 128 query heads 122, fp32 120; 4 queries of 64 sequences, 32 heads of 64 on 8, in a window of 1024:
-// 31.8; one token of one sequence of 2000: 10.7.
+// Bound by the warps' instructions (issue slots 55% used with three warps a quarter of the
+// SM, of which each instruction waits for some before it; the codes' ANDs half of the ALU), then by
+// memory, half a byte a value and 1/16 of scales.  64 query heads on 8 of 128, in a graph: one
+// token of each of 256 sequences of some 4096, 1.04 GB, 201 us (5.2 TB/s; its floor is 154); of
+// 64 sequences of 4097 68.6 us, with 128 query heads 110, in fp32 117.  One token of one sequence of
+// 2000: 10.1.  4 queries of 64 sequences, 32 heads of 64 on 8, in a window of 1024: 28.6.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -46,8 +46,9 @@ __host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? 4 * NT :
 // Registers are given out by a quarter of the SM, so what counts is the warps of a quarter: two of
 // 255 registers, three of 168 or four of 128.  Two column tiles of rows with heads of 128 need the
 // 255 (16 query rows a key head, 64 sequences of 4097, 8 key heads: 122 us, with three warps a quarter
-// and their spills 229, with one tile a step 135); else four are better, but for one column tile with
-// heads of 64 those of 15 warps (51.0 us; of 20 in four CTAs 55.9, of 16 in four 52.3).
+// and their spills 229, with one tile a step 135); else four are better, in three CTAs (256
+// sequences 206 us, in four of four warps 214, in two of eight 235; heads of 64 51 us, in four
+// CTAs of five warps 56).
 template <int D, int NT>
 __host__ __device__ constexpr int consumers() { return D == 128 && NT == 2 ? 7 : 4; }
 template <int D, int NT>
@@ -67,8 +68,8 @@ static_assert(sizeof(Item4) == 32, "two 16-byte pieces");
 constexpr int32_t kWhole = -1, kNotFirst = -2;
 // What beginning and ending an item costs, in units of 128 keys.  Without it CTAs that
 // get many short items take twice as long as the others: 4 queries of 64 sequences in a
-// window of 1024 take 50 us with 0, 36 with 1, 33.4 with 2, 31.8 with 4 and 31.3 with 6; one
-// token of 256 sequences of some 4096 261, 252, 244, 238 and 243.5.
+// window of 1024 take 45.6 us with 0, 33.8 with 1, 31.1 with 2, 29.2 with 4 and 28.7 with 6; one
+// token of 256 sequences of some 4096 231, 219, 209, 208 and 214.
 constexpr int kItemUnits = 4;
 constexpr float kSlack = 8.0f;                    // log2 by which a score may pass the row's maximum so far
 constexpr int kTopExponent = 8;                   // a row's largest p' begins in [2^8, 2^9)

@@ -184,17 +184,22 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
 // x 2 heads on 7673 (1440 units) 28.5 against 28.8, 4 x 128 queries (2048 units)
 // 43.5 against 22.0.  (What the tables have room for is all that the host knows of
 // the lengths: a wider table of the same sequences may take the other kernel.)
-bool many_queries(const lora::AttnView &v, lora_dtype_t dtype) {
+// The 4-bit cache's kernels (attn_decode4.cu in place of the first) take the same rule: 64
+// sequences of 4097, 8 heads of 128, with 16 rows 110 against 203 us, with 32 206 against 203; 64
+// queries of 32 heads on 1064 keys (1152 units) 21.0 against 24.5, 4 x 128 queries
+// (2048 units) 49 against 26.5.  Its heads of 64 take two passes of the first: with 32 rows 116
+// against 161, which a third would use up.
+bool many_queries(const lora::AttnView &v, const lora_kv_cache_t *c, lora_dtype_t dtype) {
     const int64_t rows = static_cast<int64_t>(v.max_queries) * v.group;  // of a sequence, at most
-    if (dtype != LORA_BF16 || rows <= 16) return false;
+    if (dtype != LORA_BF16 || rows <= (c->format == LORA_KV_UINT4 && c->head_dim == 64 ? 32 : 16)) return false;
     const double row_tiles = std::min(static_cast<double>(v.kv.num_seqs) * static_cast<double>((rows + 15) / 16),
                                       static_cast<double>(v.kv.rows) * v.group / 16 + v.kv.num_seqs);
     const double chunks = (static_cast<double>(v.kv.max_pages) * v.kv.page_tokens + 127) / 128;
     return row_tiles * v.kv.heads * chunks > 8.0 * lora::device_sm_count();
 }
 
-size_t workspace_bytes(const lora::AttnView &v, int head_dim, lora_dtype_t dtype) {
-    return many_queries(v, dtype) ? lora::prefill_workspace_bytes(head_dim) : lora::decode_workspace_bytes(head_dim);
+size_t workspace_bytes(const lora::AttnView &v, const lora_kv_cache_t *c, lora_dtype_t dtype) {
+    return many_queries(v, c, dtype) ? lora::prefill_workspace_bytes(c->head_dim) : lora::decode_workspace_bytes(c->head_dim);
 }
 
 }  // namespace
@@ -300,7 +305,7 @@ size_t lora_kv_attention_workspace_bytes(const lora_kv_cache_t *cache, const lor
                                          const lora_kv_attention_args_t *args) {
     lora::AttnView v;
     if (check_attention(cache, batch, args, &v) != LORA_OK) return 0;
-    return workspace_bytes(v, cache->head_dim, args->dtype);
+    return workspace_bytes(v, cache, args->dtype);
 }
 
 lora_status_t lora_kv_attention(const lora_kv_cache_t *cache, const lora_kv_batch_t *batch,
@@ -309,13 +314,13 @@ lora_status_t lora_kv_attention(const lora_kv_cache_t *cache, const lora_kv_batc
     lora_status_t s = check_attention(cache, batch, args, &v);
     if (s != LORA_OK) return s;
     if (batch->rows == 0 || batch->num_seqs == 0) return LORA_OK;
-    const size_t need = workspace_bytes(v, cache->head_dim, args->dtype);
+    const size_t need = workspace_bytes(v, cache, args->dtype);
     if (!v.workspace || args->workspace_bytes < need) return LORA_ERR_WORKSPACE;
     if (!aligned(v.workspace, 16)) return LORA_ERR_ALIGNMENT;
     cudaError_t e = lora::device_status_ptr(&v.kv.status);
     v.test_wait_ns = lora::take_test_wait_limit();
     if (e == cudaSuccess)
-        e = many_queries(v, args->dtype)
+        e = many_queries(v, cache, args->dtype)
                 ? lora::launch_attn_prefill(v, cache->format, cache->head_dim, as_stream(stream))
             : cache->format == LORA_KV_UINT4
                 ? lora::launch_attn_decode4(v, cache->head_dim, args->dtype, as_stream(stream))

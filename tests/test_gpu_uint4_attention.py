@@ -30,14 +30,14 @@ def setup(seed, news, befores, page, H, D, **kw):
     return rng, cache, table, lens, offs
 
 
-def many_queries(dtype, rows, T, G, H, table, page, max_queries):
+def many_queries(dtype, T, cache, G, table, max_queries):
     """Which kernel: the rule of the library's host side."""
     n = max_queries * G
-    if dtype != "bf16" or n <= 16:
+    if dtype != "bf16" or n <= (32 if cache.head_dim == 64 else 16):
         return False
     S, sms = table.shape[0], torch.cuda.get_device_properties(0).multi_processor_count
     row_tiles = min(S * ((n + 15) // 16), T * G / 16 + S)
-    return row_tiles * H * ((table.shape[1] * page + 127) / 128) > 8 * sms
+    return row_tiles * cache.num_heads * ((table.shape[1] * cache.page_tokens + 127) / 128) > 8 * sms
 
 
 def check(cache, rng, dtype, Hq, news, table, lens, offs, causal=True, window=0, scale=None, q_width=1.0, ref=None, use_offsets=True,
@@ -50,7 +50,7 @@ def check(cache, rng, dtype, Hq, news, table, lens, offs, causal=True, window=0,
     out, lse = cache.attention(q, dev(table), dev(lens), dev(offs) if use_offsets else None, causal=causal, window=window,
                                scale=scale, return_lse=True, max_queries=most)
     assert status() == 0
-    many = many_queries(dtype, T, T, Hq // cache.num_heads, cache.num_heads, table, cache.page_tokens, most)
+    many = many_queries(dtype, T, cache, Hq // cache.num_heads, table, most)
     rounded = "v" if many else ""
     want, wl, spread, score, vmax = U.attention(ref, qd, table, lens, offs, np.float32(sm).astype(np.float64), causal, window, rounded)
     tol, ltol = bounds(dtype, want, wl, spread, score, max(lens), vmax)
@@ -118,6 +118,16 @@ def test_many_sequences():
         check(cache, rng, "bf16", 2 * G, [1] * 200, table, lens, offs, use_offsets=False)
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+def test_more_items_than_are_described_at_once(dtype, D):
+    """Some hundred items a CTA, of one tile to three, and one of many among them."""
+    rng = np.random.default_rng(D)
+    befores = [int(x) for x in rng.integers(0, 40, 6000)]
+    befores[1234] = 3000
+    rng, cache, table, lens, offs = setup(D + 1, [1] * 6000, befores, 16, 8, D)
+    check(cache, rng, dtype, 8, [1] * 6000, table, lens, offs, use_offsets=False)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_padding_rows(n):
     """Sequences of length 0 give 0 and -inf; rows outside every sequence stay as they are."""
@@ -145,7 +155,7 @@ def test_bad_tables_read_as_zeros():
         out, lse = cache.attention(q, dev(table), dev(lens), dev(offs), max_queries=n, return_lse=True)
         st, s = device_status()
         assert st == 11 and s in (0, 1)
-        rounded = "v" if many_queries("bf16", 2 * n, 2 * n, 4, 2, table, 16, n) else ""
+        rounded = "v" if many_queries("bf16", 2 * n, cache, 4, table, n) else ""
         want, wl, spread, score, vmax = U.attention(U.Paged4(cache), qd, table, lens, offs, 0.125, True, 0, rounded)
         tol, ltol = bounds("bf16", want, wl, spread, score, max(lens), vmax)
         assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
