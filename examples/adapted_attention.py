@@ -1,8 +1,9 @@
 """The attention block of a decoder layer with an adapter per request: adapted
-q/k/v projections, rotary positions, the 8-bit key/value cache, attention over
-it, and the adapted o projection, for prompts and then single tokens.
+q/k/v projections, rotary positions (with a norm of every query and key head
+before them or without), the 8-bit or 4-bit key/value cache, attention over it,
+and the adapted o projection, for prompts and then single tokens.
 
-    python examples/adapted_attention.py [--steps 8]
+    python examples/adapted_attention.py [--steps 8] [--fmt uint4] [--norms]
 
 Weights and adapters are random; every request uses its own adapter, the last
 one none.
@@ -18,14 +19,14 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from adapter_gemm_linear_gb300 import KvCache, LoraPool, linear_forward, rope, rope_tables  # noqa: E402
+from adapter_gemm_linear_gb300 import KvCache, LoraPool, linear_forward, norm_rope, rope, rope_tables  # noqa: E402
 
 
 class AdaptedAttention:
     """One layer's attention block; the adapters of slot i belong together in all four projections."""
 
     def __init__(self, hidden=512, q_heads=8, kv_heads=2, head_dim=64, max_slots=4, rank=8, num_pages=64, page_tokens=16,
-                 fmt="int8", max_pos=4096, device="cuda", seed=0):
+                 fmt="int8", max_pos=4096, device="cuda", seed=0, norms=False):
         g = torch.Generator(device=device)
         g.manual_seed(seed)
 
@@ -45,6 +46,7 @@ class AdaptedAttention:
                 pool.load(slot, A, B, alpha=2.0 * rank)
                 self.adapters[p, slot] = (A, B, 2.0)
             self.pools[p] = pool
+        self.norms = [1.0 + normal(head_dim, std=0.1) for _ in "qk"] if norms else None
         # (decoding fills pages token by token: int8 scales grow by doubling)
         self.cache = KvCache(num_pages, kv_heads, head_dim, page_tokens, fmt, device=device, growth="doubling")
         self.cos, self.sin = rope_tables(max_pos, head_dim, device=device)
@@ -59,7 +61,10 @@ class AdaptedAttention:
         q, k, v = self.project(x, "qkv", row_adapter)
         q = q.view(-1, self.q_heads, self.head_dim)
         k, v = (t.view(-1, self.kv_heads, self.head_dim) for t in (k, v))
-        rope(q, k, self.cos, self.sin, positions, q_out=q, k_out=k)
+        if self.norms:
+            norm_rope(q, k, *self.norms, self.cos, self.sin, positions, q_out=q, k_out=k)
+        else:
+            rope(q, k, self.cos, self.sin, positions, q_out=q, k_out=k)
         self.cache.append(k, v, block_table, seq_lens, offsets)
         o = self.cache.attention(q, block_table, seq_lens, offsets, max_queries=max_queries)
         return self.project(o.view(x.shape[0], -1), "o", row_adapter)[0]
@@ -100,8 +105,10 @@ def serve(layer: AdaptedAttention, prompts, steps, seed=1):
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=8)
+    ap.add_argument("--fmt", default="int8", choices=["int8", "e4m3", "uint4"], help="of the cache")
+    ap.add_argument("--norms", action="store_true", help="norms of queries and keys")
     args = ap.parse_args()
-    layer = AdaptedAttention()
+    layer = AdaptedAttention(fmt=args.fmt, norms=args.norms)
     xs, ys, _ = serve(layer, [100, 37, 5, 260], args.steps)
     for s, (x, y) in enumerate(zip(xs, ys)):
         print(f"request {s}: {x.shape[0]} tokens, |y| {float(y.float().abs().mean()):.4f}")
