@@ -6,8 +6,12 @@
 // page's older ones; and a token's share of each 16-byte piece is whole bytes, so
 // that nothing is read before it is written.  One warp takes one 16-token tile of
 // one head, K or V, its lanes the pieces (attn_uint4.cuh).
-// Both are bound by memory in principle (a value read in its dtype, half a byte and
-// 1/16 byte of scales written, or the other way round).
+// By their bytes both are bound by memory (a value read in its dtype, half a byte and 1/16
+// byte of scales written, or the other way round).  Measured, 8 heads of 128, bf16: 262144 tokens
+// read back in 214 us (6.4 TB/s, 0.95 of a copy); 8192 tokens of 16 prompts written in 18.4 and read
+// back in 12 (24.6 together in a graph), one of each of 256 sequences in 9.4 and 8.5 (12.0).  Of the
+// write 60% of the issue slots are used, by 25 warps an SM: 22 instructions for a value and
+// lane; the rest is reads that wait for each other (sequence, page, row).
 #include <cuda_runtime.h>
 
 #include "attn_uint4.cuh"
