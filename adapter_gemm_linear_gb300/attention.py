@@ -201,6 +201,9 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[tor
     return q_out, k_out
 
 
+_norm_workspace = {}  # bytes of a backward call's workspace, by head_dim and device
+
+
 def norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
                        q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], cos: torch.Tensor,
                        sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6, unit_offset: bool = False,
@@ -226,18 +229,26 @@ def norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Te
     if (dk is None) != (k is None) or (k is not None and (dk.shape != k.shape or dk.dtype != k.dtype)):
         raise ValueError("dk must have k's shape and dtype")
     L = _lib.lib()
-    weights = [None if w is None else torch.empty(q.shape[2:], dtype=torch.float32, device=q.device)
-               for w in (q_weight, k_weight if k is not None else None)]
+    has_q, has_k = q_weight is not None, k_weight is not None and k is not None
+    D = q.shape[2]
+    dq_weight = torch.empty(D, dtype=torch.float32, device=q.device) if has_q else None
+    dk_weight = torch.empty(D, dtype=torch.float32, device=q.device) if has_k else None
     if workspace is None:
-        need = L.lora_norm_rope_backward_workspace_bytes(args) if any(w is not None for w in weights) else 0
+        need = 0
+        if has_q or has_k:
+            need = _norm_workspace.get((D, device))  # (it depends on these alone)
+            if need is None:
+                need = L.lora_norm_rope_backward_workspace_bytes(args)
+                if need:  # (0: arguments that the call will refuse)
+                    _norm_workspace[D, device] = need
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {q.device}")
     grads = _NORM_GRADS.pack(*_heads(dq, "dq", device), *((0, 0, 0) if dk is None else _heads(dk, "dk", device)),
-                             *(0 if w is None else w.data_ptr() for w in weights), workspace.data_ptr(),
+                             dq_weight.data_ptr() if has_q else 0, dk_weight.data_ptr() if has_k else 0, workspace.data_ptr(),
                              workspace.numel() * workspace.element_size())
     _call(L.lora_norm_rope_backward(args, grads, _current_stream(device)), "lora_norm_rope_backward")
-    return q_out, k_out, weights[0], weights[1]
+    return q_out, k_out, dq_weight, dk_weight
 
 
 def kv_pages_bytes(num_pages: int, num_heads: int, head_dim: int, page_tokens: int, fmt: str = "int8") -> int:
@@ -399,7 +410,8 @@ class KvCache:
         offsets, else all rows).  It and the block table's width, as a bound on
         the lengths, choose the kernel for bf16 queries: a table much wider than
         its longest sequence needs costs short calls of several queries some
-        time, and the same call with another width may differ in its last bits.
+        time, and the same call with another width may differ in its last bits
+        (of a "uint4" cache also the same call with and without lse).
         ``window`` > 0 limits a query to the last ``window`` positions up to its
         own; ``scale`` defaults to head_dim^-0.5.
         ``stream``: launch there instead of on the current stream."""
