@@ -12,12 +12,11 @@
 // its squares by shuffles; the head's values stay in registers in between.  A
 // group works on heads of q alone or of k alone, so that its weights are read
 // once, and on several heads of a row, so that the angles are.
-// Measured in a graph, bf16, 8192 rows of 72 heads of 128, three axes: 70 us (4.4 TB/s of
-// the 306 MB, which without a norm take 59), the gradient 109 (4.2); of 40 heads 40 and 65.  What is
-// left is latency: of 14 warps an SM, with 128 registers each, an instruction is issued in 39%
-// of the slots (43% in the gradient), between shuffles, reads from shared memory and the turn's
-// barrier; 80 registers and three blocks spill (89 us).  One token of 64 sequences, 40 heads:
-// 2.8 us; the gradient of 333 rows of 40 heads of 64 8.3.
+// Measured in a graph, bf16, 8192 rows of 72 heads of 128, three axes: 52 us (5.9 TB/s of
+// the 306 MB, 0.87 of a copy), the gradient 88 (5.2); of 40 heads 32 and 54, in fp32 (4096 rows)
+// 34 and 50.  The gradient waits for its own results (shuffles, reads from shared memory,
+// the turn's barrier) with the 14 warps an SM that 128 registers leave.  One token of 64
+// sequences, 40 heads: 2.8 us; the gradient of 333 rows of 40 heads of 64 8.0.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -190,7 +189,14 @@ struct Chunks {
             if (at[n].turn) x[n][1] = *reinterpret_cast<const uint4 *>(src + at[n].d1);
         }
     }
+    template <bool INTER>
     __device__ __forceinline__ void store(T *dst, int n, const F2 (&y)[N], const F2 (&z)[N]) const {
+        if (INTER && at[n].turn) {  // the pieces are a sector
+            const uint4 a = pack2<T>(y), b = pack2<T>(z);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            sm100::store_32(dst + at[n].d0, w);
+            return;
+        }
         if (has[n]) *reinterpret_cast<uint4 *>(dst + at[n].d0) = pack2<T>(y);
         if (at[n].turn) *reinterpret_cast<uint4 *>(dst + at[n].d1) = pack2<T>(z);
     }
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const __grid
         for (int n = 0; n < NC; ++n) {
             F2 y[N], z[N];
             turned<N, INTER>(u[n], v[n], A[n], B[n], two(r, r), y, z);
-            ch.store(dst, n, y, z);
+            ch.template store<INTER>(dst, n, y, z);
         }
     }
 }
@@ -280,7 +286,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const __grid
 // chain of position, angles and heads was not covered: 84 and 135 us for 8192 rows of 72
 // heads of 128 and their gradient.)
 
-template <typename T, int NC, int P, int LT>
+template <typename T, int NC, int P, bool INTER, int LT>
 struct RowPipe {
     static constexpr int VE = VecTraits<T>::kElems;
     static constexpr int kPieces = P * NC * 2;  // 16 bytes each, of a thread and head: [tensor][chunk][piece]
@@ -292,7 +298,13 @@ struct RowPipe {
     const NormRopeView &a;
     const Group<LT> &g;
     const Chunks<T, NC, LT> &ch;
-    uint32_t ring;  // [stage][head][thread][piece]: the thread's first; pieces in an order that keeps 8 threads off each other's banks
+    // [stage][head][tensor, chunk]: the thread's first piece.  The 16 bytes of a copy lie beside each other in
+    // shared memory where they do in global memory, else each half sector is a request of its own
+    // and sectors are read twice (8192 rows of 72 heads 70 us instead of 52, their gradient 109 instead of 88): [piece][thread]; interleaved, where a
+    // thread's two pieces are a sector, [thread][piece], in an order that keeps 8 threads off each
+    // other's banks.
+    uint32_t ring;
+    uint32_t stride;  // bytes of a piece of all threads
     float *angles;  // [stage, one more][row of the block][cosines, sines][pair]
     int32_t threads, half, pos[LORA_ROPE_MAX_AXES];
     bool fetches;       // the row's angles
@@ -307,7 +319,8 @@ struct RowPipe {
         : a(v), g(group), ch(c) {
         threads = Group<LT>::lanes() * blockDim.y * blockDim.z;
         const uint32_t tid = (threadIdx.z * blockDim.y + threadIdx.y) * Group<LT>::lanes() + threadIdx.x;
-        ring = sm100::smem_u32(smem) + tid * (kPieces * 16) + (tid / (8 / kPieces) % kPieces) * 16;
+        ring = sm100::smem_u32(smem) + tid * (INTER ? 32 : 16) + (INTER ? (tid / 4 % 2) * 16 : 0);
+        stride = threads * 16;
         angles = reinterpret_cast<float *>(smem + row_pipe_ring_bytes(threads, a.per_turn, P * NC));
         half = a.rope.rot_dim / 2;
         fetches = threadIdx.y == 0;
@@ -381,7 +394,10 @@ struct RowPipe {
 #pragma unroll
         for (int p = 0; p < P; ++p) src[p] += src_step[p];
     }
-    __device__ __forceinline__ uint32_t piece(int p, int n, int k) const { return at ^ (((p * NC + n) * 2 + k) * 16); }
+    __device__ __forceinline__ uint32_t piece(int p, int n, int k) const {
+        const uint32_t chunk = at + (p * NC + n) * 2 * stride;
+        return k == 0 ? chunk : INTER ? chunk ^ 16u : chunk + stride;
+    }
     __device__ __forceinline__ bool here() const { return now.row < a.rope.rows && h < g.heads; }
     __device__ __forceinline__ void fetch_head() const {
         if (ahead.row >= a.rope.rows || h_ahead >= g.heads) return;
@@ -446,7 +462,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_rows_kernel(const __gri
     const Group<LT> g(a);
     const Chunks<T, NC, LT> ch(a, g);
     const HeadsView in[1] = {g.is_k ? a.rope.k : a.rope.q}, &out = g.is_k ? a.rope.k_out : a.rope.q_out;
-    RowPipe<T, NC, 1, LT> pipe(a, g, ch, in, smem);
+    RowPipe<T, NC, 1, INTER, LT> pipe(a, g, ch, in, smem);
     const int64_t out_step = g.step * out.head;
     const float inv_d = 1.0f / static_cast<float>(a.rope.head_dim);
     pipe.begin(in);
@@ -481,7 +497,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_rows_kernel(const __gri
             for (int n = 0; n < NC; ++n) {
                 F2 y[N], z[N];
                 turned<N, INTER>(u[n], v[n], A[n], B[n], two(r, r), y, z);
-                ch.store(dst, n, y, z);
+                ch.template store<INTER>(dst, n, y, z);
             }
         }
         pipe.end_turn(t);
@@ -499,7 +515,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(cons
     const Group<LT> g(a);
     const Chunks<T, NC, LT> ch(a, g);
     const HeadsView in[2] = {g.is_k ? a.rope.k : a.rope.q, g.is_k ? a.dk : a.dq}, &out = g.is_k ? a.rope.k_out : a.rope.q_out;
-    RowPipe<T, NC, 2, LT> pipe(a, g, ch, in, smem);
+    RowPipe<T, NC, 2, INTER, LT> pipe(a, g, ch, in, smem);
     const int64_t out_step = g.step * out.head;
     // the weights lie in shared memory, and angles and weights are read where they are used:
     // registers are short, and with most of the L1 taken spilled ones cost a trip to the L2
@@ -591,7 +607,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(cons
                     y[n][e] = fma(u[n][e], b2, mul(y[n][e], r2));
                     z[n][e] = fma(v[n][e], b2, mul(z[n][e], r2));
                 }
-                ch.store(dst, n, y[n], z[n]);
+                ch.template store<INTER>(dst, n, y[n], z[n]);
             }
         }
         pipe.end_turn(turn);
