@@ -13,10 +13,10 @@
 // group works on heads of q alone or of k alone, so that its weights are read
 // once, and on several heads of a row, so that the angles are.
 // Measured in a graph, bf16, 8192 rows of 72 heads of 128, three axes: 52 us (5.9 TB/s of
-// the 306 MB, 0.87 of a copy), the gradient 88 (5.2); of 40 heads 32 and 54, in fp32 (4096 rows)
-// 34 and 50.  The gradient waits for its own results (shuffles, reads from shared memory,
+// the 306 MB, 0.87 of a copy), the gradient 88 (5.2); of 40 heads 30 and 51, of 64 15.4 and 30,
+// in fp32 (4096 rows of 128) 29 and 45.  The gradient waits for its own results (shuffles, reads from shared memory,
 // the turn's barrier) with the 14 warps an SM that 128 registers leave.  One token of 64
-// sequences, 40 heads: 2.8 us; the gradient of 333 rows of 40 heads of 64 8.0.
+// sequences, 40 heads: 2.8 us; the gradient of 333 rows of 40 heads of 64 7.8.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -32,7 +32,7 @@ namespace {
 constexpr int kNormMaxThreads = 512, kRowThreads = 256;  // of a block, at most: for few rows, and for many
 constexpr int kNormThreads = 128;                        // and about
 constexpr int kNormHeads = 3;                            // of a group and turn, where there is much work
-constexpr int kRowCtas = 3, kGradCtas = 3;               // blocks per SM, at most
+constexpr int kRowCtas = 4, kGradCtas = 4;               // blocks per SM, at most
 constexpr int kStages = 2;                               // turns on their way to shared memory
 
 // 16-byte pieces on their way, of kStages turns: threads x heads x (tensors x chunks) x 2 pieces.
@@ -456,7 +456,7 @@ struct RowPipe {
 };
 
 template <typename T, int NC, bool INTER, int LT>
-__global__ void __launch_bounds__(kRowThreads) norm_rope_rows_kernel(const __grid_constant__ NormRopeView a) {
+__global__ void __launch_bounds__(kRowThreads, 2) norm_rope_rows_kernel(const __grid_constant__ NormRopeView a) {
     constexpr int VE = VecTraits<T>::kElems, N = VE / 2;
     extern __shared__ __align__(16) unsigned char smem[];
     const Group<LT> g(a);
@@ -719,6 +719,11 @@ Rows plan_rows(NormRopeView &v, const Shape &s, int pieces, int ctas) {
     return r;
 }
 
+// Which kernel: groups of 4, 8 and 16 lanes (heads of 64 and 128 turned whole, in either type) have
+// their own, the rest (32 lanes, 0, and with two chunks a lane, 4) read their number: 40 heads
+// of 64 15.4 us instead of 20, in fp32 of 128 29 instead of 31.
+int lanes_kernel(const Shape &s, bool second) { return second ? 4 : s.block.x == 4 ? 1 : s.block.x == 8 ? 2 : s.block.x == 16 ? 3 : 0; }
+
 template <typename T, bool INTER>
 cudaError_t forward_typed(NormRopeView v, cudaStream_t stream) {
     constexpr int VE = VecTraits<T>::kElems;
@@ -732,11 +737,13 @@ cudaError_t forward_typed(NormRopeView v, cudaStream_t stream) {
         kernel<<<static_cast<unsigned>(s.row_tiles), s.block, 0, stream>>>(v);
         return cudaGetLastError();
     }
-    // (groups of 8 lanes, a head of 128 in bf16, in kernels of their own)
-    static uint64_t ctx[3][128] = {};
+    static uint64_t ctx[5][128] = {};
     const Rows r = plan_rows(v, s, second ? 2 : 1, kRowCtas);
-    const int which = second ? 2 : s.block.x == 8;
-    auto *kernel = which == 1 ? norm_rope_rows_kernel<T, 1, INTER, 8> : norm_rope_rows_kernel<T, 1, INTER, 0>;
+    const int which = lanes_kernel(s, second);
+    auto *kernel = which == 1   ? norm_rope_rows_kernel<T, 1, INTER, 4>
+                   : which == 2 ? norm_rope_rows_kernel<T, 1, INTER, 8>
+                   : which == 3 ? norm_rope_rows_kernel<T, 1, INTER, 16>
+                                : norm_rope_rows_kernel<T, 1, INTER, 0>;
     if constexpr (sizeof(T) == 4)
         if (second) kernel = norm_rope_rows_kernel<T, 2, INTER, 0>;
     const cudaError_t e = allow_smem(kernel, 227 * 1024, ctx[which]);
@@ -750,12 +757,15 @@ cudaError_t backward_typed(NormRopeView v, float *dq_weight, float *dk_weight, c
     constexpr int VE = VecTraits<T>::kElems;
     const Shape s = plan<VE>(v, true, kRowThreads);
     if (!dq_weight && !dk_weight) v.partial = nullptr;
-    static uint64_t ctx[3][128] = {};
+    static uint64_t ctx[5][128] = {};
     const bool second = sizeof(T) == 4 && s.chunks > 32;
     const Rows r = plan_rows(v, s, second ? 4 : 2, kGradCtas);
     const int32_t grid = r.grid, D = v.rope.head_dim;
-    const int which = second ? 2 : s.block.x == 8;
-    auto *kernel = which == 1 ? norm_rope_backward_kernel<T, 1, INTER, 8> : norm_rope_backward_kernel<T, 1, INTER, 0>;
+    const int which = lanes_kernel(s, second);
+    auto *kernel = which == 1   ? norm_rope_backward_kernel<T, 1, INTER, 4>
+                   : which == 2 ? norm_rope_backward_kernel<T, 1, INTER, 8>
+                   : which == 3 ? norm_rope_backward_kernel<T, 1, INTER, 16>
+                                : norm_rope_backward_kernel<T, 1, INTER, 0>;
     if constexpr (sizeof(T) == 4)
         if (second) kernel = norm_rope_backward_kernel<T, 2, INTER, 0>;
     cudaError_t e = allow_smem(kernel, 227 * 1024, ctx[which]);

@@ -112,6 +112,16 @@ def test_norm_rope(dtype, wtype, offset, rows, hq, hk, D, rot, axes, interleaved
     assert status() == 0
 
 
+@pytest.mark.parametrize("dtype,rows,hq,hk,D,rot,axes,interleaved", [
+    ("bf16", 8300, 32, 7, 64, 64, 2, False), ("bf16", 8300, 38, 0, 64, 48, 1, True), ("bf16", 4150, 33, 5, 128, 128, 3, False),
+    ("bf16", 4150, 11, 28, 128, 128, 1, True), ("bf16", 2100, 31, 8, 256, 256, 1, False), ("bf16", 1300, 25, 8, 248, 16, 1, True),
+    ("fp32", 4150, 31, 8, 64, 64, 1, True), ("fp32", 2100, 37, 2, 128, 128, 2, False), ("fp32", 1250, 2, 30, 256, 64, 2, False),
+])
+def test_many_rows(dtype, rows, hq, hk, D, rot, axes, interleaved):
+    """The kernel that takes rows in turns: groups of 4, 8, 16 and 32 lanes, and two chunks a lane."""
+    test_norm_rope(dtype, dtype, True, rows, hq, hk, D, rot, axes, interleaved)
+
+
 def test_gradient_against_differences():
     """The kernel's gradient against central differences of the float64 formula that the forward pass is tested against."""
     rng, q, qd, _, _, cos, sin, pos, ax, w = make(3, 2, 0, 32, 16, 2, "fp32")
