@@ -253,13 +253,89 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
     uint32_t taken = 0;  // steps the warp has used
     uint32_t i0 = 0;     // steps of the items before
     // (the warp has looked at its next step, so the item's entry, which came with its first step's batch, is there)
+    auto item = [&](uint32_t n) {
+        const int4 *const entry = reinterpret_cast<const int4 *>(&sm.items[n % kItemRing]);
+        const int4 e0 = entry[0], e1 = entry[1];
+        return Item4{e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+    };
+    // What the warps have written of item n joined, each thread some of a row's dimensions.
+    auto finish = [&](uint32_t n) {
+        wait(&sm.merge_full, n & 1u, 48);
+        const Item4 it = item(n);
+        const int32_t off = it.off, head = it.head, row0 = it.row_tile * ROWS, last_cta = it.last_cta;
+        const int32_t rows = min(ROWS, it.n * a.group - row0);
+        const bool whole = last_cta == kWhole;
+        // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
+        float *part = partial_at(a, blockIdx.x, last_cta >= 0 ? 1 : 0, kSlotRows, D);
+        if (last_cta >= 0 && threadIdx.x == 0)
+            join_entries(a, gridDim.x, kSlotRows, D)[blockIdx.x] = JoinEntry{last_cta, head, off, row0, rows, {}};
+        constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
+        const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
+        if (rt < rows) {
+            float M = -INFINITY, L = 0.0f, f[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][rt]);
+            const float mu = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                f[w] = ex2(sm.m[w][rt] - mu);
+                L = fmaf(sm.l[w][rt], f[w], L);
+            }
+            // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
+            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f;
+            const int32_t row = row0 + rt;
+            const int32_t qi = row / a.group, qh = head * a.group + row % a.group;
+            T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(off + qi) * a.out.row + qh * a.out.head;
+#pragma unroll
+            for (int c = c0 * 4; c < D; c += PER_ROW * 4) {
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][rt][c]);
+                    v.x = fmaf(x.x, f[w], v.x);
+                    v.y = fmaf(x.y, f[w], v.y);
+                    v.z = fmaf(x.z, f[w], v.z);
+                    v.w = fmaf(x.w, f[w], v.w);
+                }
+                if (whole) store4(dst + c, v, inv);
+                else store4(part + rt * D + c, v, inv);
+            }
+            if (c0 == 0) {
+                const float lse = M + log2f(L);
+                if (!whole) {
+                    part[kSlotRows * D + rt] = lse;
+                } else if (a.lse) {
+                    a.lse[static_cast<int64_t>(off + qi) * a.q_heads + qh] = lse * kLn2;
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.merge_empty);
+    };
+    constexpr int VE = VecTraits<T>::kElems;
     for (uint32_t ni = 0;; ++ni) {
         if (__any_sync(0xffffffffu, *dead)) break;
-        const int4 *const entry = reinterpret_cast<const int4 *>(&sm.items[ni % kItemRing]);
-        const int4 e0 = entry[0], e1 = entry[1];
-        const Item4 it{e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
-        if (it.n == 0) break;
+        const Item4 it = item(ni);
+        if (it.n == 0) {
+            if (ni > 0) finish(ni - 1);
+            break;
+        }
         const int32_t rows = min(ROWS, it.n * a.group - it.row_tile * ROWS);
+        // The lane's part of the queries (dimensions 64 h + 16 tig + 0..15 of row 8 u + g; rows past the last repeat
+        // it), on their way while the item before is finished, for which the other warps have had time to
+        // write theirs
+        uint4 q_raw[RT][H][16 / VE];
+#pragma unroll
+        for (int u = 0; u < RT; ++u) {
+            const int32_t row = it.row_tile * ROWS + min(8 * u + g, rows - 1);
+            const int32_t qi = row / a.group, qh = it.head * a.group + row % a.group;
+            const T *src = static_cast<const T *>(a.q.p) + static_cast<int64_t>(it.off + qi) * a.q.row + qh * a.q.head;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int e = 0; e < 16 / VE; ++e) q_raw[u][h][e] = *reinterpret_cast<const uint4 *>(src + 64 * h + 16 * tig + e * VE);
+        }
+        if (ni > 0) finish(ni - 1);
         const int32_t key_end = min(it.tile1 * kKvTile, it.len);
         // q as B fragments: column g of tile u is row 8 u + g, dimensions 64 h + 16 tig +
         // 4 j + 0..3 in k-step (h, j), the last two by kUnit0 / kUnit1
@@ -271,16 +347,14 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         int32_t kmin[RT][2], kmax[RT][2];
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
-            const int32_t row = it.row_tile * ROWS + min(8 * u + g, rows - 1);  // rows past the last repeat it
-            const int32_t qi = row / a.group, qh = it.head * a.group + row % a.group;
-            const T *src = static_cast<const T *>(a.q.p) + static_cast<int64_t>(it.off + qi) * a.q.row + qh * a.q.head;
+            const int32_t row = it.row_tile * ROWS + min(8 * u + g, rows - 1);
+            const int32_t qi = row / a.group;
             float x[D / 4];
             float amax = 0.0f;
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int e = 0; e < 16; e += VecTraits<T>::kElems)
-                    VecTraits<T>::load(src + 64 * h + 16 * tig + e, x + 16 * h + e);
+                for (int e = 0; e < 16 / VE; ++e) VecTraits<T>::load(reinterpret_cast<const T *>(&q_raw[u][h][e]), x + 16 * h + e * VE);
 #pragma unroll
             for (int e = 0; e < D / 4; ++e) amax = fmaxf(amax, fabsf(x[e]));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -577,7 +651,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         }
         i0 += steps;
 
-        // ---- merge the warps
+        // ---- the warp's part, for the merge
         wait(&sm.merge_empty, (ni & 1u) ^ 1u, 47);  // the buffer has been read
 #pragma unroll
         for (int u = 0; u < RT; ++u)
@@ -616,57 +690,6 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
             }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.merge_full);
-        wait(&sm.merge_full, ni & 1u, 48);
-        // (the entry again, instead of registers that would be held throughout)
-        const volatile Item4 &me = sm.items[ni % kItemRing];
-        const int32_t off = me.off, head = me.head, row0 = me.row_tile * ROWS, last_cta = me.last_cta;
-        const bool whole = last_cta == kWhole;
-        // an item that goes on in the next CTA is joined by the entry of the CTA it begins in
-        float *part = partial_at(a, blockIdx.x, last_cta >= 0 ? 1 : 0, kSlotRows, D);
-        if (last_cta >= 0 && threadIdx.x == 0)
-            join_entries(a, gridDim.x, kSlotRows, D)[blockIdx.x] = JoinEntry{last_cta, head, off, row0, rows, {}};
-        constexpr int PER_ROW = kWarps * 32 / ROWS;  // threads a row
-        const int rt = threadIdx.x / PER_ROW, c0 = threadIdx.x % PER_ROW;
-        if (rt < rows) {
-            float M = -INFINITY, L = 0.0f, f[kWarps];
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][rt]);
-            const float mu = M == -INFINITY ? 0.0f : M;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                f[w] = ex2(sm.m[w][rt] - mu);
-                L = fmaf(sm.l[w][rt], f[w], L);
-            }
-            // (a part of an item may have no key that the row sees: nothing, not 0 / 0)
-            const float inv = whole || !(L == 0.0f) ? 1.0f / L : 0.0f;
-            const int32_t row = row0 + rt;
-            const int32_t qi = row / a.group, qh = head * a.group + row % a.group;
-            T *dst = static_cast<T *>(a.out.p) + static_cast<int64_t>(off + qi) * a.out.row + qh * a.out.head;
-#pragma unroll
-            for (int c = c0 * 4; c < D; c += PER_ROW * 4) {
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][rt][c]);
-                    v.x = fmaf(x.x, f[w], v.x);
-                    v.y = fmaf(x.y, f[w], v.y);
-                    v.z = fmaf(x.z, f[w], v.z);
-                    v.w = fmaf(x.w, f[w], v.w);
-                }
-                if (whole) store4(dst + c, v, inv);
-                else store4(part + rt * D + c, v, inv);
-            }
-            if (c0 == 0) {
-                const float lse = M + log2f(L);
-                if (!whole) {
-                    part[kSlotRows * D + rt] = lse;
-                } else if (a.lse) {
-                    a.lse[static_cast<int64_t>(off + qi) * a.q_heads + qh] = lse * kLn2;
-                }
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.merge_empty);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
