@@ -23,9 +23,9 @@
 // Bound by the warps' instructions (issue slots 55% used with three warps a quarter of the
 // SM, of which each instruction waits for some before it; the codes' ANDs half of the ALU), then by
 // memory, half a byte a value and 1/16 of scales.  64 query heads on 8 of 128, in a graph: one
-// token of each of 256 sequences of some 4096, 1.04 GB, 201 us (5.2 TB/s; its floor is 154); of
-// 64 sequences of 4097 68.6 us, with 128 query heads 110, in fp32 117.  One token of one sequence of
-// 2000: 10.1.  4 queries of 64 sequences, 32 heads of 64 on 8, in a window of 1024: 28.6.
+// token of each of 256 sequences of some 4096, 1.04 GB, 197 us (5.3 TB/s; its floor is 154); of
+// 64 sequences of 4097 68.3 us, with 128 query heads 106, in fp32 115.  One token of one sequence of
+// 2000: 10.1.  4 queries of 64 sequences, 32 heads of 64 on 8, in a window of 1024: 28.5.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -67,10 +67,12 @@ struct Item4 {
 static_assert(sizeof(Item4) == 32, "two 16-byte pieces");
 constexpr int32_t kWhole = -1, kNotFirst = -2;
 // What beginning and ending an item costs, in units of 128 keys.  Without it CTAs that
-// get many short items take twice as long as the others: 4 queries of 64 sequences in a
-// window of 1024 take 45.6 us with 0, 33.8 with 1, 31.1 with 2, 29.2 with 4 and 28.7 with 6; one
-// token of 256 sequences of some 4096 231, 219, 209, 208 and 214.
-constexpr int kItemUnits = 4;
+// get many short items take twice as long as the others (4 queries of 64 sequences, heads of 64, in a
+// window of 1024: 46 us).  One token of 256 sequences of some 4096 took 197, 199 and 201 us with 2, 3
+// and 4, of some 500 46, 48 and 50; 4 queries of 256 sequences of some 700, heads of 64, 58.8, 57.0 and
+// 59.5, in that window 29.1, 28.5 and 27.8.
+template <int D, int NT>
+__host__ __device__ constexpr int item_units() { return D == 128 && NT == 1 ? 2 : 3; }
 constexpr float kSlack = 8.0f;                    // log2 by which a score may pass the row's maximum so far
 constexpr int kTopExponent = 8;                   // a row's largest p' begins in [2^8, 2^9)
 constexpr float kMostFactor = 1.152921504606847e18f;  // 2^60: fr of rows without a scale so far
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
         sm.dead = 0;
         join_entries(a, gridDim.x, kSlotRows, D)[blockIdx.x].last_cta = -1;
     }
-    const Range range = plan_line<ROWS, kThreads, kItemUnits>(a, sm.warp_sum, &sm.seq, &sm.base);
+    const Range range = plan_line<ROWS, kThreads, item_units<D, NT>()>(a, sm.warp_sum, &sm.seq, &sm.base);
     volatile int32_t *dead = &sm.dead;
     const uint64_t limit = a.test_wait_ns ? a.test_wait_ns : kWaitNs;
 
