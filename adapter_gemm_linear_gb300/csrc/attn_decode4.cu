@@ -20,8 +20,8 @@
 //    lane; only a raise takes shuffles.
 //  - A warp takes two tiles a step, whose fixed instructions (waits, looks, the checks)
 //    are shared by 32 tokens.
-// Bound by the warps' instructions (issue slots 55% used with three warps a quarter of the
-// SM, of which each instruction waits for some before it; the codes' ANDs half of the ALU), then by
+// Bound by the warps' instructions (issue slots 56% used with three warps a quarter of the
+// SM, of which each instruction waits for some before it; the ALU busy for 52%), then by
 // memory, half a byte a value and 1/16 of scales.  64 query heads on 8 of 128, in a graph: one
 // token of each of 256 sequences of some 4096, 1.04 GB, 197 us (5.3 TB/s; its floor is 154); of
 // 64 sequences of 4097 68.3 us, with 128 query heads 106, in fp32 115.  One token of one sequence of
