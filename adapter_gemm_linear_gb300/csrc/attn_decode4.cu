@@ -16,8 +16,9 @@
 //  - p' = p s enters as f16 times a factor fr of the row, a power of two that is
 //    lowered (with the row's sums) when a p' would leave f16's range, and first set
 //    so that the row's largest p' is in [2^8, 2^9); p itself is relative to a maximum
-//    that is raised when a score passes it by kSlack.  Both are looked at lane by
-//    lane; only a raise takes shuffles.
+//    that is raised when a score passes it by kSlack, and fr is raised with it, so
+//    that the largest p' there is stays above 2^8 (or fr is 2^60).  Both are looked
+//    at lane by lane; only a raise takes shuffles.
 //  - A warp takes two tiles a step, whose fixed instructions (waits, looks, the checks)
 //    are shared by 32 tokens.
 // Bound by the warps' instructions (issue slots 56% used with three warps a quarter of the
@@ -532,35 +533,18 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                     }
                 grow = grow || top[u].x > m[u][0] + kSlack || top[u].y > m[u][1] + kSlack;  // (also from m = -inf)
             }
-            if (__any_sync(0xffffffffu, grow)) {
+            auto probabilities = [&] {  // and l
 #pragma unroll
-                for (int u = 0; u < RT; ++u) {
-                    float f[2];
+                for (int u = 0; u < RT; ++u)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float mx = fmaxf(m[u][i], i ? top[u].y : top[u].x);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        f[i] = m[u][i] == -INFINITY ? 0.0f : ex2(m[u][i] - mx);
-                        m[u][i] = mx;
-                    }
-                    less[u] = two(m[u][0] == -INFINITY ? 0.0f : -m[u][0], m[u][1] == -INFINITY ? 0.0f : -m[u][1]);
-                    l[u] = mul(l[u], two(f[0], f[1]));
-                    rescale(u, two(f[0], f[1]));
-                }
-            }
-            // probabilities, and l
+                    for (int j = 0; j < TS; ++j)
 #pragma unroll
-            for (int u = 0; u < RT; ++u)
-#pragma unroll
-                for (int j = 0; j < TS; ++j)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const float2 x = apart(add(z[j][u][t], less[u]));
-                        z[j][u][t] = two(ex2(x.x), ex2(x.y));
-                        l[u] = add(l[u], z[j][u][t]);
-                    }
+                        for (int t = 0; t < 2; ++t) {
+                            const float2 x = apart(add(z[j][u][t], less[u]));
+                            z[j][u][t] = two(ex2(x.x), ex2(x.y));
+                            l[u] = add(l[u], z[j][u][t]);
+                        }
+            };
             // p' = p s fr, rows side by side: [.., token half]
             uint32_t ph[TS][H][NT][2];
             auto scaled = [&] {
@@ -584,36 +568,73 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                         }
                 return ((over + 0x04000400u) & 0x80008000u) != 0;  // (7C00 in either half)
             };
-            if (__any_sync(0xffffffffu, scaled())) {
+            // fr anew, `most` at most; f: what m's change makes of the row's sums
+            auto fit = [&](int u, float2 f, float2 most) {
+                float2 largest = make_float2(0.0f, 0.0f);  // of p s
+#pragma unroll
+                for (int j = 0; j < TS; ++j)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            const float2 x = apart(z[j][u][t]);
+                            const float vs = f16_pair(vmeta[j][t][h]).x;
+                            largest = make_float2(fmaxf(largest.x, x.x * vs), fmaxf(largest.y, x.y * vs));
+                        }
+                float now[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = i ? largest.y : largest.x;
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    // 2^(8 - exponent of the largest), where that is less
+                    const int e = static_cast<int>(__float_as_uint(x) >> 23) - 127;
+                    now[i] = fminf(__uint_as_float(static_cast<uint32_t>(127 + min(max(kTopExponent - e, -60), 60)) << 23), i ? most.y : most.x);
+                }
+                const float2 was = apart(fr[u]);
+                rescale(u, two(f.x * (now[0] / was.x), f.y * (now[1] / was.y)));
+                fr[u] = two(now[0], now[1]);
+            };
+            if (__any_sync(0xffffffffu, grow)) {
+                // A row's fr may be raised with its m, by the next power of two, so that it goes by what the keys
+                // weigh now: with the fr of large scales that have lost their weight later p' would sink to f16's
+                // least steps.  Rows that do not pass m by kSlack keep it.
+                float2 f[RT], most[RT];
 #pragma unroll
                 for (int u = 0; u < RT; ++u) {
-                    float2 most = make_float2(0.0f, 0.0f);  // of p s
-#pragma unroll
-                    for (int j = 0; j < TS; ++j)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int h = 0; h < H; ++h) {
-                                const float2 x = apart(z[j][u][t]);
-                                const float vs = f16_pair(vmeta[j][t][h]).x;
-                                most = make_float2(fmaxf(most.x, x.x * vs), fmaxf(most.y, x.y * vs));
-                            }
                     const float2 was = apart(fr[u]);
-                    float now[2];
+                    float fi[2], mi[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float x = i ? most.y : most.x;
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        // 2^(8 - exponent of the largest), where that is less than what there is
-                        const int e = static_cast<int>(__float_as_uint(x) >> 23) - 127;
-                        now[i] = fminf(__uint_as_float(static_cast<uint32_t>(127 + min(max(kTopExponent - e, -60), 60)) << 23), i ? was.y : was.x);
+                        const float old = m[u][i];
+                        float mx = fmaxf(old, i ? top[u].y : top[u].x);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        if (!(mx > old + kSlack)) mx = old;
+                        m[u][i] = mx;
+                        const float more = old == -INFINITY ? 0.0f : mx - old;
+                        fi[i] = old == -INFINITY ? 0.0f : ex2(-more);
+                        const uint32_t up = static_cast<uint32_t>(127 + static_cast<int>(ceilf(fminf(more, 120.0f)))) << 23;
+                        mi[i] = fminf((i ? was.y : was.x) * __uint_as_float(up), kMostFactor);
                     }
-                    rescale(u, two(now[0] / was.x, now[1] / was.y));
-                    fr[u] = two(now[0], now[1]);
+                    less[u] = two(m[u][0] == -INFINITY ? 0.0f : -m[u][0], m[u][1] == -INFINITY ? 0.0f : -m[u][1]);
+                    f[u] = make_float2(fi[0], fi[1]);
+                    most[u] = make_float2(mi[0], mi[1]);
+                    l[u] = mul(l[u], two(fi[0], fi[1]));
                 }
+                probabilities();
+#pragma unroll
+                for (int u = 0; u < RT; ++u) fit(u, f[u], most[u]);
                 scaled();
+            } else {
+                probabilities();
+                if (__any_sync(0xffffffffu, scaled())) {
+#pragma unroll
+                    for (int u = 0; u < RT; ++u) fit(u, make_float2(1.0f, 1.0f), apart(fr[u]));
+                    scaled();
+                }
             }
 #pragma unroll
             for (int j = 0; j < TS; ++j)

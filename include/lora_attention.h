@@ -285,7 +285,8 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * LORA_KV_UINT4: in every fp32 call, and where a bf16 call takes the kernel for few
  * queries, codes enter the products exactly, scales and least values in fp32: each p_j
  * times the token's scale has 22 and 11 bits, and is off by at most 2^-44 and 2^-33 of
- * the row's largest such product beyond that.  Where a bf16 call takes the one for many,
+ * the row's largest such product beyond that (and by 2^-96 and 2^-85 of the sum of all p_j).
+ * (fp32 calls take a value as scale (code - 8) and least + 8 scale.)  Where a bf16 call takes the one for many,
  * V's values enter rounded to f16 (11 bits), and a p_j is off by at most 2^-29 of the
  * row's largest beyond its 11 bits; K's values enter exactly if lse is given, else rounded
  * to f16, so that `out` of the same call with and without lse may differ in its last bits.
