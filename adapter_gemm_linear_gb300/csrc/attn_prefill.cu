@@ -311,9 +311,10 @@ __device__ __forceinline__ void issue_scores(PrefillSmem<D, FMT> &sm, uint32_t X
 }
 
 // Of the 4-bit cache: K's value s code + m = (code - 8) s_a + (code - 8) s_b + (m + 8 s), s_a
-// the upper seven bits of s and s_b the rest, so that both products are f16 values
-// exactly: two tiles.  The last term is one column for all dimensions of a block,
-// against the sum of q over them, which has two f16 parts: m and 8 s twice each.  There is
+// the upper seven bits of s, but not above 8128, and s_b the rest, so that both products
+// are f16 values exactly (s is 8733 at most, where least and largest value are f16's):
+// two tiles.  The last term is one column for all dimensions of a block, against the
+// sum of q over them, which has two f16 parts: m twice, and 4 s twice against twice that.  There is
 // room for one stage of the two tiles; each is given back and filled anew by itself
 // (barriers 0 and 1 of k_full and k_empty), so that the first of the next keys is there
 // when the last product with the second of these ends: 2048 queries on 34816 keys 1137 us
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
             const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
             sm.q_exponent[n_q & 1u][X * kHalf + wq * 32 + lane] = static_cast<int8_t>(e);
             float sum = 0.0f;
-            uint32_t sums[4] = {0u, 0u, 0u, 0u};  // of 64 dimensions, in two parts, twice
+            uint32_t sums[4] = {0u, 0u, 0u, 0u};  // of 64 dimensions, in two parts, and twice that
 #pragma unroll 2
             for (int i = 0; i < D / 8; ++i) {
                 uint4 *at = q_place(X, lane, i);
@@ -848,7 +849,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 if constexpr (PARTS) {
                     if (i % 8 == 7) {
                         const float hi = __half2float(__float2half_rn(sum));
-                        sums[2 * (i / 8)] = sums[2 * (i / 8) + 1] = pack_h2(hi, sum - hi);
+                        sums[2 * (i / 8)] = pack_h2(hi, sum - hi);
+                        sums[2 * (i / 8) + 1] = pack_h2(2.0f * hi, 2.0f * (sum - hi));
                         sum = 0.0f;
                     }
                 }
@@ -895,7 +897,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const uint32_t y = sc[(i / H * 2 * H + i % H) * kKvTile + tok + 2 * t], s2 = __byte_perm(y, y, 0x1010);
-                            const uint32_t sa = s2 & 0xFFF0FFF0u, by = part == 0 ? sa : less(s2, sa), m2 = __byte_perm(y, y, 0x3232);
+                            const uint32_t sa = at_most(s2 & 0xFFF0FFF0u, 0x6FF06FF0u), by = part == 0 ? sa : less(s2, sa), m2 = __byte_perm(y, y, 0x3232);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 uint32_t f[4];
@@ -910,12 +912,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 };
                 if constexpr (PARTS) {
                     wait(&sm.k_empty[0], stage ^ 1u, 61);
-                    uint32_t w[4] = {0u, 0u, 0u, 0u};  // a key a lane: least values, and 8 scales
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};  // a key a lane: least values, and 4 scales
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         const uint32_t y = sc[(lane / kKvTile * 2 * H + h) * kKvTile + lane % kKvTile];
                         w[2 * h] = __byte_perm(y, y, 0x3232);
-                        w[2 * h + 1] = times(__byte_perm(y, y, 0x1010), 0x48004800u);
+                        w[2 * h + 1] = times(__byte_perm(y, y, 0x1010), 0x44004400u);
                     }
                     extra(sm.kx, wq * 32 + lane, w);
                 }
