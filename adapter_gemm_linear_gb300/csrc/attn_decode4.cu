@@ -511,12 +511,24 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                             if (key < kmin[u][1] || key >= kmax[u][1]) x.y = -INFINITY;
                             z[j][u][t] = two(x.x, x.y);
                         }
-                    // scales of V past the sequence's end are whatever was there, and 0 * NaN is not 0
+                    // Scales and least values of V may be NaN or infinite, and 0 * NaN is not 0: past the sequence's
+                    // end they are whatever was there, and of other keys they are for the rows that see them, whose om
+                    // becomes NaN
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                    for (int t = 0; t < 2; ++t) {
+                        const int32_t key = key0 + j * kKvTile + tok + 2 * t;
 #pragma unroll
-                        for (int h = 0; h < H; ++h)
-                            if (key0 + j * kKvTile + tok + 2 * t >= key_end) vmeta[j][t][h] = 0;
+                        for (int h = 0; h < H; ++h) {
+                            const bool number = (((vmeta[j][t][h] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u) == 0;  // both
+                            if (!number && key < key_end) {
+#pragma unroll
+                                for (int u = 0; u < RT; ++u)
+                                    om[u][h] = add(om[u][h], two(key >= kmin[u][0] && key < kmax[u][0] ? NAN : 0.0f,
+                                                                 key >= kmin[u][1] && key < kmax[u][1] ? NAN : 0.0f));
+                            }
+                            if (!number || key >= key_end) vmeta[j][t][h] = 0;
+                        }
+                    }
                 }
             }
             float2 top[RT];  // the lane's largest scores
@@ -579,7 +591,8 @@ __global__ void __launch_bounds__((consumers<D, NT>() + 1) * 32, ctas_per_sm<D, 
                         for (int h = 0; h < H; ++h) {
                             const float2 x = apart(z[j][u][t]);
                             const float vs = f16_pair(vmeta[j][t][h]).x;
-                            largest = make_float2(fmaxf(largest.x, x.x * vs), fmaxf(largest.y, x.y * vs));
+                            const float2 ps = make_float2(x.x * vs, x.y * vs);  // (infinite ones are for their own dimensions)
+                            largest = make_float2(ps.x < INFINITY ? fmaxf(largest.x, ps.x) : largest.x, ps.y < INFINITY ? fmaxf(largest.y, ps.y) : largest.y);
                         }
                 float now[2];
 #pragma unroll

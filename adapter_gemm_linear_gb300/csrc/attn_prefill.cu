@@ -127,7 +127,7 @@ struct PrefillSmem : Codes<D, FMT> {
     long long warp_sum[kPreThreads / 32];
     long long base;
     int32_t seq;
-    int32_t nan_item[kItemRing];      // number (from 1) of the last item with a NaN hidden in V, by number
+    int32_t nan_item[kItemRing];      // number (from 1) of the last item with a NaN (4 bits: or infinity) hidden in V, by number
     int32_t head0, row_tile0, skip0;  // where the CTA's line begins
     uint32_t tmem;
     int32_t dead;
@@ -346,8 +346,9 @@ __device__ __forceinline__ void issue_values(PrefillSmem<D, FMT> &sm, uint32_t X
 // Of dimensions [d0, d0 + 32): a bit for each in which V is NaN at a key that
 // the row sees, [kmin, kmax), in one of the tiles [tile0, tile1) that not
 // every row sees whole.  (In those NaN codes are taken as 0 by the product,
-// as p = 0 would not keep them from the rows that do not see the key.)
-template <int D>
+// as p = 0 would not keep them from the rows that do not see the key.)  Of the
+// 4-bit cache: values that are no f16 numbers, by their scale and least value.
+template <int D, int FMT>
 __device__ __noinline__ uint32_t nan_dims(const KvView &b, int32_t seq, int32_t head, int32_t tile0, int32_t tile1, int32_t all_lo,
                                           int32_t all_hi, int32_t kmin, int32_t kmax, int32_t d0) {
     uint32_t mask = 0;
@@ -355,7 +356,15 @@ __device__ __noinline__ uint32_t nan_dims(const KvView &b, int32_t seq, int32_t 
         const int32_t key0 = k & ~(kKeys - 1);
         if ((key0 >= all_lo && key0 + kKeys <= all_hi) || k >= kmax || k + kKvTile <= kmin) continue;
         const int32_t page = b.table[static_cast<int64_t>(seq) * b.max_pages + (k >> b.page_shift)];
-        if (page < 0 || page >= b.num_pages || !(b.v_scales[static_cast<int64_t>(page) * b.heads + head] > 0.0f)) continue;
+        if (page < 0 || page >= b.num_pages) continue;
+        if (FMT == LORA_KV_UINT4) {
+            const uint32_t *scales = reinterpret_cast<const uint32_t *>(b.v_scales) +
+                                     (tile_index(b, page, head, (k & (b.page_tokens - 1)) / kKvTile) * (D / kBlockDims) + d0 / kBlockDims) * kKvTile;
+            for (int t = max(0, kmin - k); t < min(kKvTile, kmax - k); ++t)
+                if (!are_numbers(scales[t])) mask = ~0u;
+            continue;
+        }
+        if (!(b.v_scales[static_cast<int64_t>(page) * b.heads + head] > 0.0f)) continue;
         const uint32_t *v = reinterpret_cast<const uint32_t *>(
             b.v_pages + tile_offset<D>(b, page, head, (k & (b.page_tokens - 1)) / kKvTile));
         for (int q = 0; q < 4; ++q) {
@@ -671,15 +680,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 inv *= half;
                 vr *= -half;
             }
-            const bool hidden = FMT == LORA_KV_E4M3 && *static_cast<volatile int32_t *>(&sm.nan_item[n_item % kItemRing]) == static_cast<int32_t>(n_item);
+            const bool hidden = FMT != LORA_KV_INT8 && *static_cast<volatile int32_t *>(&sm.nan_item[n_item % kItemRing]) == static_cast<int32_t>(n_item);
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(to + 32 * i, o);
                 tmem_ld_wait(o);
                 if (rt < rows) {
-                    if (FMT == LORA_KV_E4M3 && __builtin_expect(hidden, 0)) {
-                        const uint32_t nan = nan_dims<D>(b, it.seq, it.head, it.tile0, it.tile1, all_lo, all_hi, kmin, kmax, 32 * i);
+                    if (FMT != LORA_KV_INT8 && __builtin_expect(hidden, 0)) {
+                        const uint32_t nan = nan_dims<D, FMT>(b, it.seq, it.head, it.tile0, it.tile1, all_lo, all_hi, kmin, kmax, 32 * i);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (nan >> e & 1u) o[e] = 0x7FFFFFFFu;
@@ -959,6 +968,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 // keys past the end: scale and least value 0 (what is there may be NaN)
                 const int have = cur.len - (cur.key0 + wq * 32 + cc * 8);
                 const uint32_t *const sc = sm.meta[n_tile & 1][wq];
+                if (cur.edge) {
+                    // what is no number at keys that not every row sees: taken out, and noted for the item (nan_dims)
+                    const uint32_t item = n_q + (first ? 1u : 0u);
+                    bool some = false;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        uint32_t *const w = &sm.meta[n_tile & 1][wq][(lane / kKvTile * 2 * H + H + h) * kKvTile + lane % kKvTile];
+                        if (cur.key0 + wq * 32 + lane < cur.len && !are_numbers(*w)) {
+                            *w = 0u;
+                            some = true;
+                        }
+                    }
+                    if (some) sm.nan_item[item % kItemRing] = static_cast<int32_t>(item);
+                    __syncwarp();
+                }
 #pragma unroll 1
                 for (int h = 0; h < H; ++h) {
                     const uint4 *y = reinterpret_cast<const uint4 *>(sc + ((cc >> 1) * 2 * H + H + h) * kKvTile + (cc & 1) * 8);

@@ -76,4 +76,10 @@ __device__ __forceinline__ void nibbles_less(uint32_t w, uint32_t (&f)[4]) {
 
 __device__ __forceinline__ float2 f16_pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
+// Whether the values of a (scale, least) pair, s code + m with codes 0 to 15, are f16 numbers.
+__device__ __forceinline__ bool are_numbers(uint32_t w) {
+    const float2 y = f16_pair(w);
+    return fabsf(y.y) < 65520.0f && fabsf(fmaf(15.0f, y.x, y.y)) < 65520.0f;
+}
+
 }  // namespace lora

@@ -268,7 +268,9 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  *
  * Query head h reads key/value head h / (num_q_heads / num_heads).  A query
  * that sees no key (padding, skipped sequences) has out = 0 and lse = -inf.
- * A NaN in the cache reaches the queries that see its token, and no others.
+ * A NaN in the cache reaches the queries that see its token, and no others; of
+ * LORA_KV_UINT4 so does a scale or least value that is infinite or NaN, of V in its 64
+ * dimensions (which become NaN or infinite).
  * Rows outside every sequence are not written.
  * max_queries bounds the rows of one sequence (it and max_pages choose the kernel); a
  * sequence with more rows is recorded (SEGMENTS) and skipped.
