@@ -302,7 +302,7 @@ struct RowPipe {
     // shared memory where they do in global memory, else each half sector is a request of its own
     // and sectors are read twice (8192 rows of 72 heads 70 us instead of 52, their gradient 109 instead of 88): [piece][thread]; interleaved, where a
     // thread's two pieces are a sector, [thread][piece], in an order that keeps 8 threads off each
-    // other's banks.
+    // other's banks (and at a multiple of 32 bytes, so that an exclusive or finds the second).
     uint32_t ring;
     uint32_t stride;  // bytes of a piece of all threads
     float *angles;  // [stage, one more][row of the block][cosines, sines][pair]
@@ -458,7 +458,7 @@ struct RowPipe {
 template <typename T, int NC, bool INTER, int LT>
 __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_rows_kernel(const __grid_constant__ NormRopeView a) {
     constexpr int VE = VecTraits<T>::kElems, N = VE / 2;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(32) unsigned char smem[];
     const Group<LT> g(a);
     const Chunks<T, NC, LT> ch(a, g);
     const HeadsView in[1] = {g.is_k ? a.rope.k : a.rope.q}, &out = g.is_k ? a.rope.k_out : a.rope.q_out;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_rows_kernel(const __
 template <typename T, int NC, bool INTER, int LT>
 __global__ void __launch_bounds__(kRowThreads, 2) norm_rope_backward_kernel(const __grid_constant__ NormRopeView a) {
     constexpr int VE = VecTraits<T>::kElems, N = VE / 2;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(32) unsigned char smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Group<LT> g(a);
     const Chunks<T, NC, LT> ch(a, g);
