@@ -1248,6 +1248,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                 const int32_t all_hi = a.causal ? len - n + row_tile * kRows / a.group + 1 : len;
                 const int32_t last_row = min((row_tile + 1) * kRows, n * a.group) - 1;
                 const int32_t all_lo = a.window > 0 ? len - n + last_row / a.group - a.window + 1 : 0;
+                // and the first that some row sees (pages that lie before it may be gone)
+                const int32_t some_lo = a.window > 0 ? len - n + row_tile * kRows / a.group - a.window + 1 : 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.item_empty[e]);
                 ++n_item;
@@ -1257,7 +1259,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attn_prefill_kernel(const __gr
                     const int32_t t = t0 + (lane >> 3), key = t * kKeys + sub * kKvTile;
                     int64_t at = -1;
                     float ks = 0.0f, vs = 0.0f;
-                    if (t < tile1 && key < len) {
+                    if (t < tile1 && key < len && key + kKvTile > some_lo) {
                         const int32_t page = read_page(b, seq, key >> b.page_shift);
                         if (page >= 0 && FMT == LORA_KV_UINT4) {
                             at = tile_index(b, page, head, (key & (b.page_tokens - 1)) / kKvTile);

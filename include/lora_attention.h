@@ -271,7 +271,8 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * A NaN in the cache reaches the queries that see its token, and no others; of
  * LORA_KV_UINT4 so does a scale or least value that is infinite or NaN, of V in its 64
  * dimensions (which become NaN or infinite).
- * Rows outside every sequence are not written.
+ * Rows outside every sequence are not written.  Pages that no row of a sequence sees
+ * (before its window) are not needed: their table entries may name no page.
  * max_queries bounds the rows of one sequence (it and max_pages choose the kernel); a
  * sequence with more rows is recorded (SEGMENTS) and skipped.
  * Precision: products with the codes exact, fp32 sums.  A probability p_j
