@@ -410,8 +410,9 @@ class KvCache:
         offsets, else all rows).  It and the block table's width, as a bound on
         the lengths, choose the kernel for bf16 queries: a table much wider than
         its longest sequence needs costs short calls of several queries some
-        time, and the same call with another width may differ in its last bits
-        (of a "uint4" cache also the same call with and without lse).
+        time, and the same call with another width may differ in its last bits.
+        Of a "uint4" cache prompts take K's values rounded to 11 bits unless an
+        lse is asked for: ask for it where keys lie far from 0 in all dimensions.
         ``window`` > 0 limits a query to the last ``window`` positions up to its
         own; ``scale`` defaults to head_dim^-0.5.
         ``stream``: launch there instead of on the current stream."""

@@ -9,7 +9,10 @@
 // By their bytes both are bound by memory (a value read in its dtype, half a byte and 1/16
 // byte of scales written, or the other way round).  Measured, 8 heads of 128, bf16: 262144 tokens
 // read back in 214 us (6.4 TB/s, 0.95 of a copy); 8192 tokens of 16 prompts written in 18.4 and read
-// back in 12 (24.6 together in a graph), one of each of 256 sequences in 9.4 and 8.5 (12.0).  Of the
+// back in 12 (24.6 together in a graph), one of each of 256 sequences in 9.4 and 8.5 (12.0).
+// (These one by one under a profiler, from a cold L2; in a graph, segments of 512, 14.6 and 9.0, in fp32 18.6
+// and 14.0; a token of 256 sequences 6.0 and 4.3, in fp32 6.7 and 4.8; 65536 tokens of 64 sequences 116 and
+// 57, in fp32 141 and 99.)  Of the
 // write 60% of the issue slots are used, by 25 warps an SM: 22 instructions for a value and
 // lane; the rest is reads that wait for each other (sequence, page, row).
 #include <cuda_runtime.h>

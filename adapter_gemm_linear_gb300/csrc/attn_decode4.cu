@@ -21,12 +21,14 @@
 //    at lane by lane; only a raise takes shuffles.
 //  - A warp takes two tiles a step, whose fixed instructions (waits, looks, the checks)
 //    are shared by 32 tokens.
-// Bound by the warps' instructions (issue slots 56% used with three warps a quarter of the
-// SM, of which each instruction waits for some before it; the ALU busy for 52%), then by
+// As it is laid out it is bound by the warps' instructions (issue slots 56% used with three warps a
+// quarter of the SM, of which each instruction waits for some before it; the ALU busy for 52%), then by
 // memory, half a byte a value and 1/16 of scales.  64 query heads on 8 of 128, in a graph: one
-// token of each of 256 sequences of some 4096, 1.04 GB, 197 us (5.3 TB/s; its floor is 154); of
-// 64 sequences of 4097 68.3 us, with 128 query heads 106, in fp32 115.  One token of one sequence of
-// 2000: 10.1.  4 queries of 64 sequences, 32 heads of 64 on 8, in a window of 1024: 28.5.
+// token of each of 256 sequences of some 4096, 1.04 GB, 199 us (5.2 TB/s; its floor is 154); of
+// 64 sequences of 4097 68.7 us, with 128 query heads 109, in fp32 113.  One token of one sequence of
+// 2000: 10.0.  4 queries of 64 sequences, 32 heads of 64 on 8, in a window of 1024: 30.3.
+// In fp32 128 queries of 32 heads of 128 on 1024 + 128 keys 46.4, 512 on their own 97: the cache is read
+// once for every eight rows.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -46,10 +48,10 @@ __host__ __device__ constexpr int tile_rows() { return sizeof(T) == 4 ? 4 * NT :
 
 // Registers are given out by a quarter of the SM, so what counts is the warps of a quarter: two of
 // 255 registers, three of 168 or four of 128.  Two column tiles of rows with heads of 128 need the
-// 255 (16 query rows a key head, 64 sequences of 4097, 8 key heads: 122 us, with three warps a quarter
-// and their spills 229, with one tile a step 135); else four are better, in three CTAs (256
-// sequences 206 us, in four of four warps 214, in two of eight 235; heads of 64 51 us, in four
-// CTAs of five warps 56).
+// 255 (16 query rows a key head, 64 sequences of 4097, 8 key heads, when this was chosen: 122 us, with
+// three warps a quarter and their spills 229, with one tile a step 135; now 109); else four are better, in
+// three CTAs (256 sequences then 206 us, in four of four warps 214, in two of eight 235, now 199; heads
+// of 64 then 51 us, in four CTAs of five warps 56, now 46).
 template <int D, int NT>
 __host__ __device__ constexpr int consumers() { return D == 128 && NT == 2 ? 7 : 4; }
 template <int D, int NT>
@@ -69,7 +71,7 @@ static_assert(sizeof(Item4) == 32, "two 16-byte pieces");
 constexpr int32_t kWhole = -1, kNotFirst = -2;
 // What beginning and ending an item costs, in units of 128 keys.  Without it CTAs that
 // get many short items take twice as long as the others (4 queries of 64 sequences, heads of 64, in a
-// window of 1024: 46 us).  One token of 256 sequences of some 4096 took 197, 199 and 201 us with 2, 3
+// window of 1024: 46 us).  When it was chosen one token of 256 sequences of some 4096 took 197, 199 and 201 us with 2, 3
 // and 4, of some 500 46, 48 and 50; 4 queries of 256 sequences of some 700, heads of 64, 58.8, 57.0 and
 // 59.5, in that window 29.1, 28.5 and 27.8.
 template <int D, int NT>

@@ -185,10 +185,10 @@ lora_status_t check_attention(const lora_kv_cache_t *c, const lora_kv_batch_t *b
 // 43.5 against 22.0.  (What the tables have room for is all that the host knows of
 // the lengths: a wider table of the same sequences may take the other kernel.)
 // The 4-bit cache's kernels (attn_decode4.cu in place of the first) take the same rule: 64
-// sequences of 4097, 8 heads of 128, with 16 rows 110 against 203 us, with 32 206 against 203; 64
-// queries of 32 heads on 1064 keys (1152 units) 21.0 against 24.5, 4 x 128 queries
-// (2048 units) 49 against 26.5.  Its heads of 64 take two passes of the first: with 32 rows 116
-// against 161, which a third would use up.
+// sequences of 4097, 8 heads of 128, with 16 rows 109 against 207 us, with 32 203 against 208; 64
+// queries of 32 heads on 1064 keys (1152 units) 22.3 against 24.5, 4 x 128 queries
+// (2048 units) 47.7 against 25.2.  Its heads of 64 take two passes of the first: with 32 rows 121
+// against 162, with 48 175 against 163.
 bool many_queries(const lora::AttnView &v, const lora_kv_cache_t *c, lora_dtype_t dtype) {
     const int64_t rows = static_cast<int64_t>(v.max_queries) * v.group;  // of a sequence, at most
     if (dtype != LORA_BF16 || rows <= (c->format == LORA_KV_UINT4 && c->head_dim == 64 ? 32 : 16)) return false;

@@ -13,10 +13,10 @@
 // group works on heads of q alone or of k alone, so that its weights are read
 // once, and on several heads of a row, so that the angles are.
 // Measured in a graph, bf16, 8192 rows of 72 heads of 128, three axes: 52 us (5.9 TB/s of
-// the 306 MB, 0.87 of a copy), the gradient 88 (5.2); of 40 heads 30 and 51, of 64 15.4 and 30,
-// in fp32 (4096 rows of 128) 29 and 45.  The gradient waits for its own results (shuffles, reads from shared memory,
-// the turn's barrier) with the 14 warps an SM that 128 registers leave.  One token of 64
-// sequences, 40 heads: 2.8 us; the gradient of 333 rows of 40 heads of 64 7.8.
+// the 306 MB, 0.87 of a copy), the gradient 88 (5.2); of 40 heads 29.5 and 51, of 64 15.1 and 30.6,
+// in fp32 (4096 rows of 128) 28.7 and 45.  The gradient waits for its own results (shuffles, reads from
+// shared memory, the turn's barrier) with the 14 warps an SM that 128 registers leave in this layout of a
+// head on its lanes.  One token of 64 sequences, 40 heads: 2.8 us; the gradient of 333 rows of 40 heads of 64 7.8.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -317,8 +317,8 @@ __device__ __forceinline__ void issue_scores(PrefillSmem<D, FMT> &sm, uint32_t X
 // sum of q over them, which has two f16 parts: m twice, and 4 s twice against twice that.  There is
 // room for one stage of the two tiles; each is given back and filled anew by itself
 // (barriers 0 and 1 of k_full and k_empty), so that the first of the next keys is there
-// when the last product with the second of these ends: 2048 queries on 34816 keys 1137 us
-// instead of 1189.
+// when the last product with the second of these ends (2048 queries on 34816 keys 1137 us
+// instead of 1189 when that was chosen).
 template <int D>
 __device__ __forceinline__ void issue_scores_part(PrefillSmem<D, LORA_KV_UINT4> &sm, uint32_t X, uint32_t part) {
     const uint64_t q = desc_kmajor_sw128(smem_u32(sm.q[0])) + X * (sizeof(sm.q[0]) >> 4);
@@ -1336,8 +1336,10 @@ size_t prefill_workspace_bytes(int head_dim) { return split_workspace_bytes(devi
 cudaError_t launch_attn_prefill(const AttnView &v, lora_kv_format_t fmt, int head_dim, cudaStream_t stream) {
     if (fmt == LORA_KV_UINT4) {
         // The scores' rounding shows in lse, which is fp32 (off by 1e-6 with K rounded), not in a
-        // bf16 result beside its own rounding (1.8e-3 from the exact one, 1.7e-3 with K in parts); in
-        // parts 2048 queries of 34816 keys (32 heads of 128, 8 of the cache) take 1137 us instead of 892.
+        // bf16 result beside its own rounding (1.76e-3 from the exact one, 1.67e-3 with K in parts), where
+        // keys lie around 0; at 10 times their spread from it 2.4e-3, at 100 times 1.2e-2 (in parts 1.7e-3
+        // both), which callers are told.  In parts 2048 queries of 34816 keys (32 heads of 128, 8 of the
+        // cache) take 1180 us instead of 912.
         if (v.lse)
             return head_dim == 64 ? prefill_typed<64, LORA_KV_UINT4, true>(v, stream) : prefill_typed<128, LORA_KV_UINT4, true>(v, stream);
         return head_dim == 64 ? prefill_typed<64, LORA_KV_UINT4>(v, stream) : prefill_typed<128, LORA_KV_UINT4>(v, stream);

@@ -86,7 +86,8 @@ lora_status_t lora_rope(const lora_rope_args_t *args, void *stream);
  *
  * (dimensions past rot_dim are normalised, not turned).  Each value is read and
  * written once.  Arithmetic in fp32, squares and their sum included, one
- * rounding to the dtype at the end.  A weight of NULL stands for W = 1.
+ * rounding to the dtype at the end.  A head with an infinity or NaN becomes NaN or 0, no
+ * other head is touched by it.  A weight of NULL stands for W = 1.
  * An output may be its own input (same pointer and strides); other overlaps are
  * not allowed.  Errors: as lora_rope, and UNSUPPORTED for head_dim over 256 or
  * `inverse`; a position out of range leaves its pairs unturned (normalised).
@@ -292,7 +293,10 @@ lora_status_t lora_kv_gather(const lora_kv_cache_t *cache, const lora_kv_batch_t
  * (fp32 calls take a value as scale (code - 8) and least + 8 scale.)  Where a bf16 call takes the one for many,
  * V's values enter rounded to f16 (11 bits), and a p_j is off by at most 2^-29 of the
  * row's largest beyond its 11 bits; K's values enter exactly if lse is given, else rounded
- * to f16, so that `out` of the same call with and without lse may differ in its last bits.
+ * to f16, which moves scores by up to 2^-12 scale sum |q k|.  Where a token's 64 values lie around
+ * 0 (a least value of up to some 15 scales) that is less than 1% of K's own step, and `out` with and
+ * without lse differs by less than bf16's rounding of it; keys far from 0 in all dimensions are another
+ * matter (near 100 and varying by 1: `out` off by 1.2% in the root mean square): give lse for those.
  * Errors: INVALID_ARG, ALIGNMENT, DTYPE, UNSUPPORTED (num_q_heads /
  * num_heads over 64; num_q_heads not a multiple; rows * num_q_heads of 2^31
  * or more), WORKSPACE, CUDA.
